@@ -75,6 +75,25 @@ class _QKV(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+PAIRINGS = {"halves": 0, "adjacent": 1}
+ROPE_WORKSPACE_BYTES = 1048576
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("inv_freq", ctypes.c_void_p),
+                ("axis", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32),
+                ("d", ctypes.c_int32)]
+
+
 class _State(ctypes.Structure):
     _fields_ = [("o_acc", ctypes.c_void_p), ("m", ctypes.c_void_p), ("l", ctypes.c_void_p)]
 
@@ -98,6 +117,11 @@ _SIGS = {
     "marble_permute_cast_bf16": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                   ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p]),
     "marble_release_memory": ([]),
+    "marble_rope": ([ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(_Rope),
+                     ctypes.POINTER(_Heads), ctypes.POINTER(_Heads), ctypes.c_void_p]),
+    "marble_rope_bwd": ([ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(_Rope),
+                         ctypes.POINTER(_Heads), ctypes.POINTER(_Heads), ctypes.POINTER(_Heads),
+                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "marble_attn_step": ([ctypes.c_void_p, ctypes.POINTER(_QKV), ctypes.c_int32, ctypes.c_int32,
                           ctypes.POINTER(_State), ctypes.c_uint32, ctypes.c_void_p]),
     "marble_attn_finalize": ([ctypes.c_void_p, ctypes.POINTER(_State), ctypes.c_int32,
@@ -266,6 +290,172 @@ class Plan:
 
     def check(self, stream=None):
         _call("marble_check", self._h, _stream(stream))
+
+
+def rope_frequencies(sections, theta: float = 10000.0, layout: str = "sections"):
+    """(inv_freq float64 [pairs], axis int32 [pairs]) of rotary positions with len(sections)
+    axes, sections[a] of the pairs belonging to axis a.  With pairs = sum(sections):
+
+    "sections"     one sequence theta^(-i / pairs) over all pairs, the first sections[0] of
+                   them turned by axis 0, the next by axis 1, ...
+    "interleaved"  the same sequence, the axes taking turns pair by pair while theirs last
+    "axial"        a sequence of its own for every axis: theta^(-j / sections[a]), axis by axis
+
+    One axis is the usual rotary position in each of them."""
+    import numpy as np
+    sec = [int(x) for x in sections]
+    if not sec or min(sec) < 0 or sum(sec) == 0:
+        raise ValueError("sections must hold the pairs of every axis")
+    if layout not in ("sections", "interleaved", "axial"):
+        raise ValueError("layout must be 'sections', 'interleaved' or 'axial'")
+    axis = np.repeat(np.arange(len(sec)), sec)
+    i = np.concatenate([np.arange(x) for x in sec])
+    if layout == "axial":
+        return float(theta) ** -(i / np.repeat(sec, sec)), axis.astype(np.int32)
+    if layout == "interleaved":
+        axis = axis[np.lexsort((axis, i))]
+    return float(theta) ** -(np.arange(len(axis)) / len(axis)), axis.astype(np.int32)
+
+
+class Rope:
+    """The frequencies of rotary positions: radians per position and the axis of every rotated
+    pair (see marble.h), host arrays of rot_dim / 2 entries; axis None: all on axis 0.
+    ``pairing``: "halves" pairs channels (i, i + rot_dim / 2), "adjacent" (2 i, 2 i + 1)."""
+
+    def __init__(self, inv_freq, axis=None, pairing: str = "halves"):
+        import numpy as np
+        # copies: the caller's arrays may change after this
+        self.inv_freq = np.array(inv_freq, dtype=np.float64)
+        self.axis = np.zeros(self.inv_freq.shape, np.int32) if axis is None \
+            else np.array(axis, dtype=np.int32)
+        if self.inv_freq.ndim != 1 or self.axis.shape != self.inv_freq.shape:
+            raise ValueError("inv_freq and axis must be 1-D arrays of one length")
+        if pairing not in PAIRINGS:
+            raise ValueError(f"pairing must be one of {sorted(PAIRINGS)}")
+        self.pairing = pairing
+        self.rot_dim = 2 * len(self.inv_freq)
+        self._tables = (self.inv_freq.ctypes.data, self.axis.ctypes.data)
+
+    def _c(self, pos, q_weight, k_weight, eps):
+        return _Rope(pos.shape[0], self.rot_dim, PAIRINGS[self.pairing], *self._tables,
+                     pos.data_ptr(),
+                     None if q_weight is None else q_weight.data_ptr(),
+                     None if k_weight is None else k_weight.data_ptr(), float(eps))
+
+
+def _heads(q, k, v, n, dtype, device, what):
+    """marble_heads_t of [n, heads, d] tensors (None: absent) whose tokens may be strided."""
+    import torch
+    hq = hkv = d = 0
+    ptr, stride = [None, None, None], [0, 0, 0]
+    for i, (t, nm) in enumerate(((q, "q"), (k, "k"), (v, "v"))):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 3:
+            raise ValueError(f"{what}{nm} must be a {dtype} tensor [n, heads, d]")
+        if t.device != device:
+            raise ValueError(f"{what}{nm} must be on {device}")
+        s = t.shape
+        if s[0] != n or (d and s[2] != d) or (i == 2 and hkv and s[1] != hkv):
+            raise ValueError(f"{what}{nm} has shape {tuple(s)}: n, d or the kv heads differ")
+        d = s[2]
+        if n > 0 and ((s[1] > 1 and t.stride(1) != d) or t.stride(2) != 1):
+            raise ValueError(f"{what}{nm}: the heads of a token must be contiguous")
+        if i == 0:
+            hq = s[1]
+        else:
+            hkv = s[1]
+        ptr[i] = t.data_ptr()
+        stride[i] = t.stride(0) if n > 1 else s[1] * d
+    return _Heads(*ptr, *stride, hq, hkv, d)
+
+
+def _rope_args(pos, plan, q_weight, k_weight, d):
+    import torch
+    if not isinstance(pos, torch.Tensor) or pos.dim() != 2:
+        raise ValueError("pos must be an int32 CUDA tensor [axes, n]")
+    _need(pos, torch.int32, "pos")
+    if plan is not None and pos.shape[1] != plan.n:
+        raise ValueError("pos must have the plan's N columns")
+    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, torch.float32, nm, (d,))
+            if w.device != pos.device:
+                raise ValueError(f"{nm} must be on {pos.device}")
+    return pos.shape[1], pos.device
+
+
+def _on_device(device):
+    import torch
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+
+
+def rope(rope: Rope, pos, q, k=None, v=None, plan: Optional[Plan] = None, q_weight=None,
+         k_weight=None, eps: float = 1e-6, out=None, stream=None):
+    """Rotary positions of q and k, after their heads' RMS norm where a weight is given, and the
+    move of q, k and v into plan order, in one pass (marble_rope).
+
+    pos: int32 [axes, n], original order.  q [n, hq, d], k and v [n, hkv, d]: bf16, original
+    order, each token's heads contiguous (slices of a fused projection are fine); k and v may
+    be None.  plan None: the order stays, any n, and ``out`` may be (q, k, v) itself.
+    Returns (q, k, v) in plan order, ``out`` or new tensors."""
+    import torch
+    n, dev = _rope_args(pos, plan, q_weight, k_weight, q.shape[-1])
+    _on_device(dev)
+    src = _heads(q, k, v, n, torch.bfloat16, dev, "")
+    if out is None:
+        with torch.cuda.stream(stream):  # new tensors belong to the stream that writes them
+            out = tuple(None if t is None else
+                        torch.empty(t.shape, dtype=torch.bfloat16, device=dev) for t in (q, k, v))
+    if [None if t is None else t.shape for t in out] != \
+            [None if t is None else t.shape for t in (q, k, v)]:
+        raise ValueError("out must hold one tensor of the same shape for each of q, k and v")
+    dst = _heads(*out, n, torch.bfloat16, dev, "out ")
+    c = rope._c(pos, q_weight, None if k is None else k_weight, eps)
+    _call("marble_rope", None if plan is None else plan.handle, n, ctypes.byref(c),
+          ctypes.byref(src), ctypes.byref(dst), _stream(stream))
+    return tuple(out)
+
+
+def rope_bwd(rope: Rope, pos, dq, dk=None, dv=None, plan: Optional[Plan] = None, q=None, k=None,
+             q_weight=None, k_weight=None, eps: float = 1e-6, out=None, stream=None):
+    """The gradient of rope() (marble_rope_bwd): fp32 gradients dq, dk, dv of its results in
+    plan order (the accumulators of backward()) to bf16 gradients of its inputs in original
+    order, in one pass.  Where the forward had a norm weight, q / k are its inputs.
+    Returns (dq, dk, dv, dq_weight, dk_weight), the first three in ``out`` (a token's heads
+    contiguous: slices of a fused gradient are fine) or new tensors, the weights' fp32 or None."""
+    import torch
+    n, dev = _rope_args(pos, plan, q_weight, k_weight, dq.shape[-1])
+    _on_device(dev)
+    if dk is None:
+        k_weight = None
+    grad = _heads(dq, dk, dv, n, torch.float32, dev, "d")
+    if out is None:
+        with torch.cuda.stream(stream):  # new tensors belong to the stream that writes them
+            out = tuple(None if t is None else
+                        torch.empty(t.shape, dtype=torch.bfloat16, device=dev)
+                        for t in (dq, dk, dv))
+    if [None if t is None else t.shape for t in out] != \
+            [None if t is None else t.shape for t in (dq, dk, dv)]:
+        raise ValueError("out must hold one tensor of the same shape for each of dq, dk and dv")
+    dx = _heads(*out, n, torch.bfloat16, dev, "out d")
+    dw, ws, x = [None, None], None, None
+    if q_weight is not None or k_weight is not None:
+        for w, t, g, nm in ((q_weight, q, dq, "q"), (k_weight, k, dk, "k")):
+            if w is not None and (t is None or t.shape != g.shape):
+                raise ValueError(f"{nm}, the input of rope(), is needed for the norm's gradient")
+        x = _heads(q if q_weight is not None else None, k if k_weight is not None else None, None,
+                   n, torch.bfloat16, dev, "")
+        with torch.cuda.stream(stream):
+            dw = [None if w is None else torch.empty_like(w) for w in (q_weight, k_weight)]
+            ws = torch.empty(ROPE_WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
+    c = rope._c(pos, q_weight, k_weight, eps)
+    _call("marble_rope_bwd", None if plan is None else plan.handle, n, ctypes.byref(c),
+          None if x is None else ctypes.byref(x), ctypes.byref(grad), ctypes.byref(dx),
+          *(None if t is None else _ptr(t) for t in dw), None if ws is None else _ptr(ws),
+          _stream(stream))
+    return (*out, *dw)
 
 
 class State:

@@ -674,6 +674,223 @@ MARBLE_API marble_status_t marble_permute_cast_bf16(const marble_plan_t* p, cons
   return MARBLE_OK;
 }
 
+// ------------------------------------------------------------------------------------
+// rotary positions
+// ------------------------------------------------------------------------------------
+namespace {
+
+// device memory of the device that is current, where the launch will run
+marble_status_t check_here(const void* p, const char* name, int align) {
+  if (!p) return fail(MARBLE_ERR_INVALID_ARG, std::string(name) + " is null");
+  if (reinterpret_cast<uintptr_t>(p) % (unsigned)align)
+    return fail(MARBLE_ERR_INVALID_ARG,
+                std::string(name) + " is not " + std::to_string(align) + "-byte aligned");
+  cudaPointerAttributes a;
+  const cudaError_t e = cudaPointerGetAttributes(&a, p);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  if (e != cudaSuccess || (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged))
+    return fail(MARBLE_ERR_INVALID_ARG, std::string(name) + " is not device memory");
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || (a.type == cudaMemoryTypeDevice && a.device != dev))
+    return fail(MARBLE_ERR_INVALID_ARG, std::string(name) + " is not on the current device");
+  return MARBLE_OK;
+}
+
+marble_status_t check_plan_here(const marble_plan_t* p) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || p->device != dev)
+    return fail(MARBLE_ERR_INVALID_ARG, "the plan is not on the current device");
+  return MARBLE_OK;
+}
+
+// is work being captured on `s`?  (an error of the query counts as a failure of the call)
+marble_status_t capturing(cudaStream_t s, bool* out) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(s, &st);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return cuda_fail(e, "capture status of the stream");
+  }
+  *out = st != cudaStreamCaptureStatusNone;
+  return MARBLE_OK;
+}
+
+// rows of `width` bytes, `stride` bytes apart
+struct Rows {
+  const char* base;
+  int64_t stride, width;
+  bool same(const Rows& o) const {
+    return base == o.base && stride == o.stride && width == o.width;
+  }
+};
+
+// may any byte belong to both?  Views of one stride are compared within a row, so that the
+// slices of a fused tensor are told apart; others by their whole ranges.
+bool rows_meet(const Rows& a, const Rows& b, int64_t n) {
+  const char* ae = a.base + (n - 1) * a.stride + a.width;
+  const char* be = b.base + (n - 1) * b.stride + b.width;
+  if (ae <= b.base || be <= a.base) return false;
+  if (a.stride != b.stride) return true;
+  const int64_t off = (((b.base - a.base) % a.stride) + a.stride) % a.stride;
+  return off < a.width || off + b.width > a.stride;
+}
+
+// the present tensors of `h` (q, k, v as bit 0, 1, 2 of `parts`) as rows of elem-byte elements
+marble_status_t check_heads(const marble_heads_t* h, const char* name, int elem, int parts,
+                            Rows (&out)[3]) {
+  const void* ptr[3] = {h->q, h->k, h->v};
+  const int64_t stride[3] = {h->q_stride, h->k_stride, h->v_stride};
+  static const char* const kPart[3] = {".q", ".k", ".v"};
+  for (int i = 0; i < 3; ++i) {
+    if (!(parts >> i & 1)) continue;
+    const std::string what = std::string(name) + kPart[i];
+    marble_status_t st = check_here(ptr[i], what.c_str(), 16);
+    if (st != MARBLE_OK) return st;
+    const int64_t width = (int64_t)(i == 0 ? h->hq : h->hkv) * h->d;
+    if (stride[i] < width || stride[i] * elem % 16 || stride[i] > ((int64_t)1 << 40))
+      return fail(MARBLE_ERR_INVALID_ARG,
+                  what + ": the stride must hold the token's heads and be a multiple of 16 bytes");
+    out[i] = Rows{static_cast<const char*>(ptr[i]), stride[i] * elem, width * elem};
+  }
+  return MARBLE_OK;
+}
+
+// what both directions check: the descriptor, the order, and that `a` and `b` (the tensors read
+// and written) hold the same heads.  *parts: the tensors that are present.
+marble_status_t check_rope(const marble_plan_t* p, int64_t n, const marble_rope_t* r,
+                           const marble_heads_t* a, const marble_heads_t* b, int* parts) {
+  if (!r || !a || !b) return fail(MARBLE_ERR_INVALID_ARG, "rope and the heads must be non-null");
+  if (n < 0 || n >= (int64_t)INT_MAX)
+    return fail(MARBLE_ERR_INVALID_ARG, "n_tokens must be in [0, 2^31 - 1)");
+  if (a->d != 64 && a->d != 128) return fail(MARBLE_ERR_INVALID_ARG, "head dim d must be 64 or 128");
+  if (a->d != b->d || a->hq != b->hq || a->hkv != b->hkv)
+    return fail(MARBLE_ERR_INVALID_ARG, "the heads of the two sides differ");
+  *parts = (a->q ? 1 : 0) | (a->k ? 2 : 0) | (a->v ? 4 : 0);
+  if (n > 0 && *parts != ((b->q ? 1 : 0) | (b->k ? 2 : 0) | (b->v ? 4 : 0)))
+    return fail(MARBLE_ERR_INVALID_ARG, "the two sides do not hold the same tensors");
+  if (((*parts & 1) && (a->hq < 1 || a->hq > 65536)) ||
+      ((*parts & 6) && (a->hkv < 1 || a->hkv > 65536)))
+    return fail(MARBLE_ERR_INVALID_ARG, "hq and hkv must be in [1, 65536]");
+  if (r->n_axes < 1 || r->n_axes > 8) return fail(MARBLE_ERR_INVALID_ARG, "n_axes must be in [1, 8]");
+  if (r->rot_dim < 16 || r->rot_dim % 16 || r->rot_dim > a->d)
+    return fail(MARBLE_ERR_INVALID_ARG, "rot_dim must be a positive multiple of 16, at most d");
+  if (r->pairing != MARBLE_PAIR_HALVES && r->pairing != MARBLE_PAIR_ADJACENT)
+    return fail(MARBLE_ERR_INVALID_ARG, "unknown pairing");
+  if (!r->inv_freq || !r->axis)
+    return fail(MARBLE_ERR_INVALID_ARG, "inv_freq and axis must be non-null");
+  for (int i = 0; i < r->rot_dim / 2; ++i) {
+    if (!std::isfinite(r->inv_freq[i]))
+      return fail(MARBLE_ERR_INVALID_ARG, "inv_freq must be finite");
+    if (r->axis[i] < 0 || r->axis[i] >= r->n_axes)
+      return fail(MARBLE_ERR_INVALID_ARG, "axis out of range");
+  }
+  if (!(r->eps >= 0.f) || std::isinf(r->eps))
+    return fail(MARBLE_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (p) {
+    if (n != p->n) return fail(MARBLE_ERR_INVALID_ARG, "n_tokens is not the plan's");
+    marble_status_t st = check_plan_here(p);
+    if (st != MARBLE_OK) return st;
+  }
+  return MARBLE_OK;
+}
+
+marble_status_t check_rope_tensors(const marble_rope_t* r) {
+  marble_status_t st;
+  if ((st = check_here(r->pos, "pos", 4)) != MARBLE_OK) return st;
+  if (r->q_weight && (st = check_here(r->q_weight, "q_weight", 4)) != MARBLE_OK) return st;
+  if (r->k_weight && (st = check_here(r->k_weight, "k_weight", 4)) != MARBLE_OK) return st;
+  return MARBLE_OK;
+}
+
+// written rows against rows read (the same rows allowed where `in_place` says so) and against
+// one another
+marble_status_t check_overlap(const Rows (&w)[3], const Rows (&r)[3], int written, int read,
+                              bool in_place, const char* what, int64_t n) {
+  for (int i = 0; i < 3; ++i) {
+    if (!(written >> i & 1)) continue;
+    for (int j = 0; j < 3; ++j) {
+      if ((read >> j & 1) && rows_meet(w[i], r[j], n) && !(in_place && i == j && w[i].same(r[j])))
+        return fail(MARBLE_ERR_INVALID_ARG, what);
+      if (j < i && (written >> j & 1) && rows_meet(w[i], w[j], n))
+        return fail(MARBLE_ERR_INVALID_ARG, "the tensors written overlap each other");
+    }
+  }
+  return MARBLE_OK;
+}
+
+}  // namespace
+
+MARBLE_API marble_status_t marble_rope(const marble_plan_t* p, int64_t n, const marble_rope_t* rope,
+                                       const marble_heads_t* src, const marble_heads_t* dst,
+                                       marble_stream_t stream) {
+  NvtxRange nvtx_("marble_rope");
+  int parts = 0;
+  marble_status_t st = check_rope(p, n, rope, src, dst, &parts);
+  if (st != MARBLE_OK || n == 0 || parts == 0) return st;
+  if ((st = check_rope_tensors(rope)) != MARBLE_OK) return st;
+  Rows a[3], b[3];
+  if ((st = check_heads(src, "src", 2, parts, a)) != MARBLE_OK) return st;
+  if ((st = check_heads(dst, "dst", 2, parts, b)) != MARBLE_OK) return st;
+  if ((st = check_overlap(b, a, parts, parts, !p, "src and dst overlap", n)) != MARBLE_OK) return st;
+  bool cap = false;
+  if ((st = capturing((cudaStream_t)stream, &cap)) != MARBLE_OK) return st;
+  const cudaError_t e = launch_rope(p, n, rope, src, dst, (cudaStream_t)stream);
+  if (p && !cap) plan_used(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "marble_rope launch");
+  return MARBLE_OK;
+}
+
+MARBLE_API marble_status_t marble_rope_bwd(const marble_plan_t* p, int64_t n,
+                                           const marble_rope_t* rope, const marble_heads_t* x,
+                                           const marble_heads_t* grad, const marble_heads_t* dx,
+                                           float* d_q_weight, float* d_k_weight, void* workspace,
+                                           marble_stream_t stream) {
+  NvtxRange nvtx_("marble_rope_bwd");
+  int parts = 0;
+  marble_status_t st = check_rope(p, n, rope, grad, dx, &parts);
+  if (st != MARBLE_OK) return st;
+  // the norms that act: those of tensors that are present (or could be, in an empty batch)
+  marble_rope_t r = *rope;
+  if (n > 0 && !(parts & 1)) r.q_weight = nullptr;
+  if (n > 0 && !(parts & 2)) r.k_weight = nullptr;
+  if (n == 0 && !d_q_weight) r.q_weight = nullptr;
+  if (n == 0 && !d_k_weight) r.k_weight = nullptr;
+  const int normed = (r.q_weight ? 1 : 0) | (r.k_weight ? 2 : 0);
+  if (n > 0 && parts == 0) return MARBLE_OK;
+  if (n == 0 && !normed) return MARBLE_OK;
+  Rows g[3], b[3], xr[3];
+  if (n > 0) {
+    if ((st = check_rope_tensors(&r)) != MARBLE_OK) return st;
+    if ((st = check_heads(grad, "grad", 4, parts, g)) != MARBLE_OK) return st;
+    if ((st = check_heads(dx, "dx", 2, parts, b)) != MARBLE_OK) return st;
+    if ((st = check_overlap(b, g, parts, parts, false, "grad and dx overlap", n)) != MARBLE_OK)
+      return st;
+  }
+  if (normed) {
+    if (n > 0) {
+      if (!x) return fail(MARBLE_ERR_INVALID_ARG, "x is null: the gradient of the norm reads it");
+      if (x->d != grad->d || ((normed & 1) && x->hq != grad->hq) ||
+          ((normed & 2) && x->hkv != grad->hkv))
+        return fail(MARBLE_ERR_INVALID_ARG, "the heads of x and grad differ");
+      if ((st = check_heads(x, "x", 2, normed, xr)) != MARBLE_OK) return st;
+      if ((st = check_overlap(b, xr, parts, normed, true, "x and dx overlap", n)) != MARBLE_OK)
+        return st;
+    }
+    if ((normed & 1) && (st = check_here(d_q_weight, "d_q_weight", 4)) != MARBLE_OK) return st;
+    if ((normed & 2) && (st = check_here(d_k_weight, "d_k_weight", 4)) != MARBLE_OK) return st;
+    if ((st = check_here(workspace, "workspace", 16)) != MARBLE_OK) return st;
+  }
+  bool cap = false;
+  if ((st = capturing((cudaStream_t)stream, &cap)) != MARBLE_OK) return st;
+  const cudaError_t e =
+      launch_rope_bwd(p, n, &r, normed ? x : nullptr, grad, dx, (normed & 1) ? d_q_weight : nullptr,
+                      (normed & 2) ? d_k_weight : nullptr, static_cast<float*>(workspace),
+                      (cudaStream_t)stream);
+  if (p && !cap) plan_used(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "marble_rope_bwd launch");
+  return MARBLE_OK;
+}
+
 constexpr uint32_t kMergeBits = MARBLE_STEP_BF16_MERGE | MARBLE_STEP_FP32_MERGE;
 
 // known bits only, and at most one merge variant

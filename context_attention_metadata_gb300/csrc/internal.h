@@ -182,6 +182,13 @@ cudaError_t launch_finalize(const marble_plan_t* p, const float* o_acc, const fl
                             const float* l, int hq, int d, void* o, float* lse, cudaStream_t s);
 cudaError_t launch_bwd_prep(const marble_plan_t* p, const void* o, const void* d_o, int hq, int d,
                             float* delta, cudaStream_t s);
+// rotary positions, head norm and move (rope.cu); arguments are checked by the caller
+cudaError_t launch_rope(const marble_plan_t* plan, int64_t n, const marble_rope_t* rope,
+                        const marble_heads_t* src, const marble_heads_t* dst, cudaStream_t s);
+cudaError_t launch_rope_bwd(const marble_plan_t* plan, int64_t n, const marble_rope_t* rope,
+                            const marble_heads_t* x, const marble_heads_t* grad,
+                            const marble_heads_t* dx, float* dwq, float* dwk, float* workspace,
+                            cudaStream_t s);
 cudaError_t launch_debug_wait(unsigned* err, uint64_t limit_ns, cudaStream_t s);
 
 // attention (attn_fwd.cu, attn_bwd.cu): a list of ring steps launched back to back on `s`

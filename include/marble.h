@@ -291,6 +291,82 @@ marble_status_t marble_permute_cast_bf16(const marble_plan_t *plan, const float 
                                          void *dst, int64_t row_elems, int32_t inverse,
                                          marble_stream_t stream);
 
+/*
+ * Rotary positions with several axes (time, height, width of a packed multimodal sequence),
+ * with the heads' RMS norm and the move into plan order in the same pass over q, k and v.
+ *
+ * Rotated pair i (0 <= i < rot_dim / 2) of a token's head, (a, b), is turned by the angle
+ *   pos[axis[i]] * inv_freq[i]:   a' = a cos - b sin,   b' = a sin + b cos,
+ * for every head of q and k.  The pair is channels (i, i + rot_dim / 2) with
+ * MARBLE_PAIR_HALVES, (2 i, 2 i + 1) with MARBLE_PAIR_ADJACENT; the channels from rot_dim on
+ * are passed through.  With a norm weight, a head is first scaled to
+ *   x * w / sqrt(mean(x^2) + eps)
+ * over its d channels (also those that are not rotated).  v is only moved.
+ * The angle is formed in 64-bit fixed point: its error does not grow with the position.  All
+ * arithmetic is in fp32, rounded to bf16 (nearest even) once.
+ */
+typedef enum {
+  MARBLE_PAIR_HALVES = 0,
+  MARBLE_PAIR_ADJACENT = 1
+} marble_pairing_t;
+
+typedef struct {
+  int32_t n_axes;         /* 1 .. 8 */
+  int32_t rot_dim;        /* rotated channels of a head: a multiple of 16, at most d */
+  int32_t pairing;        /* marble_pairing_t */
+  const double *inv_freq; /* host double[rot_dim / 2], finite: radians per position */
+  const int32_t *axis;    /* host int32[rot_dim / 2], in [0, n_axes) */
+  const int32_t *pos;     /* device int32[n_axes][n_tokens], ORIGINAL order, any values */
+  const float *q_weight;  /* device float[d], or NULL: no norm of the q heads */
+  const float *k_weight;  /* device float[d], or NULL: no norm of the k heads */
+  float eps;              /* finite, >= 0; used where there is a norm */
+} marble_rope_t;
+
+/* The heads of a layer: q [n, hq, d], k and v [n, hkv, d], each token's heads contiguous and
+ * tokens *_stride elements apart (hq * d or more; slices of one fused projection are three
+ * such views).  A NULL tensor takes no part in the call.  Pointers 16-byte aligned, strides
+ * multiples of 16 bytes; d = 64 or 128; hq and hkv are independent here. */
+typedef struct {
+  void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride; /* in elements */
+  int32_t hq, hkv, d;
+} marble_heads_t;
+
+/*
+ * dst[i] = rotated(norm(src[perm[i]])) for q and k, dst[i] = src[perm[i]] for v: original
+ * order in, plan order out, bf16 both.  plan == NULL leaves the order as it is and takes any
+ * n_tokens >= 0 (a single token of a sequence being generated, a batch of them); with a plan
+ * n_tokens is the plan's.  The same tensors are present in src and dst.
+ * dst may not overlap src, but for plan == NULL, where a tensor may be rewritten in place
+ * (the same pointer and stride).  The tensors of dst may not overlap each other; interleaved
+ * views (the slices above) do not.
+ * May be captured into a graph; the plan then has to outlive the graph.
+ * Errors: INVALID_ARG; CUDA.
+ */
+marble_status_t marble_rope(const marble_plan_t *plan, int64_t n_tokens,
+                            const marble_rope_t *rope, const marble_heads_t *src,
+                            const marble_heads_t *dst, marble_stream_t stream);
+
+/*
+ * The gradient of marble_rope: grad holds fp32 gradients of its results in plan order (the
+ * accumulators of marble_attn_bwd), dx takes those of its inputs, bf16 in original order:
+ * turned back, through the norm, scattered and cast in one pass.  Where the forward had a norm
+ * weight, x holds its bf16 inputs q and k (original order; v of x is not read), and
+ * d_q_weight / d_k_weight (device float[d]) receive the weights' gradients, summed over every
+ * token and head in fp32 in a fixed order; workspace is then device memory of
+ * MARBLE_ROPE_WORKSPACE_BYTES, used by this call alone until it has completed.  Without a norm
+ * x, workspace and the two outputs may be NULL.  dx follows the rules of dst above; a tensor of
+ * dx may also be the same tensor as x's (same pointer and stride).
+ * May be captured into a graph (one workspace per graph that may run at the same time).
+ * Errors: INVALID_ARG; CUDA.
+ */
+#define MARBLE_ROPE_WORKSPACE_BYTES 1048576
+marble_status_t marble_rope_bwd(const marble_plan_t *plan, int64_t n_tokens,
+                                const marble_rope_t *rope, const marble_heads_t *x,
+                                const marble_heads_t *grad, const marble_heads_t *dx,
+                                float *d_q_weight, float *d_k_weight, void *workspace,
+                                marble_stream_t stream);
+
 /* Queries, keys and values in plan order (layouts above). scale <= 0 selects 1/sqrt(d)
  * (LIBRA Eq. 1). */
 typedef struct {
