@@ -12,6 +12,7 @@ accumulation), s04 (sparse all-to-all, layout transforms).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, Optional
@@ -345,50 +346,69 @@ class Rope:
 
 def _heads(q, k, v, n, dtype, device, what):
     """marble_heads_t of [n, heads, d] tensors (None: absent) whose tokens may be strided."""
-    import torch
-    hq = hkv = d = 0
-    ptr, stride = [None, None, None], [0, 0, 0]
-    for i, (t, nm) in enumerate(((q, "q"), (k, "k"), (v, "v"))):
+    c = _Heads()
+    d = hkv = 0
+    for t, nm in ((q, "q"), (k, "k"), (v, "v")):
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 3:
+        try:
+            (rows, heads, dd), (s0, s1, s2) = t.shape, t.stride()
+            ok = t.dtype is dtype
+        except (AttributeError, ValueError, TypeError):
+            ok = False
+        if not ok:
             raise ValueError(f"{what}{nm} must be a {dtype} tensor [n, heads, d]")
         if t.device != device:
             raise ValueError(f"{what}{nm} must be on {device}")
-        s = t.shape
-        if s[0] != n or (d and s[2] != d) or (i == 2 and hkv and s[1] != hkv):
-            raise ValueError(f"{what}{nm} has shape {tuple(s)}: n, d or the kv heads differ")
-        d = s[2]
-        if n > 0 and ((s[1] > 1 and t.stride(1) != d) or t.stride(2) != 1):
+        if rows != n or (d and dd != d) or (nm == "v" and hkv and heads != hkv):
+            raise ValueError(f"{what}{nm} has shape {tuple(t.shape)}: n, d or the kv heads differ")
+        if n > 0 and ((heads > 1 and s1 != dd) or s2 != 1):
             raise ValueError(f"{what}{nm}: the heads of a token must be contiguous")
-        if i == 0:
-            hq = s[1]
+        d, ptr, stride = dd, t.data_ptr(), s0 if n > 1 else heads * dd
+        if nm == "q":
+            c.q, c.q_stride, c.hq = ptr, stride, heads
+        elif nm == "k":
+            c.k, c.k_stride, c.hkv = ptr, stride, heads
+            hkv = heads
         else:
-            hkv = s[1]
-        ptr[i] = t.data_ptr()
-        stride[i] = t.stride(0) if n > 1 else s[1] * d
-    return _Heads(*ptr, *stride, hq, hkv, d)
+            c.v, c.v_stride, c.hkv = ptr, stride, heads
+    c.d = d
+    return c
 
 
-def _rope_args(pos, plan, q_weight, k_weight, d):
+def _rope_args(pos, plan, q_weight, k_weight, first):
     import torch
     if not isinstance(pos, torch.Tensor) or pos.dim() != 2:
         raise ValueError("pos must be an int32 CUDA tensor [axes, n]")
     _need(pos, torch.int32, "pos")
-    if plan is not None and pos.shape[1] != plan.n:
+    if not isinstance(first, torch.Tensor) or first.dim() != 3:
+        raise ValueError("q must be a tensor [n, heads, d]")
+    n = pos.shape[1]
+    if plan is not None and n != plan.n:
         raise ValueError("pos must have the plan's N columns")
+    dev = pos.device
     for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
-            _need(w, torch.float32, nm, (d,))
-            if w.device != pos.device:
-                raise ValueError(f"{nm} must be on {pos.device}")
-    return pos.shape[1], pos.device
+            _need(w, torch.float32, nm, (first.shape[2],))
+            if w.device != dev:
+                raise ValueError(f"{nm} must be on {dev}")
+    return n, dev
 
 
-def _on_device(device):
+def _rope_out(like, out, names, dtype, device, stream):
+    """``out`` checked against the tensors it is for, or new tensors like them: those belong to
+    the stream that writes them."""
     import torch
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, which is not the current device")
+    if out is None:
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return _rope_out(like, None, names, dtype, device, None)
+        return tuple([None if t is None else torch.empty(t.shape, dtype=dtype, device=device)
+                      for t in like])
+    if len(out) != 3 or any((a is None) != (b is None) or (a is not None and a.shape != b.shape)
+                            for a, b in zip(out, like)):
+        raise ValueError(f"out must hold one tensor of the same shape for each of {names}")
+    return tuple(out)
 
 
 def rope(rope: Rope, pos, q, k=None, v=None, plan: Optional[Plan] = None, q_weight=None,
@@ -401,21 +421,15 @@ def rope(rope: Rope, pos, q, k=None, v=None, plan: Optional[Plan] = None, q_weig
     be None.  plan None: the order stays, any n, and ``out`` may be (q, k, v) itself.
     Returns (q, k, v) in plan order, ``out`` or new tensors."""
     import torch
-    n, dev = _rope_args(pos, plan, q_weight, k_weight, q.shape[-1])
-    _on_device(dev)
-    src = _heads(q, k, v, n, torch.bfloat16, dev, "")
-    if out is None:
-        with torch.cuda.stream(stream):  # new tensors belong to the stream that writes them
-            out = tuple(None if t is None else
-                        torch.empty(t.shape, dtype=torch.bfloat16, device=dev) for t in (q, k, v))
-    if [None if t is None else t.shape for t in out] != \
-            [None if t is None else t.shape for t in (q, k, v)]:
-        raise ValueError("out must hold one tensor of the same shape for each of q, k and v")
-    dst = _heads(*out, n, torch.bfloat16, dev, "out ")
+    n, dev = _rope_args(pos, plan, q_weight, k_weight, q)
+    bf16 = torch.bfloat16
+    src = _heads(q, k, v, n, bf16, dev, "")
+    out = _rope_out((q, k, v), out, "q, k and v", bf16, dev, stream)
+    dst = _heads(*out, n, bf16, dev, "out ")
     c = rope._c(pos, q_weight, None if k is None else k_weight, eps)
     _call("marble_rope", None if plan is None else plan.handle, n, ctypes.byref(c),
           ctypes.byref(src), ctypes.byref(dst), _stream(stream))
-    return tuple(out)
+    return out
 
 
 def rope_bwd(rope: Rope, pos, dq, dk=None, dv=None, plan: Optional[Plan] = None, q=None, k=None,
@@ -426,36 +440,30 @@ def rope_bwd(rope: Rope, pos, dq, dk=None, dv=None, plan: Optional[Plan] = None,
     Returns (dq, dk, dv, dq_weight, dk_weight), the first three in ``out`` (a token's heads
     contiguous: slices of a fused gradient are fine) or new tensors, the weights' fp32 or None."""
     import torch
-    n, dev = _rope_args(pos, plan, q_weight, k_weight, dq.shape[-1])
-    _on_device(dev)
+    n, dev = _rope_args(pos, plan, q_weight, k_weight, dq)
+    bf16 = torch.bfloat16
     if dk is None:
         k_weight = None
     grad = _heads(dq, dk, dv, n, torch.float32, dev, "d")
-    if out is None:
-        with torch.cuda.stream(stream):  # new tensors belong to the stream that writes them
-            out = tuple(None if t is None else
-                        torch.empty(t.shape, dtype=torch.bfloat16, device=dev)
-                        for t in (dq, dk, dv))
-    if [None if t is None else t.shape for t in out] != \
-            [None if t is None else t.shape for t in (dq, dk, dv)]:
-        raise ValueError("out must hold one tensor of the same shape for each of dq, dk and dv")
-    dx = _heads(*out, n, torch.bfloat16, dev, "out d")
-    dw, ws, x = [None, None], None, None
+    out = _rope_out((dq, dk, dv), out, "dq, dk and dv", bf16, dev, stream)
+    dx = _heads(*out, n, bf16, dev, "out d")
+    dwq = dwk = ws = x = None
     if q_weight is not None or k_weight is not None:
         for w, t, g, nm in ((q_weight, q, dq, "q"), (k_weight, k, dk, "k")):
             if w is not None and (t is None or t.shape != g.shape):
                 raise ValueError(f"{nm}, the input of rope(), is needed for the norm's gradient")
         x = _heads(q if q_weight is not None else None, k if k_weight is not None else None, None,
-                   n, torch.bfloat16, dev, "")
-        with torch.cuda.stream(stream):
-            dw = [None if w is None else torch.empty_like(w) for w in (q_weight, k_weight)]
+                   n, bf16, dev, "")
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            dwq = None if q_weight is None else torch.empty_like(q_weight)
+            dwk = None if k_weight is None else torch.empty_like(k_weight)
             ws = torch.empty(ROPE_WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
     c = rope._c(pos, q_weight, k_weight, eps)
     _call("marble_rope_bwd", None if plan is None else plan.handle, n, ctypes.byref(c),
           None if x is None else ctypes.byref(x), ctypes.byref(grad), ctypes.byref(dx),
-          *(None if t is None else _ptr(t) for t in dw), None if ws is None else _ptr(ws),
-          _stream(stream))
-    return (*out, *dw)
+          None if dwq is None else _ptr(dwq), None if dwk is None else _ptr(dwk),
+          None if ws is None else _ptr(ws), _stream(stream))
+    return (*out, dwq, dwk)
 
 
 class State:

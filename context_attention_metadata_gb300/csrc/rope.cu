@@ -179,7 +179,7 @@ __device__ __forceinline__ void weights_of(const Tables<D>& t, int which, int j,
 }
 
 template <int D, bool kAdjacent>
-__global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 4) k_rope(const __grid_constant__ RopeParams p) {
   constexpr int kTpr = D / 16, kHpi = 32 / kTpr;
   __shared__ Tables<D> t;
   fill_tables<D, kAdjacent>(p, t);
@@ -187,199 +187,208 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ RopeP
   const bool rotated = j < p.rot_chunks;
   int ca, cb;
   chunks_of<kAdjacent>(j, p.rot_chunks, &ca, &cb);
-  const int64_t warps = (int64_t)gridDim.x * kWarps;
-  const int groups = p.part[0].groups + p.part[1].groups + p.part[2].groups;
-  for (int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); w < p.n * p.split;
-       w += warps) {
-    const int64_t i = w / p.split;
+  const unsigned items = (unsigned)(p.n * p.split), warps = gridDim.x * kWarps;
+  for (unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5); w < items; w += warps) {
+    const int64_t i = p.split == 1 ? w : w / (unsigned)p.split;
     const int64_t o = p.perm ? p.perm[i] : i;
+    int g = (int)(w - (unsigned)i * p.split);  // the warp's groups: g, g + split, ...
     float c[8], s[8];
     angles<D>(p, t, j, o, c, s);
-    for (int g = (int)(w % p.split); g < groups; g += p.split) {
-      const int which = g < p.part[0].groups ? 0 : g < p.part[0].groups + p.part[1].groups ? 1 : 2;
+#pragma unroll
+    for (int which = 0; which < 3; ++which) {
       const HeadPart& hp = p.part[which];
-      const int g0 = which == 0 ? 0 : which == 1 ? p.part[0].groups : p.part[0].groups + p.part[1].groups;
-      const int h = (g - g0) * kHpi + sub;
-      const bool live = h < hp.heads;
-      const uint4* src = static_cast<const uint4*>(hp.src) + (o * hp.src_stride + (int64_t)h * D) / 8;
-      uint4* dst = static_cast<uint4*>(hp.dst) + (i * hp.dst_stride + (int64_t)h * D) / 8;
-      uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
-      if (live) {
-        ra = __ldcs(src + ca);
-        rb = __ldcs(src + cb);
-      }
-      // channels that are neither scaled nor turned keep their bits (a NaN's too)
-      if (which < 2 && (rotated || p.weight[which])) {
-        float va[8], vb[8], a[8], b[8];
-        unpack8(ra, va);
-        unpack8(rb, vb);
-        to_pairs<kAdjacent>(va, vb, a, b);
-        if (p.weight[which]) {
-          float ss = 0.f, wt[16];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) ss = fmaf(a[u], a[u], fmaf(b[u], b[u], ss));
-          const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
-          weights_of<D>(t, which, j, wt);
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            a[u] *= r * wt[u];
-            b[u] *= r * wt[8 + u];
-          }
+      const uint4* src =
+          static_cast<const uint4*>(hp.src) + (o * hp.src_stride + (g * kHpi + sub) * D) / 8;
+      uint4* dst = static_cast<uint4*>(hp.dst) + (i * hp.dst_stride + (g * kHpi + sub) * D) / 8;
+      const int step = p.split * (kHpi * D / 8);
+      for (; g < hp.groups; g += p.split, src += step, dst += step) {
+        const bool live = g * kHpi + sub < hp.heads;
+        uint4 ra = make_uint4(0, 0, 0, 0), rb = ra;
+        if (live) {
+          ra = __ldcs(src + ca);
+          rb = __ldcs(src + cb);
         }
-        if (rotated) {
+        // channels that are neither scaled nor turned keep their bits (a NaN's too)
+        if (which < 2 && (rotated || p.weight[which & 1])) {
+          float va[8], vb[8], a[8], b[8];
+          unpack8(ra, va);
+          unpack8(rb, vb);
+          to_pairs<kAdjacent>(va, vb, a, b);
+          if (p.weight[which & 1]) {
+            float ss = 0.f, wt[16];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float x = a[u], y = b[u];
-            a[u] = x * c[u] - y * s[u];
-            b[u] = x * s[u] + y * c[u];
+            for (int u = 0; u < 8; ++u) ss = fmaf(a[u], a[u], fmaf(b[u], b[u], ss));
+            const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
+            weights_of<D>(t, which & 1, j, wt);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              a[u] *= r * wt[u];
+              b[u] *= r * wt[8 + u];
+            }
           }
+          if (rotated) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const float x = a[u], y = b[u];
+              a[u] = x * c[u] - y * s[u];
+              b[u] = x * s[u] + y * c[u];
+            }
+          }
+          to_chunks<kAdjacent>(a, b, va, vb);
+          ra = pack8(va);
+          rb = pack8(vb);
         }
-        to_chunks<kAdjacent>(a, b, va, vb);
-        ra = pack8(va);
-        rb = pack8(vb);
+        if (live) {
+          dst[ca] = ra;
+          dst[cb] = rb;
+        }
       }
-      if (live) {
-        dst[ca] = ra;
-        dst[cb] = rb;
-      }
+      g -= hp.groups;
     }
   }
 }
 
 // The gradient: rows of fp32 gradients in plan order in, bf16 in original order out.  With a
-// norm, a thread sums dw of its 16 channels over every row it sees; a CTA's sums go to
-// partial[cta] and k_rope_dw adds those in a fixed order, so that dw does not depend on timing.
+// norm, a thread sums dw of its 16 channels in registers over one tensor's heads of a token, then
+// adds them to its own words of shared memory (registers for q and k both would cost a third of
+// the warps in flight); a CTA's sums go to partial[cta] and k_rope_dw adds those in a fixed
+// order, so that dw does not depend on timing.
 template <int D, bool kAdjacent, bool kNorm>
-__global__ void __launch_bounds__(kThreads) k_rope_bwd(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kNorm ? 2 : 4)
+    k_rope_bwd(const __grid_constant__ RopeParams p) {
   constexpr int kTpr = D / 16, kHpi = 32 / kTpr;
   __shared__ Tables<D> t;
+  __shared__ float4 sums[2][4][kNorm ? kThreads : 1];  // q, k: the 16 sums of every thread
   fill_tables<D, kAdjacent>(p, t);
   const int lane = threadIdx.x & 31, j = lane % kTpr, sub = lane / kTpr;
   const bool rotated = j < p.rot_chunks;
   int ca, cb;
   chunks_of<kAdjacent>(j, p.rot_chunks, &ca, &cb);
-  float dw[2][16];
+  if constexpr (kNorm) {
 #pragma unroll
-  for (int u = 0; u < 16; ++u) dw[0][u] = dw[1][u] = 0.f;
-  const int64_t warps = (int64_t)gridDim.x * kWarps;
-  const int groups = p.part[0].groups + p.part[1].groups + p.part[2].groups;
-  for (int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); w < p.n * p.split;
-       w += warps) {
-    const int64_t i = w / p.split;
+    for (int k = 0; k < 8; ++k) sums[k >> 2][k & 3][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const unsigned items = (unsigned)(p.n * p.split), warps = gridDim.x * kWarps;
+  for (unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5); w < items; w += warps) {
+    const int64_t i = p.split == 1 ? w : w / (unsigned)p.split;
     const int64_t o = p.perm ? p.perm[i] : i;
+    int g = (int)(w - (unsigned)i * p.split);  // the warp's groups: g, g + split, ...
     float c[8], s[8];
     angles<D>(p, t, j, o, c, s);
-    for (int g = (int)(w % p.split); g < groups; g += p.split) {
-      const int which = g < p.part[0].groups ? 0 : g < p.part[0].groups + p.part[1].groups ? 1 : 2;
+#pragma unroll
+    for (int which = 0; which < 3; ++which) {
       const HeadPart& hp = p.part[which];
-      const int g0 = which == 0 ? 0 : which == 1 ? p.part[0].groups : p.part[0].groups + p.part[1].groups;
-      const int h = (g - g0) * kHpi + sub;
-      const bool live = h < hp.heads;
-      const float* src = static_cast<const float*>(hp.src) + i * hp.src_stride + (int64_t)h * D;
-      uint4* dst = static_cast<uint4*>(hp.dst) + (o * hp.dst_stride + (int64_t)h * D) / 8;
-      float va[8], vb[8];
-      if (live) {
-        load8(src + ca * 8, va);
-        load8(src + cb * 8, vb);
-      } else {
+      const int at = (g * kHpi + sub) * D, step = p.split * (kHpi * D);
+      const float* src = static_cast<const float*>(hp.src) + i * hp.src_stride + at;
+      uint4* dst = static_cast<uint4*>(hp.dst) + (o * hp.dst_stride + at) / 8;
+      const uint4* x = static_cast<const uint4*>(hp.x) + (o * hp.x_stride + at) / 8;
+      const bool norm = kNorm && which < 2 && p.weight[which & 1];
+      float dw[16];
+      if (norm) {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) dw[u] = 0.f;
+      }
+      for (; g < hp.groups; g += p.split, src += step, dst += step / 8, x += step / 8) {
+        const bool live = g * kHpi + sub < hp.heads;
+        float va[8], vb[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) va[u] = vb[u] = 0.f;
-      }
-      if (which < 2) {
-        const bool norm = kNorm && p.weight[which] != nullptr;
         uint4 xa = make_uint4(0, 0, 0, 0), xb = xa;
-        if (norm && live) {
-          const uint4* x = static_cast<const uint4*>(hp.x) + (o * hp.x_stride + (int64_t)h * D) / 8;
-          xa = __ldcs(x + ca);
-          xb = __ldcs(x + cb);
-        }
-        float a[8], b[8];
-        to_pairs<kAdjacent>(va, vb, a, b);
-        if (rotated) {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float x = a[u], y = b[u];
-            a[u] = x * c[u] + y * s[u];
-            b[u] = y * c[u] - x * s[u];
+        if (live) {
+          load8(src + ca * 8, va);
+          load8(src + cb * 8, vb);
+          if (norm) {
+            xa = __ldcs(x + ca);
+            xb = __ldcs(x + cb);
           }
         }
-        if (norm) {
-          float x8a[8], x8b[8], x1[8], x2[8], wt[16], ss = 0.f, dot = 0.f;
-          unpack8(xa, x8a);
-          unpack8(xb, x8b);
-          to_pairs<kAdjacent>(x8a, x8b, x1, x2);
+        if (which < 2) {
+          float a[8], b[8];
+          to_pairs<kAdjacent>(va, vb, a, b);
+          if (rotated) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u) ss = fmaf(x1[u], x1[u], fmaf(x2[u], x2[u], ss));
-          const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
-          weights_of<D>(t, which, j, wt);
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            x1[u] *= r;
-            x2[u] *= r;
-            if (which == 0) {
-              dw[0][u] = fmaf(a[u], x1[u], dw[0][u]);
-              dw[0][8 + u] = fmaf(b[u], x2[u], dw[0][8 + u]);
-            } else {
-              dw[1][u] = fmaf(a[u], x1[u], dw[1][u]);
-              dw[1][8 + u] = fmaf(b[u], x2[u], dw[1][8 + u]);
+            for (int u = 0; u < 8; ++u) {
+              const float y = a[u], z = b[u];
+              a[u] = y * c[u] + z * s[u];
+              b[u] = z * c[u] - y * s[u];
             }
-            a[u] *= wt[u];
-            b[u] *= wt[8 + u];
-            dot = fmaf(a[u], x1[u], fmaf(b[u], x2[u], dot));
           }
-          const float m = row_sum<D>(dot) * (1.f / D);
+          if (norm) {
+            float x8a[8], x8b[8], x1[8], x2[8], wt[16], ss = 0.f, dot = 0.f;
+            unpack8(xa, x8a);
+            unpack8(xb, x8b);
+            to_pairs<kAdjacent>(x8a, x8b, x1, x2);
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            a[u] = r * (a[u] - x1[u] * m);
-            b[u] = r * (b[u] - x2[u] * m);
+            for (int u = 0; u < 8; ++u) ss = fmaf(x1[u], x1[u], fmaf(x2[u], x2[u], ss));
+            const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + p.eps);
+            weights_of<D>(t, which & 1, j, wt);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              x1[u] *= r;
+              x2[u] *= r;
+              dw[u] = fmaf(a[u], x1[u], dw[u]);
+              dw[8 + u] = fmaf(b[u], x2[u], dw[8 + u]);
+              a[u] *= wt[u];
+              b[u] *= wt[8 + u];
+              dot = fmaf(a[u], x1[u], fmaf(b[u], x2[u], dot));
+            }
+            const float m = row_sum<D>(dot) * (1.f / D);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              a[u] = r * (a[u] - x1[u] * m);
+              b[u] = r * (b[u] - x2[u] * m);
+            }
           }
+          to_chunks<kAdjacent>(a, b, va, vb);
         }
-        to_chunks<kAdjacent>(a, b, va, vb);
+        if (live) {
+          dst[ca] = pack8(va);
+          dst[cb] = pack8(vb);
+        }
       }
-      if (live) {
-        dst[ca] = pack8(va);
-        dst[cb] = pack8(vb);
+      g -= hp.groups;
+      if (norm) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float4& v = sums[which & 1][k][kNorm ? threadIdx.x : 0];
+          v = make_float4(v.x + dw[4 * k], v.y + dw[4 * k + 1], v.z + dw[4 * k + 2],
+                          v.w + dw[4 * k + 3]);
+        }
       }
     }
   }
   if constexpr (kNorm) {
-    // over the heads a warp holds at a time, then over the CTA's warps in their order
-    __shared__ float sums[kWarps][2][D];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        float v = dw[k][u];
-#pragma unroll
-        for (int off = kTpr; off < 32; off <<= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-        if (sub == 0) sums[threadIdx.x >> 5][k][channel_of<kAdjacent>(j, u, p.rot_chunks)] = v;
-      }
+    // channel x of weight k: thread j's element u, over the CTA's threads with that j in order
     __syncthreads();
     for (int x = threadIdx.x; x < 2 * D; x += kThreads) {
+      const int k = x / D, e = x % D, jj = e / 16, u = e % 16;
       float v = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) v += sums[k][x / D][x % D];
-      p.partial[(int64_t)blockIdx.x * 2 * D + x] = v;
+      for (int q = jj; q < kThreads; q += kTpr)
+        v += reinterpret_cast<const float*>(&sums[k][u >> 2][q])[u & 3];
+      p.partial[(int64_t)blockIdx.x * 2 * D + k * D + channel_of<kAdjacent>(jj, u, p.rot_chunks)] = v;
     }
   }
 }
 
-// dw[x] = the CTAs' partial sums of channel x, 32 channels a block, 8 interleaved slices of the
+// dw[x] = the CTAs' partial sums of channel x, 32 channels a block, 32 interleaved slices of the
 // CTAs each, added in a fixed order
-__global__ void __launch_bounds__(256) k_rope_dw(const float* __restrict__ partial, int ctas, int d,
-                                                 float* dwq, float* dwk) {
-  __shared__ float s[8][32];
+__global__ void __launch_bounds__(1024) k_rope_dw(const float* __restrict__ partial, int ctas,
+                                                  int d, float* dwq, float* dwk) {
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int x = blockIdx.x * 32 + lane;
   float v = 0.f;
-  for (int c = slice; c < ctas; c += 8) v += partial[(int64_t)c * 2 * d + x];
+#pragma unroll 4
+  for (int c = slice; c < ctas; c += 32) v += partial[(int64_t)c * 2 * d + x];
   s[slice][lane] = v;
   __syncthreads();
-  if (slice == 0) {
-    for (int k = 1; k < 8; ++k) v += s[k][lane];
-    float* out = x < d ? dwq : dwk;
-    if (out) out[x % d] = v;
-  }
+  // warp `slice` adds the slices of channel `slice` of the block's 32
+  v = s[lane][slice];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  const int ch = blockIdx.x * 32 + slice;
+  float* out = ch < d ? dwq : dwk;
+  if (lane == 0 && out) out[ch % d] = v;
 }
 
 // freq / (2 pi) modulo 1 as a 64-bit fixed-point fraction.  The quotient is kept as a sum of two
@@ -421,8 +430,9 @@ void set_params(const marble_plan_t* plan, int64_t n, const marble_rope_t* rope,
 
 // CTAs and warps per token.  A warp walks all heads of a token (the angles are then computed
 // once) unless that leaves the GPU without work: then a token is split over the fewest warps
-// that give every SM 16 of them, a group of heads each at the most.
-int set_grid(RopeParams* p, int max_ctas) {
+// that give every SM 16 of them, a group of heads each at the most.  No more CTAs than run at
+// once (per_sm on every SM): each fills its tables once and takes tokens until they run out.
+int set_grid(RopeParams* p, int per_sm, int max_ctas) {
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -430,7 +440,7 @@ int set_grid(RopeParams* p, int max_ctas) {
   const int64_t want = (int64_t)sms * 16;
   p->split = (int)std::max<int64_t>(1, std::min<int64_t>(groups, (want + p->n - 1) / p->n));
   const int64_t ctas = (p->n * p->split + kWarps - 1) / kWarps;
-  return (int)std::min<int64_t>(ctas, max_ctas);
+  return (int)std::min<int64_t>(ctas, std::min(sms * per_sm, max_ctas));
 }
 
 }  // namespace
@@ -444,7 +454,7 @@ cudaError_t launch_rope(const marble_plan_t* plan, int64_t n, const marble_rope_
   set_part(p.part[0], src->q, dst->q, nullptr, src->q_stride, dst->q_stride, 0, src->hq, d);
   set_part(p.part[1], src->k, dst->k, nullptr, src->k_stride, dst->k_stride, 0, src->hkv, d);
   set_part(p.part[2], src->v, dst->v, nullptr, src->v_stride, dst->v_stride, 0, src->hkv, d);
-  const int ctas = set_grid(&p, 1 << 20);
+  const int ctas = set_grid(&p, 4, 1 << 20);
   const bool adj = rope->pairing == MARBLE_PAIR_ADJACENT;
   if (d == 128)
     (adj ? k_rope<128, true> : k_rope<128, false>)<<<ctas, kThreads, 0, s>>>(p);
@@ -470,7 +480,7 @@ cudaError_t launch_rope_bwd(const marble_plan_t* plan, int64_t n, const marble_r
     set_part(p.part[0], grad->q, dx->q, xs.q, grad->q_stride, dx->q_stride, xs.q_stride, grad->hq, d);
     set_part(p.part[1], grad->k, dx->k, xs.k, grad->k_stride, dx->k_stride, xs.k_stride, grad->hkv, d);
     set_part(p.part[2], grad->v, dx->v, nullptr, grad->v_stride, dx->v_stride, 0, grad->hkv, d);
-    ctas = set_grid(&p, norm ? kPartialCtas : 1 << 20);
+    ctas = set_grid(&p, norm ? 2 : 4, norm ? kPartialCtas : 1 << 20);
     const bool adj = rope->pairing == MARBLE_PAIR_ADJACENT;
     auto kernel = d == 128 ? (adj ? (norm ? k_rope_bwd<128, true, true> : k_rope_bwd<128, true, false>)
                                   : (norm ? k_rope_bwd<128, false, true> : k_rope_bwd<128, false, false>))
@@ -480,7 +490,7 @@ cudaError_t launch_rope_bwd(const marble_plan_t* plan, int64_t n, const marble_r
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  if (norm) k_rope_dw<<<2 * d / 32, 256, 0, s>>>(workspace, ctas, d, dwq, dwk);
+  if (norm) k_rope_dw<<<2 * d / 32, 1024, 0, s>>>(workspace, ctas, d, dwq, dwk);
   return cudaGetLastError();
 }
 
