@@ -99,6 +99,10 @@ class _State(ctypes.Structure):
     _fields_ = [("o_acc", ctypes.c_void_p), ("m", ctypes.c_void_p), ("l", ctypes.c_void_p)]
 
 
+class _Score(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("slopes", ctypes.c_void_p)]
+
+
 _lib = None
 
 # every symbol the header declares, with its ctypes signature
@@ -146,6 +150,23 @@ _SIGS = {
     "marble_attn_bwd_fused": ([ctypes.c_void_p, ctypes.POINTER(_QKV), ctypes.c_void_p,
                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "marble_attn_steps_scored": ([ctypes.c_void_p, ctypes.POINTER(_QKV), ctypes.POINTER(_Score),
+                                  ctypes.c_int32, ctypes.POINTER(ctypes.c_int32),
+                                  ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_uint32),
+                                  ctypes.POINTER(_State), ctypes.c_void_p]),
+    "marble_attn_fwd_fused_scored": ([ctypes.c_void_p, ctypes.POINTER(_QKV),
+                                      ctypes.POINTER(_Score), ctypes.POINTER(_State),
+                                      ctypes.c_void_p]),
+    "marble_attn_bwd_steps_scored": ([ctypes.c_void_p, ctypes.POINTER(_QKV),
+                                      ctypes.POINTER(_Score), ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_int32,
+                                      ctypes.POINTER(ctypes.c_int32),
+                                      ctypes.POINTER(ctypes.c_int32), ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "marble_attn_bwd_fused_scored": ([ctypes.c_void_p, ctypes.POINTER(_QKV),
+                                      ctypes.POINTER(_Score), ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p]),
     "marble_cast_bf16": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
     "marble_check": ([ctypes.c_void_p, ctypes.c_void_p]),
     "marble_set_wait_limit_ns": ([ctypes.c_uint64]),
@@ -492,6 +513,34 @@ def _qkv(plan, q, k, v, scale):
     return _QKV(q.data_ptr(), k.data_ptr(), v.data_ptr(), hq, hkv, d, float(scale))
 
 
+class Score:
+    """What happens to a score before the softmax (marble_score_t): ``cap`` c > 0 makes it
+    c tanh(score / c), ``slopes`` (fp32 CUDA tensor [hq]) then takes slopes[h] * |pos_q - pos_k|
+    off.  The same Score goes to every call of a pass, forward and backward."""
+
+    def __init__(self, cap: float = 0.0, slopes=None):
+        import torch
+        if slopes is not None:
+            _need(slopes, torch.float32, "slopes")
+            if slopes.dim() != 1:
+                raise ValueError("slopes must be [hq]")
+        self.cap = float(cap)
+        self.slopes = slopes
+
+    def _c(self, hq):
+        if self.slopes is not None and self.slopes.shape[0] != hq:
+            raise ValueError(f"slopes must have {hq} entries, one for each q head")
+        return _Score(self.cap, None if self.slopes is None else self.slopes.data_ptr())
+
+
+def _call_scored(name, plan, c, score, *args):
+    """The call, or its scored variant."""
+    if score is None:
+        _call(name, plan.handle, ctypes.byref(c), *args)
+    else:
+        _call(name + "_scored", plan.handle, ctypes.byref(c), ctypes.byref(score._c(c.hq)), *args)
+
+
 def _flags(first: bool, merge) -> int:
     if merge not in _MERGE:
         raise ValueError(f"merge must be one of {sorted(k for k in _MERGE if k)}")
@@ -499,10 +548,15 @@ def _flags(first: bool, merge) -> int:
 
 
 def attn_step(plan: Plan, q, k, v, q_shard: int, kv_shard: int, state: State,
-              first: bool = False, scale: float = 0.0, stream=None, merge: str = "carried"):
+              first: bool = False, scale: float = 0.0, stream=None, merge: str = "carried",
+              score: Optional[Score] = None):
     """One forward ring step (marble_attn_step).  ``merge``: "carried" (the fp32 state
     carried across steps), "bf16" (the standard per-step merge of bf16 partials) or "fp32"
-    (the same merge of fp32 partials)."""
+    (the same merge of fp32 partials).  ``score``: cap and distance bias of the scores."""
+    if score is not None:
+        attn_steps(plan, q, k, v, [(q_shard, kv_shard, first)], state, scale=scale, stream=stream,
+                   merge=merge, score=score)
+        return
     c = _qkv(plan, q, k, v, scale)
     st = state._c()
     _call("marble_attn_step", plan.handle, ctypes.byref(c), int(q_shard), int(kv_shard),
@@ -530,9 +584,13 @@ def attn_bwd_prep(plan: Plan, o, do, delta, stream=None):
 
 
 def attn_bwd(plan: Plan, q, k, v, do, lse, delta, q_shard: int, kv_shard: int, dq_acc, dk_acc,
-             dv_acc, scale: float = 0.0, stream=None):
+             dv_acc, scale: float = 0.0, stream=None, score: Optional[Score] = None):
     """One backward ring step (marble_attn_bwd); accumulators are fp32 and caller-zeroed."""
     import torch
+    if score is not None:
+        attn_bwd_steps(plan, q, k, v, do, lse, delta, [(q_shard, kv_shard, False)], dq_acc, dk_acc,
+                       dv_acc, scale=scale, stream=stream, score=score)
+        return
     c = _qkv(plan, q, k, v, scale)
     _need(do, torch.bfloat16, "do", q.shape)
     _need(lse, torch.float32, "lse", (q.shape[1], plan.n))
@@ -612,7 +670,7 @@ def ring_schedule(num_shards: int, needed: bool = False):
 
 
 def attn_steps(plan: Plan, q, k, v, schedule, state: State, scale: float = 0.0, stream=None,
-               merge: str = "carried"):
+               merge: str = "carried", score: Optional[Score] = None):
     """A list of forward ring steps [(q_shard, kv_shard, first), ...] in one C call."""
     c = _qkv(plan, q, k, v, scale)
     st = state._c()
@@ -620,12 +678,12 @@ def attn_steps(plan: Plan, q, k, v, schedule, state: State, scale: float = 0.0, 
     qs = (ctypes.c_int32 * n)(*[int(r) for r, _, _ in schedule])
     ks = (ctypes.c_int32 * n)(*[int(j) for _, j, _ in schedule])
     fl = (ctypes.c_uint32 * n)(*[_flags(f, merge) for _, _, f in schedule])
-    _call("marble_attn_steps", plan.handle, ctypes.byref(c), n, qs, ks, fl, ctypes.byref(st),
-          _stream(stream))
+    _call_scored("marble_attn_steps", plan, c, score, n, qs, ks, fl, ctypes.byref(st),
+                 _stream(stream))
 
 
 def attn_bwd_steps(plan: Plan, q, k, v, do, lse, delta, schedule, dq_acc, dk_acc, dv_acc,
-                   scale: float = 0.0, stream=None):
+                   scale: float = 0.0, stream=None, score: Optional[Score] = None):
     """A list of backward ring steps [(q_shard, kv_shard, _), ...] in one C call."""
     import torch
     c = _qkv(plan, q, k, v, scale)
@@ -638,21 +696,21 @@ def attn_bwd_steps(plan: Plan, q, k, v, do, lse, delta, schedule, dq_acc, dk_acc
     n = len(schedule)
     qs = (ctypes.c_int32 * n)(*[int(r) for r, _, _ in schedule])
     ks = (ctypes.c_int32 * n)(*[int(j) for _, j, _ in schedule])
-    _call("marble_attn_bwd_steps", plan.handle, ctypes.byref(c), _ptr(do), _ptr(lse),
-          _ptr(delta), n, qs, ks, _ptr(dq_acc), _ptr(dk_acc), _ptr(dv_acc), _stream(stream))
+    _call_scored("marble_attn_bwd_steps", plan, c, score, _ptr(do), _ptr(lse), _ptr(delta), n, qs,
+                 ks, _ptr(dq_acc), _ptr(dk_acc), _ptr(dv_acc), _stream(stream))
 
 
-def attn_fwd_fused(plan: Plan, q, k, v, state: State, scale: float = 0.0, stream=None):
+def attn_fwd_fused(plan: Plan, q, k, v, state: State, scale: float = 0.0, stream=None,
+                   score: Optional[Score] = None):
     """Every forward ring step in one launch, the state on chip between steps
     (marble_attn_fwd_fused)."""
     c = _qkv(plan, q, k, v, scale)
     st = state._c()
-    _call("marble_attn_fwd_fused", plan.handle, ctypes.byref(c), ctypes.byref(st),
-          _stream(stream))
+    _call_scored("marble_attn_fwd_fused", plan, c, score, ctypes.byref(st), _stream(stream))
 
 
 def attn_bwd_fused(plan: Plan, q, k, v, do, lse, delta, dq_acc, dk_acc, dv_acc,
-                   scale: float = 0.0, stream=None):
+                   scale: float = 0.0, stream=None, score: Optional[Score] = None):
     """Every backward ring step, one dK/dV launch per kv shard over its ring
     (marble_attn_bwd_fused); accumulators fp32 and caller-zeroed."""
     import torch
@@ -663,37 +721,41 @@ def attn_bwd_fused(plan: Plan, q, k, v, do, lse, delta, dq_acc, dk_acc, dv_acc,
     _need(dq_acc, torch.float32, "dq_acc", q.shape)
     _need(dk_acc, torch.float32, "dk_acc", k.shape)
     _need(dv_acc, torch.float32, "dv_acc", k.shape)
-    _call("marble_attn_bwd_fused", plan.handle, ctypes.byref(c), _ptr(do), _ptr(lse),
-          _ptr(delta), _ptr(dq_acc), _ptr(dk_acc), _ptr(dv_acc), _stream(stream))
+    _call_scored("marble_attn_bwd_fused", plan, c, score, _ptr(do), _ptr(lse), _ptr(delta),
+                 _ptr(dq_acc), _ptr(dk_acc), _ptr(dv_acc), _stream(stream))
 
 
 def forward(plan: Plan, q, k, v, state: State, o, lse, needed: bool = False, scale: float = 0.0,
-            stream=None, merge: str = "carried", fused: bool = False):
+            stream=None, merge: str = "carried", fused: bool = False,
+            score: Optional[Score] = None):
     """All forward ring steps (r-major, keeping shard r's state hot in L2) + finalize;
-    ``fused``: the whole ring in one launch (marble_attn_fwd_fused)."""
+    ``fused``: the whole ring in one launch (marble_attn_fwd_fused); ``score``: cap and
+    distance bias of the scores."""
     if fused:
         if needed or merge not in (None, "carried"):
             raise ValueError("the fused ring carries the fp32 state over the ring steps only")
-        attn_fwd_fused(plan, q, k, v, state, scale=scale, stream=stream)
+        attn_fwd_fused(plan, q, k, v, state, scale=scale, stream=stream, score=score)
     else:
         attn_steps(plan, q, k, v, ring_schedule(plan.num_shards, needed), state, scale=scale,
-                   stream=stream, merge=merge)
+                   stream=stream, merge=merge, score=score)
     attn_finalize(plan, state, o, lse, stream=stream)
 
 
 def backward(plan: Plan, q, k, v, o, do, lse, delta, dq_acc, dk_acc, dv_acc,
-             needed: bool = False, scale: float = 0.0, stream=None, fused: bool = False):
+             needed: bool = False, scale: float = 0.0, stream=None, fused: bool = False,
+             score: Optional[Score] = None):
     """bwd preprocessing + all backward ring steps (accumulators must be zeroed);
-    ``fused``: one dK/dV launch per kv shard over its ring (marble_attn_bwd_fused)."""
+    ``fused``: one dK/dV launch per kv shard over its ring (marble_attn_bwd_fused);
+    ``score``: the forward's."""
     attn_bwd_prep(plan, o, do, delta, stream=stream)
     if fused:
         if needed:
             raise ValueError("the fused ring runs the ring steps, not the needed-block mode")
         attn_bwd_fused(plan, q, k, v, do, lse, delta, dq_acc, dk_acc, dv_acc, scale=scale,
-                       stream=stream)
+                       stream=stream, score=score)
     else:
         attn_bwd_steps(plan, q, k, v, do, lse, delta, ring_schedule(plan.num_shards, needed),
-                       dq_acc, dk_acc, dv_acc, scale=scale, stream=stream)
+                       dq_acc, dk_acc, dv_acc, scale=scale, stream=stream, score=score)
 
 
 def layout_vision_groups(sample, seg):

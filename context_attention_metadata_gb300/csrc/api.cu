@@ -406,6 +406,7 @@ MARBLE_API marble_status_t marble_plan(const marble_plan_desc_t* d, marble_strea
   p->chunk_tokens = d->chunk_tokens;
   p->range_cost = d->order == MARBLE_ORDER_CHUNK_SEARCH ? d->range_cost : 0;
   p->bps = nb / d->num_shards;
+  p->pos_is_index = d->pos_id == nullptr;
   marble_status_t st = build_plan(d, (cudaStream_t)stream, p);
   plan_used(p, (cudaStream_t)stream);  // the planner's kernels, also on failure
   if (st != MARBLE_OK) {
@@ -911,7 +912,7 @@ MARBLE_API marble_status_t marble_attn_step(const marble_plan_t* p, const marble
   if ((st = check_tensor(state->m, "state.m")) != MARBLE_OK) return st;
   if ((st = check_tensor(state->l, "state.l")) != MARBLE_OK) return st;
   if (!step_flags_ok(flags)) return fail(MARBLE_ERR_INVALID_ARG, "unknown or conflicting flags");
-  st = run_attn_fwd(p, qkv, 1, &q_shard, &kv_shard, &flags, state, (cudaStream_t)stream);
+  st = run_attn_fwd(p, qkv, nullptr, 1, &q_shard, &kv_shard, &flags, state, (cudaStream_t)stream);
   plan_used(p, (cudaStream_t)stream);
   return st;
 }
@@ -928,12 +929,29 @@ static marble_status_t check_step_list(const marble_plan_t* p, int32_t n_steps,
   return MARBLE_OK;
 }
 
-MARBLE_API marble_status_t marble_attn_steps(const marble_plan_t* p, const marble_qkv_t* qkv,
-                                             int32_t n_steps, const int32_t* q_shards,
-                                             const int32_t* kv_shards, const uint32_t* flags,
-                                             const marble_state_t* state,
-                                             marble_stream_t stream) {
-  NvtxRange nvtx_("marble_attn_steps");
+// a score descriptor (null: none) and where its calls may run
+static marble_status_t check_score(const marble_plan_t* p, const marble_score_t* score,
+                                   marble_stream_t stream) {
+  if (!p) return fail(MARBLE_ERR_INVALID_ARG, "plan is null");
+  marble_status_t st;
+  if (score) {
+    if (!(score->cap >= 0.f) || std::isinf(score->cap))
+      return fail(MARBLE_ERR_INVALID_ARG, "score.cap must be finite and >= 0 (0 = none)");
+    if (score->slopes && (st = check_here(score->slopes, "score.slopes", 16)) != MARBLE_OK) return st;
+  }
+  if ((st = check_plan_here(p)) != MARBLE_OK) return st;
+  bool cap = false;
+  if ((st = capturing((cudaStream_t)stream, &cap)) != MARBLE_OK) return st;
+  if (cap)
+    return fail(MARBLE_ERR_INVALID_ARG, "the stream is being captured: these calls cannot be");
+  return MARBLE_OK;
+}
+
+static marble_status_t attn_steps_impl(const marble_plan_t* p, const marble_qkv_t* qkv,
+                                    const marble_score_t* score, int32_t n_steps, const int32_t* q_shards,
+                                    const int32_t* kv_shards, const uint32_t* flags,
+                                    const marble_state_t* state,
+                                    marble_stream_t stream) {
   if (!p || !state) return fail(MARBLE_ERR_INVALID_ARG, "plan and state must be non-null");
   marble_status_t st;
   if ((st = check_qkv(p, qkv)) != MARBLE_OK) return st;
@@ -949,7 +967,50 @@ MARBLE_API marble_status_t marble_attn_steps(const marble_plan_t* p, const marbl
   if ((st = check_tensor(state->m, "state.m")) != MARBLE_OK) return st;
   if ((st = check_tensor(state->l, "state.l")) != MARBLE_OK) return st;
   if (n_steps == 0) return MARBLE_OK;
-  st = run_attn_fwd(p, qkv, n_steps, q_shards, kv_shards, flags, state, (cudaStream_t)stream);
+  st = run_attn_fwd(p, qkv, score, n_steps, q_shards, kv_shards, flags, state, (cudaStream_t)stream);
+  plan_used(p, (cudaStream_t)stream);
+  return st;
+}
+
+MARBLE_API marble_status_t marble_attn_steps(const marble_plan_t* p, const marble_qkv_t* qkv,
+                                             int32_t n_steps, const int32_t* q_shards,
+                                             const int32_t* kv_shards, const uint32_t* flags,
+                                             const marble_state_t* state,
+                                             marble_stream_t stream) {
+  NvtxRange nvtx_("marble_attn_steps");
+  return attn_steps_impl(p, qkv, nullptr, n_steps, q_shards, kv_shards, flags, state, stream);
+}
+
+MARBLE_API marble_status_t marble_attn_steps_scored(const marble_plan_t* p, const marble_qkv_t* qkv,
+                                     const marble_score_t* score, int32_t n_steps, const int32_t* q_shards,
+                                    const int32_t* kv_shards, const uint32_t* flags,
+                                    const marble_state_t* state,
+                                     marble_stream_t stream) {
+  NvtxRange nvtx_("marble_attn_steps_scored");
+  const marble_status_t st = check_score(p, score, stream);
+  if (st != MARBLE_OK) return st;
+  return attn_steps_impl(p, qkv, score, n_steps, q_shards, kv_shards, flags, state, stream);
+}
+
+static marble_status_t attn_bwd_steps_impl(const marble_plan_t* p, const marble_qkv_t* qkv,
+                                    const marble_score_t* score, const void* d_o, const float* lse,
+                                    const float* delta, int32_t n_steps, const int32_t* q_shards,
+                                    const int32_t* kv_shards, float* dq_acc,
+                                    float* dk_acc, float* dv_acc,
+                                    marble_stream_t stream) {
+  if (!p) return fail(MARBLE_ERR_INVALID_ARG, "plan is null");
+  marble_status_t st;
+  if ((st = check_qkv(p, qkv)) != MARBLE_OK) return st;
+  if ((st = check_step_list(p, n_steps, q_shards, kv_shards)) != MARBLE_OK) return st;
+  if ((st = check_tensor(d_o, "d_o")) != MARBLE_OK) return st;
+  if ((st = check_tensor(lse, "lse")) != MARBLE_OK) return st;
+  if ((st = check_tensor(delta, "delta")) != MARBLE_OK) return st;
+  if ((st = check_tensor(dq_acc, "dq_acc")) != MARBLE_OK) return st;
+  if ((st = check_tensor(dk_acc, "dk_acc")) != MARBLE_OK) return st;
+  if ((st = check_tensor(dv_acc, "dv_acc")) != MARBLE_OK) return st;
+  if (n_steps == 0) return MARBLE_OK;
+  st = run_attn_bwd(p, qkv, score, d_o, lse, delta, n_steps, q_shards, kv_shards, dq_acc, dk_acc,
+                    dv_acc, (cudaStream_t)stream);
   plan_used(p, (cudaStream_t)stream);
   return st;
 }
@@ -962,19 +1023,31 @@ MARBLE_API marble_status_t marble_attn_bwd_steps(const marble_plan_t* p, const m
                                                  float* dk_acc, float* dv_acc,
                                                  marble_stream_t stream) {
   NvtxRange nvtx_("marble_attn_bwd_steps");
-  if (!p) return fail(MARBLE_ERR_INVALID_ARG, "plan is null");
+  return attn_bwd_steps_impl(p, qkv, nullptr, d_o, lse, delta, n_steps, q_shards, kv_shards, dq_acc, dk_acc, dv_acc, stream);
+}
+
+MARBLE_API marble_status_t marble_attn_bwd_steps_scored(const marble_plan_t* p, const marble_qkv_t* qkv,
+                                     const marble_score_t* score, const void* d_o, const float* lse,
+                                    const float* delta, int32_t n_steps, const int32_t* q_shards,
+                                    const int32_t* kv_shards, float* dq_acc,
+                                    float* dk_acc, float* dv_acc,
+                                     marble_stream_t stream) {
+  NvtxRange nvtx_("marble_attn_bwd_steps_scored");
+  const marble_status_t st = check_score(p, score, stream);
+  if (st != MARBLE_OK) return st;
+  return attn_bwd_steps_impl(p, qkv, score, d_o, lse, delta, n_steps, q_shards, kv_shards, dq_acc, dk_acc, dv_acc, stream);
+}
+
+static marble_status_t attn_fwd_fused_impl(const marble_plan_t* p, const marble_qkv_t* qkv,
+                                    const marble_score_t* score, const marble_state_t* state,
+                                    marble_stream_t stream) {
+  if (!p || !state) return fail(MARBLE_ERR_INVALID_ARG, "plan and state must be non-null");
   marble_status_t st;
   if ((st = check_qkv(p, qkv)) != MARBLE_OK) return st;
-  if ((st = check_step_list(p, n_steps, q_shards, kv_shards)) != MARBLE_OK) return st;
-  if ((st = check_tensor(d_o, "d_o")) != MARBLE_OK) return st;
-  if ((st = check_tensor(lse, "lse")) != MARBLE_OK) return st;
-  if ((st = check_tensor(delta, "delta")) != MARBLE_OK) return st;
-  if ((st = check_tensor(dq_acc, "dq_acc")) != MARBLE_OK) return st;
-  if ((st = check_tensor(dk_acc, "dk_acc")) != MARBLE_OK) return st;
-  if ((st = check_tensor(dv_acc, "dv_acc")) != MARBLE_OK) return st;
-  if (n_steps == 0) return MARBLE_OK;
-  st = run_attn_bwd(p, qkv, d_o, lse, delta, n_steps, q_shards, kv_shards, dq_acc, dk_acc,
-                    dv_acc, (cudaStream_t)stream);
+  if ((st = check_tensor(state->o_acc, "state.o_acc")) != MARBLE_OK) return st;
+  if ((st = check_tensor(state->m, "state.m")) != MARBLE_OK) return st;
+  if ((st = check_tensor(state->l, "state.l")) != MARBLE_OK) return st;
+  st = run_attn_fwd_fused(p, qkv, score, state, (cudaStream_t)stream);
   plan_used(p, (cudaStream_t)stream);
   return st;
 }
@@ -983,13 +1056,33 @@ MARBLE_API marble_status_t marble_attn_fwd_fused(const marble_plan_t* p, const m
                                                  const marble_state_t* state,
                                                  marble_stream_t stream) {
   NvtxRange nvtx_("marble_attn_fwd_fused");
-  if (!p || !state) return fail(MARBLE_ERR_INVALID_ARG, "plan and state must be non-null");
+  return attn_fwd_fused_impl(p, qkv, nullptr, state, stream);
+}
+
+MARBLE_API marble_status_t marble_attn_fwd_fused_scored(const marble_plan_t* p, const marble_qkv_t* qkv,
+                                     const marble_score_t* score, const marble_state_t* state,
+                                     marble_stream_t stream) {
+  NvtxRange nvtx_("marble_attn_fwd_fused_scored");
+  const marble_status_t st = check_score(p, score, stream);
+  if (st != MARBLE_OK) return st;
+  return attn_fwd_fused_impl(p, qkv, score, state, stream);
+}
+
+static marble_status_t attn_bwd_fused_impl(const marble_plan_t* p, const marble_qkv_t* qkv,
+                                    const marble_score_t* score, const void* d_o, const float* lse,
+                                    const float* delta, float* dq_acc, float* dk_acc,
+                                    float* dv_acc,
+                                    marble_stream_t stream) {
+  if (!p) return fail(MARBLE_ERR_INVALID_ARG, "plan is null");
   marble_status_t st;
   if ((st = check_qkv(p, qkv)) != MARBLE_OK) return st;
-  if ((st = check_tensor(state->o_acc, "state.o_acc")) != MARBLE_OK) return st;
-  if ((st = check_tensor(state->m, "state.m")) != MARBLE_OK) return st;
-  if ((st = check_tensor(state->l, "state.l")) != MARBLE_OK) return st;
-  st = run_attn_fwd_fused(p, qkv, state, (cudaStream_t)stream);
+  if ((st = check_tensor(d_o, "d_o")) != MARBLE_OK) return st;
+  if ((st = check_tensor(lse, "lse")) != MARBLE_OK) return st;
+  if ((st = check_tensor(delta, "delta")) != MARBLE_OK) return st;
+  if ((st = check_tensor(dq_acc, "dq_acc")) != MARBLE_OK) return st;
+  if ((st = check_tensor(dk_acc, "dk_acc")) != MARBLE_OK) return st;
+  if ((st = check_tensor(dv_acc, "dv_acc")) != MARBLE_OK) return st;
+  st = run_attn_bwd_fused(p, qkv, score, d_o, lse, delta, dq_acc, dk_acc, dv_acc, (cudaStream_t)stream);
   plan_used(p, (cudaStream_t)stream);
   return st;
 }
@@ -1000,18 +1093,18 @@ MARBLE_API marble_status_t marble_attn_bwd_fused(const marble_plan_t* p, const m
                                                  float* dk_acc, float* dv_acc,
                                                  marble_stream_t stream) {
   NvtxRange nvtx_("marble_attn_bwd_fused");
-  if (!p) return fail(MARBLE_ERR_INVALID_ARG, "plan is null");
-  marble_status_t st;
-  if ((st = check_qkv(p, qkv)) != MARBLE_OK) return st;
-  if ((st = check_tensor(d_o, "d_o")) != MARBLE_OK) return st;
-  if ((st = check_tensor(lse, "lse")) != MARBLE_OK) return st;
-  if ((st = check_tensor(delta, "delta")) != MARBLE_OK) return st;
-  if ((st = check_tensor(dq_acc, "dq_acc")) != MARBLE_OK) return st;
-  if ((st = check_tensor(dk_acc, "dk_acc")) != MARBLE_OK) return st;
-  if ((st = check_tensor(dv_acc, "dv_acc")) != MARBLE_OK) return st;
-  st = run_attn_bwd_fused(p, qkv, d_o, lse, delta, dq_acc, dk_acc, dv_acc, (cudaStream_t)stream);
-  plan_used(p, (cudaStream_t)stream);
-  return st;
+  return attn_bwd_fused_impl(p, qkv, nullptr, d_o, lse, delta, dq_acc, dk_acc, dv_acc, stream);
+}
+
+MARBLE_API marble_status_t marble_attn_bwd_fused_scored(const marble_plan_t* p, const marble_qkv_t* qkv,
+                                     const marble_score_t* score, const void* d_o, const float* lse,
+                                    const float* delta, float* dq_acc, float* dk_acc,
+                                    float* dv_acc,
+                                     marble_stream_t stream) {
+  NvtxRange nvtx_("marble_attn_bwd_fused_scored");
+  const marble_status_t st = check_score(p, score, stream);
+  if (st != MARBLE_OK) return st;
+  return attn_bwd_fused_impl(p, qkv, score, d_o, lse, delta, dq_acc, dk_acc, dv_acc, stream);
 }
 
 MARBLE_API marble_status_t marble_attn_finalize(const marble_plan_t* p,
@@ -1070,7 +1163,7 @@ MARBLE_API marble_status_t marble_attn_bwd(const marble_plan_t* p, const marble_
   if ((st = check_tensor(dk_acc, "dk_acc")) != MARBLE_OK) return st;
   if ((st = check_tensor(dv_acc, "dv_acc")) != MARBLE_OK) return st;
   if (flags != 0) return fail(MARBLE_ERR_INVALID_ARG, "flags must be 0");
-  st = run_attn_bwd(p, qkv, d_o, lse, delta, 1, &q_shard, &kv_shard, dq_acc, dk_acc, dv_acc,
+  st = run_attn_bwd(p, qkv, nullptr, d_o, lse, delta, 1, &q_shard, &kv_shard, dq_acc, dk_acc, dv_acc,
                     (cudaStream_t)stream);
   plan_used(p, (cudaStream_t)stream);
   return st;

@@ -41,6 +41,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "score.cuh"
 #include "tma_host.h"
 
 namespace marble {
@@ -107,6 +108,7 @@ struct BwdParams {
   int nwork;                 // units with a non-empty list
   int W;
   float scale, sl2;
+  ScoreParams score;         // read by the dK/dV kernels built with a cap or a bias
 };
 
 // queue entry: head, block (plan order), list start and length; a dK/dV unit of the fused
@@ -503,7 +505,8 @@ struct DkdvSmem {
 };
 static_assert(DkdvSmem<128>::bytes() <= 232448, "shared memory budget");
 
-template <int D>
+// MOD: what happens to the scores (bits kScoreCap, kScoreBias); 0 is the plain softmax.
+template <int D, int MOD>
 __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant__ BwdParams p) {
   using Lay = DkdvSmem<D>;
   constexpr int kTile = Lay::kTile;
@@ -902,10 +905,110 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
             tmem_st16(rS + lb + half * 64 + 32 + cc * 16, dk16);
           }
         };
-        if (masked)
+        if constexpr (MOD != 0) {
+          // P^T = exp2(s - lse2[q]) of the capped and biased score s, dS^T = P^T (dP^T - delta[q])
+          // (1 - tanh^2): the gradient of the product.  In pairs; kSmall is the choice of the way
+          // to tanh (score.cuh).  The second way has one copy, with the mask's select (a warp
+          // without masked columns has all of its bits set).
+          [[maybe_unused]] const int32_t* qpos = p.tracks + 3 * n + qrow - hr;
+          [[maybe_unused]] float neg_slope = 0.f, far0 = 0.f;
+          if constexpr ((MOD & kScoreBias) != 0) {
+            neg_slope = -p.score.slopes[h] * kLog2e;
+            far0 = (float)(qpos[0] - pk);
+          }
+          auto scored = [&](auto with_mask, auto small) {
+            constexpr bool kMasked = decltype(with_mask)::value, kSmall = decltype(small)::value;
+            [[maybe_unused]] F2 d = f2(far0, far0 + 1.f);  // query t is at |far0 + t|
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+              uint32_t pk16[16], dk16[16];
+#pragma unroll
+              for (int t = 0; t < 32; t += 4) {
+                const int q0 = cc * 32 + t;
+                const float4 l4 = *reinterpret_cast<const float4*>(lse2s + q0);
+                const float4 d4 = *reinterpret_cast<const float4*>(dls + q0);
+                [[maybe_unused]] float far[4];
+                if constexpr ((MOD & kScoreBias) != 0) {
+                  if (p.score.consecutive) {
+                    split(d, &far[0], &far[1]);
+                    d = add2(d, f2(2.f));
+                    split(d, &far[2], &far[3]);
+                    d = add2(d, f2(2.f));
+                  } else {
+                    const int4 k4 = __ldg(reinterpret_cast<const int4*>(qpos + q0));
+                    far[0] = (float)(k4.x - pk);
+                    far[1] = (float)(k4.y - pk);
+                    far[2] = (float)(k4.z - pk);
+                    far[3] = (float)(k4.w - pk);
+                  }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; u += 2) {
+                  const float x0 = __uint_as_float(vs[cc][t + u]);
+                  const float x1 = __uint_as_float(vs[cc][t + u + 1]);
+                  const F2 neg_lse = u == 0 ? f2(-l4.x, -l4.y) : f2(-l4.z, -l4.w);
+                  const F2 neg_delta = u == 0 ? f2(-d4.x, -d4.y) : f2(-d4.z, -d4.w);
+                  F2 s, slope = f2(1.f);  // s - lse2, and 1 - tanh^2
+                  if constexpr ((MOD & kScoreCap) == 0) {
+                    s = fma2(f2(x0, x1), f2(sl2), neg_lse);
+                  } else if constexpr (kSmall) {
+                    const F2 c = cap_poly(f2(x0, x1), p.score);
+                    const F2 th = mul2(c, f2(p.score.inv_cap2));
+                    slope = fma2(mul2(th, f2(-1.f)), th, slope);
+                    s = add2(c, neg_lse);
+                  } else {
+                    const F2 r = f2(cap_rcp(x0, p.score), cap_rcp(x1, p.score));
+                    slope = mul2(f2(4.f), fma2(mul2(r, f2(-1.f)), r, r));
+                    s = add2(fma2(f2(-2.f * p.score.cap2), r, f2(p.score.cap2)), neg_lse);
+                  }
+                  if constexpr ((MOD & kScoreBias) != 0)
+                    s = fma2(f2(neg_slope), f2(fabsf(far[u]), fabsf(far[u + 1])), s);
+                  float p0, p1, g0, g1;
+                  split(s, &p0, &p1);
+                  p0 = fast_exp2(p0);
+                  p1 = fast_exp2(p1);
+                  if (kMasked) {
+                    p0 = ((lm[cc] >> (t + u)) & 1u) ? p0 : 0.f;
+                    p1 = ((lm[cc] >> (t + u + 1)) & 1u) ? p1 : 0.f;
+                  }
+                  F2 g = mul2(f2(p0, p1), add2(f2(__uint_as_float(vp[cc][t + u]),
+                                                  __uint_as_float(vp[cc][t + u + 1])),
+                                               neg_delta));
+                  if constexpr ((MOD & kScoreCap) != 0) g = mul2(g, slope);
+                  split(g, &g0, &g1);
+                  pk16[(t + u) >> 1] = pack_bf16(p0, p1);
+                  dk16[(t + u) >> 1] = pack_bf16(g0, g1);
+                }
+              }
+              // the box and TMEM columns of the plain loop above
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4*>(box_row + (((4 * cc + c) ^ (row & 7)) << 4)) =
+                    make_uint4(dk16[4 * c], dk16[4 * c + 1], dk16[4 * c + 2], dk16[4 * c + 3]);
+              tmem_st16(rS + lb + half * 64 + cc * 16, pk16);
+              tmem_st16(rS + lb + half * 64 + 32 + cc * 16, dk16);
+            }
+          };
+          bool small = true;
+          if constexpr ((MOD & kScoreCap) != 0) {
+            float hi = 0.f;
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+              for (int t = 0; t < 32; ++t) hi = fmaxf(hi, fabsf(__uint_as_float(vs[cc][t])));
+            small = __all_sync(0xffffffffu, hi <= p.score.lim);
+          }
+          if ((MOD & kScoreCap) != 0 && !small)
+            scored(std::true_type{}, std::false_type{});
+          else if (masked)
+            scored(std::true_type{}, std::true_type{});
+          else
+            scored(std::false_type{}, std::true_type{});
+        } else if (masked) {
           elementwise(std::true_type{});
-        else
+        } else {
           elementwise(std::false_type{});
+        }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bar[K_PFULL]);
@@ -985,8 +1088,9 @@ size_t dkdv_smem() {
 }
 
 // everything of a backward call but the step, its work list and the scratch: encoded once
-template <int D>
-marble_status_t prepare_bwd(const marble_plan_t* pl, const marble_qkv_t* qkv, const void* d_o,
+template <int D, int MOD>
+marble_status_t prepare_bwd(const marble_plan_t* pl, const marble_qkv_t* qkv,
+                            const marble_score_t* score, const void* d_o,
                             const float* lse, const float* delta, float* dq, float* dk, float* dv,
                             BwdParams* out) {
   BwdParams& prm = *out;
@@ -1035,11 +1139,16 @@ marble_status_t prepare_bwd(const marble_plan_t* pl, const marble_qkv_t* qkv, co
   prm.sl2 = prm.scale * kLog2e;
   prm.step_off = pl->step_off;
   prm.colT_j = pl->colT_j;
-  if (once_per_device(D == 128 ? 3 : 4)) {
+  if (MOD & kScoreCap) set_cap(&prm.score, score->cap, prm.scale);
+  if (MOD & kScoreBias) {
+    prm.score.slopes = score->slopes;
+    prm.score.consecutive = pl->pos_is_index;
+  }
+  if (once_per_device((D == 128 ? 3 : 4) + 4 * MOD)) {
     cudaError_t e = cudaFuncSetAttribute(k_bwd_dq<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)DqSmem<D>::bytes());
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_bwd_dkdv<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(k_bwd_dkdv<D, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)dkdv_smem<D>());
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(bwd)");
   }
@@ -1048,7 +1157,7 @@ marble_status_t prepare_bwd(const marble_plan_t* pl, const marble_qkv_t* qkv, co
     // launched with at least the registers the two budgets add up to, or the growing
     // warpgroups would wait for registers that never come (checked on every call)
     cudaFuncAttributes fa;
-    const cudaError_t e = cudaFuncGetAttributes(&fa, k_bwd_dkdv<D>);
+    const cudaError_t e = cudaFuncGetAttributes(&fa, k_bwd_dkdv<D, MOD>);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes(k_bwd_dkdv)");
     if ((long long)fa.numRegs * kThreads < 128LL * kRegsCtl + 256LL * kRegsElem)
       return fail(MARBLE_ERR_UNSUPPORTED, "dK/dV kernel built with " + std::to_string(fa.numRegs) +
@@ -1174,7 +1283,7 @@ size_t whole_slots(const marble_plan_t* pl, int hq) {
 //              (overlapping the dK/dV launches of the steps after it), and its first dK/dV
 //              launch waits until the dQ GEMM of the q shard nbuf runs earlier has read that
 //              buffer.
-template <int D>
+template <int D, int MOD>
 marble_status_t launch_whole(const marble_plan_t* pl, const marble_qkv_t* qkv, BwdParams prm,
                              int n_steps, const int* q_shards, const int* kv_shards, int nbuf,
                              int64_t buf_slots, cudaStream_t s) {
@@ -1230,7 +1339,7 @@ marble_status_t launch_whole(const marble_plan_t* pl, const marble_qkv_t* qkv, B
       const cudaStream_t sks = sk[pk.kv_shard % nsk];
       pk.sched = sched_slot(pl);
       const int span = timing_begin(sks);
-      k_bwd_dkdv<D><<<(unsigned)(pk.nwork < cap ? pk.nwork : cap), kThreads, smem_k, sks>>>(pk);
+      k_bwd_dkdv<D, MOD><<<(unsigned)(pk.nwork < cap ? pk.nwork : cap), kThreads, smem_k, sks>>>(pk);
       timing_end(span, sks, kTimeDkdv, 1);
     }
     if (++issued[r] == P && !all && err == cudaSuccess) {
@@ -1316,13 +1425,14 @@ int whole_plan(const marble_plan_t* pl, int hq, int n_steps, const int* q_shards
   return nbuf >= 2 ? (int)std::min<int64_t>(nbuf, P - 1) : 0;
 }
 
-template <int D>
-marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv, const void* d_o,
-                             const float* lse, const float* delta, int n_steps,
-                             const int* q_shards, const int* kv_shards, float* dq, float* dk,
-                             float* dv, cudaStream_t s) {
+template <int D, int MOD>
+marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv,
+                             const marble_score_t* score, const void* d_o, const float* lse,
+                             const float* delta, int n_steps, const int* q_shards,
+                             const int* kv_shards, float* dq, float* dk, float* dv,
+                             cudaStream_t s) {
   BwdParams prm;
-  marble_status_t rc = prepare_bwd<D>(pl, qkv, d_o, lse, delta, dq, dk, dv, &prm);
+  marble_status_t rc = prepare_bwd<D, MOD>(pl, qkv, score, d_o, lse, delta, dq, dk, dv, &prm);
   if (rc != MARBLE_OK) return rc;
   const int smem_k = (int)dkdv_smem<D>();
   const int sms = sm_count();
@@ -1333,7 +1443,7 @@ marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv, c
     int64_t buf_slots = 0;
     const int nbuf = whole_plan(pl, qkv->hq, n_steps, q_shards, kv_shards, &buf_slots);
     if (nbuf > 0)
-      return launch_whole<D>(pl, qkv, prm, n_steps, q_shards, kv_shards, nbuf, buf_slots, s);
+      return launch_whole<D, MOD>(pl, qkv, prm, n_steps, q_shards, kv_shards, nbuf, buf_slots, s);
   }
   // scratch for the bf16 dS^T tiles of kDsBufs steps: the dQ GEMM of step i reads buffer
   // i mod kDsBufs while the dK/dV kernels of the next steps write the others
@@ -1397,7 +1507,7 @@ marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv, c
         const int span = timing_begin(sks);
         // with several side streams, at most half the SMs (as in launch_whole)
         const int cap = (sks != s && nsk > 1) ? (sms + 1) / 2 : sms;
-        k_bwd_dkdv<D><<<(unsigned)(pk.nwork < cap ? pk.nwork : cap), kThreads, smem_k, sks>>>(pk);
+        k_bwd_dkdv<D, MOD><<<(unsigned)(pk.nwork < cap ? pk.nwork : cap), kThreads, smem_k, sks>>>(pk);
         timing_end(span, sks, kTimeDkdv, 1);
       }
       if (sks != s && err == cudaSuccess) {
@@ -1432,12 +1542,13 @@ marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv, c
 // scratch cap), keeping the kv blocks' dK/dV in TMEM across all of them and adding them to
 // dk_acc / dv_acc once per range; then the range's dQ GEMMs, one per step (q shard, j), on
 // the caller's stream.  Ranges of one kv shard run in order on one side stream.
-template <int D>
-marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv, const void* d_o,
-                             const float* lse, const float* delta, float* dq, float* dk,
-                             float* dv, cudaStream_t s) {
+template <int D, int MOD>
+marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
+                             const marble_score_t* score, const void* d_o, const float* lse,
+                             const float* delta, float* dq, float* dk, float* dv,
+                             cudaStream_t s) {
   BwdParams prm;
-  marble_status_t rc = prepare_bwd<D>(pl, qkv, d_o, lse, delta, dq, dk, dv, &prm);
+  marble_status_t rc = prepare_bwd<D, MOD>(pl, qkv, score, d_o, lse, delta, dq, dk, dv, &prm);
   if (rc != MARBLE_OK) return rc;
   const int smem_k = (int)dkdv_smem<D>();
   const int sms = sm_count();
@@ -1475,7 +1586,7 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv, c
         // with several side streams, at most half the SMs (as in launch_whole; measured a
         // little faster here, slower in the ranges below, whose dQ GEMMs interleave)
         const int cap = nsk > 1 ? (sms + 1) / 2 : sms;
-        k_bwd_dkdv<D><<<(unsigned)(pk.nwork < cap ? pk.nwork : cap), kThreads, smem_k, sks>>>(pk);
+        k_bwd_dkdv<D, MOD><<<(unsigned)(pk.nwork < cap ? pk.nwork : cap), kThreads, smem_k, sks>>>(pk);
         timing_end(span, sks, kTimeDkdv, 1);
       }
     }
@@ -1551,7 +1662,7 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv, c
     if (pk.nwork > 0 && err == cudaSuccess) {
       pk.sched = sched_slot(pl);
       const int span = timing_begin(sks);
-      k_bwd_dkdv<D><<<(unsigned)(pk.nwork < sms ? pk.nwork : sms), kThreads, smem_k, sks>>>(pk);
+      k_bwd_dkdv<D, MOD><<<(unsigned)(pk.nwork < sms ? pk.nwork : sms), kThreads, smem_k, sks>>>(pk);
       timing_end(span, sks, kTimeDkdv, 1);
     }
     if (sks != s && err == cudaSuccess) err = stream_fork(sks, s);
@@ -1577,23 +1688,24 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv, c
 }  // namespace
 
 marble_status_t run_attn_bwd_fused(const marble_plan_t* p, const marble_qkv_t* qkv,
-                                   const void* d_o, const float* lse, const float* delta,
-                                   float* dq, float* dk, float* dv, cudaStream_t s) {
+                                   const marble_score_t* score, const void* d_o, const float* lse,
+                                   const float* delta, float* dq, float* dk, float* dv,
+                                   cudaStream_t s) {
   if (p->P > kMaxShards) return fail(MARBLE_ERR_UNSUPPORTED, "more than 256 shards");
-  if (qkv->d == 128) return launch_fused<128>(p, qkv, d_o, lse, delta, dq, dk, dv, s);
-  if (qkv->d == 64) return launch_fused<64>(p, qkv, d_o, lse, delta, dq, dk, dv, s);
-  return fail(MARBLE_ERR_UNSUPPORTED, "head dim must be 64 or 128");
+  return with_variant(qkv->d, score_bits(score), [&](auto d, auto mod) {
+    return launch_fused<d(), mod()>(p, qkv, score, d_o, lse, delta, dq, dk, dv, s);
+  });
 }
 
-marble_status_t run_attn_bwd(const marble_plan_t* p, const marble_qkv_t* qkv, const void* d_o,
-                             const float* lse, const float* delta, int n_steps,
-                             const int* q_shards, const int* kv_shards, float* dq, float* dk,
-                             float* dv, cudaStream_t s) {
-  if (qkv->d == 128)
-    return launch_steps<128>(p, qkv, d_o, lse, delta, n_steps, q_shards, kv_shards, dq, dk, dv, s);
-  if (qkv->d == 64)
-    return launch_steps<64>(p, qkv, d_o, lse, delta, n_steps, q_shards, kv_shards, dq, dk, dv, s);
-  return fail(MARBLE_ERR_UNSUPPORTED, "head dim must be 64 or 128");
+marble_status_t run_attn_bwd(const marble_plan_t* p, const marble_qkv_t* qkv,
+                             const marble_score_t* score, const void* d_o, const float* lse,
+                             const float* delta, int n_steps, const int* q_shards,
+                             const int* kv_shards, float* dq, float* dk, float* dv,
+                             cudaStream_t s) {
+  return with_variant(qkv->d, score_bits(score), [&](auto d, auto mod) {
+    return launch_steps<d(), mod()>(p, qkv, score, d_o, lse, delta, n_steps, q_shards, kv_shards,
+                                    dq, dk, dv, s);
+  });
 }
 
 }  // namespace marble

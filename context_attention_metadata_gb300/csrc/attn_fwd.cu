@@ -37,6 +37,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "score.cuh"
 #include "tma_host.h"
 
 namespace marble {
@@ -109,6 +110,7 @@ struct FwdParams {
   const int32_t* qidx;      // [n] plan order -> index in the given token order (the plan's perm)
   const uint8_t* iv_block;  // [nb] 1: every key of the block has an exact interval
   float scale_log2;
+  ScoreParams score;        // read by the kernels built with a cap or a bias
 };
 
 // list range of work unit u = h * bps + i (q block i of the shard, q head h)
@@ -157,7 +159,75 @@ struct Smem {
 };
 static_assert(Smem<128>::bytes() <= 232448, "shared memory budget");
 
-template <int D>
+// A row's 64 products of this half, in place, to base-2 scores with the cap and the bias.  far0:
+// the row's distance to the half's first key where positions are consecutive; otherwise pos
+// holds the keys' positions.
+template <int MOD>
+__device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams& p, float sl2,
+                                          float neg_slope, float far0, int pq,
+                                          const int32_t* __restrict__ pos) {
+  auto pair = [&](int i) {
+    return f2(__uint_as_float(v[i >> 4][2 * (i & 15)]), __uint_as_float(v[i >> 4][2 * (i & 15) + 1]));
+  };
+  auto put = [&](int i, F2 x) {
+    float a, b;
+    split(x, &a, &b);
+    v[i >> 4][2 * (i & 15)] = __float_as_uint(a);
+    v[i >> 4][2 * (i & 15) + 1] = __float_as_uint(b);
+  };
+  F2 sc = f2(sl2);
+  if constexpr ((MOD & kScoreCap) != 0) {
+    float hi = 0.f;
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+      for (int t = 0; t < 32; ++t) hi = fmaxf(hi, fabsf(__uint_as_float(v[cc][t])));
+    if (__all_sync(0xffffffffu, hi <= p.score.lim)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) put(i, cap_poly(pair(i), p.score));
+    } else {
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+        for (int t = 0; t < 32; ++t)
+          v[cc][t] = __float_as_uint(fmaf(-2.f * p.score.cap2,
+                                          cap_rcp(__uint_as_float(v[cc][t]), p.score),
+                                          p.score.cap2));
+    }
+    sc = f2(1.f);
+  }
+  if constexpr ((MOD & kScoreBias) != 0) {
+    const F2 ns = f2(neg_slope);
+    if (p.score.consecutive) {
+      // key t of the half is at distance |far0 - t|
+      F2 d = f2(far0, far0 - 1.f);
+      const F2 two = f2(-2.f);
+      if (__all_sync(0xffffffffu, far0 >= 63.f)) {
+        // every key at or before every row
+#pragma unroll
+        for (int i = 0; i < 32; ++i, d = add2(d, two)) put(i, fma2(ns, d, mul2(pair(i), sc)));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i, d = add2(d, two)) {
+          float a, b;
+          split(d, &a, &b);
+          put(i, fma2(ns, f2(fabsf(a), fabsf(b)), mul2(pair(i), sc)));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const int4 k = __ldg(reinterpret_cast<const int4*>(pos + 2 * i));
+        put(i, fma2(ns, f2(fabsf((float)(pq - k.x)), fabsf((float)(pq - k.y))), mul2(pair(i), sc)));
+        put(i + 1, fma2(ns, f2(fabsf((float)(pq - k.z)), fabsf((float)(pq - k.w))),
+                        mul2(pair(i + 1), sc)));
+      }
+    }
+  }
+}
+
+// MOD: what happens to the scores (bits kScoreCap, kScoreBias); 0 is the plain softmax.
+template <int D, int MOD>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant__ FwdParams p) {
   using L = Smem<D>;
   constexpr int kTile = L::kTile;
@@ -412,9 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
                 pq = p.tracks[3 * n + tq];
       const int iq = p.qidx[tq];  // the interval test's coordinate: the query's index
       const uint32_t ob = tO + (uint32_t)(uc & 1) * 128;
+      [[maybe_unused]] float neg_slope = 0.f;
+      if constexpr ((MOD & kScoreBias) != 0)
+        neg_slope = -p.score.slopes[unit / p.bps] * 1.4426950408889634f;
       float m_run = -INFINITY, l_h = 0.f;
       for (int j = 0; j < T; ++j, ++g) {
         const uint32_t b = (uint32_t)(g & 1);
+        // distance of this row to the half's first key, its keys being at consecutive positions
+        [[maybe_unused]] float far0 = 0.f;
+        if constexpr ((MOD & kScoreBias) != 0)
+          far0 = (float)(pq - p.tracks[3 * n + (int64_t)p.step_col[e0 + j] * 128 + half * 64]);
         const bool partial = p.step_tag[e0 + j] == MARBLE_TILE_PARTIAL;
         uint32_t lm[2] = {~0u, ~0u};  // legal-key bits of this row in this half's 64 columns
         const int64_t kb = partial ? p.step_col[e0 + j] : 0;
@@ -494,7 +571,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         // scaled scores (-inf where masked) replace v, otherwise v keeps the raw scores
         // (scaling by a positive constant commutes with the maximum, and P takes one FMA below)
         float mx = -INFINITY;
-        if (masked) {
+        if constexpr (MOD != 0) {
+          score_row<MOD>(v, p, sl2, neg_slope, far0, pq,
+                         p.tracks + 3 * n + (int64_t)p.step_col[e0 + j] * 128 + half * 64);
+          if (masked) {
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+              for (int t = 0; t < 32; ++t)
+                if (!((lm[cc] >> t) & 1u)) v[cc][t] = __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+            for (int t = 0; t < 32; ++t) mx = fmaxf(mx, __uint_as_float(v[cc][t]));
+        } else if (masked) {
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
 #pragma unroll
@@ -548,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         // buffer: inside the fp32 columns this warp has just read
         const float base = (m_run == -INFINITY) ? 0.f : m_run;
         // v holds scaled scores where keys were masked, raw ones otherwise
-        const float vs = masked ? 1.f : sl2;
+        const float vs = (MOD != 0 || masked) ? 1.f : sl2;
         float rs = 0.f;
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
@@ -758,9 +849,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
 }
 
 // everything but the shard pair, the FIRST flag and the work list: encoded once per call
-template <int D>
+template <int D, int MOD>
 marble_status_t prepare(const marble_plan_t* pl, const marble_qkv_t* qkv,
-                        const marble_state_t* st, FwdParams* prm) {
+                        const marble_score_t* score, const marble_state_t* st, FwdParams* prm) {
   memset(prm, 0, sizeof(*prm));
   const int64_t n = pl->n;
   if (!make_rows_map(&prm->q_map, qkv->q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, n, qkv->hq, D, 64,
@@ -794,8 +885,13 @@ marble_status_t prepare(const marble_plan_t* pl, const marble_qkv_t* qkv,
   prm->W = pl->W;
   const float scale = qkv->scale > 0.f ? qkv->scale : 1.0f / sqrtf((float)D);
   prm->scale_log2 = scale * 1.4426950408889634f;
-  if (once_per_device(D == 128 ? 1 : 2)) {
-    cudaError_t e = cudaFuncSetAttribute(k_attn_fwd<D>,
+  if (MOD & kScoreCap) set_cap(&prm->score, score->cap, scale);
+  if (MOD & kScoreBias) {
+    prm->score.slopes = score->slopes;
+    prm->score.consecutive = pl->pos_is_index;
+  }
+  if (once_per_device((D == 128 ? 1 : 2) + 4 * MOD)) {
+    cudaError_t e = cudaFuncSetAttribute(k_attn_fwd<D, MOD>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Smem<D>::bytes());
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(k_attn_fwd)");
@@ -803,12 +899,12 @@ marble_status_t prepare(const marble_plan_t* pl, const marble_qkv_t* qkv,
   return MARBLE_OK;
 }
 
-template <int D>
-marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv, int n_steps,
-                             const int* q_shards, const int* kv_shards, const uint32_t* flags,
+template <int D, int MOD>
+marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv,
+                             const marble_score_t* score, int n_steps, const int* q_shards, const int* kv_shards, const uint32_t* flags,
                              const marble_state_t* st, cudaStream_t s) {
   FwdParams base;
-  marble_status_t rc = prepare<D>(pl, qkv, st, &base);
+  marble_status_t rc = prepare<D, MOD>(pl, qkv, score, st, &base);
   if (rc != MARBLE_OK) return rc;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -848,7 +944,7 @@ marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv, i
     const int cap = ns > 1 ? (sms + 1) / 2 : sms;
     const unsigned grid = (unsigned)(want < cap ? want : cap);
     const int k = prm.q_shard % ns;
-    k_attn_fwd<D><<<grid, kThreads, Smem<D>::bytes(), st_of[k]>>>(prm);
+    k_attn_fwd<D, MOD><<<grid, kThreads, Smem<D>::bytes(), st_of[k]>>>(prm);
     ++launches[k];
   }
   for (int k = 0; k < ns; ++k) timing_end(span[k], st_of[k], kTimeFwd, launches[k]);
@@ -865,11 +961,12 @@ marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv, i
 // walking its tiles in ring order (kv shard (r - s) mod P at step s, the plan's ring-ordered
 // copy of its lists) with the fp32 state held on chip from the first step to the last; the
 // state is written once, as the FIRST step of the per-step path writes it.
-template <int D>
+template <int D, int MOD>
 marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
-                             const marble_state_t* st, cudaStream_t s) {
+                             const marble_score_t* score, const marble_state_t* st,
+                             cudaStream_t s) {
   FwdParams prm;
-  marble_status_t rc = prepare<D>(pl, qkv, st, &prm);
+  marble_status_t rc = prepare<D, MOD>(pl, qkv, score, st, &prm);
   if (rc != MARBLE_OK) return rc;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -888,7 +985,7 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
   prm.sched = sched_slot(pl);
   const unsigned grid = (unsigned)(prm.units < sms ? prm.units : sms);
   const int span = timing_begin(s);
-  k_attn_fwd<D><<<grid, kThreads, Smem<D>::bytes(), s>>>(prm);
+  k_attn_fwd<D, MOD><<<grid, kThreads, Smem<D>::bytes(), s>>>(prm);
   timing_end(span, s, kTimeFwd, 1);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch k_attn_fwd (fused)");
@@ -898,20 +995,22 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
 }  // namespace
 
 marble_status_t run_attn_fwd_fused(const marble_plan_t* p, const marble_qkv_t* qkv,
-                                   const marble_state_t* st, cudaStream_t s) {
+                                   const marble_score_t* score, const marble_state_t* st,
+                                   cudaStream_t s) {
   if ((int64_t)p->nb * qkv->hq > INT_MAX)
     return fail(MARBLE_ERR_UNSUPPORTED, "too many (block, head) work units");
-  if (qkv->d == 128) return launch_fused<128>(p, qkv, st, s);
-  if (qkv->d == 64) return launch_fused<64>(p, qkv, st, s);
-  return fail(MARBLE_ERR_UNSUPPORTED, "head dim must be 64 or 128");
+  return with_variant(qkv->d, score_bits(score), [&](auto d, auto mod) {
+    return launch_fused<d(), mod()>(p, qkv, score, st, s);
+  });
 }
 
-marble_status_t run_attn_fwd(const marble_plan_t* p, const marble_qkv_t* qkv, int n_steps,
-                             const int* q_shards, const int* kv_shards, const uint32_t* flags,
-                             const marble_state_t* st, cudaStream_t s) {
-  if (qkv->d == 128) return launch_steps<128>(p, qkv, n_steps, q_shards, kv_shards, flags, st, s);
-  if (qkv->d == 64) return launch_steps<64>(p, qkv, n_steps, q_shards, kv_shards, flags, st, s);
-  return fail(MARBLE_ERR_UNSUPPORTED, "head dim must be 64 or 128");
+marble_status_t run_attn_fwd(const marble_plan_t* p, const marble_qkv_t* qkv,
+                             const marble_score_t* score, int n_steps, const int* q_shards,
+                             const int* kv_shards, const uint32_t* flags, const marble_state_t* st,
+                             cudaStream_t s) {
+  return with_variant(qkv->d, score_bits(score), [&](auto d, auto mod) {
+    return launch_steps<d(), mod()>(p, qkv, score, n_steps, q_shards, kv_shards, flags, st, s);
+  });
 }
 
 }  // namespace marble

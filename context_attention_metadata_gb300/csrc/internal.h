@@ -47,6 +47,7 @@ struct marble_plan {
   int32_t* kiv = nullptr;       // [2*n] new order: lo, hi of every key's visible query interval
   uint8_t* iv_block = nullptr;  // [nb] new order: 1 if every key of the block is exact
   int4* kiv_chunk = nullptr;    // [nb*4] per 32 keys: min lo, max lo, min hi, max hi
+  int pos_is_index = 1;         // no position track: a block's positions are consecutive
   int64_t bps = 0;           // blocks per shard
   int64_t nnz = 0, needed_total = 0;
   // device arrays (owned)
@@ -192,20 +193,25 @@ cudaError_t launch_rope_bwd(const marble_plan_t* plan, int64_t n, const marble_r
 cudaError_t launch_debug_wait(unsigned* err, uint64_t limit_ns, cudaStream_t s);
 
 // attention (attn_fwd.cu, attn_bwd.cu): a list of ring steps launched back to back on `s`
-marble_status_t run_attn_fwd(const marble_plan_t* p, const marble_qkv_t* qkv, int n_steps,
-                             const int* q_shards, const int* kv_shards, const uint32_t* flags,
-                             const marble_state_t* st, cudaStream_t s);
+// (score: cap and bias of the scores, null for neither)
+marble_status_t run_attn_fwd(const marble_plan_t* p, const marble_qkv_t* qkv,
+                             const marble_score_t* score, int n_steps, const int* q_shards,
+                             const int* kv_shards, const uint32_t* flags, const marble_state_t* st,
+                             cudaStream_t s);
 // the fused ring (attn_fwd.cu, attn_bwd.cu): every ring step of the pass in one forward
 // launch, and one dK/dV launch per kv shard over its ring
 marble_status_t run_attn_fwd_fused(const marble_plan_t* p, const marble_qkv_t* qkv,
-                                   const marble_state_t* st, cudaStream_t s);
+                                   const marble_score_t* score, const marble_state_t* st,
+                                   cudaStream_t s);
 marble_status_t run_attn_bwd_fused(const marble_plan_t* p, const marble_qkv_t* qkv,
-                                   const void* d_o, const float* lse, const float* delta,
-                                   float* dq, float* dk, float* dv, cudaStream_t s);
-marble_status_t run_attn_bwd(const marble_plan_t* p, const marble_qkv_t* qkv, const void* d_o,
-                             const float* lse, const float* delta, int n_steps,
-                             const int* q_shards, const int* kv_shards, float* dq, float* dk,
-                             float* dv, cudaStream_t s);
+                                   const marble_score_t* score, const void* d_o, const float* lse,
+                                   const float* delta, float* dq, float* dk, float* dv,
+                                   cudaStream_t s);
+marble_status_t run_attn_bwd(const marble_plan_t* p, const marble_qkv_t* qkv,
+                             const marble_score_t* score, const void* d_o, const float* lse,
+                             const float* delta, int n_steps, const int* q_shards,
+                             const int* kv_shards, float* dq, float* dk, float* dv,
+                             cudaStream_t s);
 
 // true the first time it is called for (key, current device); used for per-device set-up
 bool once_per_device(int key);

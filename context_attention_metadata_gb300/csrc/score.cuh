@@ -1,0 +1,133 @@
+// What happens to an attention score between the product and the softmax, beyond the scale: a
+// soft cap and a bias by distance, shared by the forward and the backward kernel.
+//
+// With x = q . k from the tensor core, in base-2 units (times log2 e):
+//   no cap   s = x * scale * log2 e
+//   cap c    s = c * log2 e * tanh(x * scale / c)
+//   bias     s -= slope_h * log2 e * |pos_q - pos_k|
+// and for the gradient of a capped score ds/dx = scale * (1 - tanh^2), the factor 1 - tanh^2 here.
+//
+// tanh is taken in one of two ways, decided per warp and tile:
+//   |x scale / c| <= 0.75 for all of the warp's scores: an odd polynomial, tanh y = y (a0 + a1 y^2
+//     + ... + a5 y^10), the minimax fit of tanh(y) / y in y^2 over [0, 0.75^2] (computed by the
+//     exchange algorithm), relative error 2^-25.  Its coefficients are folded with the scale on
+//     the host, so that a score costs seven multiply-adds, done two at a time (f32x2).
+//   otherwise 1 - 2 / (1 + e^(2 y)): two calls to the special function unit, which also has the
+//     softmax's exp2 to do, and an absolute error of 2^-22 c (the score's own rounding is of
+//     that size, some |score| being above 0.75 c).
+#pragma once
+
+#include <math.h>
+
+#include <cmath>
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace marble {
+
+enum : int { kScoreCap = 1, kScoreBias = 2 };  // bits of a kernel's score variant
+
+struct ScoreParams {
+  float c[6];           // s = x (c[0] + c[1] x^2 + ... + c[5] x^10) for |x| <= lim
+  float lim;
+  float ky;             // e^(2 y) = 2^(ky x)
+  float cap2;           // cap * log2 e
+  float inv_cap2;       // 1 / cap2
+  const float* slopes;  // [hq] or null
+  int consecutive;      // the positions of a block's tokens are consecutive
+};
+
+// the score variant a call needs
+inline int score_bits(const marble_score_t* s) {
+  return s ? (s->cap > 0.f ? kScoreCap : 0) | (s->slopes ? kScoreBias : 0) : 0;
+}
+
+// f(d, mod) with the head dim and the score variant as compile-time values
+template <class F>
+marble_status_t with_variant(int d, int mod, F f) {
+  auto at_d = [&](auto dd) {
+    switch (mod) {
+      case 0: return f(dd, std::integral_constant<int, 0>{});
+      case kScoreCap: return f(dd, std::integral_constant<int, kScoreCap>{});
+      case kScoreBias: return f(dd, std::integral_constant<int, kScoreBias>{});
+      default: return f(dd, std::integral_constant<int, kScoreCap | kScoreBias>{});
+    }
+  };
+  if (d == 128) return at_d(std::integral_constant<int, 128>{});
+  if (d == 64) return at_d(std::integral_constant<int, 64>{});
+  return fail(MARBLE_ERR_UNSUPPORTED, "head dim must be 64 or 128");
+}
+
+// `cap` > 0
+inline void set_cap(ScoreParams* s, float cap, float scale) {
+  static const double kA[6] = {0.9999999710138949,  -0.3333295887947679,   0.1332540601769393,
+                               -0.053344430143664245, 0.019582908187657067, -0.004716257251125382};
+  const double log2e = 1.4426950408889634, k = (double)scale / cap;
+  double f = scale * log2e;
+  bool ok = true;
+  for (int i = 0; i < 6; ++i, f *= k * k) {
+    s->c[i] = (float)(kA[i] * f);
+    ok = ok && std::isfinite(s->c[i]);
+  }
+  // x^10 has to stay finite, and so do the coefficients: caps far below the scale take the
+  // second way alone
+  s->lim = ok ? (float)fmin(0.75 / k, 1e3) : -1.f;
+  s->ky = (float)(2.0 * log2e * k);
+  s->cap2 = (float)(cap * log2e);
+  s->inv_cap2 = (float)(1.0 / (cap * log2e));
+}
+
+// two fp32 values in a register pair and the packed operations on them
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void split(F2 x, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// capped scores of a pair, |x| <= lim
+__device__ __forceinline__ F2 cap_poly(F2 x, const ScoreParams& p) {
+  const F2 u = mul2(x, x);
+  F2 r = fma2(f2(p.c[5]), u, f2(p.c[4]));
+  r = fma2(r, u, f2(p.c[3]));
+  r = fma2(r, u, f2(p.c[2]));
+  r = fma2(r, u, f2(p.c[1]));
+  r = fma2(r, u, f2(p.c[0]));
+  return mul2(x, r);
+}
+
+// 1 / (1 + e^(2 y)): the capped score is cap2 (1 - 2 r), its slope's factor 4 r (1 - r)
+__device__ __forceinline__ float cap_rcp(float x, const ScoreParams& p) {
+  return fast_rcp(1.f + fast_exp2(x * p.ky));
+}
+
+}  // namespace marble

@@ -529,6 +529,52 @@ marble_status_t marble_attn_bwd_fused(const marble_plan_t *plan, const marble_qk
                                       float *dq_acc, float *dk_acc, float *dv_acc,
                                       marble_stream_t stream);
 
+/*
+ * Attention whose scores are changed between the product and the softmax.  With s = scale * q.k
+ * of a legal pair:
+ *   cap > 0:         s <- cap * tanh(s / cap)                       (0: no cap)
+ *   slopes != NULL:  s <- s - slopes[h] * |pos_q - pos_k|           (after the cap)
+ * h is the q head, pos the tokens' original positions (their indices in the order the tracks
+ * are given in, or pos_id).  The mask is the plan's, samples (documents) and bidirectional spans
+ * (prefixes) included; a row without a legal key is as without these.  State, LSE and O mean
+ * what they mean for the plain calls, of the changed scores; the backward calls give the
+ * gradients of q, k and v through cap and bias.  slopes are constants: finite, of any sign, no
+ * gradient.  They are read when the kernels run.  Q, K, V and dO have to be finite for masked
+ * tokens too, as for the plain calls.
+ */
+typedef struct {
+  float cap;           /* finite, >= 0 */
+  const float *slopes; /* device float[hq], 16-byte aligned, or NULL */
+} marble_score_t;
+
+/*
+ * marble_attn_steps, marble_attn_fwd_fused, marble_attn_bwd_steps and marble_attn_bwd_fused with
+ * changed scores: the same arguments, results and errors, a list of one step being the single
+ * step.  The same `score` has to be given to every call of a pass, forward and backward.  score
+ * NULL, or with neither cap nor slopes, is the plain call.  The launches take ticket counters and
+ * scratch of the plan: a stream that is being captured into a graph is refused (INVALID_ARG).
+ */
+marble_status_t marble_attn_steps_scored(const marble_plan_t *plan, const marble_qkv_t *qkv,
+                                         const marble_score_t *score, int32_t n_steps,
+                                         const int32_t *q_shards, const int32_t *kv_shards,
+                                         const uint32_t *flags, const marble_state_t *state,
+                                         marble_stream_t stream);
+marble_status_t marble_attn_fwd_fused_scored(const marble_plan_t *plan, const marble_qkv_t *qkv,
+                                             const marble_score_t *score,
+                                             const marble_state_t *state, marble_stream_t stream);
+marble_status_t marble_attn_bwd_steps_scored(const marble_plan_t *plan, const marble_qkv_t *qkv,
+                                             const marble_score_t *score, const void *d_o,
+                                             const float *lse, const float *delta,
+                                             int32_t n_steps, const int32_t *q_shards,
+                                             const int32_t *kv_shards, float *dq_acc,
+                                             float *dk_acc, float *dv_acc,
+                                             marble_stream_t stream);
+marble_status_t marble_attn_bwd_fused_scored(const marble_plan_t *plan, const marble_qkv_t *qkv,
+                                             const marble_score_t *score, const void *d_o,
+                                             const float *lse, const float *delta, float *dq_acc,
+                                             float *dk_acc, float *dv_acc,
+                                             marble_stream_t stream);
+
 /* Cast fp32 -> bf16 (round to nearest even) for n elements, e.g. gradient accumulators;
  * n must be a multiple of 4 and both pointers 16-byte aligned. */
 marble_status_t marble_cast_bf16(const float *src, void *dst, int64_t n,

@@ -1,0 +1,313 @@
+"""Attention with capped scores and a bias by distance on the GPU against the fp64 oracle.
+
+Tolerances.  P and dS are rounded to bf16 before their products, O before delta: half a step,
+2^-8, each, carried to every result by the oracle's bounds; results are fp32 or rounded to bf16
+once more.  The rest is fp32: a score of size S is off by 2^-24 times (d for the sum of d
+products, 4 for cap and bias, both below 2^-22 of the scores' size), for |S| up to 40 and the sum
+of |products| up to four times that 128 * 2^-24 * 160 = 1.2e-3 at the very worst, which changes a
+weight by that factor; the root of d in place of d gives 1.1e-4, which is allowed here (SOFT) for
+the LSE and, times the size of the terms, for everything else."""
+import numpy as np
+import pytest
+import torch
+
+import context_attention_metadata_gb300 as M
+import workloads as wl
+from marble_testlib import device_tracks, rel_fro
+from oracle import mask, scored
+
+pytestmark = pytest.mark.gpu
+HALF = torch.finfo(torch.bfloat16).eps / 2
+SOFT = 1.2e-4
+INF = wl.WINDOW_INF
+
+
+def _slopes(hq, kind):
+    s = {None: None, "usual": [2.0 ** (-8 * (h + 1) / hq) for h in range(hq)],
+         "signed": [(-1) ** h * 0.01 * (h + 1) for h in range(hq)],
+         "steep": [3.0 + h for h in range(hq)], "zero": [0.0] * hq}[kind]
+    return None if s is None else torch.tensor(s, dtype=torch.float32, device="cuda")
+
+
+def _qkvdo(n, hq, hkv, d, seed, scale=1.5):
+    q, k, v, do = wl.make_qkvdo(n, hq, hkv, d, device="cuda", seed=seed)
+    return (q.float() * scale).bfloat16(), k, v, do
+
+
+def _run(pl, q, k, v, do, score, needed=False, fused=False, merge="carried", stream=None):
+    """Forward and backward, everything back in original order: O, LSE, dq, dk, dv."""
+    n, hq, d = q.shape
+    qp, kp, vp, dp = (pl.permute(x) for x in (q, k, v, do))
+    st = M.State(n, hq, d)
+    o, lse = torch.empty_like(qp), torch.empty((hq, n), device="cuda")
+    delta = torch.empty_like(lse)
+    dq, dk, dv = (torch.zeros(x.shape, device="cuda") for x in (q, k, v))
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+    M.forward(pl, qp, kp, vp, st, o, lse, needed=needed, fused=fused, merge=merge, score=score,
+              stream=stream)
+    M.backward(pl, qp, kp, vp, o, dp, lse, delta, dq, dk, dv, needed=needed, fused=fused,
+               score=score, stream=stream)
+    if stream is not None:
+        torch.cuda.current_stream().wait_stream(stream)
+    pl.check()
+    perm = pl.export("perm").long()
+    out = torch.empty_like(lse)
+    out[:, perm] = lse
+    return (pl.permute(o, inverse=True), out) + tuple(pl.permute(x, inverse=True)
+                                                      for x in (dq, dk, dv))
+
+
+def _np(x):
+    return x.double().cpu().numpy()
+
+
+def _check(got, q, k, v, do, m, cap, slopes, pos=None, scale=None, steps=1):
+    """steps: roundings of O to bf16 (one, or the bf16 merge's)."""
+    ref = scored.attention(q, k, v, m, cap, None if slopes is None else _np(slopes), pos, scale,
+                           do, HALF)
+    b = ref["bound"]
+    O, L = _np(got[0]), _np(got[1])
+    soft = SOFT / HALF  # the bounds are HALF times the size of the terms
+    # the rounding of P differs from the exact by half a step of the rounded value
+    assert (np.abs(O - ref["O"]) <= (1 + HALF) * ((1 + soft) * b["O"] +
+                                                  steps * HALF * np.abs(ref["O"]) + 1e-30)).all()
+    live = np.isfinite(ref["LSE"])
+    assert (np.isfinite(L) == live).all() and (L[~live] == -np.inf).all()
+    assert (np.abs(L - ref["LSE"])[live] <= SOFT).all(), np.abs(L - ref["LSE"])[live].max()
+    for name, x in zip(("dq", "dk", "dv"), got[2:]):
+        err = np.abs(_np(x) - ref[name])
+        # both dS and P carry the factor of the scores' error, and delta that of O
+        assert (err <= (1 + HALF) * (1 + 4 * soft) * b[name] + 1e-6).all(), \
+            (name, (err - b[name]).max())
+        # over all entries the roundings average: the error's square is at most the sum of their
+        # variances, each at most the square of half a step (a third of it, if evenly spread)
+        assert np.linalg.norm(err) <= np.sqrt(ref["noise"][name].sum()) + 1e-6, name
+
+
+MODES = [(30.0, None), (2.0, None), (0.0, "usual"), (5.0, "usual"), (1.0, "signed"),
+         (0.0, "steep"), (0.0, "signed")]
+
+
+@pytest.mark.parametrize("seed", range(14))
+def test_random_packs(seed):
+    cap, kind = MODES[seed % len(MODES)]
+    rng = np.random.default_rng(4000 + seed)
+    n = 128 * int(rng.choice([1, 2, 4, 8]))
+    tr = wl.random_pack(rng, n, max_samples=int(rng.integers(1, 5)))
+    d, hkv = int(rng.choice([64, 128])), int(rng.choice([1, 2, 3]))
+    hq = hkv * int(rng.choice([1, 2, 4]))
+    P = int(rng.choice([p for p in (1, 2, 4) if (n // 128) % p == 0]))
+    W = int(rng.choice([INF, 1, 60, 300]))
+    order = ["contiguous", "ptrr_block"][seed % 2]
+    q, k, v, do = _qkvdo(n, hq, hkv, d, seed)
+    slopes = _slopes(hq, kind)
+    pl = M.Plan(*device_tracks(tr), W, P, order)
+    m = mask.dense_mask(tr, W)
+    score = M.Score(cap, slopes)
+    for kw in ({}, {"needed": True}, {"fused": True}):
+        _check(_run(pl, q, k, v, do, score, **kw), q, k, v, do, m, cap, slopes)
+
+
+@pytest.mark.parametrize("cap,kind", [(2.0, "usual"), (20.0, None), (0.0, "signed")])
+@pytest.mark.parametrize("cid", [1, 2, 5])
+def test_small_configurations(cid, cap, kind):
+    n = 2048
+    tr = wl.config_tracks(cid, n)
+    q, k, v, do = _qkvdo(n, 4, 2, 128, cid)
+    slopes = _slopes(4, kind)
+    pl = M.Plan(*device_tracks(tr), INF, 4, "ptrr_block")
+    m = mask.dense_mask(tr, INF)
+    for fused in (False, True):
+        _check(_run(pl, q, k, v, do, M.Score(cap, slopes), fused=fused), q, k, v, do, m, cap, slopes)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_without_a_key(d):
+    tr = wl.tracks_from_samples([[wl.Span("causal", 300), wl.Span("full", 200)],
+                                 [wl.Span("causal", 12)]])
+    q, k, v, do = _qkvdo(512, 2, 1, d, 5)
+    slopes = _slopes(2, "usual")
+    pl = M.Plan(*device_tracks(tr), 0, 2)
+    m = mask.dense_mask(tr, 0)
+    for fused in (False, True):
+        got = _run(pl, q, k, v, do, M.Score(3.0, slopes), fused=fused)
+        assert (got[0][:300] == 0).all() and (got[2][:300] == 0).all()
+        _check(got, q, k, v, do, m, 3.0, slopes)
+
+
+@pytest.mark.parametrize("kind", ["usual", "signed"])
+def test_position_track(kind):
+    """A permuted pack: distances come from the position track."""
+    rng = np.random.default_rng(8)
+    samples = [[wl.Span("causal", 90), wl.Span("group", 130), wl.Span("causal", 41),
+                wl.Span("group", 200), wl.Span("causal", 51)],
+               [wl.Span("causal", 100), wl.Span("full", 156)], [wl.Span("noise", 128),
+                                                                wl.Span("causal", 128)]]
+    tr = wl.tracks_from_samples(samples)
+    n = len(tr["sample"])
+    perm = M.layout_vision_groups(tr["sample"], tr["seg"])
+    moved = {x: np.asarray(tr[x])[perm] for x in tr}
+    moved["pos"] = perm.astype(np.int32)
+    q, k, v, do = _qkvdo(n, 4, 4, 64, 8)
+    slopes = _slopes(4, kind)
+    s, g, z = device_tracks(moved)
+    pos = torch.as_tensor(moved["pos"]).cuda()
+    for P, fused in ((1, True), (2, False)):
+        pl = M.Plan(s, g, z, INF, P, "ptrr_block", pos=pos)
+        for cap in (0.0, 2.0):
+            _check(_run(pl, q, k, v, do, M.Score(cap, slopes), fused=fused), q, k, v, do,
+                   mask.dense_mask(moved, INF), cap, slopes, moved["pos"])
+    del rng
+
+
+@pytest.mark.parametrize("cap", [1e-3, 0.1, 1e4, 1e30])
+def test_extreme_caps(cap):
+    """Caps far below and far above the scores: all weights alike, and no cap at all."""
+    n = 512
+    tr = wl.random_pack(np.random.default_rng(3), n, max_samples=2)
+    q, k, v, do = _qkvdo(n, 2, 2, 64, 3)
+    pl = M.Plan(*device_tracks(tr), INF, 1)
+    m = mask.dense_mask(tr, INF)
+    for fused in (False, True):
+        _check(_run(pl, q, k, v, do, M.Score(cap), fused=fused), q, k, v, do, m, cap, None)
+    # scores of zero, whatever the coefficients
+    got = _run(pl, torch.zeros_like(q), k, v, do, M.Score(cap))
+    _check(got, torch.zeros_like(q), k, v, do, m, cap, None)
+
+
+def test_both_ways_to_tanh_in_one_pack():
+    """Rows with small and rows with large scores, tile by tile, around the border of 0.75."""
+    n = 1024
+    tr = wl.tracks_from_samples([[wl.Span("causal", 600), wl.Span("full", 424)]])
+    q, k, v, do = _qkvdo(n, 2, 1, 128, 6)
+    gain = torch.ones(n, device="cuda")
+    gain[::3], gain[1::64], gain[512:] = 0.05, 4.0, 0.3
+    q = (q.float() * gain[:, None, None]).bfloat16()
+    pl = M.Plan(*device_tracks(tr), INF, 2)
+    m = mask.dense_mask(tr, INF)
+    for cap in (2.0, 4.0, 8.0):
+        _check(_run(pl, q, k, v, do, M.Score(cap), fused=True), q, k, v, do, m, cap, None)
+
+
+def test_scale_and_merges():
+    n = 1024
+    tr = wl.config_tracks(2, n)
+    q, k, v, do = _qkvdo(n, 2, 2, 64, 7)
+    slopes = _slopes(2, "usual")
+    pl = M.Plan(*device_tracks(tr), INF, 4, "ptrr_block")
+    m = mask.dense_mask(tr, INF)
+    for merge, steps in (("fp32", 1), ("bf16", 9)):  # four partials and four merges rounded
+        got = _run(pl, q, k, v, do, M.Score(3.0, slopes), merge=merge)
+        ref = scored.attention(q, k, v, m, 3.0, _np(slopes), h=HALF)
+        # a partial is a mean over its keys: rounding it costs half a step of P |V| at the most
+        lim = (1 + HALF) * ((1 + SOFT / HALF + (steps - 1)) * ref["bound"]["O"] +
+                            HALF * np.abs(ref["O"]) + 1e-30)
+        assert (np.abs(_np(got[0]) - ref["O"]) <= lim).all()
+        assert (np.abs(_np(got[1]) - ref["LSE"]) <= SOFT).all()
+    st, o, lse = M.State(n, 2, 64), torch.empty_like(q), torch.empty((2, n), device="cuda")
+    M.forward(pl, *(pl.permute(x) for x in (q, k, v)), st, o, lse, scale=0.3, fused=True,
+              score=M.Score(3.0, slopes))
+    ref = scored.attention(q, k, v, m, 3.0, _np(slopes), scale=0.3, h=HALF)
+    lim = (1 + HALF) * ((1 + SOFT / HALF) * ref["bound"]["O"] + HALF * np.abs(ref["O"]) + 1e-30)
+    assert (np.abs(_np(pl.permute(o, inverse=True)) - ref["O"]) <= lim).all()
+
+
+def test_no_change_is_the_plain_call():
+    """A score without cap and slopes has the plain call's bits; so has a step of the list."""
+    n = 1024
+    tr = wl.config_tracks(2, n)
+    q, k, v, do = _qkvdo(n, 4, 2, 64, 9)
+    pl = M.Plan(*device_tracks(tr), INF, 2)
+    for kw in ({}, {"needed": True}, {"fused": True}):
+        for x, y in zip(_run(pl, q, k, v, do, None, **kw), _run(pl, q, k, v, do, M.Score(), **kw)):
+            assert torch.equal(x, y)
+    score = M.Score(4.0, _slopes(4, "usual"))
+    a, b = M.State(n, 4, 64), M.State(n, 4, 64)
+    M.attn_steps(pl, q, k, v, M.ring_schedule(2), a, score=score)
+    for r, j, first in M.ring_schedule(2):
+        M.attn_step(pl, q, k, v, r, j, b, first=first, score=score)
+    o, lse = torch.empty_like(q), torch.empty((4, n), device="cuda")
+    M.attn_finalize(pl, a, o, lse)
+    for x, y in ((a.o_acc, b.o_acc), (a.m, b.m), (a.l, b.l)):
+        assert torch.equal(x, y)
+    delta = torch.empty_like(lse)
+    M.attn_bwd_prep(pl, o, do, delta)
+    g, w = ([torch.zeros(x.shape, device="cuda") for x in (q, k, v)] for _ in range(2))
+    for r, j, _ in M.ring_schedule(2):
+        M.attn_bwd(pl, q, k, v, do, lse, delta, r, j, *g, score=score)
+    M.attn_bwd_steps(pl, q, k, v, do, lse, delta, M.ring_schedule(2), *w, score=score)
+    for x, y in zip(g, w):  # the list may take whole rows: summation order
+        assert rel_fro(_np(x), _np(y)) <= 1e-4
+
+
+def test_repeats_streams_and_side_streams():
+    n = 2048
+    tr = wl.config_tracks(2, n)
+    q, k, v, do = _qkvdo(n, 4, 2, 128, 10)
+    pl = M.Plan(*device_tracks(tr), INF, 4, "ptrr_block")
+    score = M.Score(6.0, _slopes(4, "usual"))
+    for fused in (False, True):
+        want = _run(pl, q, k, v, do, score, fused=fused)
+        again = [_run(pl, q, k, v, do, score, fused=fused),
+                 _run(pl, q, k, v, do, score, fused=fused, stream=torch.cuda.Stream())]
+        try:
+            M.set_side_streams(0)
+            again.append(_run(pl, q, k, v, do, score, fused=fused))
+        finally:
+            M.set_side_streams(4)
+        for got in again:
+            for x, y in zip(want, got):
+                assert torch.equal(x, y)
+
+
+def test_full_size_rows():
+    """The 64K packed configuration: rows of whole short samples against the oracle."""
+    cfg = wl.CONFIGS[2]
+    tr = wl.config_tracks(2)
+    q, k, v, do = _qkvdo(cfg.n, 4, 4, cfg.d, 11)
+    slopes = _slopes(4, "usual")
+    pl = M.Plan(*device_tracks(tr), INF, cfg.shards, cfg.order)
+    got = _run(pl, q, k, v, do, M.Score(20.0, slopes), fused=True)
+    st, en = mask.sample_runs(tr)
+    starts = np.unique(st)
+    lengths = en[starts] - starts
+    picks = [starts[i] for i in np.argsort(lengths)[[0, len(lengths) // 4, len(lengths) // 2]]]
+    picks.append([s for s in starts if en[s] - s < 2048][-1])
+    for a in picks:
+        b = int(en[a])
+        sub = {x: np.asarray(tr[x])[a:b] for x in ("sample", "seg", "noise")}
+        cut = [x[a:b] for x in (q, k, v, do)]
+        part = (got[0][a:b], got[1][:, a:b]) + tuple(x[a:b] for x in got[2:])
+        _check(part, *cut, mask.dense_mask(sub, INF), 20.0, slopes)
+
+
+def test_refusals():
+    n = 256
+    zero = torch.zeros(n, dtype=torch.int32, device="cuda")
+    none = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    pl = M.Plan(zero, none, none, INF, 1)
+    q, k, v, _ = _qkvdo(n, 2, 2, 64, 1)
+    st = M.State(n, 2, 64)
+    for cap in (-1.0, float("nan"), float("inf")):
+        with pytest.raises(M.MarbleError, match="cap"):
+            M.attn_fwd_fused(pl, q, k, v, st, score=M.Score(cap))
+    with pytest.raises(ValueError):
+        M.Score(slopes=torch.zeros(2, dtype=torch.float64, device="cuda"))
+    with pytest.raises(ValueError):
+        M.Score(slopes=torch.zeros(2))
+    with pytest.raises(ValueError):
+        M.Score(slopes=torch.zeros((2, 1), device="cuda"))
+    with pytest.raises(ValueError):
+        M.attn_fwd_fused(pl, q, k, v, st, score=M.Score(slopes=torch.zeros(3, device="cuda")))
+    with pytest.raises(M.MarbleError, match="aligned"):
+        M.attn_fwd_fused(pl, q, k, v, st,
+                         score=M.Score(slopes=torch.zeros(3, device="cuda")[1:]))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(M.MarbleError, match="captured"):
+            M.attn_fwd_fused(pl, q, k, v, st, score=M.Score(2.0))
+        st.m.zero_()
+    M.attn_fwd_fused(pl, q, k, v, st, score=M.Score(2.0))
+    pl.check()
