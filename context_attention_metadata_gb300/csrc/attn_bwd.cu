@@ -351,8 +351,9 @@ __global__ void __launch_bounds__(kGThreads, 1) k_bwd_dq(const __grid_constant__
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kId = idesc_bf16(128, D, true, true);  // A and B both MN-major
+      const uint64_t dS0 = sdesc_sw128(smem_u32(smem), 16384, 1024);
       int uc = 0, g = 0;
       bool ok = true;
       while (ok) {
@@ -367,11 +368,11 @@ __global__ void __launch_bounds__(kGThreads, 1) k_bwd_dq(const __grid_constant__
           // the unit's first MMA overwrites its buffer: the unit two back must be read out
           if (j == 0 && uc >= 2 && !mbar_wait(&bar[G_OFREE0 + ob], ((uc >> 1) - 1) & 1, w)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t aS = smem_u32(smem + s * L::kStage), aK = aS + L::kDs;
+          const uint64_t aS = sdesc_at(dS0, s * L::kStage), aK = sdesc_at(aS, L::kDs);
+          mma_ss(tQ + ob * 128, aS, aK, kId, j > 0 ? 1u : 0u);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ss(tQ + ob * 128, sdesc_sw128(aS + k * 2048, 16384, 1024),
-                   sdesc_sw128(aK + k * 2048, 16384, 1024), kId, (j > 0 || k > 0) ? 1u : 0u);
+          for (int k = 1; k < 8; ++k)
+            mma_ss(tQ + ob * 128, sdesc_at(aS, k * 2048), sdesc_at(aK, k * 2048), kId, 1u);
           mma_commit(&bar[G_EMPTY0 + s]);
           if (j == T - 1) mma_commit(&bar[G_OFULL0 + ob]);
         }
@@ -451,14 +452,16 @@ __global__ void __launch_bounds__(kGThreads, 1) k_bwd_dq(const __grid_constant__
 // TMEM: two 128-column score regions R0, R1 and the accumulators dV [256, 384), dK [384, 512).
 // Item g (counted over all units of the CTA) puts S^T(g) = K Q^T in R[g & 1] and
 // dP^T(g) = V dO^T in R[(g + 1) & 1], full width (N = 128 q columns).  The elementwise warps
-// load both into registers and say so (YFREE); the dP^T region is then free, and the MMA
-// thread issues S^T(g + 1) into it while the warps compute.  Each half of the warps writes
-// its bf16 P^T and dS^T into the 64 columns of S^T(g)'s region it has itself read (P^T of q
-// columns [64 h, 64 h + 64) in columns [64 h, 64 h + 32), dS^T in [64 h + 32, 64 h + 64)),
-// so no half waits for the other (PFULL); the MMA thread
-// issues dV += P^T dO and dK += dS^T Q (A from TMEM, K = 128 q), then dP^T(g + 1) into the
-// same region, which the tensor core writes only after the two accumulations have read it
-// (tcgen05.mma instructions of one thread execute in issue order).  Per item: 32 MMA
+// turn S^T(g) into P^T(g) first (the exponential, and with it a cap's tanh and the bias), which
+// needs no dP^T: they do it while the tensor core runs dK(g - 1) and dP^T(g).  The MMA thread
+// issues dV += P^T dO as soon as P^T is written (PFULL).  Then they load dP^T(g) and say so
+// (YFREE); its region is free, and the MMA thread issues S^T(g + 1) into it while the warps
+// compute dS^T.  Each half of the warps writes its bf16 P^T and dS^T into the 64 columns of
+// S^T(g)'s region it has itself read (P^T of q columns [64 h, 64 h + 64) in columns
+// [64 h, 64 h + 32), dS^T in [64 h + 32, 64 h + 64)), so no half waits for the other.  With dS^T
+// written (DSFULL) the MMA thread issues dK += dS^T Q (A from TMEM, K = 128 q), then dP^T(g + 1)
+// into the same region, which the tensor core writes only after the two accumulations have
+// read it (tcgen05.mma instructions of one thread execute in issue order).  Per item: 32 MMA
 // instructions, all N = 128.
 // Each half stages its bf16 dS^T (128 kv rows x 64 q columns) in a shared box of its own, from
 // which a lane of the store warp writes it to the step's scratch tile with a TMA store.
@@ -466,14 +469,15 @@ __global__ void __launch_bounds__(kGThreads, 1) k_bwd_dq(const __grid_constant__
 // unit's last MMAs are done; the epilogue hands it back to the producer) and adds them to
 // dv_acc / dk_acc with TMA reduce-adds.
 enum {
-  K_KVFULL, K_KVEMPTY, K_QFULL0, K_QFULL1, K_QEMPTY0, K_QEMPTY1, K_SDP, K_YFREE, K_PFULL,
+  K_KVFULL, K_KVEMPTY, K_QFULL0, K_QFULL1, K_QEMPTY0, K_QEMPTY1, K_S, K_DP, K_YFREE, K_PFULL,
+  K_DSFULL,
   K_ACCFULL, K_ACCFREE, K_STG0, K_STG1, K_STGR0, K_STGR1, K_TRK00, K_TRK01, K_TRK10, K_TRK11,
   K_DSSTG0, K_DSSTG1, K_DSFREE0, K_DSFREE1, K_UFULL0, K_UEMPTY0 = K_UFULL0 + kQueue,
   K_DRAIN = K_UEMPTY0 + kQueue, K_NUM
 };
 
 __host__ __device__ constexpr int dkdv_arrivals(int b) {
-  return (b == K_ACCFREE || b == K_YFREE || b == K_PFULL ||
+  return (b == K_ACCFREE || b == K_YFREE || b == K_PFULL || b == K_DSFULL ||
           (b >= K_UEMPTY0 && b < K_UEMPTY0 + kQueue))
              ? 256
              : ((b == K_STG0 || b == K_STG1 || b == K_DSSTG0 || b == K_DSSTG1 ||
@@ -618,36 +622,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
       constexpr uint32_t kIdAcc = idesc_bf16(128, D, false, true);
-      const uint32_t aK = smem_u32(sK), aV = smem_u32(sV);
+      // K-major descriptors of K, V and stage 0's Q (its dO is kTile further on), and stage 0's
+      // Q read MN-major
+      const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dQ = sdesc_sw128(smem_u32(sQ0), 16, 1024);
+      const uint64_t dQt = sdesc_sw128(smem_u32(sQ0), 16384, 1024);
       // S^T(gg) = K Q^T into R[gg & 1]; dP^T(gg) = V dO^T into R[(gg + 1) & 1]
-      auto issue_scores = [&](int gg, bool dp) {
-        const uint32_t aQ = smem_u32(sQ0 + (gg & 1) * 2 * kTile) + (dp ? kTile : 0);
-        const uint32_t aA = dp ? aV : aK;
-        const uint32_t d = tR0 + (uint32_t)(((gg + (dp ? 1 : 0)) & 1) * 128);
+      auto issue_scores = [&](int gg, auto dp) {
+        constexpr bool kDp = decltype(dp)::value;
+        constexpr uint32_t kDo = kDp ? kTile : 0;
+        const uint64_t b = sdesc_at(dQ, (gg & 1) * 2 * kTile);
+        const uint32_t d = tR0 + (uint32_t)(((gg + (kDp ? 1 : 0)) & 1) * 128);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-          mma_ss(d, sdesc_sw128(aA + off, 16, 1024), sdesc_sw128(aQ + off, 16, 1024), kIdS, k > 0);
+          mma_ss(d, sdesc_at(dK, kDo + off), sdesc_at(b, kDo + off), kIdS, k > 0);
         }
       };
-      // dV += P^T dO, dK += dS^T Q over the 128 q columns, 16 per MMA: the P^T of q columns
+      // dV += P^T dO (or dK += dS^T Q) over the 128 q columns, 16 per MMA: the P^T of q columns
       // [16 kk, 16 kk + 16) sits in columns 64 (kk / 4) + 8 (kk % 4) of R[gg & 1], the dS^T 32
       // columns further
-      auto issue_acc = [&](int gg, bool first) {
-        const uint32_t aQ = smem_u32(sQ0 + (gg & 1) * 2 * kTile), aDO = aQ + kTile;
-        const uint32_t r = tR0 + (uint32_t)((gg & 1) * 128);
+      auto issue_acc = [&](int gg, auto dk, bool first) {
+        constexpr bool kDk = decltype(dk)::value;
+        const uint64_t b = sdesc_at(dQt, (gg & 1) * 2 * kTile + (kDk ? 0 : kTile));
+        const uint32_t r = tR0 + (uint32_t)((gg & 1) * 128) + (kDk ? 32 : 0);
+        const uint32_t d = kDk ? tdK : tdV;
+        mma_ts(d, r, b, kIdAcc, first ? 0u : 1u);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tdV, r + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_sw128(aDO + kk * 2048, 16384, 1024),
-                 kIdAcc, (first && kk == 0) ? 0u : 1u);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tdK, r + (kk >> 2) * 64 + 32 + (kk & 3) * 8,
-                 sdesc_sw128(aQ + kk * 2048, 16384, 1024), kIdAcc, (first && kk == 0) ? 0u : 1u);
+        for (int kk = 1; kk < 8; ++kk)
+          mma_ts(d, r + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_at(b, kk * 2048), kIdAcc, 1u);
       };
+      constexpr std::false_type kS{}, kdV{};
+      constexpr std::true_type kdP{}, kdK{};
       int uc = 0, j = 0, g = 0, items = 0;
       bool ok = mbar_wait(&bar[K_UFULL0], 0, w) && queue.head[0] >= 0;
       if (ok) {
@@ -656,9 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
       }
       if (ok) {
         tc_fence_after();
-        issue_scores(0, false);
-        issue_scores(0, true);
-        mma_commit(&bar[K_SDP]);
+        issue_scores(0, kS);
+        mma_commit(&bar[K_S]);
+        issue_scores(0, kdP);
+        mma_commit(&bar[K_DP]);
         if (items == 1) mma_commit(&bar[K_KVEMPTY]);  // the unit's last read of K and V
       }
       while (ok) {
@@ -675,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
             itn = queue.T[slot] * p.group;
           }
         }
-        // S^T(g + 1) into dP^T(g)'s region once every elementwise thread holds its scores;
+        // S^T(g + 1) into dP^T(g)'s region once every elementwise thread holds its dP^T;
         // at a unit's end it waits until item g's accumulations are issued (below), so that
         // the load of the next unit's K and V does not hold back the unit's last dV / dK
         auto next_scores = [&]() -> bool {
@@ -683,16 +693,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
           if (newu && !mbar_wait(&bar[K_KVFULL], (uc + 1) & 1, w)) return false;
           if (!mbar_wait(&bar[K_QFULL0 + ((g + 1) & 1)], ((g + 1) >> 1) & 1, w)) return false;
           tc_fence_after();
-          issue_scores(g + 1, false);
+          issue_scores(g + 1, kS);
+          mma_commit(&bar[K_S]);
           return true;
         };
-        if (nxt && !newu && !next_scores()) break;
-        // dV / dK of item g once its P^T / dS^T are in TMEM; a unit's first accumulation
-        // overwrites dV / dK, so the previous unit's must have been read out
+        // dV of item g once its P^T is in TMEM, which is before its dP^T is even read; a unit's
+        // first accumulation overwrites dV, so the previous unit's must have been read out
         if (!mbar_wait(&bar[K_PFULL], g & 1, w)) break;
         if (j == 0 && uc >= 1 && !mbar_wait(&bar[K_ACCFREE], (uc - 1) & 1, w)) break;
         tc_fence_after();
-        issue_acc(g, j == 0);
+        issue_acc(g, kdV, j == 0);
+        if (nxt && !newu && !next_scores()) break;
+        // dK of item g once its dS^T is in TMEM
+        if (!mbar_wait(&bar[K_DSFULL], g & 1, w)) break;
+        tc_fence_after();
+        issue_acc(g, kdK, j == 0);
         // the unit's last Q/dO stage is handed back by the epilogue, which stages in it
         if (j == items - 1)
           mma_commit(&bar[K_ACCFULL]);
@@ -701,8 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         if (!nxt) break;
         if (newu && !next_scores()) break;
         // dP^T(g + 1) into S^T(g)'s region, after the accumulations that read it
-        issue_scores(g + 1, true);
-        mma_commit(&bar[K_SDP]);
+        issue_scores(g + 1, kdP);
+        mma_commit(&bar[K_DP]);
         if ((newu && itn == 1) || (!newu && j + 2 == items)) mma_commit(&bar[K_KVEMPTY]);
         ++g;
         if (newu) {
@@ -846,87 +861,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         // mask
         const bool masked = partial && __any_sync(0xffffffffu, (lm[0] & lm[1]) != ~0u);
         if (!wait_all(&bar[K_TRK00 + half * 2 + b], (g >> 1) & 1, w)) { ok = false; break; }
-        if (!wait_all(&bar[K_SDP], g & 1, w)) { ok = false; break; }
+        if (!wait_all(&bar[K_S], g & 1, w)) { ok = false; break; }
         // the scores of the unit's first item are issued: every role has read the queue entry
         if (it == 0) mbar_arrive(&bar[K_UEMPTY0 + slot]);
         tc_fence_after();
         const uint32_t rS = tR0 + (uint32_t)((g & 1) * 128);        // S^T(g), then P^T / dS^T
         const uint32_t rP = tR0 + (uint32_t)(((g + 1) & 1) * 128);  // dP^T(g)
-        uint32_t vs[2][32], vp[2][32];
+        // ---- P^T, from S^T alone: while the tensor core still has item g - 1's dK and this
+        // item's dP^T to do.  vs takes the factor of dS^T: P^T, times 1 - tanh^2 with a cap.
+        uint32_t vs[2][32];
         tmem_ld32(rS + lb + half * 64, vs[0]);
         tmem_ld32(rS + lb + half * 64 + 32, vs[1]);
-        tmem_ld32(rP + lb + half * 64, vp[0]);
-        tmem_ld32(rP + lb + half * 64 + 32, vp[1]);
         tmem_ld_wait();
-        // this thread holds its scores: once every thread has, dP^T(g)'s region may take
-        // S^T(g + 1); the columns of S^T(g)'s region this half read take its P^T / dS^T
-        tc_fence_before();
-        mbar_arrive(&bar[K_YFREE]);
-        // the half's dS^T box takes this item's tile once its previous store has read it (long
-        // done, normally): each 32-column chunk goes to the box as soon as it is packed
-        if (g >= 1 && !wait_all(&bar[K_DSFREE0 + half], (uint32_t)((g - 1) & 1), w)) { ok = false; break; }
-        fence_proxy_async_smem();
-        uint8_t* box_row = sDS + half * 16384 + row * 128;
-        // P^T = exp2(s * scale * log2 e - lse2[q]), dS^T = P^T (dP^T - delta[q]); the per-query
-        // LSE and delta are read four at a time.  Two copies of the loop, chosen per warp: with
-        // the mask's select, and without it (full tiles, and partial ones whose rows in this
-        // warp keep every column)
-        auto elementwise = [&](auto with_mask) {
-          constexpr bool kMasked = decltype(with_mask)::value;
+        // Copies of the loop, chosen per warp: with the mask's select and without it (full tiles,
+        // and partial ones whose rows in this warp keep every column); with a cap, the two ways
+        // to tanh (score.cuh), the second one with the select only (a warp without masked
+        // columns has all of its bits set).  The per-query LSE is read four at a time.
+        [[maybe_unused]] const int32_t* qpos = p.tracks + 3 * n + qrow - hr;
+        [[maybe_unused]] float neg_slope = 0.f, far0 = 0.f;
+        if constexpr ((MOD & kScoreBias) != 0) {
+          neg_slope = -p.score.slopes[h] * kLog2e;
+          far0 = (float)(qpos[0] - pk);  // where positions are consecutive, query t is |far0 + t| away
+        }
+        auto weights = [&](auto with_mask, auto small) {
+          constexpr bool kMasked = decltype(with_mask)::value, kSmall = decltype(small)::value;
+          [[maybe_unused]] F2 d = f2(far0, far0 + 1.f);
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
-            uint32_t pk16[16], dk16[16];
+            uint32_t pk16[16];
 #pragma unroll
             for (int t = 0; t < 32; t += 4) {
               const int q0 = cc * 32 + t;
               const float4 l4 = *reinterpret_cast<const float4*>(lse2s + q0);
-              const float4 d4 = *reinterpret_cast<const float4*>(dls + q0);
-              const float lq[4] = {l4.x, l4.y, l4.z, l4.w}, dq4[4] = {d4.x, d4.y, d4.z, d4.w};
-              float pv[4], dv4[4];
+              const float lq[4] = {l4.x, l4.y, l4.z, l4.w};
+              float pv[4], wv[4];
+              if constexpr (MOD == 0) {
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const float ex = fast_exp2(fmaf(__uint_as_float(vs[cc][t + u]), sl2, -lq[u]));
-                pv[u] = (kMasked && !((lm[cc] >> (t + u)) & 1u)) ? 0.f : ex;
-                dv4[u] = pv[u] * (__uint_as_float(vp[cc][t + u]) - dq4[u]);
-              }
-              pk16[t >> 1] = pack_bf16(pv[0], pv[1]);
-              pk16[(t >> 1) + 1] = pack_bf16(pv[2], pv[3]);
-              dk16[t >> 1] = pack_bf16(dv4[0], dv4[1]);
-              dk16[(t >> 1) + 1] = pack_bf16(dv4[2], dv4[3]);
-            }
-            // q columns [32 cc, 32 cc + 32) of this half: 16-byte chunks 4 cc .. 4 cc + 3 of the
-            // row, 128-byte swizzled as the TMA store reads them
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              *reinterpret_cast<uint4*>(box_row + (((4 * cc + c) ^ (row & 7)) << 4)) =
-                  make_uint4(dk16[4 * c], dk16[4 * c + 1], dk16[4 * c + 2], dk16[4 * c + 3]);
-            // q column pair c of this half -> P^T column 64 half + c, dS^T column 64 half + 32 + c
-            tmem_st16(rS + lb + half * 64 + cc * 16, pk16);
-            tmem_st16(rS + lb + half * 64 + 32 + cc * 16, dk16);
-          }
-        };
-        if constexpr (MOD != 0) {
-          // P^T = exp2(s - lse2[q]) of the capped and biased score s, dS^T = P^T (dP^T - delta[q])
-          // (1 - tanh^2): the gradient of the product.  In pairs; kSmall is the choice of the way
-          // to tanh (score.cuh).  The second way has one copy, with the mask's select (a warp
-          // without masked columns has all of its bits set).
-          [[maybe_unused]] const int32_t* qpos = p.tracks + 3 * n + qrow - hr;
-          [[maybe_unused]] float neg_slope = 0.f, far0 = 0.f;
-          if constexpr ((MOD & kScoreBias) != 0) {
-            neg_slope = -p.score.slopes[h] * kLog2e;
-            far0 = (float)(qpos[0] - pk);
-          }
-          auto scored = [&](auto with_mask, auto small) {
-            constexpr bool kMasked = decltype(with_mask)::value, kSmall = decltype(small)::value;
-            [[maybe_unused]] F2 d = f2(far0, far0 + 1.f);  // query t is at |far0 + t|
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-              uint32_t pk16[16], dk16[16];
-#pragma unroll
-              for (int t = 0; t < 32; t += 4) {
-                const int q0 = cc * 32 + t;
-                const float4 l4 = *reinterpret_cast<const float4*>(lse2s + q0);
-                const float4 d4 = *reinterpret_cast<const float4*>(dls + q0);
+                for (int u = 0; u < 4; ++u) {
+                  const float ex = fast_exp2(fmaf(__uint_as_float(vs[cc][t + u]), sl2, -lq[u]));
+                  wv[u] = pv[u] = (kMasked && !((lm[cc] >> (t + u)) & 1u)) ? 0.f : ex;
+                }
+              } else {
                 [[maybe_unused]] float far[4];
                 if constexpr ((MOD & kScoreBias) != 0) {
                   if (p.score.consecutive) {
@@ -946,15 +921,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
                 for (int u = 0; u < 4; u += 2) {
                   const float x0 = __uint_as_float(vs[cc][t + u]);
                   const float x1 = __uint_as_float(vs[cc][t + u + 1]);
-                  const F2 neg_lse = u == 0 ? f2(-l4.x, -l4.y) : f2(-l4.z, -l4.w);
-                  const F2 neg_delta = u == 0 ? f2(-d4.x, -d4.y) : f2(-d4.z, -d4.w);
-                  F2 s, slope = f2(1.f);  // s - lse2, and 1 - tanh^2
+                  const F2 neg_lse = f2(-lq[u], -lq[u + 1]);
+                  F2 s, slope;  // s - lse2, and 1 - tanh^2
                   if constexpr ((MOD & kScoreCap) == 0) {
                     s = fma2(f2(x0, x1), f2(sl2), neg_lse);
                   } else if constexpr (kSmall) {
                     const F2 c = cap_poly(f2(x0, x1), p.score);
                     const F2 th = mul2(c, f2(p.score.inv_cap2));
-                    slope = fma2(mul2(th, f2(-1.f)), th, slope);
+                    slope = fma2(mul2(th, f2(-1.f)), th, f2(1.f));
                     s = add2(c, neg_lse);
                   } else {
                     const F2 r = f2(cap_rcp(x0, p.score), cap_rcp(x1, p.score));
@@ -963,55 +937,88 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
                   }
                   if constexpr ((MOD & kScoreBias) != 0)
                     s = fma2(f2(neg_slope), f2(fabsf(far[u]), fabsf(far[u + 1])), s);
-                  float p0, p1, g0, g1;
-                  split(s, &p0, &p1);
-                  p0 = fast_exp2(p0);
-                  p1 = fast_exp2(p1);
-                  if (kMasked) {
-                    p0 = ((lm[cc] >> (t + u)) & 1u) ? p0 : 0.f;
-                    p1 = ((lm[cc] >> (t + u + 1)) & 1u) ? p1 : 0.f;
+                  split(s, &pv[u], &pv[u + 1]);
+#pragma unroll
+                  for (int y = u; y < u + 2; ++y) {
+                    const float ex = fast_exp2(pv[y]);
+                    pv[y] = (kMasked && !((lm[cc] >> (t + y)) & 1u)) ? 0.f : ex;
                   }
-                  F2 g = mul2(f2(p0, p1), add2(f2(__uint_as_float(vp[cc][t + u]),
-                                                  __uint_as_float(vp[cc][t + u + 1])),
-                                               neg_delta));
-                  if constexpr ((MOD & kScoreCap) != 0) g = mul2(g, slope);
-                  split(g, &g0, &g1);
-                  pk16[(t + u) >> 1] = pack_bf16(p0, p1);
-                  dk16[(t + u) >> 1] = pack_bf16(g0, g1);
+                  if constexpr ((MOD & kScoreCap) != 0) {
+                    split(mul2(f2(pv[u], pv[u + 1]), slope), &wv[u], &wv[u + 1]);
+                  } else {
+                    wv[u] = pv[u];
+                    wv[u + 1] = pv[u + 1];
+                  }
                 }
               }
-              // the box and TMEM columns of the plain loop above
+              pk16[t >> 1] = pack_bf16(pv[0], pv[1]);
+              pk16[(t >> 1) + 1] = pack_bf16(pv[2], pv[3]);
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                *reinterpret_cast<uint4*>(box_row + (((4 * cc + c) ^ (row & 7)) << 4)) =
-                    make_uint4(dk16[4 * c], dk16[4 * c + 1], dk16[4 * c + 2], dk16[4 * c + 3]);
-              tmem_st16(rS + lb + half * 64 + cc * 16, pk16);
-              tmem_st16(rS + lb + half * 64 + 32 + cc * 16, dk16);
+              for (int u = 0; u < 4; ++u) vs[cc][t + u] = __float_as_uint(wv[u]);
             }
-          };
-          bool small = true;
-          if constexpr ((MOD & kScoreCap) != 0) {
-            float hi = 0.f;
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-              for (int t = 0; t < 32; ++t) hi = fmaxf(hi, fabsf(__uint_as_float(vs[cc][t])));
-            small = __all_sync(0xffffffffu, hi <= p.score.lim);
+            // q column pair c of this half -> P^T column 64 half + c
+            tmem_st16(rS + lb + half * 64 + cc * 16, pk16);
           }
-          if ((MOD & kScoreCap) != 0 && !small)
-            scored(std::true_type{}, std::false_type{});
-          else if (masked)
-            scored(std::true_type{}, std::true_type{});
-          else
-            scored(std::false_type{}, std::true_type{});
-        } else if (masked) {
-          elementwise(std::true_type{});
-        } else {
-          elementwise(std::false_type{});
+        };
+        bool small = true;
+        if constexpr ((MOD & kScoreCap) != 0) {
+          float hi[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int t = 0; t < 64; ++t)
+            hi[t & 3] = fmaxf(hi[t & 3], fabsf(__uint_as_float(vs[t >> 5][t & 31])));
+          small = __all_sync(0xffffffffu,
+                             fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])) <= p.score.lim);
         }
+        if ((MOD & kScoreCap) != 0 && !small)
+          weights(std::true_type{}, std::false_type{});
+        else if (masked)
+          weights(std::true_type{}, std::true_type{});
+        else
+          weights(std::false_type{}, std::true_type{});
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bar[K_PFULL]);
+        // ---- dS^T = factor (dP^T - delta[q])
+        if (!wait_all(&bar[K_DP], g & 1, w)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t vp[2][32];
+        tmem_ld32(rP + lb + half * 64, vp[0]);
+        tmem_ld32(rP + lb + half * 64 + 32, vp[1]);
+        tmem_ld_wait();
+        // this thread holds its dP^T: once every thread has, the region may take S^T(g + 1)
+        tc_fence_before();
+        mbar_arrive(&bar[K_YFREE]);
+        // the half's dS^T box takes this item's tile once its previous store has read it (long
+        // done, normally): each 32-column chunk goes to the box as soon as it is packed
+        if (g >= 1 && !wait_all(&bar[K_DSFREE0 + half], (uint32_t)((g - 1) & 1), w)) { ok = false; break; }
+        fence_proxy_async_smem();
+        uint8_t* box_row = sDS + half * 16384 + row * 128;
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          uint32_t dk16[16];
+#pragma unroll
+          for (int t = 0; t < 32; t += 4) {
+            const float4 d4 = *reinterpret_cast<const float4*>(dls + cc * 32 + t);
+            const float dq4[4] = {d4.x, d4.y, d4.z, d4.w};
+            float dv4[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              dv4[u] = __uint_as_float(vs[cc][t + u]) * (__uint_as_float(vp[cc][t + u]) - dq4[u]);
+            dk16[t >> 1] = pack_bf16(dv4[0], dv4[1]);
+            dk16[(t >> 1) + 1] = pack_bf16(dv4[2], dv4[3]);
+          }
+          // q columns [32 cc, 32 cc + 32) of this half: 16-byte chunks 4 cc .. 4 cc + 3 of the
+          // row, 128-byte swizzled as the TMA store reads them
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(box_row + (((4 * cc + c) ^ (row & 7)) << 4)) =
+                make_uint4(dk16[4 * c], dk16[4 * c + 1], dk16[4 * c + 2], dk16[4 * c + 3]);
+          // q column pair c of this half -> dS^T column 64 half + 32 + c
+          tmem_st16(rS + lb + half * 64 + 32 + cc * 16, dk16);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bar[K_DSFULL]);
         // ---- this half's bf16 dS^T (its 64 q columns, staged in its box above) to the tile's
         // scratch slot for the dQ GEMM
         if (row == 0) ds_mail[half] = slot_ds;

@@ -356,10 +356,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
       constexpr uint32_t kIdO = idesc_bf16(128, D, false, true);
-      const uint32_t aQ0 = smem_u32(sQ), aK0 = smem_u32(sK), aV0 = smem_u32(sV);
+      const uint64_t dQ0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dK0 = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t dV0 = sdesc_sw128(smem_u32(sV), 16384, 1024);
       // Event loop over two cursors into the work queue: issue whichever of the next PV
       // (priority: it feeds the softmax and the epilogue) and the next S (at most two tiles
       // ahead of the next PV) has its inputs ready, polling with non-blocking tests.
@@ -398,12 +400,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
               (cp.j != 0 || cp.uc < 2 || mbar_test(&bar[B_OFREE0 + ob], ((cp.uc >> 1) - 1) & 1));
           if (ready) {
             tc_fence_after();
-            const uint32_t aV = aV0 + s * kTile;
+            const uint64_t dV = sdesc_at(dV0, s * kTile);
             // P of half h sits in columns [64 h, 64 h + 32) of the S buffer
+            mma_ts(tO + ob * 128, tS + b * 128, dV, kIdO, cp.j > 0 ? 1u : 0u);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 1; k < 8; ++k)
               mma_ts(tO + ob * 128, tS + b * 128 + (k >> 2) * 64 + (k & 3) * 8,
-                     sdesc_sw128(aV + k * 2048, 16384, 1024), kIdO, (cp.j > 0 || k > 0) ? 1u : 0u);
+                     sdesc_at(dV, k * 2048), kIdO, 1u);
             mma_commit(&bar[B_PVDONE]);
             mma_commit(&bar[B_VEMPTY0 + s]);
             if (cp.j == cp.T - 1) mma_commit(&bar[B_OFULL0 + ob]);
@@ -421,12 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
                              mbar_test(&bar[B_KFULL0 + s], ring_parity(g));
           if (ready) {
             tc_fence_after();
-            const uint32_t aQ = aQ0 + qb * kTile, aK = aK0 + s * kTile;
+            const uint64_t dQ = sdesc_at(dQ0, qb * kTile), dK = sdesc_at(dK0, s * kTile);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-              mma_ss(tS + b * 128, sdesc_sw128(aQ + off, 16, 1024),
-                     sdesc_sw128(aK + off, 16, 1024), kIdS, k > 0);
+              mma_ss(tS + b * 128, sdesc_at(dQ, off), sdesc_at(dK, off), kIdS, k > 0);
             }
             mma_commit(&bar[B_SFULL0 + b]);
             mma_commit(&bar[B_KEMPTY0 + s]);

@@ -343,6 +343,23 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
   return d;
 }
 
+// The descriptor of the operand `bytes` (a multiple of 16) further on.  A descriptor is built once
+// per tile and moved by constants: built anew for every MMA it costs the issuing thread more
+// than the 64 cycles that a 128 x 128 x 16 MMA takes (measured: 125-135 cycles per MMA).
+__device__ __forceinline__ uint64_t sdesc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
+// one thread of a converged warp; code under it is known to run in a single thread, which lets
+// the MMAs' descriptors go through uniform registers directly
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Byte offset of element (row, col) of a bf16 tile stored as 128-byte-swizzled atoms of
 // 64 columns (the layout a TMA load with 128-byte swizzle produces); `rows` is the
 // number of rows of the tile (atom-column stride = rows * 128 bytes).
