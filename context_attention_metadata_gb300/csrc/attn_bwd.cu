@@ -789,45 +789,71 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
       // lo_k <= i_q < hi_k instead of the four-track predicate
       const bool ivt = p.iv_block[nk] != 0;
       const int klo = p.kiv[tk], khi = p.kiv[n + tk];
-      for (int it = 0; it < items; ++it, ++g) {
-        const int h = kh * p.group + it / L;
-        const int64_t e = list_entry(c0, c1, La, it % L);
-        const int64_t qrow = (int64_t)p.colT_row[e] * 128 + half * 64 + hr;
-        const bool partial = p.colT_tag[e] == MARBLE_TILE_PARTIAL;
-        // the tile's dS^T scratch slot (row 0 of the half), looked up now so that the loads
-        // are done by the time the box is full: its row-list entry (whole rows), or the step's
-        // tiles in row-list order; q heads innermost
-        long long slot_ds = 0;
+      // What an item needs from global memory is loaded while the item before it is worked on: its
+      // query block and tag at the top, then, from the query block, the rows' LSE and delta and
+      // (row 0 of the half) the pieces of the tile's dS^T scratch slot.  Only a unit's first item
+      // waits for these loads (with every item doing so they took half of an item's time).
+      struct Item {
+        int nq, tag, i0, j, off;       // query block, tag, index of its first query, slot pieces
+        float lse, delta;
+        int64_t sp, sp0;
+      };
+      const int kvs = (int)(nk / p.bps), opt = p.kv_shard >= 0 ? p.kv_shard : p.P;
+      auto load_entry = [&](Item& m, int x) {
+        const int64_t e = list_entry(c0, c1, La, x);
+        m.nq = p.colT_row[e];
+        m.tag = p.colT_tag[e];
+        if (row == 0) m.j = p.colT_j[e];
+      };
+      auto load_rows = [&](Item& m, int h) {
+        if (row < 64) {
+          const int64_t at = (int64_t)h * n + (int64_t)m.nq * 128 + half * 64 + hr;
+          m.lse = p.lse[at];
+          m.delta = p.delta[at];
+        }
+        m.i0 = p.qidx[(int64_t)m.nq * 128];
         if (row == 0) {
-          const int64_t nq = p.colT_row[e];
-          if (p.whole) {
-            slot_ds = p.ds_base[nq / p.bps] +
-                      (p.step_ptr[nq * p.P + nk / p.bps] + p.colT_j[e]) * p.hq + h;
-          } else {
-            const int opt = p.kv_shard >= 0 ? p.kv_shard : p.P;
-            int64_t jj = p.colT_j[e];
-            if (opt == p.P) jj += p.step_ptr[nq * p.P + nk / p.bps] - p.step_ptr[nq * p.P];
-            const long long base = p.ring_len > 0 ? p.ds_base[nq / p.bps] : p.ds_slot0;
-            slot_ds = base + ((int64_t)p.step_off[nq * (p.P + 1) + opt] + jj) * p.hq + h;
-          }
+          const int64_t at = (int64_t)m.nq * p.P;
+          m.sp = p.step_ptr[at + kvs];
+          m.sp0 = p.step_ptr[at];
+          m.off = p.step_off[(int64_t)m.nq * (p.P + 1) + opt];
         }
-        // stage this half's per-query LSE (base 2) and delta (threads of rows [0, 64))
+      };
+      // the half's per-query LSE (base 2) and delta of item gg
+      auto stage_rows = [&](const Item& m, int gg) {
+        if (row < 64) {
+          float* st = stg + (half * 2 + (gg & 1)) * 128;
+          const float l2 = m.lse * kLog2e;
+          st[hr] = (l2 == -INFINITY) ? INFINITY : l2;
+          st[64 + hr] = m.delta;
+        }
+        mbar_arrive(&bar[K_TRK00 + half * 2 + (gg & 1)]);
+      };
+      Item cur{}, next{};
+      load_entry(cur, 0);
+      load_rows(cur, kh * p.group);
+      stage_rows(cur, g);
+      int lx = 0, lh = 0;  // the item's place in the list, its head of the group
+      for (int it = 0; it < items; ++it, ++g) {
+        const int h = kh * p.group + lh;
+        const int64_t qrow0 = (int64_t)cur.nq * 128 + half * 64;  // the half's first query
+        const bool partial = cur.tag == MARBLE_TILE_PARTIAL;
+        const bool more = it + 1 < items;
+        if (++lx == L) {
+          lx = 0;
+          ++lh;
+        }
+        if (more) load_entry(next, lx);
         const int b = g & 1;
-        float* lse2s = stg + (half * 2 + b) * 128;
-        float* dls = lse2s + 64;
-        if ((row >> 6) == 0) {
-          const float l2 = p.lse[(int64_t)h * n + qrow] * kLog2e;
-          lse2s[hr] = (l2 == -INFINITY) ? INFINITY : l2;
-          dls[hr] = p.delta[(int64_t)h * n + qrow];
-        }
-        mbar_arrive(&bar[K_TRK00 + half * 2 + b]);
+        const float* lse2s = stg + (half * 2 + b) * 128;
+        const float* dls = lse2s + 64;
         uint32_t lm[2] = {~0u, ~0u};
         if (partial && ivt) {
           // lo_k <= i_q < hi_k, i_q the query's index in the given token order.  The plan moves
           // whole 128-token blocks, so the half's 64 queries have the consecutive indices
           // i0, i0 + 1, ..., and the legal ones are the columns [lo_k - i0, hi_k - i0) cut to
           // [0, 64): one range of bits
-          const int64_t i0 = (int64_t)p.qidx[(int64_t)p.colT_row[e] * 128] + half * 64;
+          const int64_t i0 = (int64_t)cur.i0 + half * 64;
           const int64_t a = min(max((int64_t)klo - i0, (int64_t)0), (int64_t)64);
           const int64_t c = min(max((int64_t)khi - i0, (int64_t)0), (int64_t)64);
           const uint64_t below_c = c >= 64 ? ~0ull : ((1ull << c) - 1ull);
@@ -838,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         } else if (partial) {
           // the half's 64 queries' tracks, read straight from global memory (the same
           // addresses for every lane: broadcast loads), four queries per load
-          const int32_t* qt = p.tracks + (int64_t)p.colT_row[e] * 128 + half * 64;
+          const int32_t* qt = p.tracks + qrow0;
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
             uint32_t bits = 0;
@@ -877,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         // and partial ones whose rows in this warp keep every column); with a cap, the two ways
         // to tanh (score.cuh), the second one with the select only (a warp without masked
         // columns has all of its bits set).  The per-query LSE is read four at a time.
-        [[maybe_unused]] const int32_t* qpos = p.tracks + 3 * n + qrow - hr;
+        [[maybe_unused]] const int32_t* qpos = p.tracks + 3 * n + qrow0;
         [[maybe_unused]] float neg_slope = 0.f, far0 = 0.f;
         if constexpr ((MOD & kScoreBias) != 0) {
           neg_slope = -p.score.slopes[h] * kLog2e;
@@ -978,6 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bar[K_PFULL]);
+        if (more) load_rows(next, kh * p.group + lh);
         // ---- dS^T = factor (dP^T - delta[q])
         if (!wait_all(&bar[K_DP], g & 1, w)) { ok = false; break; }
         tc_fence_after();
@@ -991,7 +1018,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         // the half's dS^T box takes this item's tile once its previous store has read it (long
         // done, normally): each 32-column chunk goes to the box as soon as it is packed
         if (g >= 1 && !wait_all(&bar[K_DSFREE0 + half], (uint32_t)((g - 1) & 1), w)) { ok = false; break; }
-        fence_proxy_async_smem();
         uint8_t* box_row = sDS + half * 16384 + row * 128;
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
@@ -1021,9 +1047,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         mbar_arrive(&bar[K_DSFULL]);
         // ---- this half's bf16 dS^T (its 64 q columns, staged in its box above) to the tile's
         // scratch slot for the dQ GEMM
-        if (row == 0) ds_mail[half] = slot_ds;
+        if (row == 0) {
+          // the tile's scratch slot: its row-list entry (whole rows), or the step's tiles in
+          // row-list order; q heads innermost
+          const long long base = p.whole || p.ring_len > 0
+                                     ? p.ds_base[(unsigned)cur.nq / (unsigned)p.bps]
+                                     : p.ds_slot0;
+          const int64_t at = p.whole ? cur.sp + cur.j
+                                     : cur.off + (opt == p.P ? cur.sp - cur.sp0 : 0) + cur.j;
+          ds_mail[half] = base + at * p.hq + h;
+        }
         fence_proxy_async_smem();
         mbar_arrive(&bar[K_DSSTG0 + half]);
+        // The next item's LSE and delta go to the buffer of the item before this one, which no
+        // thread of the half reads any more: each was past that item when it arrived for this
+        // one's buffer.  The arrival for the next item's is this thread's last act on this item.
+        if (more) {
+          stage_rows(next, g + 1);
+          cur = next;
+        }
       }
       if (!ok) break;
       // ---- the unit's dV and dK (dv_acc += dV, dk_acc += scale * dK): round 0 stages this
