@@ -477,9 +477,10 @@ enum {
 };
 
 __host__ __device__ constexpr int dkdv_arrivals(int b) {
-  return (b == K_ACCFREE || b == K_YFREE || b == K_PFULL || b == K_DSFULL ||
-          (b >= K_UEMPTY0 && b < K_UEMPTY0 + kQueue))
+  return (b == K_ACCFREE || b == K_YFREE || b == K_PFULL || b == K_DSFULL)
              ? 256
+         : (b >= K_UEMPTY0 && b < K_UEMPTY0 + kQueue)
+             ? 258  // the elementwise threads and the two that store dS^T
              : ((b == K_STG0 || b == K_STG1 || b == K_DSSTG0 || b == K_DSSTG1 ||
                  (b >= K_TRK00 && b <= K_TRK11))
                     ? 128
@@ -494,7 +495,6 @@ struct DkdvShared {
   uint32_t tmem_base;
   int abort_flag;
   int epi_count;
-  long long ds_mail[2];  // per half: scratch slot of the staged dS^T (-1: no more)
 };
 
 // shared memory of the dK/dV kernel: K, V, two Q/dO stages (6 tiles), one 16 KB dS^T box per
@@ -537,7 +537,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
   uint32_t& tmem_base = sv.tmem_base;
   int& abort_flag = sv.abort_flag;
   int& epi_count = sv.epi_count;
-  long long* ds_mail = sv.ds_mail;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long n = p.n;
@@ -738,14 +737,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
     // hands the box back once the TMA has read it, so that no elementwise warp waits for it
     if (lane < 2) {
       const int half = lane;
-      for (int g = 0;; ++g) {
-        if (!mbar_wait(&bar[K_DSSTG0 + half], (uint32_t)(g & 1), w)) break;
-        const long long slot_ds = ds_mail[half];
-        if (slot_ds < 0) break;
-        tma_store_3d(&p.ds_map, sDS + half * 16384, half * 64, (int)(slot_ds * 128), 0);
-        bulk_commit();
-        bulk_wait_read_all();
-        mbar_arrive(&bar[K_DSFREE0 + half]);
+      const int opt = p.kv_shard >= 0 ? p.kv_shard : p.P;
+      bool ok = true;
+      for (int uc = 0, g = 0; ok; ++uc) {
+        const int slot = uc % kQueue;
+        if (!mbar_wait(&bar[K_UFULL0 + slot], (uc / kQueue) & 1, w)) break;
+        const int kh = queue.head[slot];
+        if (kh < 0) break;
+        const int64_t nk = queue.blk[slot];
+        const int L = queue.T[slot], La = queue.La[slot];
+        const int64_t c0 = queue.e0[slot], c1 = queue.e1[slot];
+        mbar_arrive(&bar[K_UEMPTY0 + slot]);
+        const int kvs = (int)(nk / p.bps);
+        for (int hh = 0; hh < p.group && ok; ++hh) {
+          for (int x = 0; x < L; ++x, ++g) {
+            // the tile's scratch slot, looked up before its dS^T is there: its row-list entry
+            // (whole rows), or the step's tiles in row-list order; q heads innermost
+            const int64_t e = list_entry(c0, c1, La, x);
+            const int nq = p.colT_row[e];
+            const int64_t rp = (int64_t)nq * p.P;
+            int64_t at = p.colT_j[e];
+            if (p.whole)
+              at += p.step_ptr[rp + kvs];
+            else
+              at += p.step_off[(int64_t)nq * (p.P + 1) + opt] +
+                    (opt == p.P ? p.step_ptr[rp + kvs] - p.step_ptr[rp] : 0);
+            const long long base = p.whole || p.ring_len > 0
+                                       ? p.ds_base[(unsigned)nq / (unsigned)p.bps]
+                                       : p.ds_slot0;
+            const int64_t slot_ds = base + at * p.hq + kh * p.group + hh;
+            if (!mbar_wait(&bar[K_DSSTG0 + half], (uint32_t)(g & 1), w)) { ok = false; break; }
+            tma_store_3d(&p.ds_map, sDS + half * 16384, half * 64, (int)(slot_ds * 128), 0);
+            bulk_commit();
+            bulk_wait_read_all();
+            mbar_arrive(&bar[K_DSFREE0 + half]);
+          }
+        }
       }
       // the global writes of every store this lane issued have completed
       bulk_wait_all();
@@ -769,15 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
       const int slot = uc % kQueue;
       if (!wait_all(&bar[K_UFULL0 + slot], (uc / kQueue) & 1, w)) break;
       const int kh = queue.head[slot];
-      if (kh < 0) {
-        // no more work: each half posts the end of its dS^T stores once its last one is read
-        if (row == 0) {
-          if (g >= 1) mbar_wait(&bar[K_DSFREE0 + half], (uint32_t)((g - 1) & 1), w);
-          ds_mail[half] = -1;
-        }
-        mbar_arrive(&bar[K_DSSTG0 + half]);
-        break;
-      }
+      if (kh < 0) break;
       const int64_t nk = queue.blk[slot];
       const int L = queue.T[slot], La = queue.La[slot];
       const int64_t c0 = queue.e0[slot], c1 = queue.e1[slot];
@@ -790,20 +809,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
       const bool ivt = p.iv_block[nk] != 0;
       const int klo = p.kiv[tk], khi = p.kiv[n + tk];
       // What an item needs from global memory is loaded while the item before it is worked on: its
-      // query block and tag at the top, then, from the query block, the rows' LSE and delta and
-      // (row 0 of the half) the pieces of the tile's dS^T scratch slot.  Only a unit's first item
-      // waits for these loads (with every item doing so they took half of an item's time).
+      // query block and tag at the top, then, from the query block, the rows' LSE and delta.  Only
+      // a unit's first item waits for these loads (with every item doing so they took half of an
+      // item's time).
       struct Item {
-        int nq, tag, i0, j, off;       // query block, tag, index of its first query, slot pieces
-        float lse, delta;
-        int64_t sp, sp0;
+        int nq, tag, i0;  // query block, tag, index of its first query
+        float lse, delta, slope;
       };
-      const int kvs = (int)(nk / p.bps), opt = p.kv_shard >= 0 ? p.kv_shard : p.P;
       auto load_entry = [&](Item& m, int x) {
         const int64_t e = list_entry(c0, c1, La, x);
         m.nq = p.colT_row[e];
         m.tag = p.colT_tag[e];
-        if (row == 0) m.j = p.colT_j[e];
       };
       auto load_rows = [&](Item& m, int h) {
         if (row < 64) {
@@ -812,19 +828,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
           m.delta = p.delta[at];
         }
         m.i0 = p.qidx[(int64_t)m.nq * 128];
-        if (row == 0) {
-          const int64_t at = (int64_t)m.nq * p.P;
-          m.sp = p.step_ptr[at + kvs];
-          m.sp0 = p.step_ptr[at];
-          m.off = p.step_off[(int64_t)m.nq * (p.P + 1) + opt];
-        }
+        if constexpr ((MOD & kScoreBias) != 0) m.slope = p.score.slopes[h] * kLog2e;
+      };
+      // Where positions are consecutive and the item's queries all come after (before) the unit's
+      // keys, the bias of query t of the half is linear, -+ slope (i0 + t - pos_k): the part in t
+      // goes with the LSE, the rest is one number per thread (side: +1, -1; 0 otherwise).
+      [[maybe_unused]] const int k0 = pk - row;
+      auto side_of = [&](const Item& m) {
+        return !p.score.consecutive || m.i0 == k0 ? 0.f : m.i0 > k0 ? 1.f : -1.f;
       };
       // the half's per-query LSE (base 2) and delta of item gg
       auto stage_rows = [&](const Item& m, int gg) {
         if (row < 64) {
           float* st = stg + (half * 2 + (gg & 1)) * 128;
-          const float l2 = m.lse * kLog2e;
-          st[hr] = (l2 == -INFINITY) ? INFINITY : l2;
+          float l2 = m.lse * kLog2e;
+          if (l2 == -INFINITY) l2 = INFINITY;
+          if constexpr ((MOD & kScoreBias) != 0) l2 = fmaf(side_of(m) * (float)hr, m.slope, l2);
+          st[hr] = l2;
           st[64 + hr] = m.delta;
         }
         mbar_arrive(&bar[K_TRK00 + half * 2 + (gg & 1)]);
@@ -835,7 +855,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
       stage_rows(cur, g);
       int lx = 0, lh = 0;  // the item's place in the list, its head of the group
       for (int it = 0; it < items; ++it, ++g) {
-        const int h = kh * p.group + lh;
         const int64_t qrow0 = (int64_t)cur.nq * 128 + half * 64;  // the half's first query
         const bool partial = cur.tag == MARBLE_TILE_PARTIAL;
         const bool more = it + 1 < items;
@@ -900,18 +919,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         tmem_ld32(rS + lb + half * 64 + 32, vs[1]);
         tmem_ld_wait();
         // Copies of the loop, chosen per warp: with the mask's select and without it (full tiles,
-        // and partial ones whose rows in this warp keep every column); with a cap, the two ways
-        // to tanh (score.cuh), the second one with the select only (a warp without masked
-        // columns has all of its bits set).  The per-query LSE is read four at a time.
-        [[maybe_unused]] const int32_t* qpos = p.tracks + 3 * n + qrow0;
-        [[maybe_unused]] float neg_slope = 0.f, far0 = 0.f;
+        // and partial ones whose rows in this warp keep every column).  With a cap or a bias a
+        // third one takes every other case, with the select (a warp without masked columns has
+        // all of its bits set): the second way to tanh (score.cuh), and distances that are not
+        // linear in the query (the diagonal block, a position track).  The per-query LSE is read
+        // four at a time.
+        [[maybe_unused]] float side = 1.f, own = 0.f;
         if constexpr ((MOD & kScoreBias) != 0) {
-          neg_slope = -p.score.slopes[h] * kLog2e;
-          far0 = (float)(qpos[0] - pk);  // where positions are consecutive, query t is |far0 + t| away
+          side = side_of(cur);
+          own = -side * cur.slope * (float)(cur.i0 + half * 64 - pk);
         }
-        auto weights = [&](auto with_mask, auto small) {
-          constexpr bool kMasked = decltype(with_mask)::value, kSmall = decltype(small)::value;
-          [[maybe_unused]] F2 d = f2(far0, far0 + 1.f);
+        auto weights = [&](auto with_mask, auto usual) {
+          constexpr bool kMasked = decltype(with_mask)::value, kUsual = decltype(usual)::value;
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
             uint32_t pk16[16];
@@ -921,60 +940,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
               const float4 l4 = *reinterpret_cast<const float4*>(lse2s + q0);
               const float lq[4] = {l4.x, l4.y, l4.z, l4.w};
               float pv[4], wv[4];
-              if constexpr (MOD == 0) {
+              [[maybe_unused]] int4 k4;
+              if constexpr (!kUsual && (MOD & kScoreBias) != 0)
+                k4 = __ldg(reinterpret_cast<const int4*>(p.tracks + 3 * n + qrow0 + q0));
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const float ex = fast_exp2(fmaf(__uint_as_float(vs[cc][t + u]), sl2, -lq[u]));
-                  wv[u] = pv[u] = (kMasked && !((lm[cc] >> (t + u)) & 1u)) ? 0.f : ex;
-                }
-              } else {
-                [[maybe_unused]] float far[4];
-                if constexpr ((MOD & kScoreBias) != 0) {
-                  if (p.score.consecutive) {
-                    split(d, &far[0], &far[1]);
-                    d = add2(d, f2(2.f));
-                    split(d, &far[2], &far[3]);
-                    d = add2(d, f2(2.f));
-                  } else {
-                    const int4 k4 = __ldg(reinterpret_cast<const int4*>(qpos + q0));
-                    far[0] = (float)(k4.x - pk);
-                    far[1] = (float)(k4.y - pk);
-                    far[2] = (float)(k4.z - pk);
-                    far[3] = (float)(k4.w - pk);
-                  }
-                }
-#pragma unroll
-                for (int u = 0; u < 4; u += 2) {
-                  const float x0 = __uint_as_float(vs[cc][t + u]);
-                  const float x1 = __uint_as_float(vs[cc][t + u + 1]);
-                  const F2 neg_lse = f2(-lq[u], -lq[u + 1]);
-                  F2 s, slope;  // s - lse2, and 1 - tanh^2
+              for (int u = 0; u < 4; u += 2) {
+                const float x0 = __uint_as_float(vs[cc][t + u]);
+                const float x1 = __uint_as_float(vs[cc][t + u + 1]);
+                if constexpr (MOD == 0) {
+                  pv[u] = fmaf(x0, sl2, -lq[u]);
+                  pv[u + 1] = fmaf(x1, sl2, -lq[u + 1]);
+                } else if constexpr (kUsual) {
+                  F2 bias = f2(-lq[u], -lq[u + 1]);
+                  if constexpr ((MOD & kScoreBias) != 0) bias = add2(bias, f2(own));
+                  F2 s;
                   if constexpr ((MOD & kScoreCap) == 0) {
-                    s = fma2(f2(x0, x1), f2(sl2), neg_lse);
-                  } else if constexpr (kSmall) {
-                    const F2 c = cap_poly(f2(x0, x1), p.score);
-                    const F2 th = mul2(c, f2(p.score.inv_cap2));
-                    slope = fma2(mul2(th, f2(-1.f)), th, f2(1.f));
-                    s = add2(c, neg_lse);
+                    s = fma2(f2(x0, x1), f2(sl2), bias);
                   } else {
-                    const F2 r = f2(cap_rcp(x0, p.score), cap_rcp(x1, p.score));
-                    slope = mul2(f2(4.f), fma2(mul2(r, f2(-1.f)), r, r));
-                    s = add2(fma2(f2(-2.f * p.score.cap2), r, f2(p.score.cap2)), neg_lse);
+                    const F2 c = cap_poly(f2(x0, x1), p.score);
+                    split(fma2(mul2(c, c), f2(p.score.neg_inv_cap2_sq), f2(1.f)), &wv[u], &wv[u + 1]);
+                    s = add2(c, bias);
                   }
-                  if constexpr ((MOD & kScoreBias) != 0)
-                    s = fma2(f2(neg_slope), f2(fabsf(far[u]), fabsf(far[u + 1])), s);
                   split(s, &pv[u], &pv[u + 1]);
+                } else {
 #pragma unroll
                   for (int y = u; y < u + 2; ++y) {
-                    const float ex = fast_exp2(pv[y]);
-                    pv[y] = (kMasked && !((lm[cc] >> (t + y)) & 1u)) ? 0.f : ex;
+                    const float x = y == u ? x0 : x1;
+                    float bias = -lq[y];
+                    if constexpr ((MOD & kScoreBias) != 0) {
+                      // with a side the LSE holds the part in t already
+                      const int kq = y == 0 ? k4.x : y == 1 ? k4.y : y == 2 ? k4.z : k4.w;
+                      bias += side != 0.f ? own : -cur.slope * fabsf((float)(kq - pk));
+                    }
+                    if constexpr ((MOD & kScoreCap) == 0) {
+                      pv[y] = fmaf(x, sl2, bias);
+                    } else {
+                      const float r = cap_rcp(x, p.score);
+                      wv[y] = 4.f * fmaf(-r, r, r);
+                      pv[y] = fmaf(-2.f * p.score.cap2, r, p.score.cap2) + bias;
+                    }
                   }
-                  if constexpr ((MOD & kScoreCap) != 0) {
-                    split(mul2(f2(pv[u], pv[u + 1]), slope), &wv[u], &wv[u + 1]);
-                  } else {
-                    wv[u] = pv[u];
-                    wv[u + 1] = pv[u + 1];
-                  }
+                }
+#pragma unroll
+                for (int y = u; y < u + 2; ++y) {
+                  const float ex = fast_exp2(pv[y]);
+                  pv[y] = (kMasked && !((lm[cc] >> (t + y)) & 1u)) ? 0.f : ex;
+                }
+                // the factor of dS^T
+                if constexpr ((MOD & kScoreCap) != 0) {
+                  split(mul2(f2(pv[u], pv[u + 1]), f2(wv[u], wv[u + 1])), &wv[u], &wv[u + 1]);
+                } else {
+                  wv[u] = pv[u];
+                  wv[u + 1] = pv[u + 1];
                 }
               }
               pk16[t >> 1] = pack_bf16(pv[0], pv[1]);
@@ -986,16 +1003,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
             tmem_st16(rS + lb + half * 64 + cc * 16, pk16);
           }
         };
-        bool small = true;
+        bool usual = true;
         if constexpr ((MOD & kScoreCap) != 0) {
           float hi[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int t = 0; t < 64; ++t)
             hi[t & 3] = fmaxf(hi[t & 3], fabsf(__uint_as_float(vs[t >> 5][t & 31])));
-          small = __all_sync(0xffffffffu,
+          usual = __all_sync(0xffffffffu,
                              fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])) <= p.score.lim);
         }
-        if ((MOD & kScoreCap) != 0 && !small)
+        if constexpr ((MOD & kScoreBias) != 0) usual = usual && side != 0.f;
+        if (MOD != 0 && !usual)
           weights(std::true_type{}, std::false_type{});
         else if (masked)
           weights(std::true_type{}, std::true_type{});
@@ -1047,16 +1065,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         mbar_arrive(&bar[K_DSFULL]);
         // ---- this half's bf16 dS^T (its 64 q columns, staged in its box above) to the tile's
         // scratch slot for the dQ GEMM
-        if (row == 0) {
-          // the tile's scratch slot: its row-list entry (whole rows), or the step's tiles in
-          // row-list order; q heads innermost
-          const long long base = p.whole || p.ring_len > 0
-                                     ? p.ds_base[(unsigned)cur.nq / (unsigned)p.bps]
-                                     : p.ds_slot0;
-          const int64_t at = p.whole ? cur.sp + cur.j
-                                     : cur.off + (opt == p.P ? cur.sp - cur.sp0 : 0) + cur.j;
-          ds_mail[half] = base + at * p.hq + h;
-        }
         fence_proxy_async_smem();
         mbar_arrive(&bar[K_DSSTG0 + half]);
         // The next item's LSE and delta go to the buffer of the item before this one, which no

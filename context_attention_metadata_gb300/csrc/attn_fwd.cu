@@ -159,68 +159,57 @@ struct Smem {
 };
 static_assert(Smem<128>::bytes() <= 232448, "shared memory budget");
 
-// A row's 64 products of this half, in place, to base-2 scores with the cap and the bias.  far0:
-// the row's distance to the half's first key where positions are consecutive; otherwise pos
-// holds the keys' positions.
+// A row's 64 products of this half, in place, to base-2 scores with the cap and the bias.
+// side: +1 or -1 where the tile's keys all come before (after) its queries and positions are
+// consecutive, so that the bias is linear in the key; 0 otherwise.  far0: the row's distance to
+// the half's first key; pos: the keys' positions.
 template <int MOD>
 __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams& p, float sl2,
-                                          float neg_slope, float far0, int pq,
+                                          float slope, float side, float far0, int pq,
                                           const int32_t* __restrict__ pos) {
-  auto pair = [&](int i) {
-    return f2(__uint_as_float(v[i >> 4][2 * (i & 15)]), __uint_as_float(v[i >> 4][2 * (i & 15) + 1]));
-  };
-  auto put = [&](int i, F2 x) {
-    float a, b;
-    split(x, &a, &b);
-    v[i >> 4][2 * (i & 15)] = __float_as_uint(a);
-    v[i >> 4][2 * (i & 15) + 1] = __float_as_uint(b);
-  };
-  F2 sc = f2(sl2);
+  bool usual = true;
   if constexpr ((MOD & kScoreCap) != 0) {
-    float hi = 0.f;
+    float hi[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-      for (int t = 0; t < 32; ++t) hi = fmaxf(hi, fabsf(__uint_as_float(v[cc][t])));
-    if (__all_sync(0xffffffffu, hi <= p.score.lim)) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) put(i, cap_poly(pair(i), p.score));
-    } else {
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-        for (int t = 0; t < 32; ++t)
-          v[cc][t] = __float_as_uint(fmaf(-2.f * p.score.cap2,
-                                          cap_rcp(__uint_as_float(v[cc][t]), p.score),
-                                          p.score.cap2));
-    }
-    sc = f2(1.f);
+    for (int t = 0; t < 64; ++t)
+      hi[t & 3] = fmaxf(hi[t & 3], fabsf(__uint_as_float(v[t >> 5][t & 31])));
+    usual = __all_sync(0xffffffffu,
+                       fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])) <= p.score.lim);
   }
-  if constexpr ((MOD & kScoreBias) != 0) {
-    const F2 ns = f2(neg_slope);
-    if (p.score.consecutive) {
-      // key t of the half is at distance |far0 - t|
-      F2 d = f2(far0, far0 - 1.f);
-      const F2 two = f2(-2.f);
-      if (__all_sync(0xffffffffu, far0 >= 63.f)) {
-        // every key at or before every row
+  // key t of the half is at side (far0 - t): the bias is own + t * step
+  const float own = -side * slope * far0, step = side * slope;
+  if ((MOD & kScoreBias) == 0 ? usual : usual && side != 0.f) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i, d = add2(d, two)) put(i, fma2(ns, d, mul2(pair(i), sc)));
+    for (int t = 0; t < 64; t += 2) {
+      const F2 x = f2(__uint_as_float(v[t >> 5][t & 31]), __uint_as_float(v[t >> 5][(t & 31) + 1]));
+      F2 s;
+      if constexpr ((MOD & kScoreCap) == 0) {
+        s = fma2(x, f2(sl2), fma2(f2((float)t, (float)(t + 1)), f2(step), f2(own)));
       } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i, d = add2(d, two)) {
-          float a, b;
-          split(d, &a, &b);
-          put(i, fma2(ns, f2(fabsf(a), fabsf(b)), mul2(pair(i), sc)));
-        }
+        s = cap_poly(x, p.score);
+        if constexpr ((MOD & kScoreBias) != 0)
+          s = add2(s, fma2(f2((float)t, (float)(t + 1)), f2(step), f2(own)));
       }
-    } else {
+      float s0, s1;
+      split(s, &s0, &s1);
+      v[t >> 5][t & 31] = __float_as_uint(s0);
+      v[t >> 5][(t & 31) + 1] = __float_as_uint(s1);
+    }
+  } else {
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const int4 k = __ldg(reinterpret_cast<const int4*>(pos + 2 * i));
-        put(i, fma2(ns, f2(fabsf((float)(pq - k.x)), fabsf((float)(pq - k.y))), mul2(pair(i), sc)));
-        put(i + 1, fma2(ns, f2(fabsf((float)(pq - k.z)), fabsf((float)(pq - k.w))),
-                        mul2(pair(i + 1), sc)));
+    for (int t = 0; t < 64; t += 4) {
+      [[maybe_unused]] int4 k4;
+      if constexpr ((MOD & kScoreBias) != 0) k4 = __ldg(reinterpret_cast<const int4*>(pos + t));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float x = __uint_as_float(v[t >> 5][(t & 31) + u]);
+        float bias = 0.f;
+        if constexpr ((MOD & kScoreBias) != 0)
+          bias = -slope * fabsf((float)(pq - (u == 0 ? k4.x : u == 1 ? k4.y : u == 2 ? k4.z : k4.w)));
+        const float s = (MOD & kScoreCap) == 0
+                            ? fmaf(x, sl2, bias)
+                            : fmaf(-2.f * p.score.cap2, cap_rcp(x, p.score), p.score.cap2) + bias;
+        v[t >> 5][(t & 31) + u] = __float_as_uint(s);
       }
     }
   }
@@ -484,16 +473,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
                 pq = p.tracks[3 * n + tq];
       const int iq = p.qidx[tq];  // the interval test's coordinate: the query's index
       const uint32_t ob = tO + (uint32_t)(uc & 1) * 128;
-      [[maybe_unused]] float neg_slope = 0.f;
+      [[maybe_unused]] float slope = 0.f;
       if constexpr ((MOD & kScoreBias) != 0)
-        neg_slope = -p.score.slopes[unit / p.bps] * 1.4426950408889634f;
+        slope = p.score.slopes[unit / p.bps] * 1.4426950408889634f;
       float m_run = -INFINITY, l_h = 0.f;
       for (int j = 0; j < T; ++j, ++g) {
         const uint32_t b = (uint32_t)(g & 1);
-        // distance of this row to the half's first key, its keys being at consecutive positions
-        [[maybe_unused]] float far0 = 0.f;
-        if constexpr ((MOD & kScoreBias) != 0)
-          far0 = (float)(pq - p.tracks[3 * n + (int64_t)p.step_col[e0 + j] * 128 + half * 64]);
+        [[maybe_unused]] float far0 = 0.f, side = 0.f;  // see score_row
+        if constexpr ((MOD & kScoreBias) != 0) {
+          const int k0 = p.tracks[3 * n + (int64_t)p.step_col[e0 + j] * 128];
+          far0 = (float)(pq - k0 - half * 64);
+          if (p.score.consecutive) side = pq - row > k0 ? 1.f : pq - row < k0 ? -1.f : 0.f;
+        }
         const bool partial = p.step_tag[e0 + j] == MARBLE_TILE_PARTIAL;
         uint32_t lm[2] = {~0u, ~0u};  // legal-key bits of this row in this half's 64 columns
         const int64_t kb = partial ? p.step_col[e0 + j] : 0;
@@ -574,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         // (scaling by a positive constant commutes with the maximum, and P takes one FMA below)
         float mx = -INFINITY;
         if constexpr (MOD != 0) {
-          score_row<MOD>(v, p, sl2, neg_slope, far0, pq,
+          score_row<MOD>(v, p, sl2, slope, side, far0, pq,
                          p.tracks + 3 * n + (int64_t)p.step_col[e0 + j] * 128 + half * 64);
           if (masked) {
 #pragma unroll
@@ -583,10 +574,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
               for (int t = 0; t < 32; ++t)
                 if (!((lm[cc] >> t) & 1u)) v[cc][t] = __float_as_uint(-INFINITY);
           }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-            for (int t = 0; t < 32; ++t) mx = fmaxf(mx, __uint_as_float(v[cc][t]));
+          for (int t = 0; t < 64; ++t) m4[t & 3] = fmaxf(m4[t & 3], __uint_as_float(v[t >> 5][t & 31]));
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         } else if (masked) {
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {

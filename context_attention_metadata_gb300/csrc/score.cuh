@@ -8,13 +8,13 @@
 // and for the gradient of a capped score ds/dx = scale * (1 - tanh^2), the factor 1 - tanh^2 here.
 //
 // tanh is taken in one of two ways, decided per warp and tile:
-//   |x scale / c| <= 0.75 for all of the warp's scores: an odd polynomial, tanh y = y (a0 + a1 y^2
-//     + ... + a5 y^10), the minimax fit of tanh(y) / y in y^2 over [0, 0.75^2] (computed by the
-//     exchange algorithm), relative error 2^-25.  Its coefficients are folded with the scale on
-//     the host, so that a score costs seven multiply-adds, done two at a time (f32x2).
+//   |x scale / c| <= 0.45 for all of the warp's scores: an odd polynomial, tanh y = y (a0 + a1 y^2
+//     + a2 y^4 + a3 y^6), the minimax fit of tanh(y) / y in y^2 over [0, 0.45^2] (computed by the
+//     exchange algorithm), relative error 2^-22.  Its coefficients are folded with the scale on
+//     the host, so that a score costs five multiply-adds.
 //   otherwise 1 - 2 / (1 + e^(2 y)): two calls to the special function unit, which also has the
 //     softmax's exp2 to do, and an absolute error of 2^-22 c (the score's own rounding is of
-//     that size, some |score| being above 0.75 c).
+//     that size, some |score| being above 0.45 c).
 #pragma once
 
 #include <math.h>
@@ -30,11 +30,11 @@ namespace marble {
 enum : int { kScoreCap = 1, kScoreBias = 2 };  // bits of a kernel's score variant
 
 struct ScoreParams {
-  float c[6];           // s = x (c[0] + c[1] x^2 + ... + c[5] x^10) for |x| <= lim
+  float c[4];           // s = x (c[0] + c[1] x^2 + c[2] x^4 + c[3] x^6) for |x| <= lim
   float lim;
   float ky;             // e^(2 y) = 2^(ky x)
   float cap2;           // cap * log2 e
-  float inv_cap2;       // 1 / cap2
+  float neg_inv_cap2_sq;  // -1 / cap2^2
   const float* slopes;  // [hq] or null
   int consecutive;      // the positions of a block's tokens are consecutive
 };
@@ -62,24 +62,25 @@ marble_status_t with_variant(int d, int mod, F f) {
 
 // `cap` > 0
 inline void set_cap(ScoreParams* s, float cap, float scale) {
-  static const double kA[6] = {0.9999999710138949,  -0.3333295887947679,   0.1332540601769393,
-                               -0.053344430143664245, 0.019582908187657067, -0.004716257251125382};
+  static const double kA[4] = {0.9999997567401877, -0.3332946719023316, 0.13236369052147212,
+                               -0.0460281937984787};
   const double log2e = 1.4426950408889634, k = (double)scale / cap;
   double f = scale * log2e;
   bool ok = true;
-  for (int i = 0; i < 6; ++i, f *= k * k) {
+  for (int i = 0; i < 4; ++i, f *= k * k) {
     s->c[i] = (float)(kA[i] * f);
     ok = ok && std::isfinite(s->c[i]);
   }
-  // x^10 has to stay finite, and so do the coefficients: caps far below the scale take the
+  // x^6 has to stay finite, and so do the coefficients: caps far below the scale take the
   // second way alone
-  s->lim = ok ? (float)fmin(0.75 / k, 1e3) : -1.f;
+  s->lim = ok ? (float)fmin(0.45 / k, 1e5) : -1.f;
   s->ky = (float)(2.0 * log2e * k);
   s->cap2 = (float)(cap * log2e);
-  s->inv_cap2 = (float)(1.0 / (cap * log2e));
+  s->neg_inv_cap2_sq = (float)(-1.0 / (cap * log2e) / (cap * log2e));
 }
 
-// two fp32 values in a register pair and the packed operations on them
+// two fp32 values in a register pair and the packed operations on them: an instruction for two
+// scores, where issuing instructions is what the elementwise warps run out of
 struct F2 {
   unsigned long long v;
 };
@@ -117,12 +118,8 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // capped scores of a pair, |x| <= lim
 __device__ __forceinline__ F2 cap_poly(F2 x, const ScoreParams& p) {
   const F2 u = mul2(x, x);
-  F2 r = fma2(f2(p.c[5]), u, f2(p.c[4]));
-  r = fma2(r, u, f2(p.c[3]));
-  r = fma2(r, u, f2(p.c[2]));
-  r = fma2(r, u, f2(p.c[1]));
-  r = fma2(r, u, f2(p.c[0]));
-  return mul2(x, r);
+  const F2 r = fma2(fma2(f2(p.c[3]), u, f2(p.c[2])), u, f2(p.c[1]));
+  return mul2(x, fma2(r, u, f2(p.c[0])));
 }
 
 // 1 / (1 + e^(2 y)): the capped score is cap2 (1 - 2 r), its slope's factor 4 r (1 - r)
