@@ -837,15 +837,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
       auto side_of = [&](const Item& m) {
         return !p.score.consecutive || m.i0 == k0 ? 0.f : m.i0 > k0 ? 1.f : -1.f;
       };
-      // the half's per-query LSE (base 2) and delta of item gg
+      // the half's per-query LSE (base 2) and delta of item gg, both negated: they are added
       auto stage_rows = [&](const Item& m, int gg) {
         if (row < 64) {
           float* st = stg + (half * 2 + (gg & 1)) * 128;
           float l2 = m.lse * kLog2e;
           if (l2 == -INFINITY) l2 = INFINITY;
           if constexpr ((MOD & kScoreBias) != 0) l2 = fmaf(side_of(m) * (float)hr, m.slope, l2);
-          st[hr] = l2;
-          st[64 + hr] = m.delta;
+          st[hr] = -l2;
+          st[64 + hr] = -m.delta;
         }
         mbar_arrive(&bar[K_TRK00 + half * 2 + (gg & 1)]);
       };
@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
             for (int t = 0; t < 32; t += 4) {
               const int q0 = cc * 32 + t;
               const float4 l4 = *reinterpret_cast<const float4*>(lse2s + q0);
-              const float lq[4] = {l4.x, l4.y, l4.z, l4.w};
+              const float nl[4] = {l4.x, l4.y, l4.z, l4.w};
               float pv[4], wv[4];
               [[maybe_unused]] int4 k4;
               if constexpr (!kUsual && (MOD & kScoreBias) != 0)
@@ -948,10 +948,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
                 const float x0 = __uint_as_float(vs[cc][t + u]);
                 const float x1 = __uint_as_float(vs[cc][t + u + 1]);
                 if constexpr (MOD == 0) {
-                  pv[u] = fmaf(x0, sl2, -lq[u]);
-                  pv[u + 1] = fmaf(x1, sl2, -lq[u + 1]);
+                  pv[u] = fmaf(x0, sl2, nl[u]);
+                  pv[u + 1] = fmaf(x1, sl2, nl[u + 1]);
                 } else if constexpr (kUsual) {
-                  F2 bias = f2(-lq[u], -lq[u + 1]);
+                  F2 bias = f2(nl[u], nl[u + 1]);
                   if constexpr ((MOD & kScoreBias) != 0) bias = add2(bias, f2(own));
                   F2 s;
                   if constexpr ((MOD & kScoreCap) == 0) {
@@ -966,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
 #pragma unroll
                   for (int y = u; y < u + 2; ++y) {
                     const float x = y == u ? x0 : x1;
-                    float bias = -lq[y];
+                    float bias = nl[y];
                     if constexpr ((MOD & kScoreBias) != 0) {
                       // with a side the LSE holds the part in t already
                       const int kq = y == 0 ? k4.x : y == 1 ? k4.y : y == 2 ? k4.z : k4.w;
@@ -1024,6 +1024,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         mbar_arrive(&bar[K_PFULL]);
         if (more) load_rows(next, kh * p.group + lh);
         // ---- dS^T = factor (dP^T - delta[q])
+        // (the half's dS^T box takes this item's tile once its previous store has read it, which
+        // is long done, normally)
+        if (g >= 1 && !wait_all(&bar[K_DSFREE0 + half], (uint32_t)((g - 1) & 1), w)) { ok = false; break; }
         if (!wait_all(&bar[K_DP], g & 1, w)) { ok = false; break; }
         tc_fence_after();
         uint32_t vp[2][32];
@@ -1033,9 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         // this thread holds its dP^T: once every thread has, the region may take S^T(g + 1)
         tc_fence_before();
         mbar_arrive(&bar[K_YFREE]);
-        // the half's dS^T box takes this item's tile once its previous store has read it (long
-        // done, normally): each 32-column chunk goes to the box as soon as it is packed
-        if (g >= 1 && !wait_all(&bar[K_DSFREE0 + half], (uint32_t)((g - 1) & 1), w)) { ok = false; break; }
+        // each 32-column chunk goes to the box as soon as it is packed
         uint8_t* box_row = sDS + half * 16384 + row * 128;
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
@@ -1043,11 +1044,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
 #pragma unroll
           for (int t = 0; t < 32; t += 4) {
             const float4 d4 = *reinterpret_cast<const float4*>(dls + cc * 32 + t);
-            const float dq4[4] = {d4.x, d4.y, d4.z, d4.w};
             float dv4[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              dv4[u] = __uint_as_float(vs[cc][t + u]) * (__uint_as_float(vp[cc][t + u]) - dq4[u]);
+            for (int u = 0; u < 4; u += 2) {
+              const F2 dp = f2(__uint_as_float(vp[cc][t + u]), __uint_as_float(vp[cc][t + u + 1]));
+              const F2 f = f2(__uint_as_float(vs[cc][t + u]), __uint_as_float(vs[cc][t + u + 1]));
+              split(mul2(f, add2(dp, u == 0 ? f2(d4.x, d4.y) : f2(d4.z, d4.w))), &dv4[u], &dv4[u + 1]);
+            }
             dk16[t >> 1] = pack_bf16(dv4[0], dv4[1]);
             dk16[(t >> 1) + 1] = pack_bf16(dv4[2], dv4[3]);
           }

@@ -179,16 +179,19 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
   // key t of the half is at side (far0 - t): the bias is own + t * step
   const float own = -side * slope * far0, step = side * slope;
   if ((MOD & kScoreBias) == 0 ? usual : usual && side != 0.f) {
+    [[maybe_unused]] F2 at[2] = {f2(0.f, 1.f), f2(2.f, 3.f)};
 #pragma unroll
     for (int t = 0; t < 64; t += 2) {
       const F2 x = f2(__uint_as_float(v[t >> 5][t & 31]), __uint_as_float(v[t >> 5][(t & 31) + 1]));
       F2 s;
-      if constexpr ((MOD & kScoreCap) == 0) {
-        s = fma2(x, f2(sl2), fma2(f2((float)t, (float)(t + 1)), f2(step), f2(own)));
-      } else {
-        s = cap_poly(x, p.score);
-        if constexpr ((MOD & kScoreBias) != 0)
-          s = add2(s, fma2(f2((float)t, (float)(t + 1)), f2(step), f2(own)));
+      if constexpr ((MOD & kScoreCap) == 0)
+        s = fma2(x, f2(sl2), f2(own));
+      else
+        s = (MOD & kScoreBias) != 0 ? add2(cap_poly(x, p.score), f2(own)) : cap_poly(x, p.score);
+      if constexpr ((MOD & kScoreBias) != 0) {
+        // whole numbers counted up, so that the column's part is rounded once
+        s = fma2(at[(t >> 1) & 1], f2(step), s);
+        at[(t >> 1) & 1] = add2(at[(t >> 1) & 1], f2(4.f));
       }
       float s0, s1;
       split(s, &s0, &s1);
@@ -476,14 +479,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
       [[maybe_unused]] float slope = 0.f;
       if constexpr ((MOD & kScoreBias) != 0)
         slope = p.score.slopes[unit / p.bps] * 1.4426950408889634f;
+      // for a bias the tile's kv block and its first key's position are loaded one tile ahead
+      [[maybe_unused]] int kb_n = 0, k0_n = 0;
+      if constexpr ((MOD & kScoreBias) != 0) {
+        kb_n = p.step_col[e0];
+        k0_n = p.tracks[3 * n + (int64_t)kb_n * 128];
+      }
       float m_run = -INFINITY, l_h = 0.f;
       for (int j = 0; j < T; ++j, ++g) {
         const uint32_t b = (uint32_t)(g & 1);
         [[maybe_unused]] float far0 = 0.f, side = 0.f;  // see score_row
+        [[maybe_unused]] const int32_t* kpos = nullptr;
         if constexpr ((MOD & kScoreBias) != 0) {
-          const int k0 = p.tracks[3 * n + (int64_t)p.step_col[e0 + j] * 128];
-          far0 = (float)(pq - k0 - half * 64);
-          if (p.score.consecutive) side = pq - row > k0 ? 1.f : pq - row < k0 ? -1.f : 0.f;
+          far0 = (float)(pq - k0_n - half * 64);
+          if (p.score.consecutive) side = pq - row > k0_n ? 1.f : pq - row < k0_n ? -1.f : 0.f;
+          kpos = p.tracks + 3 * n + (int64_t)kb_n * 128 + half * 64;
+          if (j + 1 < T) kb_n = p.step_col[e0 + j + 1];
         }
         const bool partial = p.step_tag[e0 + j] == MARBLE_TILE_PARTIAL;
         uint32_t lm[2] = {~0u, ~0u};  // legal-key bits of this row in this half's 64 columns
@@ -565,8 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         // (scaling by a positive constant commutes with the maximum, and P takes one FMA below)
         float mx = -INFINITY;
         if constexpr (MOD != 0) {
-          score_row<MOD>(v, p, sl2, slope, side, far0, pq,
-                         p.tracks + 3 * n + (int64_t)p.step_col[e0 + j] * 128 + half * 64);
+          score_row<MOD>(v, p, sl2, slope, side, far0, pq, kpos);
+          if constexpr ((MOD & kScoreBias) != 0) k0_n = p.tracks[3 * n + (int64_t)kb_n * 128];
           if (masked) {
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc)
