@@ -881,25 +881,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
           lm[0] = (uint32_t)bits;
           lm[1] = (uint32_t)(bits >> 32);
         } else if (partial) {
-          // the half's 64 queries' tracks, read straight from global memory (the same
-          // addresses for every lane: broadcast loads), four queries per load
-          const int32_t* qt = p.tracks + qrow0;
+          // every lane holds the ids of one query of a 32-query chunk
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
-            uint32_t bits = 0;
+            const int32_t* qt = p.tracks + qrow0 + cc * 32;
+            const int qs = __ldg(qt + lane), qg = __ldg(qt + n + lane), qz = __ldg(qt + 2 * n + lane);
+            uint32_t causal = 0;
+            if (p.score.consecutive) {
+              // query t is at distance t - a after the key
+              const int64_t a = (int64_t)pk - (cur.i0 + half * 64 + cc * 32);
+              causal = bits32(a, a + p.W);
+            } else {
 #pragma unroll
-            for (int t2 = 0; t2 < 32; t2 += 4) {
-              const int q = cc * 32 + t2;
-              const int4 s4 = __ldg(reinterpret_cast<const int4*>(qt + q));
-              const int4 g4 = __ldg(reinterpret_cast<const int4*>(qt + n + q));
-              const int4 z4 = __ldg(reinterpret_cast<const int4*>(qt + 2 * n + q));
-              const int4 p4 = __ldg(reinterpret_cast<const int4*>(qt + 3 * n + q));
-              bits |= (mask_legal(s4.x, g4.x, z4.x, p4.x, sk, gk, zk, pk, p.W) ? 1u : 0u) << t2;
-              bits |= (mask_legal(s4.y, g4.y, z4.y, p4.y, sk, gk, zk, pk, p.W) ? 1u : 0u) << (t2 + 1);
-              bits |= (mask_legal(s4.z, g4.z, z4.z, p4.z, sk, gk, zk, pk, p.W) ? 1u : 0u) << (t2 + 2);
-              bits |= (mask_legal(s4.w, g4.w, z4.w, p4.w, sk, gk, zk, pk, p.W) ? 1u : 0u) << (t2 + 3);
+              for (int t2 = 0; t2 < 32; t2 += 4) {
+                const int4 q4 = __ldg(reinterpret_cast<const int4*>(qt + 3 * n + t2));
+                causal |= ((unsigned)(q4.x - pk) < (unsigned)p.W ? 1u : 0u) << t2;
+                causal |= ((unsigned)(q4.y - pk) < (unsigned)p.W ? 1u : 0u) << (t2 + 1);
+                causal |= ((unsigned)(q4.z - pk) < (unsigned)p.W ? 1u : 0u) << (t2 + 2);
+                causal |= ((unsigned)(q4.w - pk) < (unsigned)p.W ? 1u : 0u) << (t2 + 3);
+              }
             }
-            lm[cc] = bits;
+            lm[cc] = mask_chunk<false>(sk, gk, zk, qs, qg, qz, causal);
           }
         }
         // a partial tile on which every row of this warp keeps all 64 of its columns needs no
@@ -1200,10 +1202,8 @@ marble_status_t prepare_bwd(const marble_plan_t* pl, const marble_qkv_t* qkv,
   prm.step_off = pl->step_off;
   prm.colT_j = pl->colT_j;
   if (MOD & kScoreCap) set_cap(&prm.score, score->cap, prm.scale);
-  if (MOD & kScoreBias) {
-    prm.score.slopes = score->slopes;
-    prm.score.consecutive = pl->pos_is_index;
-  }
+  if (MOD & kScoreBias) prm.score.slopes = score->slopes;
+  prm.score.consecutive = pl->pos_is_index;
   if (once_per_device((D == 128 ? 3 : 4) + 4 * MOD)) {
     cudaError_t e = cudaFuncSetAttribute(k_bwd_dq<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)DqSmem<D>::bytes());

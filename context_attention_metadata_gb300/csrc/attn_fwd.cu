@@ -24,8 +24,9 @@
 //               columns; the row max is exchanged through shared memory.  Row max, exp2,
 //               row sum, bf16 P back into TMEM, lazy O rescale; at a unit's end they hand
 //               the row's (m, l) to the epilogue and go on with the next unit at once.  On
-//               partial tiles they stage the keys' tracks and evaluate the mask once per
-//               pair; full tiles skip it; empty tiles are never listed, so never loaded.
+//               partial tiles they evaluate the mask (mask_chunk: once per row and run of keys
+//               with the same ids); full tiles skip it; empty tiles are never listed, so never
+//               loaded.
 //   warps 10..13 epilogue, one thread per row: merge the unit's (O, m, l) into the stored
 //               state through a staged TMA store / reduce-add, while the softmax warps and
 //               the tensor core work on the next unit in the other O buffer.
@@ -61,7 +62,6 @@ enum {
   B_OFULL0, B_OFULL1,                // O buffer (unit & 1): the unit's last PV completed
   B_OFREE0, B_OFREE1,                // O buffer read out by the epilogue (128 arrivals)
   B_MX0, B_MX1,                      // per-row max exchanged between the two halves
-  B_TRK0, B_TRK1,                    // key tracks of a partial tile staged
   B_EPIRDY0, B_EPIRDY1,              // (m, l) of the unit handed over (256 arrivals)
   B_HFREE0, B_HFREE1,                // hand-over slot read by the epilogue (128 arrivals)
   B_EVOTE,                           // per unit: epilogue's merge-mode vote (128 arrivals)
@@ -74,8 +74,8 @@ enum {
 };
 
 __host__ __device__ constexpr int arrivals(int b) {
-  return (b == B_PFULL0 || b == B_PFULL1 || b == B_MX0 || b == B_MX1 || b == B_TRK0 ||
-          b == B_TRK1 || b == B_EPIRDY0 || b == B_EPIRDY1)
+  return (b == B_PFULL0 || b == B_PFULL1 || b == B_MX0 || b == B_MX1 ||
+          b == B_EPIRDY0 || b == B_EPIRDY1)
              ? kSoftmax
              : ((b == B_OFREE0 || b == B_OFREE1 || b == B_HFREE0 || b == B_HFREE1 ||
                  b == B_EVOTE || b == B_STG)
@@ -140,8 +140,8 @@ struct Queue {
 __device__ __forceinline__ uint32_t ring_slot(int g) { return (uint32_t)(g & 1); }
 __device__ __forceinline__ uint32_t ring_parity(int g) { return (uint32_t)((g >> 1) & 1); }
 
-// shared memory: Q (2) | K ring (2) | V ring (2) | staging (one 128 x 32 fp32 box) | key
-// tracks [2][4][128] int32 | row-max exchange [2][2][128] f32 | hand-over m [2][128] and
+// shared memory: Q (2) | K ring (2) | V ring (2) | staging (one 128 x 32 fp32 box) | row-max
+// exchange [2][2][128] f32 | hand-over m [2][128] and
 // l [2][2][128] f32
 template <int D>
 struct Smem {
@@ -150,8 +150,7 @@ struct Smem {
   static constexpr int kK = 2 * kTile;
   static constexpr int kV = 4 * kTile;
   static constexpr int kStg = 6 * kTile;
-  static constexpr int kTrk = kStg + 16384;
-  static constexpr int kMx = kTrk + 2 * 512 * 4;
+  static constexpr int kMx = kStg + 16384;
   static constexpr int kHm = kMx + 2 * 2 * 128 * 4;
   static constexpr int kHl = kHm + 2 * 128 * 4;
   static constexpr int kEnd = kHl + 2 * 2 * 128 * 4;
@@ -230,7 +229,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   uint8_t* sK = smem + L::kK;
   uint8_t* sV = smem + L::kV;
   uint8_t* sStg = smem + L::kStg;
-  int32_t* ktr = reinterpret_cast<int32_t*>(smem + L::kTrk);
   float* mxs = reinterpret_cast<float*>(smem + L::kMx);
   float* hm = reinterpret_cast<float*>(smem + L::kHm);
   float* hl = reinterpret_cast<float*>(smem + L::kHl);
@@ -462,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     const int row = quarter * 32 + lane;
     const uint32_t lb = (uint32_t)(quarter * 32) << 16;
     const float sl2 = p.scale_log2;
-    int uc = 0, g = 0, n_partial = 0;
+    int uc = 0, g = 0;
     bool ok = true;
     while (ok) {
       const int slot = uc % kQueue;
@@ -531,34 +529,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
             lm[cc] = bits;
           }
         } else if (partial) {
-          // stage the 128 keys' tracks in one of two buffers (the two halves load two tracks
-          // each); every softmax thread arrives before any reads, so a buffer is rewritten
-          // only after every thread left its previous use
-          const int bb = n_partial & 1;
-          const uint32_t par = (n_partial >> 1) & 1;
-          ++n_partial;
-          int32_t* kt = ktr + bb * 512;
-          const int64_t t = kb * 128 + row;
-          if (half == 0) {
-            kt[row] = p.tracks[t];
-            kt[128 + row] = p.tracks[n + t];
-          } else {
-            kt[256 + row] = p.tracks[2 * n + t];
-            kt[384 + row] = p.tracks[3 * n + t];
-          }
-          mbar_arrive(&bar[B_TRK0 + bb]);
-          if (!wait_all(&bar[B_TRK0 + bb], par, w)) { ok = false; break; }
+          // every lane holds the ids of one key of a 32-key chunk
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
-            const int kc0 = (2 * half + cc) * 32;
-            uint32_t bits = 0;
+            const int32_t* kt = p.tracks + kb * 128 + (2 * half + cc) * 32;
+            const int ks = __ldg(kt + lane), kg = __ldg(kt + n + lane), kz = __ldg(kt + 2 * n + lane);
+            uint32_t causal = 0;
+            if (p.score.consecutive) {
+              const int64_t d = (int64_t)pq - __ldg(kt + 3 * n);  // key t is d - t before the row
+              causal = bits32(d - p.W + 1, d + 1);
+            } else {
 #pragma unroll
-            for (int t2 = 0; t2 < 32; ++t2) {
-              const int kc = kc0 + t2;
-              bits |= (mask_legal(sq, gq, zq, pq, kt[kc], kt[128 + kc], kt[256 + kc],
-                                  kt[384 + kc], p.W) ? 1u : 0u) << t2;
+              for (int t2 = 0; t2 < 32; t2 += 4) {
+                const int4 k4 = __ldg(reinterpret_cast<const int4*>(kt + 3 * n + t2));
+                causal |= ((unsigned)(pq - k4.x) < (unsigned)p.W ? 1u : 0u) << t2;
+                causal |= ((unsigned)(pq - k4.y) < (unsigned)p.W ? 1u : 0u) << (t2 + 1);
+                causal |= ((unsigned)(pq - k4.z) < (unsigned)p.W ? 1u : 0u) << (t2 + 2);
+                causal |= ((unsigned)(pq - k4.w) < (unsigned)p.W ? 1u : 0u) << (t2 + 3);
+              }
             }
-            lm[cc] = bits;
+            lm[cc] = mask_chunk<true>(sq, gq, zq, ks, kg, kz, causal);
           }
         }
         // a partial tile on which every row of this warp keeps all 64 of its keys takes the
@@ -890,10 +880,8 @@ marble_status_t prepare(const marble_plan_t* pl, const marble_qkv_t* qkv,
   const float scale = qkv->scale > 0.f ? qkv->scale : 1.0f / sqrtf((float)D);
   prm->scale_log2 = scale * 1.4426950408889634f;
   if (MOD & kScoreCap) set_cap(&prm->score, score->cap, scale);
-  if (MOD & kScoreBias) {
-    prm->score.slopes = score->slopes;
-    prm->score.consecutive = pl->pos_is_index;
-  }
+  if (MOD & kScoreBias) prm->score.slopes = score->slopes;
+  prm->score.consecutive = pl->pos_is_index;
   if (once_per_device((D == 128 ? 1 : 2) + 4 * MOD)) {
     cudaError_t e = cudaFuncSetAttribute(k_attn_fwd<D, MOD>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,

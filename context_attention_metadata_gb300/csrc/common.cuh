@@ -141,11 +141,43 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, const W
   return __all_sync(0xffffffffu, ok);
 }
 
-// the packed-mask predicate of MARBLE s01 for one (query, key) pair of tracks
+// the packed-mask predicate of MARBLE s01 for one (query, key) pair of tracks, without branches
+// (0 <= dp < W in one unsigned comparison: W >= 0)
 __device__ __forceinline__ bool mask_legal(int sq, int gq, int zq, int pq, int sk, int gk, int zk,
                                            int pk, int W) {
-  const int dp = pq - pk;
-  return ((dp >= 0 && dp < W) || (gq >= 0 && gq == gk)) && (zk < 0 || zk == zq) && (sk == sq);
+  const bool causal = (unsigned)(pq - pk) < (unsigned)W;
+  const bool span = (gq >= 0) & (gq == gk);
+  const bool keep = (zk < 0) | (zk == zq);
+  return (causal | span) & keep & (sk == sq);
+}
+
+// bits [lo, hi) cut to [0, 32)
+__device__ __forceinline__ uint32_t bits32(int64_t lo, int64_t hi) {
+  const int a = (int)max(min(lo, (int64_t)32), (int64_t)0);
+  const int b = (int)max(min(hi, (int64_t)32), (int64_t)0);
+  return a < b ? (~0u >> (32 - (b - a))) << a : 0u;
+}
+
+// The predicate for one token (the thread's: its sample, segment and noise id) against the 32
+// tokens of a chunk, of which lane t holds token t's: a chunk has few different triples of ids,
+// often one, and each is decided once.  `causal`: the tokens that the causal term allows the
+// thread's.  `kQuery`: the thread's token is the query (otherwise the key).  Whole warp.
+template <bool kQuery>
+__device__ __forceinline__ uint32_t mask_chunk(int s, int g, int z, int cs, int cg, int cz,
+                                               uint32_t causal) {
+  uint32_t left = ~0u, bits = 0;
+  while (left) {
+    const int from = __ffs(left) - 1;
+    const int s0 = __shfl_sync(0xffffffffu, cs, from), g0 = __shfl_sync(0xffffffffu, cg, from);
+    const int z0 = __shfl_sync(0xffffffffu, cz, from);
+    const uint32_t run = __ballot_sync(0xffffffffu, (cs == s0) & (cg == g0) & (cz == z0));
+    left &= ~run;
+    const int zk = kQuery ? z0 : z;  // the key's noise id
+    const bool keep = ((zk < 0) | (z == z0)) & (s == s0);
+    const bool span = (g >= 0) & (g == g0);
+    bits |= keep ? (span ? run : run & causal) : 0u;
+  }
+  return bits;
 }
 
 // ------------------------------------------------------------------------------------

@@ -36,7 +36,7 @@ struct ScoreParams {
   float cap2;           // cap * log2 e
   float neg_inv_cap2_sq;  // -1 / cap2^2
   const float* slopes;  // [hq] or null
-  int consecutive;      // the positions of a block's tokens are consecutive
+  int consecutive;      // set for every variant: the positions of a block's tokens are consecutive
 };
 
 // the score variant a call needs
