@@ -959,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
                   if constexpr ((MOD & kScoreCap) == 0) {
                     s = fma2(f2(x0, x1), f2(sl2), bias);
                   } else {
-                    const F2 c = cap_poly(f2(x0, x1), p.score);
+                    const F2 c = cap_poly<6>(f2(x0, x1), p.score);
                     split(fma2(mul2(c, c), f2(p.score.neg_inv_cap2_sq), f2(1.f)), &wv[u], &wv[u + 1]);
                     s = add2(c, bias);
                   }

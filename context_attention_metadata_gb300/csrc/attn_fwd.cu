@@ -166,18 +166,17 @@ template <int MOD>
 __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams& p, float sl2,
                                           float slope, float side, float far0, int pq,
                                           const int32_t* __restrict__ pos) {
-  bool usual = true;
+  float top = 0.f;
   if constexpr ((MOD & kScoreCap) != 0) {
     float hi[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < 64; ++t)
       hi[t & 3] = fmaxf(hi[t & 3], fabsf(__uint_as_float(v[t >> 5][t & 31])));
-    usual = __all_sync(0xffffffffu,
-                       fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])) <= p.score.lim);
+    top = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
   }
   // key t of the half is at side (far0 - t): the bias is own + t * step
   const float own = -side * slope * far0, step = side * slope;
-  if ((MOD & kScoreBias) == 0 ? usual : usual && side != 0.f) {
+  auto pairs = [&](auto terms) {
     [[maybe_unused]] F2 at[2] = {f2(0.f, 1.f), f2(2.f, 3.f)};
 #pragma unroll
     for (int t = 0; t < 64; t += 2) {
@@ -186,9 +185,10 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
       if constexpr ((MOD & kScoreCap) == 0)
         s = fma2(x, f2(sl2), f2(own));
       else
-        s = (MOD & kScoreBias) != 0 ? add2(cap_poly(x, p.score), f2(own)) : cap_poly(x, p.score);
+        s = cap_poly<decltype(terms)::value>(x, p.score);
       if constexpr ((MOD & kScoreBias) != 0) {
         // whole numbers counted up, so that the column's part is rounded once
+        if constexpr ((MOD & kScoreCap) != 0) s = add2(s, f2(own));
         s = fma2(at[(t >> 1) & 1], f2(step), s);
         at[(t >> 1) & 1] = add2(at[(t >> 1) & 1], f2(4.f));
       }
@@ -197,6 +197,15 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
       v[t >> 5][t & 31] = __float_as_uint(s0);
       v[t >> 5][(t & 31) + 1] = __float_as_uint(s1);
     }
+  };
+  // A cap alone leaves registers for a third copy, with four terms: 2050 us against 2340 on the
+  // 64K packed configuration (d = 128, cap 50); with a bias too that copy spills (2720, and
+  // 3070 against 2770 where scores need six terms).
+  const bool linear = (MOD & kScoreBias) == 0 || side != 0.f;
+  if (MOD == kScoreCap && __all_sync(0xffffffffu, top <= p.score.lim_n)) {
+    pairs(std::integral_constant<int, 4>{});
+  } else if (linear && ((MOD & kScoreCap) == 0 || __all_sync(0xffffffffu, top <= p.score.lim))) {
+    pairs(std::integral_constant<int, 6>{});
   } else {
 #pragma unroll
     for (int t = 0; t < 64; t += 4) {

@@ -8,13 +8,14 @@
 // and for the gradient of a capped score ds/dx = scale * (1 - tanh^2), the factor 1 - tanh^2 here.
 //
 // tanh is taken in one of two ways, decided per warp and tile:
-//   |x scale / c| <= 0.45 for all of the warp's scores: an odd polynomial, tanh y = y (a0 + a1 y^2
-//     + a2 y^4 + a3 y^6), the minimax fit of tanh(y) / y in y^2 over [0, 0.45^2] (computed by the
-//     exchange algorithm), relative error 2^-22.  Its coefficients are folded with the scale on
-//     the host, so that a score costs five multiply-adds.
+//   |x scale / c| <= 0.875 for all of the warp's scores: an odd polynomial, tanh y = y (a0 +
+//     a1 y^2 + ... + a5 y^10), the minimax fit of tanh(y) / y in y^2 over [0, 0.875^2] (computed
+//     by the exchange algorithm), relative error 2^-22.7.  Its coefficients are folded with the
+//     scale on the host, so that a score costs seven multiply-adds.
+//   <= 0.45, in the forward with a cap alone: the same with four terms, relative error 2^-22.
 //   otherwise 1 - 2 / (1 + e^(2 y)): two calls to the special function unit, which also has the
 //     softmax's exp2 to do, and an absolute error of 2^-22 c (the score's own rounding is of
-//     that size, some |score| being above 0.45 c).
+//     that size, some |score| being above 0.875 c).
 #pragma once
 
 #include <math.h>
@@ -30,8 +31,10 @@ namespace marble {
 enum : int { kScoreCap = 1, kScoreBias = 2 };  // bits of a kernel's score variant
 
 struct ScoreParams {
-  float c[4];           // s = x (c[0] + c[1] x^2 + c[2] x^4 + c[3] x^6) for |x| <= lim
+  float c[6];           // s = x (c[0] + c[1] x^2 + ... + c[5] x^10) for |x| <= lim
   float lim;
+  float cn[4];          // the same with four terms, for |x| <= lim_n
+  float lim_n;
   float ky;             // e^(2 y) = 2^(ky x)
   float cap2;           // cap * log2 e
   float neg_inv_cap2_sq;  // -1 / cap2^2
@@ -62,18 +65,24 @@ marble_status_t with_variant(int d, int mod, F f) {
 
 // `cap` > 0
 inline void set_cap(ScoreParams* s, float cap, float scale) {
-  static const double kA[4] = {0.9999997567401877, -0.3332946719023316, 0.13236369052147212,
-                               -0.0460281937984787};
+  static const double kA[6] = {0.9999998509502919,   -0.33331914077818203, 0.1331109766192674,
+                               -0.0526657826506247,  0.018277444003715584, -0.003840352757762384};
+  static const double kAn[4] = {0.9999997567401877, -0.3332946719023316, 0.13236369052147212,
+                                -0.0460281937984787};
   const double log2e = 1.4426950408889634, k = (double)scale / cap;
-  double f = scale * log2e;
-  bool ok = true;
-  for (int i = 0; i < 4; ++i, f *= k * k) {
-    s->c[i] = (float)(kA[i] * f);
-    ok = ok && std::isfinite(s->c[i]);
-  }
-  // x^6 has to stay finite, and so do the coefficients: caps far below the scale take the
-  // second way alone
-  s->lim = ok ? (float)fmin(0.45 / k, 1e5) : -1.f;
+  // the highest power of x has to stay finite, and so do the coefficients: caps far below the
+  // scale take the last way alone
+  auto fold = [&](const double* a, float* c, int terms, double top) {
+    double f = scale * log2e;
+    bool ok = true;
+    for (int i = 0; i < terms; ++i, f *= k * k) {
+      c[i] = (float)(a[i] * f);
+      ok = ok && std::isfinite(c[i]);
+    }
+    return ok ? (float)fmin(top / k, 1e3) : -1.f;
+  };
+  s->lim = fold(kA, s->c, 6, 0.875);
+  s->lim_n = fold(kAn, s->cn, 4, 0.45);
   s->ky = (float)(2.0 * log2e * k);
   s->cap2 = (float)(cap * log2e);
   s->neg_inv_cap2_sq = (float)(-1.0 / (cap * log2e) / (cap * log2e));
@@ -115,11 +124,15 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
-// capped scores of a pair, |x| <= lim
+// capped scores of a pair: six terms, |x| <= lim, or four, |x| <= lim_n
+template <int kTerms>
 __device__ __forceinline__ F2 cap_poly(F2 x, const ScoreParams& p) {
+  const float* const c = kTerms == 4 ? p.cn : p.c;
   const F2 u = mul2(x, x);
-  const F2 r = fma2(fma2(f2(p.c[3]), u, f2(p.c[2])), u, f2(p.c[1]));
-  return mul2(x, fma2(r, u, f2(p.c[0])));
+  F2 r = f2(c[kTerms - 1]);
+#pragma unroll
+  for (int i = kTerms - 2; i >= 0; --i) r = fma2(r, u, f2(c[i]));
+  return mul2(x, r);
 }
 
 // 1 / (1 + e^(2 y)): the capped score is cap2 (1 - 2 r), its slope's factor 4 r (1 - r)
