@@ -10,7 +10,7 @@
 // Kernel structure (sm_103a): one persistent CTA per SM takes work units (q block, q head)
 // from a shared ticket counter, in the plan's order for the step (longest tile list first),
 // and runs them through a pipeline of warp roles that meet at mbarriers:
-//   warp 14     scheduler: draws a ticket, turns it into a unit and its tile-list range and
+//   warp 2      scheduler: draws a ticket, turns it into a unit and its tile-list range and
 //               posts it in a 4-entry queue in shared memory; every other role reads the
 //               queue in order, and the epilogue frees an entry once all roles are past it.
 //   warp 0      TMA producer: Q of each unit into one of two slots, K_j and V_j through
@@ -20,14 +20,14 @@
 //               tcgen05.mma -- S = Q K^T up to two tiles ahead of the softmax, O += P V with P
 //               as bf16 in TMEM over its S buffer and V read MN-major -- polling its inputs
 //               and issuing whichever of the next PV and the next S is ready.
-//   warps 2..9  softmax: two warps per TMEM lane quarter, each owning 64 of a row's 128
+//   warps 4..11 softmax: two warps per TMEM lane quarter, each owning 64 of a row's 128
 //               columns; the row max is exchanged through shared memory.  Row max, exp2,
 //               row sum, bf16 P back into TMEM, lazy O rescale; at a unit's end they hand
 //               the row's (m, l) to the epilogue and go on with the next unit at once.  On
 //               partial tiles they evaluate the mask (mask_chunk: once per row and run of keys
 //               with the same ids); full tiles skip it; empty tiles are never listed, so never
 //               loaded.
-//   warps 10..13 epilogue, one thread per row: merge the unit's (O, m, l) into the stored
+//   warps 12..15 epilogue, one thread per row: merge the unit's (O, m, l) into the stored
 //               state through a staged TMA store / reduce-add, while the softmax warps and
 //               the tensor core work on the next unit in the other O buffer.
 // Scores are kept in base-2 units (s * scale * log2 e); the stored m is in the same units
@@ -44,11 +44,21 @@
 namespace marble {
 namespace {
 
-constexpr int kThreads = 480;              // 15 warps, roles above
-constexpr int kSoftmax = 256;              // softmax threads (warps 2..9)
-constexpr int kEpi = 128;                  // epilogue threads (warps 10..13)
-constexpr int kWarpEpi0 = 10;
-constexpr int kWarpSched = 14;
+constexpr int kThreads = 512;              // 16 warps, roles above
+constexpr int kSoftmax = 256;              // softmax threads (warps 4..11)
+constexpr int kEpi = 128;                  // epilogue threads (warps 12..15)
+constexpr int kWarpSched = 2;
+constexpr int kWarpSoft0 = 4;
+constexpr int kWarpEpi0 = 12;
+// registers per thread: the launch gives every thread 128 (512 x 128 = the SM's 65,536); the
+// control warps and the epilogue hand theirs to the two softmax warpgroups, which would spill
+// with 128: 128 x 56 + 256 x 168 + 128 x 112 <= 512 x 128
+constexpr int kRegsLaunch = 128;
+constexpr int kRegsCtl = 56;
+constexpr int kRegsSoft = 168;
+constexpr int kRegsEpi = 112;
+static_assert(128 * kRegsCtl + kSoftmax * kRegsSoft + kEpi * kRegsEpi <= kThreads * kRegsLaunch,
+              "register split");
 constexpr float kRescaleThreshold = 8.0f;  // base-2 units: rescale O when max grows > 2^8
 constexpr int kQueue = 4;                  // work-queue entries
 
@@ -266,6 +276,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   const uint32_t tS = tmem_base;        // S buffers at +0 and +128
   const uint32_t tO = tmem_base + 256;  // O buffers at +0 and +128
 
+  if (warp < kWarpSoft0) {
+  // warpgroup 0: scheduler, producer, MMA issuer (and a warp without a role)
+  regs_shrink<kRegsCtl>();
   if (warp == kWarpSched) {
     // ------------------------------------------------------------------ scheduler
     if (lane == 0) {
@@ -460,12 +473,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     }
     __syncwarp();
   }
-  else if (warp < kWarpEpi0) {
+  } else if (warp < kWarpEpi0) {
     // ------------------------------------------------------------------ softmax warps
+    regs_grow<kRegsSoft>();
     // two warps per TMEM lane quarter: `half` owns S columns [64 half, 64 half + 64) and O
     // columns [D/2 half, D/2 half + D/2) of its row
     const int quarter = warp & 3;
-    const int half = (warp - 2) >> 2;
+    const int half = (warp - kWarpSoft0) >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t lb = (uint32_t)(quarter * 32) << 16;
     const float sl2 = p.scale_log2;
@@ -673,6 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   }
   else {
     // ------------------------------------------------------------------ epilogue warps
+    regs_shrink<kRegsEpi>();
     // one thread per row (warp w owns TMEM lane quarter w & 3)
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
@@ -896,6 +911,16 @@ marble_status_t prepare(const marble_plan_t* pl, const marble_qkv_t* qkv,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Smem<D>::bytes());
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(k_attn_fwd)");
+  }
+  {
+    // the warpgroups' budgets are drawn from the registers that the block is launched with:
+    // with fewer the growing warpgroups would wait for ever (checked on every call)
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, k_attn_fwd<D, MOD>);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes(k_attn_fwd)");
+    if (fa.numRegs < kRegsLaunch)
+      return fail(MARBLE_ERR_UNSUPPORTED, "forward kernel built with " + std::to_string(fa.numRegs) +
+                                              " registers per thread, fewer than its split needs");
   }
   return MARBLE_OK;
 }
