@@ -208,11 +208,8 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
       v[t >> 5][(t & 31) + 1] = __float_as_uint(s1);
     }
   };
-  // A cap alone leaves registers for a third copy, with four terms: 2050 us against 2340 on the
-  // 64K packed configuration (d = 128, cap 50); with a bias too that copy spills (2720, and
-  // 3070 against 2770 where scores need six terms).
   const bool linear = (MOD & kScoreBias) == 0 || side != 0.f;
-  if (MOD == kScoreCap && __all_sync(0xffffffffu, top <= p.score.lim_n)) {
+  if ((MOD & kScoreCap) != 0 && linear && __all_sync(0xffffffffu, top <= p.score.lim_n)) {
     pairs(std::integral_constant<int, 4>{});
   } else if (linear && ((MOD & kScoreCap) == 0 || __all_sync(0xffffffffu, top <= p.score.lim))) {
     pairs(std::integral_constant<int, 6>{});
