@@ -200,15 +200,16 @@ def lib():
 
 
 def _call(name, *args):
-    st = getattr(lib(), name)(*args)
+    st = getattr(_lib or lib(), name)(*args)
     if st != OK:
         raise MarbleError(st, lib().marble_last_error().decode())
 
 
 def _stream(stream):
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # read directly: a stream object costs as much as a small call's kernel
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _ptr(t):
@@ -216,6 +217,9 @@ def _ptr(t):
 
 
 def _need(t, dtype, name, shape=None):
+    if getattr(t, "dtype", None) is dtype and t.is_cuda and t.is_contiguous() and \
+            (shape is None or t.shape == shape):
+        return
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -365,71 +369,69 @@ class Rope:
                      None if k_weight is None else k_weight.data_ptr(), float(eps))
 
 
-def _heads(q, k, v, n, dtype, device, what):
-    """marble_heads_t of [n, heads, d] tensors (None: absent) whose tokens may be strided."""
-    c = _Heads()
-    d = hkv = 0
-    for t, nm in ((q, "q"), (k, "k"), (v, "v")):
+def _heads(parts, n, dtype, index, what):
+    """marble_heads_t of the tensors q, k, v in ``parts``, [n, heads, d] on GPU ``index`` (None:
+    absent), whose tokens may be strided."""
+    ptr, step, count = [None, None, None], [0, 0, 0], [0, 0, 0]
+    d = 0
+    for i, t in enumerate(parts):
         if t is None:
             continue
         try:
             (rows, heads, dd), (s0, s1, s2) = t.shape, t.stride()
-            ok = t.dtype is dtype
+            ok = t.dtype is dtype and t.is_cuda
         except (AttributeError, ValueError, TypeError):
             ok = False
-        if not ok:
-            raise ValueError(f"{what}{nm} must be a {dtype} tensor [n, heads, d]")
-        if t.device != device:
-            raise ValueError(f"{what}{nm} must be on {device}")
-        if rows != n or (d and dd != d) or (nm == "v" and hkv and heads != hkv):
-            raise ValueError(f"{what}{nm} has shape {tuple(t.shape)}: n, d or the kv heads differ")
+        if not ok or t.get_device() != index:
+            raise ValueError(f"{what}{'qkv'[i]} must be a {dtype} tensor [n, heads, d] on cuda:{index}")
+        if rows != n or (d and dd != d) or (i == 2 and count[1] and heads != count[1]):
+            raise ValueError(f"{what}{'qkv'[i]} has shape {tuple(t.shape)}: n, d or the kv heads "
+                             "differ")
         if n > 0 and ((heads > 1 and s1 != dd) or s2 != 1):
-            raise ValueError(f"{what}{nm}: the heads of a token must be contiguous")
-        d, ptr, stride = dd, t.data_ptr(), s0 if n > 1 else heads * dd
-        if nm == "q":
-            c.q, c.q_stride, c.hq = ptr, stride, heads
-        elif nm == "k":
-            c.k, c.k_stride, c.hkv = ptr, stride, heads
-            hkv = heads
-        else:
-            c.v, c.v_stride, c.hkv = ptr, stride, heads
-    c.d = d
-    return c
+            raise ValueError(f"{what}{'qkv'[i]}: the heads of a token must be contiguous")
+        d, count[i], ptr[i], step[i] = dd, heads, t.data_ptr(), s0 if n > 1 else heads * dd
+    return _Heads(*ptr, *step, count[0], count[1] or count[2], d)
 
 
-def _rope_args(pos, plan, q_weight, k_weight, first):
-    import torch
-    if not isinstance(pos, torch.Tensor) or pos.dim() != 2:
-        raise ValueError("pos must be an int32 CUDA tensor [axes, n]")
-    _need(pos, torch.int32, "pos")
-    if not isinstance(first, torch.Tensor) or first.dim() != 3:
-        raise ValueError("q must be a tensor [n, heads, d]")
-    n = pos.shape[1]
+def _rope_args(torch, pos, plan, q_weight, k_weight, first):
+    """(n, GPU) of a rotary call, its small tensors checked."""
+    try:
+        n, d = pos.shape[1], first.shape[2]
+        ok = pos.dim() == 2 and pos.dtype is torch.int32 and pos.is_cuda and pos.is_contiguous()
+    except (AttributeError, IndexError):
+        ok = False
+    if not ok:
+        raise ValueError("pos must be a contiguous int32 CUDA tensor [axes, n], q a tensor "
+                         "[n, heads, d]")
     if plan is not None and n != plan.n:
         raise ValueError("pos must have the plan's N columns")
-    dev = pos.device
+    index = pos.get_device()
     for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
-            _need(w, torch.float32, nm, (first.shape[2],))
-            if w.device != dev:
-                raise ValueError(f"{nm} must be on {dev}")
-    return n, dev
+            _need(w, torch.float32, nm, (d,))
+            if w.get_device() != index:
+                raise ValueError(f"{nm} must be on cuda:{index}")
+    return n, index
 
 
-def _rope_out(like, out, names, dtype, device, stream):
+def _rope_out(torch, like, out, names, dtype, stream):
     """``out`` checked against the tensors it is for, or new tensors like them: those belong to
     the stream that writes them."""
-    import torch
     if out is None:
         if stream is not None:
             with torch.cuda.stream(stream):
-                return _rope_out(like, None, names, dtype, device, None)
-        return tuple([None if t is None else torch.empty(t.shape, dtype=dtype, device=device)
-                      for t in like])
+                return _rope_out(torch, like, None, names, dtype, None)
+        return tuple([None if t is None else t.new_empty(t.shape, dtype=dtype) for t in like])
     if len(out) != 3 or any((a is None) != (b is None) or (a is not None and a.shape != b.shape)
                             for a, b in zip(out, like)):
         raise ValueError(f"out must hold one tensor of the same shape for each of {names}")
     return tuple(out)
+
+
+def _raw_stream(torch, stream, index):
+    """The stream's handle; None: the current stream of GPU ``index`` (read directly: building
+    the stream object would cost a single-token call as much as its kernel takes)."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def rope(rope: Rope, pos, q, k=None, v=None, plan: Optional[Plan] = None, q_weight=None,
@@ -442,14 +444,15 @@ def rope(rope: Rope, pos, q, k=None, v=None, plan: Optional[Plan] = None, q_weig
     be None.  plan None: the order stays, any n, and ``out`` may be (q, k, v) itself.
     Returns (q, k, v) in plan order, ``out`` or new tensors."""
     import torch
-    n, dev = _rope_args(pos, plan, q_weight, k_weight, q)
+    n, index = _rope_args(torch, pos, plan, q_weight, k_weight, q)
     bf16 = torch.bfloat16
-    src = _heads(q, k, v, n, bf16, dev, "")
-    out = _rope_out((q, k, v), out, "q, k and v", bf16, dev, stream)
-    dst = _heads(*out, n, bf16, dev, "out ")
+    parts = (q, k, v)
+    src = _heads(parts, n, bf16, index, "")
+    out = _rope_out(torch, parts, out, "q, k and v", bf16, stream)
+    dst = _heads(out, n, bf16, index, "out ")
     c = rope._c(pos, q_weight, None if k is None else k_weight, eps)
     _call("marble_rope", None if plan is None else plan.handle, n, ctypes.byref(c),
-          ctypes.byref(src), ctypes.byref(dst), _stream(stream))
+          ctypes.byref(src), ctypes.byref(dst), _raw_stream(torch, stream, index))
     return out
 
 
@@ -461,29 +464,30 @@ def rope_bwd(rope: Rope, pos, dq, dk=None, dv=None, plan: Optional[Plan] = None,
     Returns (dq, dk, dv, dq_weight, dk_weight), the first three in ``out`` (a token's heads
     contiguous: slices of a fused gradient are fine) or new tensors, the weights' fp32 or None."""
     import torch
-    n, dev = _rope_args(pos, plan, q_weight, k_weight, dq)
+    n, index = _rope_args(torch, pos, plan, q_weight, k_weight, dq)
     bf16 = torch.bfloat16
     if dk is None:
         k_weight = None
-    grad = _heads(dq, dk, dv, n, torch.float32, dev, "d")
-    out = _rope_out((dq, dk, dv), out, "dq, dk and dv", bf16, dev, stream)
-    dx = _heads(*out, n, bf16, dev, "out d")
+    parts = (dq, dk, dv)
+    grad = _heads(parts, n, torch.float32, index, "d")
+    out = _rope_out(torch, parts, out, "dq, dk and dv", bf16, stream)
+    dx = _heads(out, n, bf16, index, "out d")
     dwq = dwk = ws = x = None
     if q_weight is not None or k_weight is not None:
         for w, t, g, nm in ((q_weight, q, dq, "q"), (k_weight, k, dk, "k")):
             if w is not None and (t is None or t.shape != g.shape):
                 raise ValueError(f"{nm}, the input of rope(), is needed for the norm's gradient")
-        x = _heads(q if q_weight is not None else None, k if k_weight is not None else None, None,
-                   n, bf16, dev, "")
+        x = _heads((q if q_weight is not None else None, k if k_weight is not None else None, None),
+                   n, bf16, index, "")
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
             dwq = None if q_weight is None else torch.empty_like(q_weight)
             dwk = None if k_weight is None else torch.empty_like(k_weight)
-            ws = torch.empty(ROPE_WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
+            ws = pos.new_empty(ROPE_WORKSPACE_BYTES, dtype=torch.uint8)
     c = rope._c(pos, q_weight, k_weight, eps)
     _call("marble_rope_bwd", None if plan is None else plan.handle, n, ctypes.byref(c),
           None if x is None else ctypes.byref(x), ctypes.byref(grad), ctypes.byref(dx),
           None if dwq is None else _ptr(dwq), None if dwk is None else _ptr(dwk),
-          None if ws is None else _ptr(ws), _stream(stream))
+          None if ws is None else _ptr(ws), _raw_stream(torch, stream, index))
     return (*out, dwq, dwk)
 
 

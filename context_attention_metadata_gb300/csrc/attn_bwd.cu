@@ -105,6 +105,8 @@ struct BwdParams {
   long long n;
   int P, bps, q_shard, kv_shard;
   int hq, hkv, group;
+  int kv_div;                // dK/dV kernel: unit head u reads kv head u / kv_div (1, or the q
+                             // heads of a kv head where each has a unit of its own)
   int nwork;                 // units with a non-empty list
   int W;
   float scale, sl2;
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(kGThreads, 1) k_bwd_dq(const __grid_constant__
       const int64_t nq = queue.blk[slot];
       const int T = queue.T[slot];
       const int64_t e0 = queue.e0[slot];
-      const int kvh = h / p.group;
+      const int kvh = h / (p.group * p.kv_div);
       // the unit's first dS^T slot: by row-list entry (whole backward) or in the step's order
       const int64_t sl0 = p.whole ? p.ds_base[nq / p.bps] + e0 * p.hq + h
                                   : p.ds_slot0 + p.step_off[nq * (p.P + 1) + opt] * p.hq + h;
@@ -589,8 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
       if (lane == 0) {
         mbar_arrive_expect_tx(&bar[K_KVFULL], 2 * kTile);
         for (int a = 0; a < kAtoms; ++a) {
-          tma_load_3d(sK + a * 16384, &p.k_map, &bar[K_KVFULL], a * 64, (int)(nk * 128), kh);
-          tma_load_3d(sV + a * 16384, &p.v_map, &bar[K_KVFULL], a * 64, (int)(nk * 128), kh);
+          tma_load_3d(sK + a * 16384, &p.k_map, &bar[K_KVFULL], a * 64, (int)(nk * 128),
+                      kh / p.kv_div);
+          tma_load_3d(sV + a * 16384, &p.v_map, &bar[K_KVFULL], a * 64, (int)(nk * 128),
+                      kh / p.kv_div);
         }
       }
       ++kv_fills;
@@ -1196,6 +1200,7 @@ marble_status_t prepare_bwd(const marble_plan_t* pl, const marble_qkv_t* qkv,
   prm.hq = qkv->hq;
   prm.hkv = qkv->hkv;
   prm.group = qkv->hq / qkv->hkv;
+  prm.kv_div = 1;
   prm.W = pl->W;
   prm.scale = qkv->scale > 0.f ? qkv->scale : 1.0f / sqrtf((float)D);
   prm.sl2 = prm.scale * kLog2e;
@@ -1446,16 +1451,21 @@ bool rows_balance(int64_t longest, int64_t tiles, int hq) {
   return 2 * longest * sm_count() <= tiles * (int64_t)hq;
 }
 
-// every tile of the pack at once, with one dQ GEMM over all q blocks
-bool whole_all(const marble_plan_t* pl, int hq) {
+// every tile of the pack at once, with one dQ GEMM over all q blocks.  Scored calls also take it
+// for rows that do not balance but are short: a tile of a lone unit takes 0.3 us, each of the
+// P * P launches of the other way 4 us or more (4096 tokens, 8/2 heads of 64, P = 4: the dQ part
+// 100 us in 16 launches, 17 in one).  Plain calls keep the choice they had, and with it the order
+// in which their gradients are summed.
+bool whole_all(const marble_plan_t* pl, int hq, bool scored) {
   if (whole_slots(pl, hq) == 0) return false;
   int64_t longest = 0;
   for (int r = 0; r < pl->P; ++r)
     longest = std::max(longest, pl->h_step_max[(size_t)r * (pl->P + 1) + pl->P]);
-  return rows_balance(longest, pl->nnz, hq);
+  return rows_balance(longest, pl->nnz, hq) ||
+         (scored && longest <= 4 * (int64_t)pl->P * pl->P);
 }
 
-int whole_plan(const marble_plan_t* pl, int hq, int n_steps, const int* q_shards,
+int whole_plan(const marble_plan_t* pl, int hq, bool scored, int n_steps, const int* q_shards,
                const int* kv_shards, int64_t* buf_slots) {
   const int P = pl->P;
   if (n_steps != P * P) return 0;
@@ -1472,7 +1482,7 @@ int whole_plan(const marble_plan_t* pl, int hq, int n_steps, const int* q_shards
       runs = false;
     }
   }
-  if (whole_all(pl, hq)) return P;
+  if (whole_all(pl, hq, scored)) return P;
   if (!runs) return 0;
   int64_t mx = 0;
   for (int r = 0; r < P; ++r) {
@@ -1501,7 +1511,7 @@ marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv,
   // whole-row dQ GEMMs when its scratch allows (launch_whole)
   {
     int64_t buf_slots = 0;
-    const int nbuf = whole_plan(pl, qkv->hq, n_steps, q_shards, kv_shards, &buf_slots);
+    const int nbuf = whole_plan(pl, qkv->hq, MOD != 0, n_steps, q_shards, kv_shards, &buf_slots);
     if (nbuf > 0)
       return launch_whole<D, MOD>(pl, qkv, prm, n_steps, q_shards, kv_shards, nbuf, buf_slots, s);
   }
@@ -1597,6 +1607,72 @@ marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv,
   return MARBLE_OK;
 }
 
+// dst[t, kh, :] += the sum over the q heads of kv head kh of src[t, q head, :], in head order
+// (row4: float4 of a head)
+__global__ void k_group_sum(const float4* __restrict__ src, float4* __restrict__ dst, int64_t n4,
+                            int row4, int group) {
+  for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < n4;
+       x += (int64_t)gridDim.x * blockDim.x) {
+    const float4* from = src + x / row4 * group * row4 + x % row4;
+    float4 v = dst[x];
+    for (int g = 0; g < group; ++g) {
+      const float4 a = from[g * row4];
+      v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+    }
+    dst[x] = v;
+  }
+}
+
+// dK/dV of every q head, where a group's q heads have units of their own: [n, hq, d] fp32 each,
+// from the library's pool for the length of a call
+struct GroupScratch {
+  float* mem = nullptr;
+  cudaStream_t stream = nullptr;
+  int64_t n = 0;
+  int hq = 0, d = 0, group = 1;
+
+  marble_status_t open(const marble_plan_t* pl, const marble_qkv_t& qkv, BwdParams* prm,
+                       cudaStream_t s) {
+    n = pl->n;
+    hq = qkv.hq;
+    d = qkv.d;
+    group = prm->group;
+    stream = s;
+    const size_t one = (size_t)n * hq * d;
+    void* q = nullptr;
+    if (dev_alloc(&q, 2 * one * sizeof(float), s) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return fail(MARBLE_ERR_OOM, "allocation of the grouped dK/dV scratch failed");
+    }
+    mem = static_cast<float*>(q);
+    const cudaError_t e = cudaMemsetAsync(mem, 0, 2 * one * sizeof(float), s);
+    if (e != cudaSuccess) return cuda_fail(e, "clearing the grouped dK/dV scratch");
+    const auto f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!make_rows_map(&prm->dk_map, mem, f32, 4, n, hq, d, 32, 128, sw) ||
+        !make_rows_map(&prm->dv_map, mem + one, f32, 4, n, hq, d, 32, 128, sw))
+      return fail(MARBLE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the grouped dK/dV scratch");
+    prm->hkv = hq;
+    prm->kv_div = group;
+    prm->group = 1;
+    return MARBLE_OK;
+  }
+
+  void add_up(float* dk, float* dv, cudaStream_t s) const {
+    if (!mem) return;
+    const int64_t n4 = n * (hq / group) * d / 4;
+    const unsigned grid = (unsigned)std::min<int64_t>((n4 + 255) / 256, 4096);
+    const float4* src = reinterpret_cast<const float4*>(mem);
+    k_group_sum<<<grid, 256, 0, s>>>(src, reinterpret_cast<float4*>(dk), n4, d / 4, group);
+    k_group_sum<<<grid, 256, 0, s>>>(src + (size_t)n * hq * d / 4, reinterpret_cast<float4*>(dv),
+                                     n4, d / 4, group);
+  }
+
+  ~GroupScratch() {
+    if (mem) dev_free(mem, stream);  // in stream order, after everything joined into the stream
+  }
+};
+
 // The fused ring: for every kv shard j, one dK/dV launch over the ring steps of a range
 // (q shards j, j + 1, ... in ring order; the whole ring unless its dS^T tiles exceed the
 // scratch cap), keeping the kv blocks' dK/dV in TMEM across all of them and adding them to
@@ -1614,7 +1690,18 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
   const int sms = sm_count();
   const int P = pl->P;
   const int64_t hq = qkv->hq;
-  if (whole_all(pl, (int)hq)) {
+  // Few units and grouped heads: every q head of a group gets a unit of its own, with dK/dV of its
+  // own in a scratch, which are added up in head order at the end (4096 tokens, 8/2 heads of 64:
+  // 64 units, the longest of 128 items, become 256; the backward 310 -> SPLIT us).  Scored calls
+  // only: plain calls keep the order in which their gradients are summed.
+  int64_t units = 0;
+  for (int j = 0; j < P; ++j) units += pl->h_bwd_nwork[(size_t)j * (P + 1) + P];
+  GroupScratch split;
+  if (MOD != 0 && prm.group > 1 && units * qkv->hkv < sms) {
+    rc = split.open(pl, *qkv, &prm, s);
+    if (rc != MARBLE_OK) return rc;
+  }
+  if (whole_all(pl, (int)hq, MOD != 0)) {
     // the whole backward: one dK/dV launch per kv shard over its whole ring, storing every
     // dS^T tile by its row-list entry, then one dQ GEMM over every q block
     rc = ds_scratch(pl, whole_slots(pl, (int)hq), s, &prm);
@@ -1638,7 +1725,7 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
       pk.ring_len = P;
       const int64_t seg = (int64_t)j * (P + 1) + P;
       pk.order = pl->bwd_order + seg * pl->bps;
-      pk.nwork = pl->h_bwd_nwork[seg] * qkv->hkv;
+      pk.nwork = pl->h_bwd_nwork[seg] * prm.hkv;
       if (pk.nwork > 0) {
         const cudaStream_t sks = sk[j % nsk];
         pk.sched = sched_slot(pl);
@@ -1655,6 +1742,7 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
       if (sk[k] != s) err = stream_fork(sk[k], s);
     if (err != cudaSuccess) return cuda_fail(err, "ordering of the fused backward streams");
     launch_dq_whole<D>(pl, prm, -1, (int)hq, sms, s);
+    split.add_up(dk, dv, s);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "launch of the fused backward kernels");
     return MARBLE_OK;
@@ -1716,7 +1804,7 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
     // range are skipped by the scheduler)
     const int64_t seg = (int64_t)g.j * (P + 1) + P;
     pk.order = pl->bwd_order + seg * pl->bps;
-    pk.nwork = pl->h_bwd_nwork[seg] * qkv->hkv;
+    pk.nwork = pl->h_bwd_nwork[seg] * prm.hkv;
     const cudaStream_t sks = sk[g.j % nsk];
     if (sks != s && i >= nbuf) err = cudaStreamWaitEvent(sks, ev_q[i - nbuf], 0);
     if (pk.nwork > 0 && err == cudaSuccess) {
@@ -1740,6 +1828,7 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
   for (cudaEvent_t ev : ev_q)
     if (ev) cudaEventDestroy(ev);
   if (err != cudaSuccess) return cuda_fail(err, "ordering of the fused backward streams");
+  split.add_up(dk, dv, s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "launch of the fused backward kernels");
   return MARBLE_OK;

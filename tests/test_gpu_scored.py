@@ -261,6 +261,31 @@ def test_repeats_streams_and_side_streams():
                 assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("hq,hkv,P", [(8, 2, 1), (6, 1, 4), (12, 3, 2)])
+def test_grouped_heads_of_small_packs(hq, hkv, P):
+    """Few units and grouped heads: the fused backward gives every q head units of its own.  Its
+    gradients are within the bounds, add to what the accumulators hold, and repeat."""
+    n = 1024
+    tr = wl.config_tracks(2, n)
+    q, k, v, do = _qkvdo(n, hq, hkv, 64, 13)
+    slopes = _slopes(hq, "usual")
+    pl = M.Plan(*device_tracks(tr), INF, P)
+    score = M.Score(8.0, slopes)
+    m = mask.dense_mask(tr, INF)
+    got = _run(pl, q, k, v, do, score, fused=True)
+    _check(got, q, k, v, do, m, 8.0, slopes)
+    for x, y in zip(got, _run(pl, q, k, v, do, score, fused=True)):
+        assert torch.equal(x, y)
+    lse, delta = got[1].contiguous(), torch.empty_like(got[1])
+    M.attn_bwd_prep(pl, got[0], do, delta)
+    ones = [torch.ones(x.shape, device="cuda") for x in (q, k, v)]
+    M.attn_bwd_fused(pl, q, k, v, do, lse, delta, *ones, score=score)
+    for x, y in zip(ones, got[2:]):
+        # 1 + g is rounded to fp32 once for every addition to the accumulator (at most the heads
+        # of a group, or P steps of a row), to half a step of values below 64
+        assert (x - 1 - y).abs().max() <= max(hq // hkv, P) * 64 * 2.0 ** -24 + 1e-6
+
+
 def test_full_size_rows():
     """The 64K packed configuration: rows of whole short samples against the oracle."""
     cfg = wl.CONFIGS[2]
