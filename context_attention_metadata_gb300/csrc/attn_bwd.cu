@@ -471,7 +471,8 @@ __global__ void __launch_bounds__(kGThreads, 1) k_bwd_dq(const __grid_constant__
 // unit's last MMAs are done; the epilogue hands it back to the producer) and adds them to
 // dv_acc / dk_acc with TMA reduce-adds.
 enum {
-  K_KVFULL, K_KVEMPTY, K_QFULL0, K_QFULL1, K_QEMPTY0, K_QEMPTY1, K_S, K_DP, K_YFREE, K_PFULL,
+  K_KVFULL, K_KVEMPTY, K_QFULL0, K_QFULL1, K_QEMPTY0, K_QEMPTY1, K_OFULL0, K_OFULL1,
+  K_OEMPTY0, K_OEMPTY1, K_S, K_DP, K_YFREE, K_PFULL,
   K_DSFULL,
   K_ACCFULL, K_ACCFREE, K_STG0, K_STG1, K_STGR0, K_STGR1, K_TRK00, K_TRK01, K_TRK10, K_TRK11,
   K_DSSTG0, K_DSSTG1, K_DSFREE0, K_DSFREE1, K_UFULL0, K_UEMPTY0 = K_UFULL0 + kQueue,
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
       tma_prefetch_desc(&p.v_map);
       tma_prefetch_desc(&p.do_map);
     }
-    int uc = 0, g = 0, kv_fills = 0, q_fills[2] = {0, 0};
+    int uc = 0, g = 0, kv_fills = 0, q_fills[2] = {0, 0}, o_fills[2] = {0, 0};
     bool ok = true;
     while (ok) {
       const int slot = uc % kQueue;
@@ -600,17 +601,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
       ++kv_fills;
       for (int it = 0; it < items; ++it) {
         const int s = g & 1;
-        if (g >= 2 && !wait_all(&bar[K_QEMPTY0 + s], ((g >> 1) - 1) & 1, w)) { ok = false; break; }
         const int h = kh * p.group + it / L;
         const int nqb = p.colT_row[list_entry(c0, c1, La, it % L)];
+        uint8_t* sQ = sQ0 + s * 2 * kTile;
+        uint8_t* sDO = sQ + kTile;
+        // dO first: the item two back is done with its dO (dV) well before its Q (dK)
+        if (g >= 2 && !wait_all(&bar[K_OEMPTY0 + s], ((g >> 1) - 1) & 1, w)) { ok = false; break; }
         if (lane == 0) {
-          uint8_t* sQ = sQ0 + s * 2 * kTile;
-          uint8_t* sDO = sQ + kTile;
-          mbar_arrive_expect_tx(&bar[K_QFULL0 + s], 2 * kTile);
-          for (int a = 0; a < kAtoms; ++a) {
+          mbar_arrive_expect_tx(&bar[K_OFULL0 + s], kTile);
+          for (int a = 0; a < kAtoms; ++a)
+            tma_load_3d(sDO + a * 16384, &p.do_map, &bar[K_OFULL0 + s], a * 64, nqb * 128, h);
+        }
+        ++o_fills[s];
+        if (g >= 2 && !wait_all(&bar[K_QEMPTY0 + s], ((g >> 1) - 1) & 1, w)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bar[K_QFULL0 + s], kTile);
+          for (int a = 0; a < kAtoms; ++a)
             tma_load_3d(sQ + a * 16384, &p.q_map, &bar[K_QFULL0 + s], a * 64, nqb * 128, h);
-            tma_load_3d(sDO + a * 16384, &p.do_map, &bar[K_QFULL0 + s], a * 64, nqb * 128, h);
-          }
         }
         ++q_fills[s];
         ++g;
@@ -619,8 +626,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
     }
     if (lane == 0) {
       if (kv_fills) drain_wait(&bar[K_KVFULL], (kv_fills - 1) & 1, p.wait_ns, p.err);
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < 2; ++s) {
         if (q_fills[s]) drain_wait(&bar[K_QFULL0 + s], (q_fills[s] - 1) & 1, p.wait_ns, p.err);
+        if (o_fills[s]) drain_wait(&bar[K_OFULL0 + s], (o_fills[s] - 1) & 1, p.wait_ns, p.err);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -670,6 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         tc_fence_after();
         issue_scores(0, kS);
         mma_commit(&bar[K_S]);
+        ok = mbar_wait(&bar[K_OFULL0], 0, w);
+      }
+      if (ok) {
+        tc_fence_after();
         issue_scores(0, kdP);
         mma_commit(&bar[K_DP]);
         if (items == 1) mma_commit(&bar[K_KVEMPTY]);  // the unit's last read of K and V
@@ -706,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         if (j == 0 && uc >= 1 && !mbar_wait(&bar[K_ACCFREE], (uc - 1) & 1, w)) break;
         tc_fence_after();
         issue_acc(g, kdV, j == 0);
+        if (j != items - 1) mma_commit(&bar[K_OEMPTY0 + (g & 1)]);
         if (nxt && !newu && !next_scores()) break;
         // dK of item g once its dS^T is in TMEM
         if (!mbar_wait(&bar[K_DSFULL], g & 1, w)) break;
@@ -719,6 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         if (!nxt) break;
         if (newu && !next_scores()) break;
         // dP^T(g + 1) into S^T(g)'s region, after the accumulations that read it
+        if (!mbar_wait(&bar[K_OFULL0 + ((g + 1) & 1)], ((g + 1) >> 1) & 1, w)) break;
+        tc_fence_after();
         issue_scores(g + 1, kdP);
         mma_commit(&bar[K_DP]);
         if ((newu && itn == 1) || (!newu && j + 2 == items)) mma_commit(&bar[K_KVEMPTY]);
@@ -1130,6 +1146,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
           // the second half to finish hands the Q/dO stage back to the producer
           if (r == 1 && atomicAdd(&epi_count, 1) == 1) {
             epi_count = 0;
+            mbar_arrive(&bar[K_OEMPTY0 + ((g - 1) & 1)]);
             mbar_arrive(&bar[K_QEMPTY0 + ((g - 1) & 1)]);
           }
         }
