@@ -84,6 +84,8 @@ struct BwdParams {
   // across them; the dS^T tile of q block nq lands at ds_base[nq / bps] + (its index in the
   // step's numbering) * hq + head
   int ring_s0, ring_len;
+  int every_kv;              // fused ring with whole rows: the launch's order holds the kv blocks of
+                             // every shard, each visiting the q shards from its own on
   // whole rows (whole != 0; 2: the dQ GEMM over every q block): the dK/dV kernel stores the
   // dS^T tile of row-list entry e (the plan's row lists, every kv shard) of a q block of shard
   // r at slot ds_base[r] + e * hq + head, and the dQ kernel runs one unit per (q block, q head)
@@ -172,13 +174,16 @@ __device__ __forceinline__ void dkdv_unit(const BwdParams& p, unsigned t, int* k
   *kh = (int)(t % (unsigned)p.hkv);
   const unsigned i = t / (unsigned)p.hkv;
   int64_t nk;
-  if (p.kv_shard >= 0)
+  if (p.every_kv)
+    nk = p.order[i];
+  else if (p.kv_shard >= 0)
     nk = (int64_t)p.kv_shard * p.bps + p.order[i];
   else
     nk = p.needed[p.needed_ptr[p.q_shard] + i];
   *blk = (int)nk;
   if (p.ring_len > 0) {
-    const int a = (p.kv_shard + p.ring_s0) % p.P, b = a + p.ring_len;
+    const int j = p.every_kv ? (int)(nk / p.bps) : p.kv_shard;
+    const int a = (j + p.ring_s0) % p.P, b = a + p.ring_len;
     *c0 = p.colT_ptr[nk * p.P + a];
     if (b <= p.P) {
       *La = *T = (int)(p.colT_ptr[nk * p.P + b] - *c0);
@@ -1329,8 +1334,8 @@ void launch_dq_whole(const marble_plan_t* pl, const BwdParams& prm, int q_shard,
   if (q_shard < 0) {
     pq.whole = 2;
     pq.q_shard = 0;
-    pq.order = pl->fwd_order_all;
-    pq.nwork = pl->h_fwd_nwork_all * hq;
+    pq.order = pl->order_all;
+    pq.nwork = pl->h_nwork_all[0] * hq;
   } else {
     const int64_t seg = (int64_t)q_shard * (pl->P + 1) + pl->P;
     pq.q_shard = q_shard;
@@ -1711,53 +1716,33 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
   // own in a scratch, which are added up in head order at the end (4096 tokens, 8/2 heads of 64:
   // 64 units, the longest of 128 items, become 256; the backward 310 -> 165 us).  Scored calls
   // only: plain calls keep the order in which their gradients are summed.
-  int64_t units = 0;
-  for (int j = 0; j < P; ++j) units += pl->h_bwd_nwork[(size_t)j * (P + 1) + P];
   GroupScratch split;
-  if (MOD != 0 && prm.group > 1 && units * qkv->hkv < sms) {
+  if (MOD != 0 && prm.group > 1 && (int64_t)pl->h_nwork_all[1] * qkv->hkv < sms) {
     rc = split.open(pl, *qkv, &prm, s);
     if (rc != MARBLE_OK) return rc;
   }
   if (whole_all(pl, (int)hq, MOD != 0)) {
-    // the whole backward: one dK/dV launch per kv shard over its whole ring, storing every
-    // dS^T tile by its row-list entry, then one dQ GEMM over every q block
+    // the whole backward: one dK/dV launch over every kv block, each over its whole ring, storing
+    // every dS^T tile by its row-list entry, then one dQ GEMM over every q block.  (A launch for
+    // each kv shard, four of them at a time, ends with its longest unit: 16K tokens, 8 heads, 8
+    // shards, image groups: ONE.)
     rc = ds_scratch(pl, whole_slots(pl, (int)hq), s, &prm);
     if (rc != MARBLE_OK) return rc;
     prm.whole = 1;
-    cudaStream_t sk[kDkdvStreams];
-    int nsk = 0;
-    for (int k = 0; k < kDkdvStreams; ++k) {
-      cudaStream_t x = side_stream(k);
-      if (!x) break;
-      cudaError_t e = stream_fork(s, x);
-      if (e != cudaSuccess) return cuda_fail(e, "fork of the backward streams");
-      sk[nsk++] = x;
+    BwdParams pk = prm;
+    pk.kv_shard = 0;
+    pk.q_shard = 0;
+    pk.ring_s0 = 0;
+    pk.ring_len = P;
+    pk.every_kv = 1;
+    pk.order = pl->order_all + pl->nb;
+    pk.nwork = pl->h_nwork_all[1] * prm.hkv;
+    if (pk.nwork > 0) {
+      pk.sched = sched_slot(pl);
+      const int span = timing_begin(s);
+      k_bwd_dkdv<D, MOD><<<(unsigned)(pk.nwork < sms ? pk.nwork : sms), kThreads, smem_k, s>>>(pk);
+      timing_end(span, s, kTimeDkdv, 1);
     }
-    if (nsk == 0) sk[nsk++] = s;
-    for (int j = 0; j < P; ++j) {
-      BwdParams pk = prm;
-      pk.kv_shard = j;
-      pk.q_shard = 0;
-      pk.ring_s0 = 0;
-      pk.ring_len = P;
-      const int64_t seg = (int64_t)j * (P + 1) + P;
-      pk.order = pl->bwd_order + seg * pl->bps;
-      pk.nwork = pl->h_bwd_nwork[seg] * prm.hkv;
-      if (pk.nwork > 0) {
-        const cudaStream_t sks = sk[j % nsk];
-        pk.sched = sched_slot(pl);
-        const int span = timing_begin(sks);
-        // with several side streams, at most half the SMs (as in launch_whole; measured a
-        // little faster here, slower in the ranges below, whose dQ GEMMs interleave)
-        const int cap = nsk > 1 ? (sms + 1) / 2 : sms;
-        k_bwd_dkdv<D, MOD><<<(unsigned)(pk.nwork < cap ? pk.nwork : cap), kThreads, smem_k, sks>>>(pk);
-        timing_end(span, sks, kTimeDkdv, 1);
-      }
-    }
-    cudaError_t err = cudaSuccess;
-    for (int k = 0; k < nsk && err == cudaSuccess; ++k)
-      if (sk[k] != s) err = stream_fork(sk[k], s);
-    if (err != cudaSuccess) return cuda_fail(err, "ordering of the fused backward streams");
     launch_dq_whole<D>(pl, prm, -1, (int)hq, sms, s);
     split.add_up(dk, dv, s);
     cudaError_t e = cudaGetLastError();

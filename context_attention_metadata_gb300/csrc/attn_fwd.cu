@@ -1002,9 +1002,9 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
   prm.lse_merge = 0;
   prm.step_col = pl->ring_col;
   prm.step_tag = pl->ring_tag;
-  prm.order = pl->fwd_order_all;
+  prm.order = pl->order_all;
   prm.units = (int)(pl->nb * qkv->hq);
-  prm.nwork = pl->h_fwd_nwork_all * qkv->hq;
+  prm.nwork = pl->h_nwork_all[0] * qkv->hq;
   prm.sched = sched_slot(pl);
   const unsigned grid = (unsigned)(prm.units < sms ? prm.units : sms);
   const int span = timing_begin(s);

@@ -76,13 +76,14 @@ struct marble_plan {
   int32_t* bwd_order = nullptr;      // [P*(P+1)*bps] over colT_ptr (kv blocks)
   int32_t* bwd_nwork = nullptr;      // [P*(P+1)]
   std::vector<int32_t> h_fwd_nwork, h_bwd_nwork;
-  // the fused forward: row lists in ring order (same CSR ranges as step_ptr over all kv
-  // shards) and the work order of every block of the pack, longest row first
+  // the fused ring: row lists in ring order (same CSR ranges as step_ptr over all kv shards) and
+  // the work orders of every block of the pack, longest list first: q blocks over their rows,
+  // kv blocks over their columns
   int32_t* ring_col = nullptr;       // [nnz]
   uint8_t* ring_tag = nullptr;       // [nnz]
-  int32_t* fwd_order_all = nullptr;  // [nb]
-  int32_t* fwd_nwork_all = nullptr;  // [1]
-  int32_t h_fwd_nwork_all = 0;
+  int32_t* order_all = nullptr;      // [2*nb]
+  int32_t* nwork_all = nullptr;      // [2]
+  int32_t h_nwork_all[2] = {0, 0};
   // compact tile numbering of each step (the backward's dS tiles): step_off[nq*(P+1)+opt] is
   // the number of tiles of the q blocks before nq in its q shard, for option opt (kv shard opt,
   // or every kv shard when opt == P); colT_j[e] the index of column-list entry e's kv block in

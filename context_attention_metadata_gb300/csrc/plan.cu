@@ -950,12 +950,15 @@ __global__ void __launch_bounds__(1024) k_work_order(const int64_t* __restrict__
   work_order_segment(ptr, P, bps, s, c_lo, c_hi, order + (int64_t)seg * bps, nwork + seg);
 }
 
-// the same order over every block of the pack, by the length of its whole row (every kv
-// shard): the work order of the fused forward (one CTA)
-__global__ void __launch_bounds__(1024) k_work_order_all(const int64_t* __restrict__ ptr, int P,
+// the same order over every block of the pack: q blocks by the length of their whole row (every
+// kv shard), the work order of the fused forward (CTA 0), and kv blocks by the length of their
+// whole column, that of the fused backward (CTA 1).  order [2][nb], nwork [2].
+__global__ void __launch_bounds__(1024) k_work_order_all(const int64_t* __restrict__ rows,
+                                                         const int64_t* __restrict__ cols, int P,
                                                          int64_t nb, int32_t* __restrict__ order,
                                                          int32_t* __restrict__ nwork) {
-  work_order_segment(ptr, P, nb, 0, 0, P, order, nwork);
+  const int i = blockIdx.x;
+  work_order_segment(i == 0 ? rows : cols, P, nb, 0, 0, P, order + i * nb, nwork + i);
 }
 
 __device__ void work_order_segment(const int64_t* __restrict__ ptr, int P, int64_t bps, int s,
@@ -1399,21 +1402,21 @@ marble_status_t build_plan(const marble_plan_desc_t* d, cudaStream_t s, marble_p
   k_work_order<<<P * (P + 1), 1024, 0, s>>>(p->step_ptr, P, bps, p->fwd_order, p->fwd_nwork);
   k_work_order<<<P * (P + 1), 1024, 0, s>>>(p->colT_ptr, P, bps, p->bwd_order, p->bwd_nwork);
   MARBLE_CK(cudaGetLastError());
-  // the fused forward: row lists in ring order and the order of all blocks
+  // the fused ring: row lists in ring order and the order of all blocks
   MARBLE_TRY(dalloc(p, &p->ring_col, nnz));
   MARBLE_TRY(dalloc(p, &p->ring_tag, nnz));
-  MARBLE_TRY(dalloc(p, &p->fwd_order_all, nb));
-  MARBLE_TRY(dalloc(p, &p->fwd_nwork_all, 1));
+  MARBLE_TRY(dalloc(p, &p->order_all, 2 * nb));
+  MARBLE_TRY(dalloc(p, &p->nwork_all, 2));
   k_ring_write<<<warp_ctas, 32 * kWarpsPerCta, 0, s>>>(p->step_ptr, p->step_col, p->step_tag, nb,
                                                        P, bps, p->ring_col, p->ring_tag);
-  k_work_order_all<<<1, 1024, 0, s>>>(p->step_ptr, P, nb, p->fwd_order_all, p->fwd_nwork_all);
+  k_work_order_all<<<2, 1024, 0, s>>>(p->step_ptr, p->colT_ptr, P, nb, p->order_all, p->nwork_all);
   MARBLE_CK(cudaGetLastError());
   p->h_fwd_nwork.resize((size_t)P * (P + 1));
   p->h_bwd_nwork.resize((size_t)P * (P + 1));
   p->h_step_tiles.resize((size_t)P * (P + 1));
   p->h_step_max.resize((size_t)P * (P + 1));
   const size_t pp = (size_t)P * (P + 1);
-  MARBLE_CK(read_back(s, {{&p->h_fwd_nwork_all, p->fwd_nwork_all, sizeof(int32_t)},
+  MARBLE_CK(read_back(s, {{p->h_nwork_all, p->nwork_all, 2 * sizeof(int32_t)},
                           {p->h_fwd_nwork.data(), p->fwd_nwork, pp * sizeof(int32_t)},
                           {p->h_bwd_nwork.data(), p->bwd_nwork, pp * sizeof(int32_t)},
                           {p->h_step_tiles.data(), p->step_tiles, pp * sizeof(int64_t)},
