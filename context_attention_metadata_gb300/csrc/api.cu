@@ -53,13 +53,16 @@ bool once_per_device(int key) {
 // the most side streams the step-list calls may use (marble_set_side_streams)
 std::atomic<int> g_side_limit{kSideStreams};
 
-static cudaMemPool_t mem_pool() {
+// Two pools per device, the backward's scratch having its own: a plan's small arrays, which live
+// longer, then never sit in the memory that a freed scratch leaves (a pool gives memory back to
+// the device only where nothing in it is in use).
+static cudaMemPool_t mem_pool(bool scratch) {
   static std::mutex mu;
-  static std::map<int, cudaMemPool_t> pools;
+  static std::map<std::pair<int, bool>, cudaMemPool_t> pools;
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lock(mu);
-  auto it = pools.find(dev);
+  auto it = pools.find({dev, scratch});
   if (it != pools.end()) return it->second;
   cudaMemPoolProps props;
   memset(&props, 0, sizeof(props));
@@ -73,12 +76,12 @@ static cudaMemPool_t mem_pool() {
   }
   uint64_t keep = UINT64_MAX;  // freed blocks stay in the pool
   cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
-  pools[dev] = pool;
+  pools[{dev, scratch}] = pool;
   return pool;
 }
 
-cudaError_t dev_alloc(void** p, size_t bytes, cudaStream_t s) {
-  cudaMemPool_t pool = mem_pool();
+cudaError_t dev_alloc(void** p, size_t bytes, cudaStream_t s, bool scratch) {
+  cudaMemPool_t pool = mem_pool(scratch);
   if (!pool) return cudaErrorMemoryAllocation;
   return cudaMallocFromPoolAsync(p, bytes, pool, s);
 }
@@ -935,8 +938,8 @@ static marble_status_t check_score(const marble_plan_t* p, const marble_score_t*
   if (!p) return fail(MARBLE_ERR_INVALID_ARG, "plan is null");
   marble_status_t st;
   if (score) {
-    if (!(score->cap >= 0.f) || std::isinf(score->cap))
-      return fail(MARBLE_ERR_INVALID_ARG, "score.cap must be finite and >= 0 (0 = none)");
+    if (score->cap != 0.f && !(score->cap >= 1e-30f && score->cap <= 1e30f))
+      return fail(MARBLE_ERR_INVALID_ARG, "score.cap must be 0 (none) or in [1e-30, 1e30]");
     if (score->slopes && (st = check_here(score->slopes, "score.slopes", 16)) != MARBLE_OK) return st;
   }
   if ((st = check_plan_here(p)) != MARBLE_OK) return st;
@@ -1228,8 +1231,10 @@ MARBLE_API marble_status_t marble_release_memory(void) {
   }
   const cudaError_t e = cudaStreamSynchronize(fs);
   if (err == cudaSuccess) err = e;
-  cudaMemPool_t pool = mem_pool();
-  if (err == cudaSuccess && pool) err = cudaMemPoolTrimTo(pool, 0);
+  for (bool scratch : {false, true}) {
+    cudaMemPool_t pool = mem_pool(scratch);
+    if (err == cudaSuccess && pool) err = cudaMemPoolTrimTo(pool, 0);
+  }
   if (err != cudaSuccess) return cuda_fail(err, "marble_release_memory");
   return MARBLE_OK;
 }

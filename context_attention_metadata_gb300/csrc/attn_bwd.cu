@@ -1268,7 +1268,7 @@ marble_status_t ds_scratch(const marble_plan_t* pl, size_t slots, cudaStream_t s
     }
     size_t got = need;
     void* q = scratch_take(need, s, &got);
-    if (!q && dev_alloc(&q, need, s) != cudaSuccess) {
+    if (!q && dev_alloc(&q, need, s, true) != cudaSuccess) {
       (void)cudaGetLastError();
       return fail(MARBLE_ERR_OOM, "allocation of the backward dS scratch failed (" +
                                       std::to_string(need) + " bytes)");
@@ -1662,7 +1662,7 @@ struct GroupScratch {
     stream = s;
     const size_t one = (size_t)n * hq * d;
     void* q = nullptr;
-    if (dev_alloc(&q, 2 * one * sizeof(float), s) != cudaSuccess) {
+    if (dev_alloc(&q, 2 * one * sizeof(float), s, true) != cudaSuccess) {
       (void)cudaGetLastError();
       return fail(MARBLE_ERR_OOM, "allocation of the grouped dK/dV scratch failed");
     }

@@ -217,11 +217,11 @@ marble_status_t run_attn_bwd(const marble_plan_t* p, const marble_qkv_t* qkv,
 // true the first time it is called for (key, current device); used for per-device set-up
 bool once_per_device(int key);
 
-// Device memory of plans, planner temporaries and the backward scratch comes from a
-// library-owned memory pool per device, allocated and freed in stream order: no call
-// synchronises the device (cudaFree does), and freed blocks stay in the pool for the next
+// Device memory of plans and planner temporaries, and of the backward's scratch, comes from two
+// library-owned memory pools per device, allocated and freed in stream order: no call
+// synchronises the device (cudaFree does), and freed blocks stay in their pool for the next
 // plan.
-cudaError_t dev_alloc(void** p, size_t bytes, cudaStream_t s);
+cudaError_t dev_alloc(void** p, size_t bytes, cudaStream_t s, bool scratch = false);
 cudaError_t dev_free(void* p, cudaStream_t s);
 
 // side stream idx of the current device (nullptr if it cannot be created or idx is at or

@@ -7,15 +7,17 @@
 //   bias     s -= slope_h * log2 e * |pos_q - pos_k|
 // and for the gradient of a capped score ds/dx = scale * (1 - tanh^2), the factor 1 - tanh^2 here.
 //
-// tanh is taken in one of two ways, decided per warp and tile:
-//   |x scale / c| <= 0.875 for all of the warp's scores: an odd polynomial, tanh y = y (a0 +
-//     a1 y^2 + ... + a5 y^10), the minimax fit of tanh(y) / y in y^2 over [0, 0.875^2] (computed
-//     by the exchange algorithm), relative error 2^-22.7.  Its coefficients are folded with the
-//     scale on the host, so that a score costs seven multiply-adds.
-//   <= 0.45, in the forward with a cap alone: the same with four terms, relative error 2^-22.
+// With y = x scale / c, tanh y is taken in one of these ways, decided per warp and tile:
+//   |y| <= 0.875 for all of the warp's scores: an odd polynomial, y (a0 + a1 y^2 + ... + a5 y^10),
+//     the minimax fit of tanh(y) / y in y^2 over [0, 0.875^2] (computed by the exchange
+//     algorithm), relative error 2^-22.7.  Its coefficients are folded with the scale on the
+//     host, so that a capped score costs seven multiply-adds from x.
+//   |y| <= 0.45, in the forward: the same with four terms, relative error 2^-22.
 //   otherwise 1 - 2 / (1 + e^(2 y)): two calls to the special function unit, which also has the
 //     softmax's exp2 to do, and an absolute error of 2^-22 c (the score's own rounding is of
 //     that size, some |score| being above 0.875 c).
+// Folded coefficients leave fp32's range for caps far from the scores' size; set_cap then lowers
+// the first two ways' limits to where the lost terms do not matter.
 #pragma once
 
 #include <math.h>
@@ -31,15 +33,15 @@ namespace marble {
 enum : int { kScoreCap = 1, kScoreBias = 2 };  // bits of a kernel's score variant
 
 struct ScoreParams {
-  float c[6];           // s = x (c[0] + c[1] x^2 + ... + c[5] x^10) for |x| <= lim
+  float c[6];             // s = x (c[0] + c[1] x^2 + ... + c[5] x^10) for |x| <= lim
   float lim;
-  float cn[4];          // the same with four terms, for |x| <= lim_n
+  float cn[4];            // the same with four terms, |x| <= lim_n
   float lim_n;
-  float ky;             // e^(2 y) = 2^(ky x)
-  float cap2;           // cap * log2 e
+  float ky;               // e^(2 y) = 2^(ky x)
+  float cap2;             // cap * log2 e
   float neg_inv_cap2_sq;  // -1 / cap2^2
-  const float* slopes;  // [hq] or null
-  int consecutive;      // set for every variant: the positions of a block's tokens are consecutive
+  const float* slopes;    // [hq] or null
+  int consecutive;        // set for every variant: the positions of a block's tokens are consecutive
 };
 
 // the score variant a call needs
@@ -63,29 +65,31 @@ marble_status_t with_variant(int d, int mod, F f) {
   return fail(MARBLE_ERR_UNSUPPORTED, "head dim must be 64 or 128");
 }
 
-// `cap` > 0
+// `cap` in [1e-30, 1e30]
 inline void set_cap(ScoreParams* s, float cap, float scale) {
   static const double kA[6] = {0.9999998509502919,   -0.33331914077818203, 0.1331109766192674,
                                -0.0526657826506247,  0.018277444003715584, -0.003840352757762384};
   static const double kAn[4] = {0.9999997567401877, -0.3332946719023316, 0.13236369052147212,
                                 -0.0460281937984787};
-  const double log2e = 1.4426950408889634, k = (double)scale / cap;
-  // the highest power of x has to stay finite, and so do the coefficients: caps far below the
-  // scale take the last way alone
+  const double log2e = 1.4426950408889634, k = (double)scale / cap, cap2 = cap * log2e;
+  // c[i] = a[i] scale log2e k^(2i); returns the limit for |x|: `top` in y, less where a term is
+  // lost below fp32's range (then up to where it is 2^-24 of the first), none where one is above
   auto fold = [&](const double* a, float* c, int terms, double top) {
     double f = scale * log2e;
-    bool ok = true;
     for (int i = 0; i < terms; ++i, f *= k * k) {
       c[i] = (float)(a[i] * f);
-      ok = ok && std::isfinite(c[i]);
+      if (!std::isfinite(c[i])) return -1.f;
+      if (i > 0 && std::fabs(a[i] * f) < 1e-36)
+        top = fmin(top, std::pow(0x1p-24 / std::fabs(a[i]), 0.5 / i));
     }
-    return ok ? (float)fmin(top / k, 1e3) : -1.f;
+    return (float)fmin(top / k, 1e18);
   };
   s->lim = fold(kA, s->c, 6, 0.875);
   s->lim_n = fold(kAn, s->cn, 4, 0.45);
   s->ky = (float)(2.0 * log2e * k);
-  s->cap2 = (float)(cap * log2e);
-  s->neg_inv_cap2_sq = (float)(-1.0 / (cap * log2e) / (cap * log2e));
+  s->cap2 = (float)cap2;
+  s->neg_inv_cap2_sq = (float)(-1.0 / (cap2 * cap2));
+  if (!std::isfinite(s->neg_inv_cap2_sq)) s->lim = s->lim_n = -1.f;
 }
 
 // two fp32 values in a register pair and the packed operations on them: an instruction for two
@@ -124,15 +128,23 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
-// capped scores of a pair: six terms, |x| <= lim, or four, |x| <= lim_n
+// x (c[0] + c[1] x^2 + ...) of a pair
 template <int kTerms>
-__device__ __forceinline__ F2 cap_poly(F2 x, const ScoreParams& p) {
-  const float* const c = kTerms == 4 ? p.cn : p.c;
+__device__ __forceinline__ F2 odd_poly(F2 x, const float (&c)[kTerms]) {
   const F2 u = mul2(x, x);
   F2 r = f2(c[kTerms - 1]);
 #pragma unroll
   for (int i = kTerms - 2; i >= 0; --i) r = fma2(r, u, f2(c[i]));
   return mul2(x, r);
+}
+
+// capped scores of a pair: six terms, |x| <= lim, or four, |x| <= lim_n
+template <int kTerms>
+__device__ __forceinline__ F2 cap_poly(F2 x, const ScoreParams& p) {
+  if constexpr (kTerms == 4)
+    return odd_poly(x, p.cn);
+  else
+    return odd_poly(x, p.c);
 }
 
 // 1 / (1 + e^(2 y)): the capped score is cap2 (1 - 2 r), its slope's factor 4 r (1 - r)

@@ -543,7 +543,7 @@ marble_status_t marble_attn_bwd_fused(const marble_plan_t *plan, const marble_qk
  * tokens too, as for the plain calls.
  */
 typedef struct {
-  float cap;           /* finite, >= 0 */
+  float cap;           /* 0, or in [1e-30, 1e30] */
   const float *slopes; /* device float[hq], 16-byte aligned, or NULL */
 } marble_score_t;
 

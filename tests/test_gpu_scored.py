@@ -161,7 +161,7 @@ def test_position_track(kind):
     del rng
 
 
-@pytest.mark.parametrize("cap", [1e-3, 0.1, 1e4, 1e30])
+@pytest.mark.parametrize("cap", [1e-30, 1e-3, 0.1, 1e4, 1e30])
 def test_extreme_caps(cap):
     """Caps far below and far above the scores: all weights alike, and no cap at all."""
     n = 512
@@ -171,9 +171,48 @@ def test_extreme_caps(cap):
     m = mask.dense_mask(tr, INF)
     for fused in (False, True):
         _check(_run(pl, q, k, v, do, M.Score(cap), fused=fused), q, k, v, do, m, cap, None)
-    # scores of zero, whatever the coefficients
+    # scores of zero, whatever the cap
     got = _run(pl, torch.zeros_like(q), k, v, do, M.Score(cap))
     _check(got, torch.zeros_like(q), k, v, do, m, cap, None)
+
+
+@pytest.mark.parametrize("cap", [2.5e3, 4e4, 1e6])
+def test_large_products_under_large_caps(cap):
+    """Products of some thousands, caps around and above them.  Few keys have weight, and a score
+    of size S is off by 2^-22 S (the sum of d products, the polynomial), so the keys and scale are
+    chosen for scores up to 0.9 caps or 4000 that differ between keys by less than 1."""
+    n, d = 256, 64
+    tr = wl.tracks_from_samples([[wl.Span("causal", 200), wl.Span("full", 56)]])
+    q, k, v, do = _qkvdo(n, 1, 1, d, 4)
+    q.zero_()
+    q[..., 0] = 8.0   # exact products: 8 * 8 * 64, and small ones beside them
+    q[..., 1] = torch.linspace(-1, 1, n, device="cuda").bfloat16()[:, None]
+    k.zero_()
+    k[..., 0] = 8.0
+    k[..., 1] = torch.linspace(1, -1, n, device="cuda").bfloat16()[:, None]
+    scale = min(0.9 * cap, 4000.0) / 64
+    q[..., 1] /= scale
+    pl = M.Plan(*device_tracks(tr), INF, 1)
+    st, o, lse = M.State(n, 1, d), torch.empty_like(q), torch.empty((1, n), device="cuda")
+    score = M.Score(cap)
+    M.forward(pl, q, k, v, st, o, lse, fused=True, scale=scale, score=score)
+    m = mask.dense_mask(tr, INF)
+    ref = scored.attention(q, k, v, m, cap, scale=scale, do=do, h=HALF)
+    S = scale * 64 + 1
+    off = 2.0 ** -21 * S  # the score and its maximum
+    # the LSE is a score plus a logarithm, rounded to fp32
+    assert (np.abs(_np(lse) - ref["LSE"]) <= off + 2.0 ** -22 * S).all()
+    lim = (1 + HALF) * ((1 + 2 * off / HALF) * ref["bound"]["O"] + HALF * np.abs(ref["O"]))
+    assert (np.abs(_np(o) - ref["O"]) <= lim + 1e-30).all()
+    delta = torch.empty_like(lse)
+    dq, dk, dv = (torch.zeros(x.shape, device="cuda") for x in (q, k, v))
+    M.backward(pl, q, k, v, o, do, lse, delta, dq, dk, dv, fused=True, scale=scale, score=score)
+    pl.check()
+    for name, x in zip(("dq", "dk", "dv"), (dq, dk, dv)):
+        err = np.abs(_np(x) - ref[name])
+        # 1 - tanh^2 is off by 2^-21 of one, 2^-18 of itself at 0.9 caps
+        lim = (1 + HALF) * (1 + (8 * off + 2.0 ** -18) / HALF) * ref["bound"][name]
+        assert (err <= lim + 1e-6 * scale).all(), (name, (err - lim).max())
 
 
 def test_both_ways_to_tanh_in_one_pack():
@@ -314,7 +353,7 @@ def test_refusals():
     pl = M.Plan(zero, none, none, INF, 1)
     q, k, v, _ = _qkvdo(n, 2, 2, 64, 1)
     st = M.State(n, 2, 64)
-    for cap in (-1.0, float("nan"), float("inf")):
+    for cap in (-1.0, float("nan"), float("inf"), 1e31, 1e-31):
         with pytest.raises(M.MarbleError, match="cap"):
             M.attn_fwd_fused(pl, q, k, v, st, score=M.Score(cap))
     with pytest.raises(ValueError):
@@ -336,3 +375,63 @@ def test_refusals():
         st.m.zero_()
     M.attn_fwd_fused(pl, q, k, v, st, score=M.Score(2.0))
     pl.check()
+
+
+@pytest.mark.parametrize("stream", [False, True])
+def test_a_layer_with_rotary_positions(stream):
+    """What a layer does with the two together: the fused projection's q, k and v normed, rotated
+    by (t, h, w) and moved into plan order, attention with capped scores and a bias, its backward,
+    and the projection's gradient back in original order."""
+    from oracle import rope as R
+    n, hq, hkv, d = 1024, 6, 2, 64
+    tr = wl.config_tracks(2, n)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    qkv = torch.randn((n, hq + 2 * hkv, d), generator=g, device="cuda").bfloat16()
+    do = torch.randn((n, hq, d), generator=g, device="cuda").bfloat16()
+    wq, wk = (1 + 0.2 * torch.randn(d, generator=g, device="cuda") for _ in range(2))
+    pos = torch.randint(0, 64, (3, n), generator=g, device="cuda", dtype=torch.int32)
+    freq, axis = M.rope_frequencies((16, 8, 8))
+    rope = M.Rope(freq, axis)
+    slopes = _slopes(hq, "usual")
+    pl = M.Plan(*device_tracks(tr), INF, 2, "ptrr_block")
+    q, k, v = qkv.split((hq, hkv, hkv), 1)
+    score = M.Score(10.0, slopes)
+    s = torch.cuda.Stream() if stream else None
+    if s:
+        s.wait_stream(torch.cuda.current_stream())
+    kw = dict(plan=pl, q_weight=wq, k_weight=wk, stream=s)
+    qp, kp, vp = M.rope(rope, pos, q, k, v, **kw)
+    with torch.cuda.stream(s):
+        st = M.State(n, hq, d)
+        o, lse = torch.empty_like(qp), torch.empty((hq, n), device="cuda")
+        delta = torch.empty_like(lse)
+        dq, dk, dv = (torch.zeros(x.shape, device="cuda") for x in (qp, kp, vp))
+        dp = pl.permute(do, stream=s)
+        out = torch.empty_like(qkv)
+    M.forward(pl, qp, kp, vp, st, o, lse, fused=True, score=score, stream=s)
+    M.backward(pl, qp, kp, vp, o, dp, lse, delta, dq, dk, dv, fused=True, score=score, stream=s)
+    dwq, dwk = M.rope_bwd(rope, pos, dq, dk, dv, q=q, k=k, out=out.split((hq, hkv, hkv), 1), **kw)[3:]
+    pl.check(stream=s)
+    torch.cuda.synchronize()
+    # the attention of the rotated q and k that the kernel rounded (their own error is tested with
+    # the rotary calls), in original order
+    qr, kr, vr = (pl.permute(x, inverse=True) for x in (qp, kp, vp))
+    ref = scored.attention(qr, kr, vr, mask.dense_mask(tr, INF), 10.0, _np(slopes), None, None, do,
+                           HALF)
+    p = pos.cpu().numpy()
+    for got, x, w, name, dw in ((out[:, :hq], q, wq, "dq", dwq),
+                                (out[:, hq:hq + hkv], k, wk, "dk", dwk)):
+        x, w = _np(x), _np(w)
+        want, want_w = R.backward(ref[name], x, p, freq, axis, "halves", w)
+        # turning keeps the size of an error, the norm's gradient multiplies it by r max |w| at
+        # most; the result is rounded once
+        r = 1 / np.sqrt((x * x).mean(-1) + 1e-6)
+        noise = np.sqrt(ref["noise"][name].sum())
+        err = np.linalg.norm(_np(got) - want)
+        assert err <= r.max() * np.abs(w).max() * noise + HALF * np.linalg.norm(want)
+        # a weight's gradient is the sum over the rows of gradient times x r, at most sqrt(d)
+        assert np.linalg.norm(_np(dw) - want_w) <= np.sqrt(d) * np.sqrt(x.shape[0] * x.shape[1]) * \
+            noise
+    err = np.linalg.norm(_np(out[:, hq + hkv:]) - ref["dv"])
+    assert err <= np.sqrt(ref["noise"]["dv"].sum()) + HALF * np.linalg.norm(ref["dv"])
