@@ -25,8 +25,8 @@
  *   - The caller owns every tensor it passes.  A plan owns only its own device
  *     workspace: allocated by marble_plan, grown by the backward calls for their scratch
  *     of bf16 dS tiles, and freed by marble_plan_destroy (which keeps up to two dS
- *     scratch buffers per device for later plans).  This memory comes from a
- *     stream-ordered pool the library keeps per device.  The calls that read sizes or
+ *     scratch buffers per device for later plans).  This memory comes from
+ *     stream-ordered pools the library keeps per device.  The calls that read sizes or
  *     status back to the host (marble_plan, marble_plan_stats, marble_check) do so through
  *     a small pinned host buffer the library keeps per calling thread.  No call allocates
  *     memory that the caller sees.
@@ -513,13 +513,13 @@ marble_status_t marble_attn_fwd_fused(const marble_plan_t *plan, const marble_qk
 /*
  * The whole backward ring (MARBLE s03: each kv shard's fp32 dK/dV accumulator travels with
  * the shard around the ring while dQ is carried per q shard): the same result as
- * marble_attn_bwd_steps over every (r, (r - s) mod P), up to fp32 rounding.  For every kv
- * shard j, one dK/dV launch visits the q shards in ring order (j, j + 1, ..., j - 1) and keeps
- * the dK/dV of each of its kv blocks in TMEM across all of them, adding it to dk_acc / dv_acc
- * once.  When the dS tiles of the whole pack fit the 32 GB scratch cap (and the rows balance,
- * as in marble_attn_bwd_steps), one dQ GEMM over every q block's whole row follows all of
- * them.  Otherwise
- * the dQ GEMM of each step (q shard, j) follows its kv shard's launch, and when the dS tiles
+ * marble_attn_bwd_steps over every (r, (r - s) mod P), up to fp32 rounding.  Every kv block of
+ * kv shard j visits the q shards in ring order (j, j + 1, ..., j - 1) with its dK/dV in TMEM
+ * across all of them, adding it to dk_acc / dv_acc once.  When the dS tiles of the whole pack
+ * fit the 32 GB scratch cap (and the rows balance, as in marble_attn_bwd_steps), one dK/dV
+ * launch over every kv block is followed by one dQ GEMM over every q block's whole row.
+ * Otherwise every kv shard has a dK/dV launch, followed by
+ * the dQ GEMM of each step (q shard, j), and when the dS tiles
  * of a kv shard's whole ring would exceed half of the cap, its ring is split into consecutive
  * ranges of steps, each added once.  Accumulators must be zeroed by the caller; scratch and
  * ordering as marble_attn_bwd_steps.  Errors: as marble_attn_bwd_steps.
@@ -551,8 +551,10 @@ typedef struct {
  * marble_attn_steps, marble_attn_fwd_fused, marble_attn_bwd_steps and marble_attn_bwd_fused with
  * changed scores: the same arguments, results and errors, a list of one step being the single
  * step.  The same `score` has to be given to every call of a pass, forward and backward.  score
- * NULL, or with neither cap nor slopes, is the plain call.  The launches take ticket counters and
- * scratch of the plan: a stream that is being captured into a graph is refused (INVALID_ARG).
+ * NULL, or with neither cap nor slopes, is the plain call.  The fused backward of a small pack
+ * with grouped heads takes 8 * N * hq * d bytes of the library's pool for its length.  The
+ * launches take ticket counters and scratch of the plan: a stream that is being captured into a
+ * graph is refused (INVALID_ARG).
  */
 marble_status_t marble_attn_steps_scored(const marble_plan_t *plan, const marble_qkv_t *qkv,
                                          const marble_score_t *score, int32_t n_steps,
@@ -602,7 +604,7 @@ marble_status_t marble_set_side_streams(int32_t n);
 /*
  * Give back to the device the memory the library keeps for reuse on the current device:
  * the dS^T scratch buffers that destroyed plans left for later plans, and the unused part
- * of the library's memory pool (which otherwise keeps freed blocks for later allocations).
+ * of the library's memory pools (which otherwise keep freed blocks for later allocations).
  * Memory of plans that are still alive is not touched.  Waits for the library's teardown
  * stream, so that every free queued by marble_plan_destroy has happened; queues no work on
  * any other stream.  Errors: CUDA.
