@@ -37,13 +37,13 @@ import time
 # with the digest of the kernel's source files at the time of the capture: a figure is
 # reported only while the source is unchanged, null otherwise.
 KERNEL_DRAM_BYTES_PER_LAUNCH = {
-    "k_bwd_dkdv": (468.4e6, "profiles/k_bwd_dkdv_packed_multimodal.md", "d72216ed9c132231"),
-    "k_bwd_dq": (12848.1e6, "profiles/k_bwd_dq_packed_multimodal.md", "d72216ed9c132231"),
-    "k_attn_fwd": (151.3e6, "profiles/k_attn_fwd_packed_multimodal.md", "5ac2f710191f7577"),
+    "k_bwd_dkdv": (468.8e6, "profiles/k_bwd_dkdv_packed_multimodal.md", "3f846fd1806f5510"),
+    "k_bwd_dq": (12844.4e6, "profiles/k_bwd_dq_packed_multimodal.md", "3f846fd1806f5510"),
+    "k_attn_fwd": (151.2e6, "profiles/k_attn_fwd_packed_multimodal.md", "94038e4aa05a3643"),
 }
-KERNEL_SOURCES = {"k_bwd_dkdv": ("attn_bwd.cu", "common.cuh"),
-                  "k_bwd_dq": ("attn_bwd.cu", "common.cuh"),
-                  "k_attn_fwd": ("attn_fwd.cu", "common.cuh")}
+KERNEL_SOURCES = {"k_bwd_dkdv": ("attn_bwd.cu", "common.cuh", "score.cuh"),
+                  "k_bwd_dq": ("attn_bwd.cu", "common.cuh", "score.cuh"),
+                  "k_attn_fwd": ("attn_fwd.cu", "common.cuh", "score.cuh")}
 
 
 def kernel_source_digest(kernel: str) -> str:
@@ -603,8 +603,8 @@ def run_marble(args, rank, world, local, dist):
                       "tflops": {k_: flops_fwd / (v_ / 1e3) / 1e12 for k_, v_ in merge_ms.items()}}
 
     # The fused ring beside the per-step path: every forward ring step in one launch with the
-    # state on chip between steps, then one dK/dV launch per kv shard over its ring (dK/dV on
-    # chip across q shards) with the per-step dQ GEMMs; same inputs, same FLOPs, same
+    # state on chip between steps, then one dK/dV launch over every kv block (dK/dV on chip
+    # across q shards) and one dQ GEMM over every q block; same inputs, same FLOPs, same
     # finalize and bwd_prep, device-timed over the same number of steps.
     fused = None
     if not needed:

@@ -414,18 +414,24 @@ def _rope_args(torch, pos, plan, q_weight, k_weight, first):
     return n, index
 
 
-def _rope_out(torch, like, out, names, dtype, stream):
-    """``out`` checked against the tensors it is for, or new tensors like them: those belong to
-    the stream that writes them."""
+def _rope_out(torch, like, heads, out, n, dtype, index, what, stream):
+    """(tensors, their marble_heads_t): ``out`` checked against the tensors it is for (``heads``:
+    theirs), or new tensors like them, which belong to the stream that writes them."""
     if out is None:
         if stream is not None:
             with torch.cuda.stream(stream):
-                return _rope_out(torch, like, None, names, dtype, None)
-        return tuple([None if t is None else t.new_empty(t.shape, dtype=dtype) for t in like])
+                return _rope_out(torch, like, heads, None, n, dtype, index, what, None)
+        dense = torch.contiguous_format
+        out = tuple([None if t is None else torch.empty_like(t, dtype=dtype, memory_format=dense)
+                     for t in like])
+        d, hq, hkv = heads.d, heads.hq, heads.hkv
+        return out, _Heads(*[None if t is None else t.data_ptr() for t in out],
+                           hq * d, hkv * d, hkv * d, hq, hkv, d)
     if len(out) != 3 or any((a is None) != (b is None) or (a is not None and a.shape != b.shape)
                             for a, b in zip(out, like)):
-        raise ValueError(f"out must hold one tensor of the same shape for each of {names}")
-    return tuple(out)
+        raise ValueError("out must hold one tensor of the same shape for each of "
+                         f"{what}q, {what}k and {what}v")
+    return tuple(out), _heads(out, n, dtype, index, "out " + what)
 
 
 def _raw_stream(torch, stream, index):
@@ -448,8 +454,7 @@ def rope(rope: Rope, pos, q, k=None, v=None, plan: Optional[Plan] = None, q_weig
     bf16 = torch.bfloat16
     parts = (q, k, v)
     src = _heads(parts, n, bf16, index, "")
-    out = _rope_out(torch, parts, out, "q, k and v", bf16, stream)
-    dst = _heads(out, n, bf16, index, "out ")
+    out, dst = _rope_out(torch, parts, src, out, n, bf16, index, "", stream)
     c = rope._c(pos, q_weight, None if k is None else k_weight, eps)
     _call("marble_rope", None if plan is None else plan.handle, n, ctypes.byref(c),
           ctypes.byref(src), ctypes.byref(dst), _raw_stream(torch, stream, index))
@@ -470,8 +475,7 @@ def rope_bwd(rope: Rope, pos, dq, dk=None, dv=None, plan: Optional[Plan] = None,
         k_weight = None
     parts = (dq, dk, dv)
     grad = _heads(parts, n, torch.float32, index, "d")
-    out = _rope_out(torch, parts, out, "dq, dk and dv", bf16, stream)
-    dx = _heads(out, n, bf16, index, "out d")
+    out, dx = _rope_out(torch, parts, grad, out, n, bf16, index, "d", stream)
     dwq = dwk = ws = x = None
     if q_weight is not None or k_weight is not None:
         for w, t, g, nm in ((q_weight, q, dq, "q"), (k_weight, k, dk, "k")):
@@ -715,7 +719,7 @@ def attn_fwd_fused(plan: Plan, q, k, v, state: State, scale: float = 0.0, stream
 
 def attn_bwd_fused(plan: Plan, q, k, v, do, lse, delta, dq_acc, dk_acc, dv_acc,
                    scale: float = 0.0, stream=None, score: Optional[Score] = None):
-    """Every backward ring step, one dK/dV launch per kv shard over its ring
+    """Every backward ring step, dK/dV of a kv block kept on chip over its whole ring
     (marble_attn_bwd_fused); accumulators fp32 and caller-zeroed."""
     import torch
     c = _qkv(plan, q, k, v, scale)
@@ -749,7 +753,7 @@ def backward(plan: Plan, q, k, v, o, do, lse, delta, dq_acc, dk_acc, dv_acc,
              needed: bool = False, scale: float = 0.0, stream=None, fused: bool = False,
              score: Optional[Score] = None):
     """bwd preprocessing + all backward ring steps (accumulators must be zeroed);
-    ``fused``: one dK/dV launch per kv shard over its ring (marble_attn_bwd_fused);
+    ``fused``: dK/dV of a kv block kept on chip over its whole ring (marble_attn_bwd_fused);
     ``score``: the forward's."""
     attn_bwd_prep(plan, o, do, delta, stream=stream)
     if fused:

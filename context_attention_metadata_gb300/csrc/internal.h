@@ -200,7 +200,7 @@ marble_status_t run_attn_fwd(const marble_plan_t* p, const marble_qkv_t* qkv,
                              const int* kv_shards, const uint32_t* flags, const marble_state_t* st,
                              cudaStream_t s);
 // the fused ring (attn_fwd.cu, attn_bwd.cu): every ring step of the pass in one forward
-// launch, and one dK/dV launch per kv shard over its ring
+// launch, and one dK/dV launch over every kv block (or one per kv shard) over its ring
 marble_status_t run_attn_fwd_fused(const marble_plan_t* p, const marble_qkv_t* qkv,
                                    const marble_score_t* score, const marble_state_t* st,
                                    cudaStream_t s);
