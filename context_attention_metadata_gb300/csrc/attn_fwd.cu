@@ -36,6 +36,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "score.cuh"
@@ -111,7 +113,9 @@ struct FwdParams {
   int P, bps, q_shard, kv_shard;
   int hq, group;
   int units;  // bps * hq
-  int nwork;  // units with at least one tile: nonempty blocks of the order x hq
+  int nwork;  // units with at least one tile: nonempty blocks of the order x hq (x parts)
+  int parts;  // scored kernels: pieces of every unit's list, work units of their own (1: whole)
+  long long n_out;  // their output's tokens: piece i of a row is row i * n of o_acc, m and l
   int W;
   int first;
   int lse_merge;   // 0 carried state; 1 merge of bf16 partials (standard ring); 2 of fp32 ones
@@ -142,9 +146,17 @@ __device__ __forceinline__ int unit_tiles(const FwdParams& p, int u, int64_t* e0
 // the work queue in shared memory: entry uc of this CTA sits in slot uc % kQueue
 struct Queue {
   int unit[kQueue];  // -1: no more work
+  int part[kQueue];  // scored kernels: piece of the unit's list
   int T[kQueue];
   long long e0[kQueue];
 };
+
+constexpr int kMaxParts = 8;
+
+// tiles of each piece of a list of T tiles (the last may have fewer, or there may be fewer pieces)
+__device__ __forceinline__ int part_tiles(int T, int parts) {
+  return (int)(((unsigned)T + parts - 1) / (unsigned)parts);
+}
 
 // two-slot rings indexed by the tile counter g: slot g & 1, phase parity (g >> 1) & 1
 __device__ __forceinline__ uint32_t ring_slot(int g) { return (uint32_t)(g & 1); }
@@ -285,10 +297,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         int unit = -1, T = 0;
         int64_t e0 = 0;
         // longest lists first, the q heads of a block one after the other
-        const unsigned t = atomicAdd(p.sched, 1u);
-        if (t < (unsigned)p.nwork) {
-          unit = (int)(t % (unsigned)p.hq) * p.bps + p.order[t / (unsigned)p.hq];
-          T = unit_tiles(p, unit, &e0);
+        unsigned t = atomicAdd(p.sched, 1u);
+        if constexpr (MOD == 0) {
+          if (t < (unsigned)p.nwork) {
+            unit = (int)(t % (unsigned)p.hq) * p.bps + p.order[t / (unsigned)p.hq];
+            T = unit_tiles(p, unit, &e0);
+          }
+        } else {
+          int part = 0;
+          for (; T == 0 && t < (unsigned)p.nwork; t = T == 0 ? atomicAdd(p.sched, 1u) : t) {
+            const unsigned b = t / (unsigned)p.parts;
+            part = (int)(t - b * (unsigned)p.parts);
+            unit = (int)(b % (unsigned)p.hq) * p.bps + p.order[b / (unsigned)p.hq];
+            const int all = unit_tiles(p, unit, &e0), len = part_tiles(all, p.parts);
+            T = max(0, min(len, all - part * len));  // 0: the list ends before this piece
+            e0 += part * len;
+          }
+          if (T == 0) unit = -1;
+          queue.part[slot] = part;
         }
         queue.unit[slot] = unit;
         queue.T[slot] = T;
@@ -689,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lb = (uint32_t)(quarter * 32) << 16;
-    if (p.first) {
+    if (p.first && (MOD == 0 || p.parts == 1)) {
       // rows of units without a tile in this step start from (O = 0, m = -inf, l = 0)
       for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
         int64_t e0;
@@ -727,7 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
       const int h = unit / p.bps;
       const int64_t q0 = ((int64_t)p.q_shard * p.bps + unit % p.bps) * 128;
       const int64_t tq = q0 + row;
-      const int64_t gi = (int64_t)h * n + tq;
+      const int64_t out0 = MOD == 0 ? 0 : queue.part[slot] * (int64_t)n;
+      const int64_t gi = (int64_t)h * (MOD == 0 ? n : p.n_out) + out0 + tq;
       float m_old = -INFINITY, l_old = 0.f;
       if (!p.first) {
         m_old = p.m[gi];
@@ -831,9 +858,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         if (row == 0) {
           if (mbar_wait(&bar[B_STG], k & 1, w)) {
             if (mode == 1)
-              tma_reduce_add_3d(&p.o_map, sStg, r * 32, (int)q0, h);
+              tma_reduce_add_3d(&p.o_map, sStg, r * 32, (int)(out0 + q0), h);
             else
-              tma_store_3d(&p.o_map, sStg, r * 32, (int)q0, h);
+              tma_store_3d(&p.o_map, sStg, r * 32, (int)(out0 + q0), h);
             bulk_commit();
             bulk_wait_read_all();
           }
@@ -891,7 +918,8 @@ marble_status_t prepare(const marble_plan_t* pl, const marble_qkv_t* qkv,
   prm->l = st->l;
   prm->err = pl->err;
   prm->wait_ns = wait_limit_ns();
-  prm->n = n;
+  prm->n = prm->n_out = n;
+  prm->parts = 1;
   prm->P = pl->P;
   prm->bps = (int)pl->bps;
   prm->hq = qkv->hq;
@@ -980,6 +1008,82 @@ marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv,
   return MARBLE_OK;
 }
 
+// Few and long rows: the fused forward's units are then fewer than the SMs, or the longest of them
+// sets the launch's length.  Each row's list is cut into `parts` pieces of one length, units of
+// their own that write (O, m, l) to a scratch; this kernel joins a row's pieces.  Their m are
+// integers, so that every factor is an exact power of two, and they are added in order.
+struct JoinParams {
+  const float *o, *m, *l;  // [parts * n][hq][D], [hq][parts * n] twice
+  float *o_out, *m_out, *l_out;
+  const int64_t* step_ptr;
+  long long n;
+  int P, hq, parts;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ JoinParams p) {
+  constexpr unsigned kRow4 = D / 4;
+  const unsigned x = blockIdx.x * 256 + threadIdx.x, th = x / kRow4;  // (token, head)
+  const unsigned tq = th / (unsigned)p.hq, h = th - tq * (unsigned)p.hq;
+  if (tq >= (unsigned)p.n) return;
+  const unsigned nq = tq / 128;
+  const int T = (int)(p.step_ptr[(size_t)(nq + 1) * p.P] - p.step_ptr[(size_t)nq * p.P]);
+  const int len = part_tiles(T, p.parts);
+  const size_t one = (size_t)p.n * p.hq;
+  const float4* from = reinterpret_cast<const float4*>(p.o) + x;
+  float m[kMaxParts], l[kMaxParts], top = -INFINITY;
+  float4 v[kMaxParts];
+#pragma unroll
+  for (int i = 0; i < kMaxParts; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < p.parts && i * len < T) {  // (T 0: no piece)
+      const size_t at = ((size_t)h * p.parts + i) * p.n + tq;
+      m[i] = p.m[at];
+      l[i] = p.l[at];
+      v[i] = __ldcs(from + i * one * kRow4);
+    }
+    top = fmaxf(top, m[i]);
+  }
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxParts; ++i) {
+    // a piece without a legal key has m = -inf and zeros; its factor is 0 (or 1 where all are
+    // so), not left out, so that a NaN in it stays one
+    const float f = m[i] == top ? 1.f : ldexpf(1.f, (int)fmaxf(m[i] - top, -1000.f));
+    sum = fmaf(l[i], f, sum);
+    o = make_float4(fmaf(v[i].x, f, o.x), fmaf(v[i].y, f, o.y), fmaf(v[i].z, f, o.z),
+                    fmaf(v[i].w, f, o.w));
+  }
+  reinterpret_cast<float4*>(p.o_out)[x] = o;
+  if (x % kRow4 == 0) {
+    p.m_out[(size_t)h * p.n + tq] = top;
+    p.l_out[(size_t)h * p.n + tq] = sum;
+  }
+}
+
+// The pieces of a row (1: whole rows), for scored calls: plain calls keep the order in which they
+// sum.  A tile takes a lone unit 1.2 us.  Whole rows take the longest one's time; pieces an SM's
+// share of all tiles and half a piece more, and then the join: a launch, about 5 tiles, and the
+// pieces' bytes, 4 MB a tile (at most 1 GB of them).  Causal rows, d = 128, capped, whole / in
+// pieces, with the finalize: 2048 tokens 2 heads 35 / 28 us, 4096 tokens 1 head 53 / 32, 8192
+// tokens 1 head 92 / 53, 2 heads 93 / 83, 16384 tokens 1 head 169 / 134.  Where the rule keeps
+// whole rows: 2048 tokens 4 heads 35 / 35, 4096 tokens 4 heads 55 / 57.
+int row_parts(const marble_plan_t* pl, int64_t hq, int d, int sms) {
+  int64_t longest = 0;
+  for (int r = 0; r < pl->P; ++r)
+    longest = std::max<int64_t>(longest, pl->h_step_max[(size_t)r * (pl->P + 1) + pl->P]);
+  const int64_t share = (pl->nnz * hq + sms - 1) / sms;
+  const int64_t parts = std::min<int64_t>(kMaxParts, longest / std::max<int64_t>(share, 4));
+  if (parts < 2) return 1;
+  const int64_t piece = (longest + parts - 1) / parts;
+  const int64_t saved = longest - std::max(piece, share + piece / 2);
+  const int64_t bytes = (parts + 1) * pl->n * hq * d * 4;
+  return bytes <= int64_t(1) << 30 && saved > 5 + (bytes >> 22) ? (int)parts : 1;
+}
+
 // The fused forward: one launch over every (q block, q head) of every shard, each row
 // walking its tiles in ring order (kv shard (r - s) mod P at step s, the plan's ring-ordered
 // copy of its lists) with the fp32 state held on chip from the first step to the last; the
@@ -1006,11 +1110,41 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
   prm.units = (int)(pl->nb * qkv->hq);
   prm.nwork = pl->h_nwork_all[0] * qkv->hq;
   prm.sched = sched_slot(pl);
+  void* pieces = nullptr;
+  if constexpr (MOD != 0) {
+    const int parts = row_parts(pl, qkv->hq, D, sms);
+    const int64_t rows = parts * pl->n * qkv->hq;
+    if (parts > 1 && dev_alloc(&pieces, rows * (D + 2) * sizeof(float), s, true) != cudaSuccess) {
+      (void)cudaGetLastError();  // no room for pieces: whole rows
+      pieces = nullptr;
+    }
+    if (pieces) {
+      prm.parts = parts;
+      prm.n_out = parts * pl->n;
+      prm.nwork *= parts;
+      prm.units *= parts;
+      prm.o_acc = static_cast<float*>(pieces);
+      prm.m = prm.o_acc + rows * D;
+      prm.l = prm.m + rows;
+      if (!make_rows_map(&prm.o_map, prm.o_acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, prm.n_out,
+                         qkv->hq, D, 32, 128, CU_TENSOR_MAP_SWIZZLE_128B)) {
+        dev_free(pieces, s);
+        return fail(MARBLE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the rows' pieces");
+      }
+    }
+  }
   const unsigned grid = (unsigned)(prm.units < sms ? prm.units : sms);
   const int span = timing_begin(s);
   k_attn_fwd<D, MOD><<<grid, kThreads, Smem<D>::bytes(), s>>>(prm);
-  timing_end(span, s, kTimeFwd, 1);
+  if (pieces) {
+    const JoinParams j{prm.o_acc, prm.m, prm.l, st->o_acc, st->m, st->l, pl->step_ptr, pl->n,
+                       pl->P, qkv->hq, prm.parts};
+    const int64_t n4 = pl->n * qkv->hq * (D / 4);
+    k_attn_join<D><<<(unsigned)((n4 + 255) / 256), 256, 0, s>>>(j);
+  }
+  timing_end(span, s, kTimeFwd, pieces ? 2 : 1);
   cudaError_t e = cudaGetLastError();
+  if (pieces) dev_free(pieces, s);
   if (e != cudaSuccess) return cuda_fail(e, "launch k_attn_fwd (fused)");
   return MARBLE_OK;
 }

@@ -136,6 +136,62 @@ def test_rows_without_a_key(d):
         _check(got, q, k, v, do, m, 3.0, slopes)
 
 
+# Long rows on few heads, which the fused forward cuts into pieces: one long sample; an odd number
+# of blocks; short samples, whose rows have fewer tiles than there are pieces, beside a long one;
+# rows that see no key (window 0) beside a long bidirectional span
+LONG = [
+    ([[wl.Span("causal", 2048)]], INF, 4, 2, 1, 64, 2.0, "usual"),
+    ([[wl.Span("causal", 2944)]], INF, 1, 1, 1, 128, 0.0, "steep"),
+    ([[wl.Span("causal", 1900)]] + [[wl.Span("causal", 55), wl.Span("full", 45)]] * 6 +
+     [[wl.Span("noise", 60)]], INF, 4, 2, 2, 64, 30.0, None),
+    ([[wl.Span("causal", 300), wl.Span("full", 1700)], [wl.Span("causal", 48)]], 0, 2, 2, 1, 128, 3.0,
+     "signed"),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_rows_in_pieces(case):
+    samples, W, P, hq, hkv, d, cap, kind = LONG[case]
+    tr = wl.tracks_from_samples(samples)
+    pad = -len(tr["sample"]) % (128 * P)
+    if pad:
+        tr = wl.tracks_from_samples(samples + [[wl.Span("causal", pad)]])
+    n = len(tr["sample"])
+    q, k, v, do = _qkvdo(n, hq, hkv, d, 60 + case)
+    slopes = _slopes(hq, kind)
+    pl = M.Plan(*device_tracks(tr), W, P, "ptrr_block")
+    score = M.Score(cap, slopes)
+    M.timing_enable(True)
+    M.timing_read()
+    got = _run(pl, q, k, v, do, score, fused=True)
+    launches = M.timing_read()["fwd_launches"]
+    M.timing_enable(False)
+    assert launches == 2  # the pieces and their join
+    _check(got, q, k, v, do, mask.dense_mask(tr, W), cap, slopes)
+    again = _run(pl, q, k, v, do, score, fused=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_pieces_keep_nan_and_infinity():
+    """A key's NaN or infinite value reaches the rows that see it, and no row of an earlier block
+    (a masked key's weight is a zero of the product)."""
+    n = 2048
+    tr = wl.tracks_from_samples([[wl.Span("causal", n)]])
+    q, k, v, _ = _qkvdo(n, 1, 1, 64, 70)
+    pl = M.Plan(*device_tracks(tr), INF, 1)
+    for key, bad in ((700, float("nan")), (5, float("inf")), (1500, float("-inf"))):
+        x = v.clone()
+        x[key, 0, 3] = bad
+        st, o, lse = M.State(n, 1, 64), torch.empty_like(q), torch.empty((1, n), device="cuda")
+        M.forward(pl, q, k, x, st, o, lse, fused=True, score=M.Score(5.0))
+        pl.check()
+        assert torch.isfinite(lse).all()
+        hit = ~torch.isfinite(o[:, 0])
+        assert hit[key:, 3].all() and not hit[: key // 128 * 128].any()
+        hit[:, 3] = False
+        assert not hit.any()
+
+
 @pytest.mark.parametrize("kind", ["usual", "signed"])
 def test_position_track(kind):
     """A permuted pack: distances come from the position track."""
