@@ -551,10 +551,12 @@ typedef struct {
  * marble_attn_steps, marble_attn_fwd_fused, marble_attn_bwd_steps and marble_attn_bwd_fused with
  * changed scores: the same arguments, results and errors, a list of one step being the single
  * step.  The same `score` has to be given to every call of a pass, forward and backward.  score
- * NULL, or with neither cap nor slopes, is the plain call.  The fused backward of a small pack
- * with grouped heads takes 8 * N * hq * d bytes of the library's pool for its length.  The
- * launches take ticket counters and scratch of the plan: a stream that is being captured into a
- * graph is refused (INVALID_ARG).
+ * NULL, or with neither cap nor slopes, is the plain call.  The fused forward of few and long
+ * rows works on up to 8 pieces of each at once and joins them (sums in another order than the
+ * plain call's); their states, 4 * pieces * N * hq * (d + 2) bytes and at most about 1 GB, are in
+ * the library's pool for the call's length.  The fused backward of a small pack with grouped heads
+ * takes 8 * N * hq * d bytes there.  The launches take ticket counters and scratch of the plan: a
+ * stream that is being captured into a graph is refused (INVALID_ARG).
  */
 marble_status_t marble_attn_steps_scored(const marble_plan_t *plan, const marble_qkv_t *qkv,
                                          const marble_score_t *score, int32_t n_steps,
