@@ -740,7 +740,7 @@ bool rows_meet(const Rows& a, const Rows& b, int64_t n) {
 }
 
 // the present tensors of `h` (q, k, v as bit 0, 1, 2 of `parts`) as rows of elem-byte elements
-marble_status_t check_heads(const marble_heads_t* h, const char* name, int elem, int parts,
+marble_status_t check_heads(const marble_heads_t* h, const char* name, int elem, int parts, int64_t n,
                             Rows (&out)[3]) {
   const void* ptr[3] = {h->q, h->k, h->v};
   const int64_t stride[3] = {h->q_stride, h->k_stride, h->v_stride};
@@ -751,7 +751,8 @@ marble_status_t check_heads(const marble_heads_t* h, const char* name, int elem,
     marble_status_t st = check_here(ptr[i], what.c_str(), 16);
     if (st != MARBLE_OK) return st;
     const int64_t width = (int64_t)(i == 0 ? h->hq : h->hkv) * h->d;
-    if (stride[i] < width || stride[i] * elem % 16 || stride[i] > ((int64_t)1 << 40))
+    // (n rows within 2^60 bytes: products of n and a stride do not overflow)
+    if (stride[i] < width || stride[i] > ((int64_t)1 << 58) / n || stride[i] * elem % 16)
       return fail(MARBLE_ERR_INVALID_ARG,
                   what + ": the stride must hold the token's heads and be a multiple of 16 bytes");
     out[i] = Rows{static_cast<const char*>(ptr[i]), stride[i] * elem, width * elem};
@@ -833,8 +834,8 @@ MARBLE_API marble_status_t marble_rope(const marble_plan_t* p, int64_t n, const 
   if (st != MARBLE_OK || n == 0 || parts == 0) return st;
   if ((st = check_rope_tensors(rope)) != MARBLE_OK) return st;
   Rows a[3], b[3];
-  if ((st = check_heads(src, "src", 2, parts, a)) != MARBLE_OK) return st;
-  if ((st = check_heads(dst, "dst", 2, parts, b)) != MARBLE_OK) return st;
+  if ((st = check_heads(src, "src", 2, parts, n, a)) != MARBLE_OK) return st;
+  if ((st = check_heads(dst, "dst", 2, parts, n, b)) != MARBLE_OK) return st;
   if ((st = check_overlap(b, a, parts, parts, !p, "src and dst overlap", n)) != MARBLE_OK) return st;
   bool cap = false;
   if ((st = capturing((cudaStream_t)stream, &cap)) != MARBLE_OK) return st;
@@ -865,8 +866,8 @@ MARBLE_API marble_status_t marble_rope_bwd(const marble_plan_t* p, int64_t n,
   Rows g[3], b[3], xr[3];
   if (n > 0) {
     if ((st = check_rope_tensors(&r)) != MARBLE_OK) return st;
-    if ((st = check_heads(grad, "grad", 4, parts, g)) != MARBLE_OK) return st;
-    if ((st = check_heads(dx, "dx", 2, parts, b)) != MARBLE_OK) return st;
+    if ((st = check_heads(grad, "grad", 4, parts, n, g)) != MARBLE_OK) return st;
+    if ((st = check_heads(dx, "dx", 2, parts, n, b)) != MARBLE_OK) return st;
     if ((st = check_overlap(b, g, parts, parts, false, "grad and dx overlap", n)) != MARBLE_OK)
       return st;
   }
@@ -876,7 +877,7 @@ MARBLE_API marble_status_t marble_rope_bwd(const marble_plan_t* p, int64_t n,
       if (x->d != grad->d || ((normed & 1) && x->hq != grad->hq) ||
           ((normed & 2) && x->hkv != grad->hkv))
         return fail(MARBLE_ERR_INVALID_ARG, "the heads of x and grad differ");
-      if ((st = check_heads(x, "x", 2, normed, xr)) != MARBLE_OK) return st;
+      if ((st = check_heads(x, "x", 2, normed, n, xr)) != MARBLE_OK) return st;
       if ((st = check_overlap(b, xr, parts, normed, true, "x and dx overlap", n)) != MARBLE_OK)
         return st;
     }

@@ -396,3 +396,15 @@ def test_refusals_on_the_gpu():
     with pytest.raises(M.MarbleError, match="aligned"):
         M.rope(rope, pos, odd[4:4 + n * hq * d].view(n, hq, d))
     assert ctypes.sizeof(M._Heads) == 64
+
+
+def test_rows_beyond_any_memory_are_refused():
+    """2^30 tokens 2^39 elements apart: more bytes than an address has, refused before any launch."""
+    q = torch.empty((2, 1, 64), dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    rope = M.Rope(*M.rope_frequencies((32,)))
+    c = rope._c(pos, None, None, 1e-6)
+    far = M._Heads(q.data_ptr(), None, None, 1 << 39, 0, 0, 1, 0, 64)
+    with pytest.raises(M.MarbleError, match="stride"):
+        M._call("marble_rope", None, 1 << 30, ctypes.byref(c), ctypes.byref(far),
+                ctypes.byref(far), M._stream(None))
