@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
                   if constexpr ((MOD & kScoreCap) == 0) {
                     s = fma2(f2(x0, x1), f2(sl2), bias);
                   } else {
-                    const F2 c = cap_poly<6>(f2(x0, x1), p.score);
+                    const F2 x = f2(x0, x1), c = mul2(x, cap_factor<6>(x, p.score));
                     split(fma2(mul2(c, c), f2(p.score.neg_inv_cap2_sq), f2(1.f)), &wv[u], &wv[u + 1]);
                     s = add2(c, bias);
                   }
@@ -1631,17 +1631,19 @@ marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv,
 
 // dst[t, kh, :] += the sum over the q heads of kv head kh of src[t, q head, :], in head order
 // (row4: float4 of a head)
-__global__ void k_group_sum(const float4* __restrict__ src, float4* __restrict__ dst, int64_t n4,
-                            int row4, int group) {
-  for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < n4;
+__global__ void k_group_sum(const float4* __restrict__ src, float4* __restrict__ dk,
+                            float4* __restrict__ dv, int64_t n4, int row4, int group) {
+  for (int64_t x = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; x < 2 * n4;
        x += (int64_t)gridDim.x * blockDim.x) {
+    // src: dK of every q head, then dV; both n4 * group long
     const float4* from = src + x / row4 * group * row4 + x % row4;
-    float4 v = dst[x];
+    float4* to = x < n4 ? dk + x : dv + (x - n4);
+    float4 v = *to;
     for (int g = 0; g < group; ++g) {
       const float4 a = from[g * row4];
       v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
     }
-    dst[x] = v;
+    *to = v;
   }
 }
 
@@ -1683,10 +1685,9 @@ struct GroupScratch {
   void add_up(float* dk, float* dv, cudaStream_t s) const {
     if (!mem) return;
     const int64_t n4 = n * (hq / group) * d / 4;
-    const unsigned grid = (unsigned)std::min<int64_t>((n4 + 255) / 256, 4096);
-    const float4* src = reinterpret_cast<const float4*>(mem);
-    k_group_sum<<<grid, 256, 0, s>>>(src, reinterpret_cast<float4*>(dk), n4, d / 4, group);
-    k_group_sum<<<grid, 256, 0, s>>>(src + (size_t)n * hq * d / 4, reinterpret_cast<float4*>(dv),
+    const unsigned grid = (unsigned)std::min<int64_t>((2 * n4 + 255) / 256, 4096);
+    k_group_sum<<<grid, 256, 0, s>>>(reinterpret_cast<const float4*>(mem),
+                                     reinterpret_cast<float4*>(dk), reinterpret_cast<float4*>(dv),
                                      n4, d / 4, group);
   }
 

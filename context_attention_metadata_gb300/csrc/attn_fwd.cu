@@ -203,16 +203,17 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
 #pragma unroll
     for (int t = 0; t < 64; t += 2) {
       const F2 x = f2(__uint_as_float(v[t >> 5][t & 31]), __uint_as_float(v[t >> 5][(t & 31) + 1]));
-      F2 s;
+      F2 factor, s;
       if constexpr ((MOD & kScoreCap) == 0)
-        s = fma2(x, f2(sl2), f2(own));
+        factor = f2(sl2);
       else
-        s = cap_poly<decltype(terms)::value>(x, p.score);
+        factor = cap_factor<decltype(terms)::value>(x, p.score);
       if constexpr ((MOD & kScoreBias) != 0) {
-        // whole numbers counted up, so that the column's part is rounded once
-        if constexpr ((MOD & kScoreCap) != 0) s = add2(s, f2(own));
-        s = fma2(at[(t >> 1) & 1], f2(step), s);
+        // whole numbers counted up, so that the bias is rounded once
+        s = fma2(x, factor, fma2(at[(t >> 1) & 1], f2(step), f2(own)));
         at[(t >> 1) & 1] = add2(at[(t >> 1) & 1], f2(4.f));
+      } else {
+        s = mul2(x, factor);
       }
       float s0, s1;
       split(s, &s0, &s1);

@@ -16,13 +16,12 @@
 //   otherwise 1 - 2 / (1 + e^(2 y)): two calls to the special function unit, which also has the
 //     softmax's exp2 to do, and an absolute error of 2^-22 c (the score's own rounding is of
 //     that size, some |score| being above 0.875 c).
-// The special function unit is what these two spare: it gives 16 results a clock on an SM, half
-// the rate of everything else here, and the softmax's exp2 takes one a score.  A
-// forward over 64K packed tokens (16 heads of 128) takes 1659 us without a cap, 2011 with nearly
-// every tile within the four-term range (cap 50), 2187 within the six-term one (cap 18), 2782
-// where most tiles go through the exponential (cap 5); the dK/dV kernel 3046, 3645, 3659 and
-// 4287 us.  A polynomial in y
-// instead of x needs one multiplication more a score: 3 to 9% slower.
+// The special function unit is what these two spare: it gives 16 results a clock on an SM, where
+// multiply-adds have 128, and the softmax's exp2 takes one a score.  A forward over 64K packed
+// tokens (16 heads of 128) takes 1669 us without a cap, 2005 with nearly every tile within the
+// four-term range (cap 50), 2209 within the six-term one (cap 18), 2782 where most tiles go
+// through the exponential (cap 5); the dK/dV kernel 3046, 3645, 3659 and 4287 us.  A polynomial in
+// y instead of x needs one multiplication more a score: 3 to 9% slower.
 // Folded coefficients leave fp32's range for caps far from the scores' size; set_cap then lowers
 // the first two ways' limits to where the lost terms do not matter.
 #pragma once
@@ -135,23 +134,23 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
-// x (c[0] + c[1] x^2 + ...) of a pair
+// c[0] + c[1] x^2 + ... of a pair
 template <int kTerms>
-__device__ __forceinline__ F2 odd_poly(F2 x, const float (&c)[kTerms]) {
+__device__ __forceinline__ F2 even_poly(F2 x, const float (&c)[kTerms]) {
   const F2 u = mul2(x, x);
   F2 r = f2(c[kTerms - 1]);
 #pragma unroll
   for (int i = kTerms - 2; i >= 0; --i) r = fma2(r, u, f2(c[i]));
-  return mul2(x, r);
+  return r;
 }
 
-// capped scores of a pair: six terms, |x| <= lim, or four, |x| <= lim_n
+// a pair's capped scores over its products: six terms, |x| <= lim, or four, |x| <= lim_n
 template <int kTerms>
-__device__ __forceinline__ F2 cap_poly(F2 x, const ScoreParams& p) {
+__device__ __forceinline__ F2 cap_factor(F2 x, const ScoreParams& p) {
   if constexpr (kTerms == 4)
-    return odd_poly(x, p.cn);
+    return even_poly(x, p.cn);
   else
-    return odd_poly(x, p.c);
+    return even_poly(x, p.c);
 }
 
 // 1 / (1 + e^(2 y)): the capped score is cap2 (1 - 2 r), its slope's factor 4 r (1 - r)

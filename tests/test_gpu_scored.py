@@ -172,6 +172,32 @@ def test_rows_in_pieces(case):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+def test_pieces_of_two_streams_at_once():
+    """Two forwards of one plan on two streams, over and over: each has pieces of its own."""
+    n = 2048
+    tr = wl.tracks_from_samples([[wl.Span("causal", n)]])
+    pl = M.Plan(*device_tracks(tr), INF, 1)
+    runs = []
+    for seed in (71, 72):
+        q, k, v, _ = _qkvdo(n, 2, 1, 64, seed)
+        runs.append((q, k, v, M.State(n, 2, 64), torch.empty_like(q),
+                     torch.empty((2, n), device="cuda"), torch.cuda.Stream()))
+    score = M.Score(5.0)
+    want = []
+    for q, k, v, st, o, lse, _ in runs:
+        M.forward(pl, q, k, v, st, o, lse, fused=True, score=score)
+        want.append((o.clone(), lse.clone()))
+        o.zero_(), lse.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for q, k, v, st, o, lse, stream in runs:
+            M.forward(pl, q, k, v, st, o, lse, fused=True, score=score, stream=stream)
+    torch.cuda.synchronize()
+    pl.check()
+    for (q, k, v, st, o, lse, _), (a, b) in zip(runs, want):
+        assert torch.equal(o, a) and torch.equal(lse, b)
+
+
 def test_pieces_keep_nan_and_infinity():
     """A key's NaN or infinite value reaches the rows that see it, and no row of an earlier block
     (a masked key's weight is a zero of the product)."""
