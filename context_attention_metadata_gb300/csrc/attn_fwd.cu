@@ -180,7 +180,8 @@ struct Smem {
 };
 static_assert(Smem<128>::bytes() <= 232448, "shared memory budget");
 
-// A row's 64 products of this half, in place, to base-2 scores with the cap and the bias.
+// A row's 64 products of this half, in place, to base-2 scores with the cap and the bias (less
+// kFixedMax where that is the stabiliser).
 // side: +1 or -1 where the tile's keys all come before (after) its queries and positions are
 // consecutive, so that the bias is linear in the key; 0 otherwise.  far0: the row's distance to
 // the half's first key; pos: the keys' positions.
@@ -212,6 +213,8 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
         // whole numbers counted up, so that the bias is rounded once
         s = fma2(x, factor, fma2(at[(t >> 1) & 1], f2(step), f2(own)));
         at[(t >> 1) & 1] = add2(at[(t >> 1) & 1], f2(4.f));
+      } else if constexpr ((MOD & kScoreFixed) != 0) {
+        s = fma2(x, factor, f2(-kFixedMax));
       } else {
         s = mul2(x, factor);
       }
@@ -239,7 +242,9 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
           bias = -slope * fabsf((float)(pq - (u == 0 ? k4.x : u == 1 ? k4.y : u == 2 ? k4.z : k4.w)));
         const float s = (MOD & kScoreCap) == 0
                             ? fmaf(x, sl2, bias)
-                            : fmaf(-2.f * p.score.cap2, cap_rcp(x, p.score), p.score.cap2) + bias;
+                            : fmaf(-2.f * p.score.cap2, cap_rcp(x, p.score),
+                                   (MOD & kScoreFixed) == 0 ? p.score.cap2
+                                                            : p.score.cap2 - kFixedMax) + bias;
         v[t >> 5][(t & 31) + u] = __float_as_uint(s);
       }
     }
@@ -611,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         // this half's row maximum of the scaled, masked scores; where a key is masked the
         // scaled scores (-inf where masked) replace v, otherwise v keeps the raw scores
         // (scaling by a positive constant commutes with the maximum, and P takes one FMA below)
-        float mx = -INFINITY;
+        [[maybe_unused]] float mx = -INFINITY;
         if constexpr (MOD != 0) {
           score_row<MOD>(v, p, sl2, slope, side, far0, pq, kpos);
           if constexpr ((MOD & kScoreBias) != 0) k0_n = p.tracks[3 * n + (int64_t)kb_n * 128];
@@ -622,6 +627,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
               for (int t = 0; t < 32; ++t)
                 if (!((lm[cc] >> t) & 1u)) v[cc][t] = __float_as_uint(-INFINITY);
           }
+        }
+        if constexpr ((MOD & kScoreFixed) != 0) {
+          m_run = kFixedMax;
+        } else if constexpr (MOD != 0) {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int t = 0; t < 64; ++t) m4[t & 3] = fmaxf(m4[t & 3], __uint_as_float(v[t >> 5][t & 31]));
@@ -643,52 +652,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
             for (int t = 0; t < 32; ++t) mx = fmaxf(mx, __uint_as_float(v[cc][t]));
           mx *= sl2;
         }
-        float* mxb = mxs + b * 256;
-        mxb[half * 128 + row] = mx;
-        mbar_arrive(&bar[B_MX0 + b]);
-        if (!wait_all(&bar[B_MX0 + b], (g >> 1) & 1, w)) { ok = false; break; }
-        mx = fmaxf(mx, mxb[(1 - half) * 128 + row]);
-        // the running max is kept integral (base 2): every rescale factor below is then an
-        // exact power of two, and bf16 rounding of P does not depend on which keys a step
-        // happened to see first
-        const float m_new = ceilf(mx);
-        const bool grow = m_new > m_run + kRescaleThreshold;
-        const bool need = grow && (m_run != -INFINITY);  // earlier tiles of this unit to rescale
-        const float alpha = need ? ldexpf(1.f, (int)(m_run - m_new)) : 1.f;
-        if (grow) {
-          l_h *= alpha;
-          m_run = m_new;
-        }
-        // tcgen05.ld/st are warp-collective: the whole warp rescales when any of its rows
-        // must (alpha = 1 on the others).  A row that needs it has a finite max from an
-        // earlier tile of this unit, so PV(g-1) is the accumulation to wait for.
-        if (__any_sync(0xffffffffu, need)) {
-          if (!wait_all(&bar[B_PVDONE], (g - 1) & 1, w)) { ok = false; break; }
-          tc_fence_after();
+        if constexpr ((MOD & kScoreFixed) == 0) {
+          float* mxb = mxs + b * 256;
+          mxb[half * 128 + row] = mx;
+          mbar_arrive(&bar[B_MX0 + b]);
+          if (!wait_all(&bar[B_MX0 + b], (g >> 1) & 1, w)) { ok = false; break; }
+          mx = fmaxf(mx, mxb[(1 - half) * 128 + row]);
+          // the running max is kept integral (base 2): every rescale factor below is then an
+          // exact power of two, and bf16 rounding of P does not depend on which keys a step
+          // happened to see first
+          const float m_new = ceilf(mx);
+          const bool grow = m_new > m_run + kRescaleThreshold;
+          const bool need = grow && (m_run != -INFINITY);  // earlier tiles of this unit to rescale
+          const float alpha = need ? ldexpf(1.f, (int)(m_run - m_new)) : 1.f;
+          if (grow) {
+            l_h *= alpha;
+            m_run = m_new;
+          }
+          // tcgen05.ld/st are warp-collective: the whole warp rescales when any of its rows
+          // must (alpha = 1 on the others).  A row that needs it has a finite max from an
+          // earlier tile of this unit, so PV(g-1) is the accumulation to wait for.
+          if (__any_sync(0xffffffffu, need)) {
+            if (!wait_all(&bar[B_PVDONE], (g - 1) & 1, w)) { ok = false; break; }
+            tc_fence_after();
 #pragma unroll 1
-          for (int cc = 0; cc < D / 64; ++cc) {
-            const uint32_t col = half * (D / 2) + cc * 32;
-            uint32_t x[32];
-            tmem_ld32(ob + lb + col, x);
-            tmem_ld_wait();
+            for (int cc = 0; cc < D / 64; ++cc) {
+              const uint32_t col = half * (D / 2) + cc * 32;
+              uint32_t x[32];
+              tmem_ld32(ob + lb + col, x);
+              tmem_ld_wait();
 #pragma unroll
-            for (int t = 0; t < 32; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * alpha);
-            tmem_st32(ob + lb + col, x);
+              for (int t = 0; t < 32; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * alpha);
+              tmem_st32(ob + lb + col, x);
+            }
           }
         }
         // P = exp2(s - m_run) as bf16, packed into columns [64 half, 64 half + 32) of the S
         // buffer: inside the fp32 columns this warp has just read
-        const float base = (m_run == -INFINITY) ? 0.f : m_run;
+        [[maybe_unused]] const float base = (m_run == -INFINITY) ? 0.f : m_run;
         // v holds scaled scores where keys were masked, raw ones otherwise
-        const float vs = (MOD != 0 || masked) ? 1.f : sl2;
+        [[maybe_unused]] const float vs = (MOD != 0 || masked) ? 1.f : sl2;
+        auto weight = [&](uint32_t x) {
+          const float s = __uint_as_float(x);
+          return fast_exp2((MOD & kScoreFixed) != 0 ? s : fmaf(s, vs, -base));
+        };
         float rs = 0.f;
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           uint32_t pk[16];
 #pragma unroll
           for (int t = 0; t < 32; t += 2) {
-            const float p0 = fast_exp2(fmaf(__uint_as_float(v[cc][t]), vs, -base));
-            const float p1 = fast_exp2(fmaf(__uint_as_float(v[cc][t + 1]), vs, -base));
+            const float p0 = weight(v[cc][t]), p1 = weight(v[cc][t + 1]);
             rs += p0 + p1;
             pk[t >> 1] = pack_bf16(p0, p1);
           }
@@ -763,8 +777,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
       }
       const int ub = uc & 1;
       if (!wait_all(&bar[B_EPIRDY0 + ub], (uc >> 1) & 1, w)) break;
-      const float m_run = hm[ub * 128 + row];
+      float m_run = hm[ub * 128 + row];
       const float l_run = hl[ub * 256 + row] + hl[ub * 256 + 128 + row];
+      // (rows without a legal key have no maximum)
+      if ((MOD & kScoreFixed) != 0 && l_run == 0.f) m_run = -INFINITY;
       mbar_arrive(&bar[B_HFREE0 + ub]);
       // the merge mode is one per unit: the four warps vote
       const bool grows = !p.first && m_old != -INFINITY && m_run > m_old + kRescaleThreshold;
@@ -1150,6 +1166,19 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
   return MARBLE_OK;
 }
 
+// f(d, mod) with the forward's variant of the score
+template <class F>
+marble_status_t with_fwd_variant(int d, const marble_score_t* score, F f) {
+  const int bits = score_bits(score);
+  return with_variant(d, bits, [&](auto dd, auto mod) {
+    if constexpr (mod() == kScoreCap) {
+      if (score->cap * 1.4426950408889634f <= kFixedCap)
+        return f(dd, std::integral_constant<int, kScoreCap | kScoreFixed>{});
+    }
+    return f(dd, mod);
+  });
+}
+
 }  // namespace
 
 marble_status_t run_attn_fwd_fused(const marble_plan_t* p, const marble_qkv_t* qkv,
@@ -1157,7 +1186,7 @@ marble_status_t run_attn_fwd_fused(const marble_plan_t* p, const marble_qkv_t* q
                                    cudaStream_t s) {
   if ((int64_t)p->nb * qkv->hq > INT_MAX)
     return fail(MARBLE_ERR_UNSUPPORTED, "too many (block, head) work units");
-  return with_variant(qkv->d, score_bits(score), [&](auto d, auto mod) {
+  return with_fwd_variant(qkv->d, score, [&](auto d, auto mod) {
     return launch_fused<d(), mod()>(p, qkv, score, st, s);
   });
 }
@@ -1166,7 +1195,7 @@ marble_status_t run_attn_fwd(const marble_plan_t* p, const marble_qkv_t* qkv,
                              const marble_score_t* score, int n_steps, const int* q_shards,
                              const int* kv_shards, const uint32_t* flags, const marble_state_t* st,
                              cudaStream_t s) {
-  return with_variant(qkv->d, score_bits(score), [&](auto d, auto mod) {
+  return with_fwd_variant(qkv->d, score, [&](auto d, auto mod) {
     return launch_steps<d(), mod()>(p, qkv, score, n_steps, q_shards, kv_shards, flags, st, s);
   });
 }

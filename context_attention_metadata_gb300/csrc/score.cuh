@@ -18,8 +18,8 @@
 //     that size, some |score| being above 0.875 c).
 // The special function unit is what these two spare: it gives 16 results a clock on an SM, where
 // multiply-adds have 128, and the softmax's exp2 takes one a score.  A forward over 64K packed
-// tokens (16 heads of 128) takes 1669 us without a cap, 2005 with nearly every tile within the
-// four-term range (cap 50), 2209 within the six-term one (cap 18), 2782 where most tiles go
+// tokens (16 heads of 128) takes 1669 us without a cap, 1670 with nearly every tile within the
+// four-term range (cap 50), 1855 within the six-term one (cap 18), 2407 where most tiles go
 // through the exponential (cap 5); the dK/dV kernel 3046, 3645, 3659 and 4287 us.  A polynomial in
 // y instead of x needs one multiplication more a score: 3 to 9% slower.
 // Folded coefficients leave fp32's range for caps far from the scores' size; set_cap then lowers
@@ -36,7 +36,16 @@
 
 namespace marble {
 
-enum : int { kScoreCap = 1, kScoreBias = 2 };  // bits of a kernel's score variant
+// bits of a kernel's score variant; kScoreFixed (forward, with a cap alone): see kFixedMax
+enum : int { kScoreCap = 1, kScoreBias = 2, kScoreFixed = 4 };
+
+// A capped score without a bias lies in [-cap2, cap2], so the softmax needs no running maximum:
+// where cap2 is at most kFixedCap, every row's stabiliser is kFixedMax.  A row's largest weight is
+// then 2^(-80 - 16) at least, and 2^(80 - 16) at most: sums over 2^20 keys of values up to 2^43
+// stay finite, and outputs keep 8 bits down to values of 2^-22 in a row whose scores all are -cap.
+// Saved are the maximum, its exchange between the two warps of a row and the rescaling (forward of
+// 64K packed tokens, 16 heads of 128: cap 50 2000 -> 1670 us, cap 18 2190 -> 1855).
+constexpr float kFixedCap = 80.f, kFixedMax = 16.f;
 
 struct ScoreParams {
   float c[6];             // s = x (c[0] + c[1] x^2 + ... + c[5] x^10) for |x| <= lim

@@ -297,6 +297,34 @@ def test_large_products_under_large_caps(cap):
         assert (err <= lim + 1e-6 * scale).all(), (name, (err - lim).max())
 
 
+@pytest.mark.parametrize("cap", [3.0, 50.0, 55.0, 60.0])
+@pytest.mark.parametrize("size", [1e-4, 1.0, 1e6])
+def test_saturated_scores(cap, size):
+    """Rows whose scores all are near -cap, rows near +cap and rows with both, small and large
+    values: caps on both sides of where the forward does without a running maximum (cap log2 e
+    of 80)."""
+    n, d = 512, 64
+    tr = wl.tracks_from_samples([[wl.Span("causal", 300), wl.Span("full", 212)]])
+    q, k, v, do = _qkvdo(n, 2, 1, d, 9)
+    # scores of 4 caps in size: channel 0 of the keys has signs by thirds
+    k[..., 0] = 8.0
+    k[150:300, :, 0] = -8.0
+    q[..., 0] = 4 * cap / 8 * (-1) ** (torch.arange(n, device="cuda") // 7)[:, None]
+    v *= size
+    pl = M.Plan(*device_tracks(tr), INF, 2)
+    m = mask.dense_mask(tr, INF)
+    st, o, lse = M.State(n, 2, d), torch.empty_like(q), torch.empty((2, n), device="cuda")
+    ref = scored.attention(q, k, v, m, cap, scale=1.0, do=do, h=HALF)
+    for fused in (False, True):
+        M.forward(pl, q, k, v, st, o, lse, fused=fused, scale=1.0, score=M.Score(cap))
+        pl.check()
+        # a score of up to 80 log2 e is off by its roundings, 2^-20 of the cap in all
+        off = 2.0 ** -20 * cap
+        assert (np.abs(_np(lse) - ref["LSE"]) <= off + 2.0 ** -18).all()
+        lim = (1 + HALF) * ((1 + 2 * off / HALF) * ref["bound"]["O"] + HALF * np.abs(ref["O"]))
+        assert (np.abs(_np(o) - ref["O"]) <= lim + 1e-30).all()
+
+
 def test_both_ways_to_tanh_in_one_pack():
     """Rows with small and rows with large scores, tile by tile, around the border of 0.75."""
     n = 1024
