@@ -180,15 +180,15 @@ struct Smem {
 };
 static_assert(Smem<128>::bytes() <= 232448, "shared memory budget");
 
-// A row's 64 products of this half, in place, to base-2 scores with the cap and the bias (less
-// kFixedMax where that is the stabiliser).
+// A row's 64 products of this half, in place, to base-2 scores with the cap and the bias, less
+// `fixed`: kFixedMax where that is the stabiliser, or 0 (a cap always has the one or the other).
 // side: +1 or -1 where the tile's keys all come before (after) its queries and positions are
 // consecutive, so that the bias is linear in the key; 0 otherwise.  far0: the row's distance to
 // the half's first key; pos: the keys' positions.
 template <int MOD>
 __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams& p, float sl2,
                                           float slope, float side, float far0, int pq,
-                                          const int32_t* __restrict__ pos) {
+                                          const int32_t* __restrict__ pos, float fixed) {
   float top = 0.f;
   if constexpr ((MOD & kScoreCap) != 0) {
     float hi[4] = {0.f, 0.f, 0.f, 0.f};
@@ -198,7 +198,7 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
     top = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
   }
   // key t of the half is at side (far0 - t): the bias is own + t * step
-  const float own = -side * slope * far0, step = side * slope;
+  const float own = fmaf(-side * slope, far0, -fixed), step = side * slope;
   auto pairs = [&](auto terms) {
     [[maybe_unused]] F2 at[2] = {f2(0.f, 1.f), f2(2.f, 3.f)};
 #pragma unroll
@@ -214,7 +214,7 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
         s = fma2(x, factor, fma2(at[(t >> 1) & 1], f2(step), f2(own)));
         at[(t >> 1) & 1] = add2(at[(t >> 1) & 1], f2(4.f));
       } else if constexpr ((MOD & kScoreFixed) != 0) {
-        s = fma2(x, factor, f2(-kFixedMax));
+        s = fma2(x, factor, f2(-fixed));
       } else {
         s = mul2(x, factor);
       }
@@ -243,8 +243,7 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
         const float s = (MOD & kScoreCap) == 0
                             ? fmaf(x, sl2, bias)
                             : fmaf(-2.f * p.score.cap2, cap_rcp(x, p.score),
-                                   (MOD & kScoreFixed) == 0 ? p.score.cap2
-                                                            : p.score.cap2 - kFixedMax) + bias;
+                                   p.score.cap2 - fixed) + bias;
         v[t >> 5][(t & 31) + u] = __float_as_uint(s);
       }
     }
@@ -512,6 +511,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     const int row = quarter * 32 + lane;
     const uint32_t lb = (uint32_t)(quarter * 32) << 16;
     const float sl2 = p.scale_log2;
+    constexpr bool kMayBeFixed = MOD == (kScoreCap | kScoreBias);  // decided unit by unit
+    [[maybe_unused]] int exchanges = 0;  // tiles whose row maxima were exchanged
     int uc = 0, g = 0;
     bool ok = true;
     while (ok) {
@@ -535,6 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         kb_n = p.step_col[e0];
         k0_n = p.tracks[3 * n + (int64_t)kb_n * 128];
       }
+      // one stabiliser for every row: with a bias, where it only lowers scores (see kFixedMax)
+      const bool fixed = (MOD & kScoreFixed) != 0 || (kMayBeFixed && p.score.small && slope >= 0.f);
       float m_run = -INFINITY, l_h = 0.f;
       for (int j = 0; j < T; ++j, ++g) {
         const uint32_t b = (uint32_t)(g & 1);
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         // (scaling by a positive constant commutes with the maximum, and P takes one FMA below)
         [[maybe_unused]] float mx = -INFINITY;
         if constexpr (MOD != 0) {
-          score_row<MOD>(v, p, sl2, slope, side, far0, pq, kpos);
+          score_row<MOD>(v, p, sl2, slope, side, far0, pq, kpos, fixed ? kFixedMax : 0.f);
           if constexpr ((MOD & kScoreBias) != 0) k0_n = p.tracks[3 * n + (int64_t)kb_n * 128];
           if (masked) {
 #pragma unroll
@@ -628,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
                 if (!((lm[cc] >> t) & 1u)) v[cc][t] = __float_as_uint(-INFINITY);
           }
         }
-        if constexpr ((MOD & kScoreFixed) != 0) {
+        if (fixed) {
           m_run = kFixedMax;
         } else if constexpr (MOD != 0) {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -652,11 +655,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
             for (int t = 0; t < 32; ++t) mx = fmaxf(mx, __uint_as_float(v[cc][t]));
           mx *= sl2;
         }
-        if constexpr ((MOD & kScoreFixed) == 0) {
-          float* mxb = mxs + b * 256;
+        if (!fixed) {
+          const int x = kMayBeFixed ? exchanges++ : g;
+          float* mxb = mxs + (x & 1) * 256;
           mxb[half * 128 + row] = mx;
-          mbar_arrive(&bar[B_MX0 + b]);
-          if (!wait_all(&bar[B_MX0 + b], (g >> 1) & 1, w)) { ok = false; break; }
+          mbar_arrive(&bar[B_MX0 + (x & 1)]);
+          if (!wait_all(&bar[B_MX0 + (x & 1)], (x >> 1) & 1, w)) { ok = false; break; }
           mx = fmaxf(mx, mxb[(1 - half) * 128 + row]);
           // the running max is kept integral (base 2): every rescale factor below is then an
           // exact power of two, and bf16 rounding of P does not depend on which keys a step
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         }
         // P = exp2(s - m_run) as bf16, packed into columns [64 half, 64 half + 32) of the S
         // buffer: inside the fp32 columns this warp has just read
-        [[maybe_unused]] const float base = (m_run == -INFINITY) ? 0.f : m_run;
+        [[maybe_unused]] const float base = fixed || m_run == -INFINITY ? 0.f : m_run;
         // v holds scaled scores where keys were masked, raw ones otherwise
         [[maybe_unused]] const float vs = (MOD != 0 || masked) ? 1.f : sl2;
         auto weight = [&](uint32_t x) {
@@ -779,8 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
       if (!wait_all(&bar[B_EPIRDY0 + ub], (uc >> 1) & 1, w)) break;
       float m_run = hm[ub * 128 + row];
       const float l_run = hl[ub * 256 + row] + hl[ub * 256 + 128 + row];
-      // (rows without a legal key have no maximum)
-      if ((MOD & kScoreFixed) != 0 && l_run == 0.f) m_run = -INFINITY;
+      // (rows without a legal key have no maximum, but may have got the fixed one)
+      if ((MOD & kScoreCap) != 0 && l_run == 0.f) m_run = -INFINITY;
       mbar_arrive(&bar[B_HFREE0 + ub]);
       // the merge mode is one per unit: the four warps vote
       const bool grows = !p.first && m_old != -INFINITY && m_run > m_old + kRescaleThreshold;

@@ -43,8 +43,11 @@ enum : int { kScoreCap = 1, kScoreBias = 2, kScoreFixed = 4 };
 // where cap2 is at most kFixedCap, every row's stabiliser is kFixedMax.  A row's largest weight is
 // then 2^(-80 - 16) at least, and 2^(80 - 16) at most: sums over 2^20 keys of values up to 2^43
 // stay finite, and outputs keep 8 bits down to values of 2^-22 in a row whose scores all are -cap.
+// A bias with a slope >= 0 only lowers scores, and not that of a row's own key, which is legal in
+// every row that has a legal key: the same holds, decided for each head on the device.
 // Saved are the maximum, its exchange between the two warps of a row and the rescaling (forward of
-// 64K packed tokens, 16 heads of 128: cap 50 2000 -> 1670 us, cap 18 2190 -> 1855).
+// 64K packed tokens, 16 heads of 128: cap 50 2000 -> 1670 us, cap 18 2190 -> 1855, cap 50 with a
+// bias 2517 -> 2117).
 constexpr float kFixedCap = 80.f, kFixedMax = 16.f;
 
 struct ScoreParams {
@@ -56,6 +59,7 @@ struct ScoreParams {
   float cap2;             // cap * log2 e
   float neg_inv_cap2_sq;  // -1 / cap2^2
   const float* slopes;    // [hq] or null
+  int small;              // cap2 <= kFixedCap
   int consecutive;        // set for every variant: the positions of a block's tokens are consecutive
 };
 
@@ -103,6 +107,7 @@ inline void set_cap(ScoreParams* s, float cap, float scale) {
   s->lim_n = fold(kAn, s->cn, 4, 0.45);
   s->ky = (float)(2.0 * log2e * k);
   s->cap2 = (float)cap2;
+  s->small = s->cap2 <= kFixedCap;
   s->neg_inv_cap2_sq = (float)(-1.0 / (cap2 * cap2));
   if (!std::isfinite(s->neg_inv_cap2_sq)) s->lim = s->lim_n = -1.f;
 }

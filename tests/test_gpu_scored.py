@@ -325,6 +325,22 @@ def test_saturated_scores(cap, size):
         assert (np.abs(_np(o) - ref["O"]) <= lim + 1e-30).all()
 
 
+@pytest.mark.parametrize("kind", ["usual", "steep", "signed"])
+@pytest.mark.parametrize("W", [INF, 40])
+def test_bias_beside_a_cap_that_bounds_the_scores(kind, W):
+    """Heads whose slopes lower scores do without a running maximum, the others in the same launch
+    do not; steep slopes leave a row little more than its own key."""
+    n, cap = 1024, 50.0
+    tr = wl.random_pack(np.random.default_rng(31), n, max_samples=4)
+    q, k, v, do = _qkvdo(n, 4, 2, 128, 31, scale=20.0)
+    slopes = _slopes(4, kind)
+    pl = M.Plan(*device_tracks(tr), W, 2, "ptrr_block")
+    m = mask.dense_mask(tr, W)
+    assert (m.diagonal() == m.any(1)).all()
+    for kw in ({}, {"fused": True}, {"merge": "fp32"}):
+        _check(_run(pl, q, k, v, do, M.Score(cap, slopes), **kw), q, k, v, do, m, cap, slopes)
+
+
 def test_both_ways_to_tanh_in_one_pack():
     """Rows with small and rows with large scores, tile by tile, around the border of 0.75."""
     n = 1024
