@@ -349,18 +349,48 @@ class Rope:
     ``pairing``: "halves" pairs channels (i, i + rot_dim / 2), "adjacent" (2 i, 2 i + 1)."""
 
     def __init__(self, inv_freq, axis=None, pairing: str = "halves"):
-        import numpy as np
-        # copies: the caller's arrays may change after this
-        self.inv_freq = np.array(inv_freq, dtype=np.float64)
-        self.axis = np.zeros(self.inv_freq.shape, np.int32) if axis is None \
-            else np.array(axis, dtype=np.int32)
-        if self.inv_freq.ndim != 1 or self.axis.shape != self.inv_freq.shape:
-            raise ValueError("inv_freq and axis must be 1-D arrays of one length")
         if pairing not in PAIRINGS:
             raise ValueError(f"pairing must be one of {sorted(PAIRINGS)}")
         self.pairing = pairing
-        self.rot_dim = 2 * len(self.inv_freq)
-        self._tables = (self.inv_freq.ctypes.data, self.axis.ctypes.data)
+        self._set(inv_freq, axis)
+
+    def _set(self, inv_freq, axis):
+        import numpy as np
+        # copies: the caller's arrays may change after this
+        freq = np.array(inv_freq, dtype=np.float64)
+        axis = np.zeros(freq.shape, np.int32) if axis is None else np.array(axis, dtype=np.int32)
+        if freq.ndim != 1 or axis.shape != freq.shape:
+            raise ValueError("inv_freq and axis must be 1-D arrays of one length")
+        self._freq, self._axis = freq, axis
+        self._tables = (freq.ctypes.data, axis.ctypes.data)  # of these two arrays, no others
+
+    # a copy (copy, pickle) has arrays, and with them addresses, of its own
+    def __getstate__(self):
+        return {"inv_freq": self._freq, "axis": self._axis, "pairing": self.pairing}
+
+    def __setstate__(self, state):
+        self.pairing = state["pairing"]
+        self._set(state["inv_freq"], state["axis"])
+
+    @property
+    def inv_freq(self):
+        return self._freq
+
+    @inv_freq.setter
+    def inv_freq(self, value):
+        self._set(value, self._axis)
+
+    @property
+    def axis(self):
+        return self._axis
+
+    @axis.setter
+    def axis(self, value):
+        self._set(self._freq, value)
+
+    @property
+    def rot_dim(self):
+        return 2 * len(self._freq)
 
     def _c(self, pos, q_weight, k_weight, eps):
         return _Rope(pos.shape[0], self.rot_dim, PAIRINGS[self.pairing], *self._tables,
