@@ -433,8 +433,11 @@ def _rope_args(torch, pos, plan, q_weight, k_weight, first):
     if not ok:
         raise ValueError("pos must be a contiguous int32 CUDA tensor [axes, n], q a tensor "
                          "[n, heads, d]")
-    if plan is not None and n != plan.n:
-        raise ValueError("pos must have the plan's N columns")
+    if plan is not None:
+        if plan.handle is None:  # NULL would be "no plan": the tokens left in their order
+            raise ValueError("the plan is closed")
+        if n != plan.n:
+            raise ValueError("pos must have the plan's N columns")
     index = pos.get_device()
     for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:

@@ -62,3 +62,52 @@ def test_a_changed_descriptor_is_what_the_call_reads():
         with pytest.raises(ValueError):
             rope.inv_freq = bad
     np.testing.assert_array_equal(_tables(rope)[0], [3.0, 5.0])
+
+
+class _Tensor:
+    """A tensor on the GPU, as far as the binding looks before it makes the call."""
+    is_cuda = True
+
+    def __init__(self, torch, shape, dtype):
+        self.shape, self.dtype = shape, dtype
+        self.base = torch.empty(shape, device="meta")
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self):
+        return self.base.stride()
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return 4096
+
+
+def test_a_closed_plan_is_refused(monkeypatch):
+    """A closed plan has no handle, which the C calls take for "no plan": the tokens' order would
+    silently stay."""
+    import torch
+    called = []
+    monkeypatch.setattr(M, "_call", lambda name, *args: called.append(name))
+    plan = object.__new__(M.Plan)
+    plan._h, plan.n = None, 128
+    rope = M.Rope([1.0] * 8)
+    pos = _Tensor(torch, (1, 128), torch.int32)
+    q, dq = (_Tensor(torch, (128, 2, 64), t) for t in (torch.bfloat16, torch.float32))
+    out = (_Tensor(torch, (128, 2, 64), torch.bfloat16), None, None)
+    stream = type("S", (), {"cuda_stream": 0})()
+    with pytest.raises(ValueError, match="closed"):
+        M.rope(rope, pos, q, plan=plan, out=out, stream=stream)
+    with pytest.raises(ValueError, match="closed"):
+        M.rope_bwd(rope, pos, dq, plan=plan, out=out, stream=stream)
+    assert called == []
+    plan._h = ctypes.c_void_p(1)  # an open one goes through (closing it would free it)
+    M.rope(rope, pos, q, plan=plan, out=out, stream=stream)
+    M.rope_bwd(rope, pos, dq, plan=plan, out=out, stream=stream)
+    assert called == ["marble_rope", "marble_rope_bwd"]
+    plan._h = None
