@@ -205,11 +205,21 @@ def _call(name, *args):
         raise MarbleError(st, lib().marble_last_error().decode())
 
 
+def _raw_stream(torch, stream, index=None):
+    """The stream's handle; None: the current stream of GPU ``index`` (None: the current GPU).
+    That one is read directly where this torch has the (private) call for it: building the stream
+    object costs a single-token call as much as its kernel takes."""
+    if stream is not None:
+        return stream.cuda_stream
+    direct = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if direct is None:
+        return torch.cuda.current_stream(index).cuda_stream
+    return direct(torch.cuda.current_device() if index is None else index)
+
+
 def _stream(stream):
     import torch
-    if stream is None:  # read directly: a stream object costs as much as a small call's kernel
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
-    return ctypes.c_void_p(stream.cuda_stream)
+    return ctypes.c_void_p(_raw_stream(torch, stream))
 
 
 def _ptr(t):
@@ -465,12 +475,6 @@ def _rope_out(torch, like, heads, out, n, dtype, index, what, stream):
         raise ValueError("out must hold one tensor of the same shape for each of "
                          f"{what}q, {what}k and {what}v")
     return tuple(out), _heads(out, n, dtype, index, "out " + what)
-
-
-def _raw_stream(torch, stream, index):
-    """The stream's handle; None: the current stream of GPU ``index`` (read directly: building
-    the stream object would cost a single-token call as much as its kernel takes)."""
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def rope(rope: Rope, pos, q, k=None, v=None, plan: Optional[Plan] = None, q_weight=None,
