@@ -946,18 +946,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
         tmem_ld32(rS + lb + half * 64 + 32, vs[1]);
         tmem_ld_wait();
         // Copies of the loop, chosen per warp: with the mask's select and without it (full tiles,
-        // and partial ones whose rows in this warp keep every column).  With a cap or a bias a
-        // third one takes every other case, with the select (a warp without masked columns has
-        // all of its bits set): the second way to tanh (score.cuh), and distances that are not
-        // linear in the query (the diagonal block, a position track).  The per-query LSE is read
-        // four at a time.
+        // and partial ones whose rows in this warp keep every column).  Scored calls have two more,
+        // with the select (a warp without masked columns has all of its bits set): one where
+        // distances are not linear in the query (the diagonal block, a position track), and with
+        // a cap one for tanh by the exponential (two: kWideCap, score.cuh), whatever the distances.
+        // The per-query LSE is read four at a time.
         [[maybe_unused]] float side = 1.f, own = 0.f;
         if constexpr ((MOD & kScoreBias) != 0) {
           side = side_of(cur);
           own = -side * cur.slope * (float)(cur.i0 + half * 64 - pk);
         }
-        auto weights = [&](auto with_mask, auto usual) {
-          constexpr bool kMasked = decltype(with_mask)::value, kUsual = decltype(usual)::value;
+        // way: to tanh, 0 the polynomial, 1 the exponential, 2 that or the polynomial
+        auto weights = [&](auto with_mask, auto way, auto any_distance) {
+          constexpr bool kMasked = decltype(with_mask)::value;
+          constexpr int kWay = decltype(way)::value;
+          constexpr bool kAny = decltype(any_distance)::value && (MOD & kScoreBias) != 0;
+          // four positions at a time, loaded one group ahead: more in flight spill registers (64K
+          // pack, cap 50, bias: backward 8730 -> 8050 us)
+          [[maybe_unused]] int4 k4, ahead;
+          [[maybe_unused]] const int32_t* qpos = p.tracks + 3 * n + qrow0;
+          if constexpr (kAny) ahead = __ldg(reinterpret_cast<const int4*>(qpos));
 #pragma unroll
           for (int cc = 0; cc < 2; ++cc) {
             uint32_t pk16[16];
@@ -967,9 +975,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
               const float4 l4 = *reinterpret_cast<const float4*>(lse2s + q0);
               const float nl[4] = {l4.x, l4.y, l4.z, l4.w};
               float pv[4], wv[4];
-              [[maybe_unused]] int4 k4;
-              if constexpr (!kUsual && (MOD & kScoreBias) != 0)
-                k4 = __ldg(reinterpret_cast<const int4*>(p.tracks + 3 * n + qrow0 + q0));
+              if constexpr (kAny) {
+                k4 = ahead;
+                if (q0 + 4 < 64) ahead = __ldg(reinterpret_cast<const int4*>(qpos + q0 + 4));
+              }
 #pragma unroll
               for (int u = 0; u < 4; u += 2) {
                 const float x0 = __uint_as_float(vs[cc][t + u]);
@@ -977,36 +986,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
                 if constexpr (MOD == 0) {
                   pv[u] = fmaf(x0, sl2, nl[u]);
                   pv[u + 1] = fmaf(x1, sl2, nl[u + 1]);
-                } else if constexpr (kUsual) {
+                } else {
                   F2 bias = f2(nl[u], nl[u + 1]);
-                  if constexpr ((MOD & kScoreBias) != 0) bias = add2(bias, f2(own));
+                  if constexpr (kAny) {
+                    // (where there is a side the LSE holds the part in t already)
+                    const float d0 = fabsf((float)((u == 0 ? k4.x : k4.z) - pk));
+                    const float d1 = fabsf((float)((u == 0 ? k4.y : k4.w) - pk));
+                    bias = side != 0.f ? add2(bias, f2(own))
+                                       : fma2(f2(d0, d1), f2(-cur.slope), bias);
+                  } else if constexpr ((MOD & kScoreBias) != 0) {
+                    bias = add2(bias, f2(own));
+                  }
                   F2 s;
                   if constexpr ((MOD & kScoreCap) == 0) {
                     s = fma2(f2(x0, x1), f2(sl2), bias);
+                  } else if constexpr (kWay > 0) {
+                    float r[2];
+                    s = add2(cap_far<kWay == 2>(x0, x1, p.score, r), bias);
+                    wv[u] = 4.f * fmaf(-r[0], r[0], r[0]);
+                    wv[u + 1] = 4.f * fmaf(-r[1], r[1], r[1]);
                   } else {
                     const F2 x = f2(x0, x1), c = mul2(x, cap_factor<6>(x, p.score));
                     split(fma2(mul2(c, c), f2(p.score.neg_inv_cap2_sq), f2(1.f)), &wv[u], &wv[u + 1]);
                     s = add2(c, bias);
                   }
                   split(s, &pv[u], &pv[u + 1]);
-                } else {
-#pragma unroll
-                  for (int y = u; y < u + 2; ++y) {
-                    const float x = y == u ? x0 : x1;
-                    float bias = nl[y];
-                    if constexpr ((MOD & kScoreBias) != 0) {
-                      // with a side the LSE holds the part in t already
-                      const int kq = y == 0 ? k4.x : y == 1 ? k4.y : y == 2 ? k4.z : k4.w;
-                      bias += side != 0.f ? own : -cur.slope * fabsf((float)(kq - pk));
-                    }
-                    if constexpr ((MOD & kScoreCap) == 0) {
-                      pv[y] = fmaf(x, sl2, bias);
-                    } else {
-                      const float r = cap_rcp(x, p.score);
-                      wv[y] = 4.f * fmaf(-r, r, r);
-                      pv[y] = fmaf(-2.f * p.score.cap2, r, p.score.cap2) + bias;
-                    }
-                  }
                 }
 #pragma unroll
                 for (int y = u; y < u + 2; ++y) {
@@ -1030,22 +1034,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_bwd_dkdv(const __grid_constant_
             tmem_st16(rS + lb + half * 64 + cc * 16, pk16);
           }
         };
-        bool usual = true;
+        constexpr std::true_type kYes{};
+        constexpr std::false_type kNo{};
+        [[maybe_unused]] bool far = false;
         if constexpr ((MOD & kScoreCap) != 0) {
           float hi[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int t = 0; t < 64; ++t)
             hi[t & 3] = fmaxf(hi[t & 3], fabsf(__uint_as_float(vs[t >> 5][t & 31])));
-          usual = __all_sync(0xffffffffu,
-                             fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])) <= p.score.lim);
+          far = !__all_sync(0xffffffffu,
+                            fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3])) <= p.score.lim);
         }
-        if constexpr ((MOD & kScoreBias) != 0) usual = usual && side != 0.f;
-        if (MOD != 0 && !usual)
-          weights(std::true_type{}, std::false_type{});
+        constexpr std::integral_constant<int, 0> kPoly{};
+        constexpr std::integral_constant<int, (MOD & kScoreCap) != 0 ? 1 : 0> kExp{};
+        constexpr std::integral_constant<int, (MOD & kScoreCap) != 0 ? 2 : 0> kWide{};
+        if ((MOD & kScoreCap) != 0 && far && p.score.wide)
+          weights(kYes, kWide, kYes);
+        else if ((MOD & kScoreCap) != 0 && far)
+          weights(kYes, kExp, kYes);
+        else if ((MOD & kScoreBias) != 0 && side == 0.f)
+          weights(kYes, kPoly, kYes);
         else if (masked)
-          weights(std::true_type{}, std::true_type{});
+          weights(kYes, kPoly, kNo);
         else
-          weights(std::false_type{}, std::true_type{});
+          weights(kNo, kPoly, kNo);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bar[K_PFULL]);

@@ -14,8 +14,11 @@
 //     host, so that a capped score costs seven multiply-adds from x.
 //   |y| <= 0.45, in the forward: the same with four terms, relative error 2^-22.
 //   otherwise 1 - 2 / (1 + e^(2 y)): two calls to the special function unit, which also has the
-//     softmax's exp2 to do, and an absolute error of 2^-22 c (the score's own rounding is of
-//     that size, some |score| being above 0.875 c).
+//     softmax's exp2 to do, and an absolute error of 2^-22 c.  That is the rounding of a score
+//     above 0.875 c, but the warp's other scores may be far smaller: where it would be more than
+//     2^-14 (kWideCap), a score with |y| <= 0.875 takes the polynomial here too, score by score.
+// The bias has no part in this choice: whether it is linear over the tile (the tile off the
+// diagonal block, and no position track) decides only how the distances are had.
 // The special function unit is what these two spare: it gives 16 results a clock on an SM, where
 // multiply-adds have 128, and the softmax's exp2 takes one a score.  A forward over 64K packed
 // tokens (16 heads of 128) takes 1669 us without a cap, 1670 with nearly every tile within the
@@ -50,6 +53,19 @@ enum : int { kScoreCap = 1, kScoreBias = 2, kScoreFixed = 4 };
 // bias 2517 -> 2117).
 constexpr float kFixedCap = 80.f, kFixedMax = 16.f;
 
+// cap2 above which a small score must not take the exponential's absolute error, 2^-22 cap2 (at
+// 256 a weight is off by 2^-14 of itself, a 64th of its rounding to bf16)
+constexpr float kWideCap = 256.f;
+
+// tanh(y) / y in y^2: over |y| <= 0.875, and over |y| <= 0.45
+__host__ __device__ constexpr double tanh_coef(int i) {
+  constexpr double a[6] = {0.9999998509502919,   -0.33331914077818203, 0.1331109766192674,
+                           -0.0526657826506247,  0.018277444003715584, -0.003840352757762384};
+  return a[i];
+}
+constexpr double kTanhNear[4] = {0.9999997567401877, -0.3332946719023316, 0.13236369052147212,
+                                 -0.0460281937984787};
+
 struct ScoreParams {
   float c[6];             // s = x (c[0] + c[1] x^2 + ... + c[5] x^10) for |x| <= lim
   float lim;
@@ -58,6 +74,8 @@ struct ScoreParams {
   float ky;               // e^(2 y) = 2^(ky x)
   float cap2;             // cap * log2 e
   float neg_inv_cap2_sq;  // -1 / cap2^2
+  float y_of_x;           // scale / cap
+  int wide;               // cap2 > kWideCap
   const float* slopes;    // [hq] or null
   int small;              // cap2 <= kFixedCap
   int consecutive;        // set for every variant: the positions of a block's tokens are consecutive
@@ -86,13 +104,12 @@ marble_status_t with_variant(int d, int mod, F f) {
 
 // `cap` in [1e-30, 1e30]
 inline void set_cap(ScoreParams* s, float cap, float scale) {
-  static const double kA[6] = {0.9999998509502919,   -0.33331914077818203, 0.1331109766192674,
-                               -0.0526657826506247,  0.018277444003715584, -0.003840352757762384};
-  static const double kAn[4] = {0.9999997567401877, -0.3332946719023316, 0.13236369052147212,
-                                -0.0460281937984787};
+  double far[6];
+  for (int i = 0; i < 6; ++i) far[i] = tanh_coef(i);
   const double log2e = 1.4426950408889634, k = (double)scale / cap, cap2 = cap * log2e;
   // c[i] = a[i] scale log2e k^(2i); returns the limit for |x|: `top` in y, less where a term is
   // lost below fp32's range (then up to where it is 2^-24 of the first), none where one is above
+  // (and up to 1e18 for x and the score, whose squares are taken)
   auto fold = [&](const double* a, float* c, int terms, double top) {
     double f = scale * log2e;
     for (int i = 0; i < terms; ++i, f *= k * k) {
@@ -101,12 +118,14 @@ inline void set_cap(ScoreParams* s, float cap, float scale) {
       if (i > 0 && std::fabs(a[i] * f) < 1e-36)
         top = fmin(top, std::pow(0x1p-24 / std::fabs(a[i]), 0.5 / i));
     }
-    return (float)fmin(top / k, 1e18);
+    return (float)fmin(top / k, 1e18 / fmax(1.0, scale * log2e));
   };
-  s->lim = fold(kA, s->c, 6, 0.875);
-  s->lim_n = fold(kAn, s->cn, 4, 0.45);
+  s->lim = fold(far, s->c, 6, 0.875);
+  s->lim_n = fold(kTanhNear, s->cn, 4, 0.45);
   s->ky = (float)(2.0 * log2e * k);
   s->cap2 = (float)cap2;
+  s->y_of_x = (float)k;
+  s->wide = s->cap2 > kWideCap;
   s->small = s->cap2 <= kFixedCap;
   s->neg_inv_cap2_sq = (float)(-1.0 / (cap2 * cap2));
   if (!std::isfinite(s->neg_inv_cap2_sq)) s->lim = s->lim_n = -1.f;
@@ -170,6 +189,31 @@ __device__ __forceinline__ F2 cap_factor(F2 x, const ScoreParams& p) {
 // 1 / (1 + e^(2 y)): the capped score is cap2 (1 - 2 r), its slope's factor 4 r (1 - r)
 __device__ __forceinline__ float cap_rcp(float x, const ScoreParams& p) {
   return fast_rcp(1.f + fast_exp2(x * p.ky));
+}
+
+// The capped scores of a pair by the exponential, and with kWide by it or the polynomial.
+// rcp: the two 1 / (1 + e^(2 y)).  Whole warp.
+template <bool kWide>
+__device__ __forceinline__ F2 cap_far(float x0, float x1, const ScoreParams& p, float (&rcp)[2]) {
+  rcp[0] = cap_rcp(x0, p);
+  rcp[1] = cap_rcp(x1, p);
+  float s0 = fmaf(-2.f * p.cap2, rcp[0], p.cap2), s1 = fmaf(-2.f * p.cap2, rcp[1], p.cap2);
+  if constexpr (kWide) {
+    // (in y, whose powers stay in range where the folded coefficients' do not)
+    const F2 y = mul2(f2(x0, x1), f2(p.y_of_x));
+    float y0, y1, t0, t1;
+    split(y, &y0, &y1);
+    if (__any_sync(0xffffffffu, fminf(fabsf(y0), fabsf(y1)) <= 0.875f)) {
+      const F2 u = mul2(y, y);
+      F2 t = f2((float)tanh_coef(5));
+#pragma unroll
+      for (int i = 4; i >= 0; --i) t = fma2(t, u, f2((float)tanh_coef(i)));
+      split(mul2(mul2(t, y), f2(p.cap2)), &t0, &t1);
+      s0 = fabsf(y0) <= 0.875f ? t0 : s0;
+      s1 = fabsf(y1) <= 0.875f ? t1 : s1;
+    }
+  }
+  return f2(s0, s1);
 }
 
 }  // namespace marble
