@@ -561,8 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         kb_n = p.step_col[e0];
         k0_n = p.tracks[3 * n + (int64_t)kb_n * 128];
       }
-      // one stabiliser for every row: with a bias, where it only lowers scores (see kFixedMax)
-      const bool fixed = (MOD & kScoreFixed) != 0 || (kMayBeFixed && p.score.small && slope >= 0.f);
+      // one stabiliser for every row: with a bias, where it only lowers scores and the launch's
+      // lists hold the rows' own keys (see kFixedMax)
+      const bool fixed = (MOD & kScoreFixed) != 0 || (kMayBeFixed && p.score.bias_fixed && slope >= 0.f);
       float m_run = -INFINITY, l_h = 0.f;
       for (int j = 0; j < T; ++j, ++g) {
         const uint32_t b = (uint32_t)(g & 1);
@@ -1028,6 +1029,8 @@ marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv,
     prm.kv_shard = kv_shards[i];
     prm.first = (flags[i] & MARBLE_STEP_FIRST) ? 1 : 0;
     prm.lse_merge = (flags[i] & MARBLE_STEP_BF16_MERGE) ? 1 : (flags[i] & MARBLE_STEP_FP32_MERGE) ? 2 : 0;
+    // one stabiliser beside a bias needs the rows' own keys among the step's (see kFixedMax)
+    if (prm.kv_shard >= 0 && prm.kv_shard != prm.q_shard) prm.score.bias_fixed = 0;
     const int64_t seg = (int64_t)prm.q_shard * (pl->P + 1) + (prm.kv_shard >= 0 ? prm.kv_shard : pl->P);
     prm.order = pl->fwd_order + seg * pl->bps;
     prm.nwork = pl->h_fwd_nwork[seg] * qkv->hq;

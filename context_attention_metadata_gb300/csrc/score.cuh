@@ -47,7 +47,11 @@ enum : int { kScoreCap = 1, kScoreBias = 2, kScoreFixed = 4 };
 // then 2^(-80 - 16) at least, and 2^(80 - 16) at most: sums over 2^20 keys of values up to 2^43
 // stay finite, and outputs keep 8 bits down to values of 2^-22 in a row whose scores all are -cap.
 // A bias with a slope >= 0 only lowers scores, and not that of a row's own key, which is legal in
-// every row that has a legal key: the same holds, decided for each head on the device.
+// every row that has a legal key.  So the same holds for launches whose lists have the rows' own
+// blocks (the fused ring, every needed block, the step of a shard with itself), decided for each
+// head on the device; a step between different shards may hold nothing but far keys, all of whose
+// weights 2^(s - 16) can be below fp32's range, and keeps the running maximum.  (A piece of a row
+// without the own key may lose its weights, which beside that key's are below 2^-30.)
 // Saved are the maximum, its exchange between the two warps of a row and the rescaling (forward of
 // 64K packed tokens, 16 heads of 128: cap 50 2000 -> 1670 us, cap 18 2190 -> 1855, cap 50 with a
 // bias 2517 -> 2117).
@@ -77,7 +81,7 @@ struct ScoreParams {
   float y_of_x;           // scale / cap
   int wide;               // cap2 > kWideCap
   const float* slopes;    // [hq] or null
-  int small;              // cap2 <= kFixedCap
+  int bias_fixed;         // cap2 <= kFixedCap, and the launch's lists hold the rows' own blocks
   int consecutive;        // set for every variant: the positions of a block's tokens are consecutive
 };
 
@@ -126,7 +130,7 @@ inline void set_cap(ScoreParams* s, float cap, float scale) {
   s->cap2 = (float)cap2;
   s->y_of_x = (float)k;
   s->wide = s->cap2 > kWideCap;
-  s->small = s->cap2 <= kFixedCap;
+  s->bias_fixed = s->cap2 <= kFixedCap;
   s->neg_inv_cap2_sq = (float)(-1.0 / (cap2 * cap2));
   if (!std::isfinite(s->neg_inv_cap2_sq)) s->lim = s->lim_n = -1.f;
 }
