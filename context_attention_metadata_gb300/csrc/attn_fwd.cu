@@ -180,15 +180,14 @@ struct Smem {
 };
 static_assert(Smem<128>::bytes() <= 232448, "shared memory budget");
 
-// A row's 64 products of this half, in place, to base-2 scores with the cap and the bias, less
-// `fixed`: kFixedMax where that is the stabiliser, or 0 (a cap always has the one or the other).
+// A row's 64 products of this half, in place, to base-2 scores with the cap and the bias.
 // side: +1 or -1 where the tile's keys all come before (after) its queries and positions are
 // consecutive, so that the bias is linear in the key; 0 otherwise.  far0: the row's distance to
 // the half's first key; pos: the keys' positions.
 template <int MOD>
 __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams& p, float sl2,
                                           float slope, float side, float far0, int pq,
-                                          const int32_t* __restrict__ pos, float fixed) {
+                                          const int32_t* __restrict__ pos) {
   constexpr bool kCap = (MOD & kScoreCap) != 0, kBias = (MOD & kScoreBias) != 0;
   float top = 0.f;
   if constexpr (kCap) {
@@ -199,7 +198,7 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
     top = fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]));
   }
   // key t of the half is at side (far0 - t): the bias is own + t * step
-  const float own = fmaf(-side * slope, far0, -fixed), step = side * slope;
+  const float own = -side * slope * far0, step = side * slope;
   // terms: of the polynomial; 0: the exponential, -1: that or the polynomial, score by score
   auto pairs = [&](auto terms, auto linear) {
     constexpr int kTerms = decltype(terms)::value;
@@ -219,7 +218,7 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
       for (int u = 0; u < 4; u += 2) {
         uint32_t &v0 = v[t >> 5][(t & 31) + u], &v1 = v[t >> 5][(t & 31) + u + 1];
         const F2 x = f2(__uint_as_float(v0), __uint_as_float(v1));
-        F2 off = f2(-fixed);
+        [[maybe_unused]] F2 off;
         if constexpr (kBias && kLinear) {
           // whole numbers counted up, so that the bias is rounded once
           off = fma2(at[u >> 1], f2(step), f2(own));
@@ -227,17 +226,18 @@ __device__ __forceinline__ void score_row(uint32_t (&v)[2][32], const FwdParams&
         } else if constexpr (kBias) {
           const float d0 = fabsf((float)(pq - (u == 0 ? k4.x : k4.z)));
           const float d1 = fabsf((float)(pq - (u == 0 ? k4.y : k4.w)));
-          off = fma2(f2(d0, d1), f2(-slope), off);
+          off = mul2(f2(d0, d1), f2(-slope));
         }
         F2 s;
         if constexpr (kCap && kTerms <= 0) {
           float r[2], x0, x1;
           split(x, &x0, &x1);
-          s = add2(cap_far<(kTerms < 0)>(x0, x1, p.score, r), off);
+          s = cap_far<(kTerms < 0)>(x0, x1, p.score, r);
+          if constexpr (kBias) s = add2(s, off);
         } else {
           F2 factor = f2(sl2);
           if constexpr (kCap) factor = cap_factor<kTerms>(x, p.score);
-          if constexpr (kBias || (MOD & kScoreFixed) != 0)
+          if constexpr (kBias)
             s = fma2(x, factor, off);
           else
             s = mul2(x, factor);
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         k0_n = p.tracks[3 * n + (int64_t)kb_n * 128];
       }
       // one stabiliser for every row: with a bias, where it only lowers scores and the launch's
-      // lists hold the rows' own keys (see kFixedMax)
+      // lists hold the rows' own keys (see kFixedCap)
       const bool fixed = (MOD & kScoreFixed) != 0 || (kMayBeFixed && p.score.bias_fixed && slope >= 0.f);
       float m_run = -INFINITY, l_h = 0.f;
       for (int j = 0; j < T; ++j, ++g) {
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         // (scaling by a positive constant commutes with the maximum, and P takes one FMA below)
         [[maybe_unused]] float mx = -INFINITY;
         if constexpr (MOD != 0) {
-          score_row<MOD>(v, p, sl2, slope, side, far0, pq, kpos, fixed ? kFixedMax : 0.f);
+          score_row<MOD>(v, p, sl2, slope, side, far0, pq, kpos);
           if constexpr ((MOD & kScoreBias) != 0) k0_n = p.tracks[3 * n + (int64_t)kb_n * 128];
           if (masked) {
 #pragma unroll
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           }
         }
         if (fixed) {
-          m_run = kFixedMax;
+          m_run = 0.f;
         } else if constexpr (MOD != 0) {
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         }
         // P = exp2(s - m_run) as bf16, packed into columns [64 half, 64 half + 32) of the S
         // buffer: inside the fp32 columns this warp has just read
-        [[maybe_unused]] const float base = fixed || m_run == -INFINITY ? 0.f : m_run;
+        [[maybe_unused]] const float base = m_run == -INFINITY ? 0.f : m_run;
         // v holds scaled scores where keys were masked, raw ones otherwise
         [[maybe_unused]] const float vs = (MOD != 0 || masked) ? 1.f : sl2;
         auto weight = [&](uint32_t x) {
@@ -1029,7 +1029,7 @@ marble_status_t launch_steps(const marble_plan_t* pl, const marble_qkv_t* qkv,
     prm.kv_shard = kv_shards[i];
     prm.first = (flags[i] & MARBLE_STEP_FIRST) ? 1 : 0;
     prm.lse_merge = (flags[i] & MARBLE_STEP_BF16_MERGE) ? 1 : (flags[i] & MARBLE_STEP_FP32_MERGE) ? 2 : 0;
-    // one stabiliser beside a bias needs the rows' own keys among the step's (see kFixedMax)
+    // one stabiliser beside a bias needs the rows' own keys among the step's (see kFixedCap)
     if (prm.kv_shard >= 0 && prm.kv_shard != prm.q_shard) prm.score.bias_fixed = 0;
     const int64_t seg = (int64_t)prm.q_shard * (pl->P + 1) + (prm.kv_shard >= 0 ? prm.kv_shard : pl->P);
     prm.order = pl->fwd_order + seg * pl->bps;

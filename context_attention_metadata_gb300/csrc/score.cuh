@@ -39,23 +39,25 @@
 
 namespace marble {
 
-// bits of a kernel's score variant; kScoreFixed (forward, with a cap alone): see kFixedMax
+// bits of a kernel's score variant; kScoreFixed (forward, with a cap alone): see kFixedCap
 enum : int { kScoreCap = 1, kScoreBias = 2, kScoreFixed = 4 };
 
 // A capped score without a bias lies in [-cap2, cap2], so the softmax needs no running maximum:
-// where cap2 is at most kFixedCap, every row's stabiliser is kFixedMax.  A row's largest weight is
-// then 2^(-80 - 16) at least, and 2^(80 - 16) at most: sums over 2^20 keys of values up to 2^43
-// stay finite, and outputs keep 8 bits down to values of 2^-22 in a row whose scores all are -cap.
+// where cap2 is at most kFixedCap, every row's stabiliser is 2^0.  A row's largest weight is then
+// between 2^-80 and 2^80, and the middle of fp32's range is what is left to the values: sums over
+// a row of values up to 2^47 / its keys stay finite in a row whose scores all are +cap, and values
+// down to 2^-50 keep their bits in one whose scores all are -cap (a product of 2^-130 has 19 of
+// fp32's, which the tensor core keeps below its normal range too).
 // A bias with a slope >= 0 only lowers scores, and not that of a row's own key, which is legal in
 // every row that has a legal key.  So the same holds for launches whose lists have the rows' own
 // blocks (the fused ring, every needed block, the step of a shard with itself), decided for each
 // head on the device; a step between different shards may hold nothing but far keys, all of whose
-// weights 2^(s - 16) can be below fp32's range, and keeps the running maximum.  (A piece of a row
-// without the own key may lose its weights, which beside that key's are below 2^-30.)
+// weights 2^s can be below fp32's range, and keeps the running maximum.  (A piece of a row
+// without the own key may lose its weights, which beside that key's are below 2^-46.)
 // Saved are the maximum, its exchange between the two warps of a row and the rescaling (forward of
 // 64K packed tokens, 16 heads of 128: cap 50 2000 -> 1670 us, cap 18 2190 -> 1855, cap 50 with a
 // bias 2517 -> 2117).
-constexpr float kFixedCap = 80.f, kFixedMax = 16.f;
+constexpr float kFixedCap = 80.f;
 
 // cap2 above which a small score must not take the exponential's absolute error, 2^-22 cap2 (at
 // 256 a weight is off by 2^-14 of itself, a 64th of its rounding to bf16)

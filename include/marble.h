@@ -538,8 +538,10 @@ marble_status_t marble_attn_bwd_fused(const marble_plan_t *plan, const marble_qk
  * are given in, or pos_id).  The mask is the plan's, samples (documents) and bidirectional spans
  * (prefixes) included; a row without a legal key is as without these.  State, LSE and O mean
  * what they mean for the plain calls, of the changed scores, but with a cap of at most 55 (and no
- * slope below 0) m is 16 in every row that has seen a legal key, and sums of values above 2^63 /
- * (keys of a row) can overflow where the scores are near the cap; the backward calls give the
+ * slope below 0) m may be 0 in place of a maximum.  The values v may then be of 2^-50 to 2^47 /
+ * (keys of a row) in size, or 0: in rows whose scores all are near +cap the sums of larger ones can
+ * overflow, and in rows whose scores all are near -cap smaller ones lose bits (with lower caps, or
+ * scores away from the cap, the range is wider by as much).  The backward calls give the
  * gradients of q, k and v through cap and bias.  slopes are constants: finite, of any sign, no
  * gradient.  They are read when the kernels run.  Q, K, V and dO have to be finite for masked
  * tokens too, as for the plain calls.
