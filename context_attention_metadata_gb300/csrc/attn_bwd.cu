@@ -1485,18 +1485,23 @@ bool rows_balance(int64_t longest, int64_t tiles, int hq) {
   return 2 * longest * sm_count() <= tiles * (int64_t)hq;
 }
 
-// every tile of the pack at once, with one dQ GEMM over all q blocks.  Scored calls also take it
-// for rows that do not balance but are short: a tile of a lone unit takes 0.3 us, each of the
-// P * P launches of the other way 4 us or more (4096 tokens, 8/2 heads of 64, P = 4: the dQ part
-// 100 us in 16 launches, 17 in one).  Plain calls keep the choice they had, and with it the order
-// in which their gradients are summed.
-bool whole_all(const marble_plan_t* pl, int hq, bool scored) {
-  if (whole_slots(pl, hq) == 0) return false;
+// tiles of the pack's longest row
+int64_t longest_row(const marble_plan_t* pl) {
   int64_t longest = 0;
   for (int r = 0; r < pl->P; ++r)
     longest = std::max(longest, pl->h_step_max[(size_t)r * (pl->P + 1) + pl->P]);
-  return rows_balance(longest, pl->nnz, hq) ||
-         (scored && longest <= 4 * (int64_t)pl->P * pl->P);
+  return longest;
+}
+
+// every tile of the pack at once, with one dQ GEMM over all q blocks.  Scored calls take it for
+// rows that do not balance too: the P * P launches of the other way cost more than a GEMM that
+// ends with one long unit.  Fused backward, d = 128, capped, one causal sample, whole / other way
+// (us): 16 tiles a row, 4 heads, P = 2 83 / 127, P = 8 84 / 747; 64 tiles 312 / 539 and 313 / 1123;
+// 256 tiles 2949 / 4023 and 2947 / 7310; with P = 1 the two differ by 4% at most.  Step lists: 108 /
+// 123, 362 / 815; 343 / 369, 641 / 988; 3034 / 3004, 3811 / 4764.  Plain calls keep the choice they
+// had, and with it the order in which their gradients are summed.
+bool whole_all(const marble_plan_t* pl, int hq, bool scored) {
+  return whole_slots(pl, hq) != 0 && (scored || rows_balance(longest_row(pl), pl->nnz, hq));
 }
 
 int whole_plan(const marble_plan_t* pl, int hq, bool scored, int n_steps, const int* q_shards,
@@ -1663,6 +1668,23 @@ __global__ void k_group_sum(const float4* __restrict__ src, float4* __restrict__
 // from the library's pool for the length of a call.  Without room for them (the pool's, or the
 // scratch cap's) the heads of a group stay one unit, and `mem` null.
 struct GroupScratch {
+  // Is it worth it?  A launch over units of at most L items takes L items' time, or an SM's share
+  // of all items and half a unit more; an item takes 2.1 us (d = 128; 1.3 for d = 64).  Against
+  // what shorter units save stand two launches and four passes over the scratch, 0.65 us a MB.
+  // (A column's length is taken from the longest row: causal and bidirectional samples have rows
+  // and columns of the same lengths.)  Fused backward, d = 128, P = 4, split / not (us): 16 tiles a
+  // row, 16 blocks, 8 heads on 1 103 / 315, 2 on 1 94 / 118, 16 on 8 151 / 135; 256 tiles, 8 on 4 heads
+  // 5790 / 6411; rows of 4 tiles, 16 blocks, 2 on 1 64 / 64, 128 blocks 95 / 69.  Over 318 packs of
+  // 16 to 256 blocks, groups of 2, 4 and 8 and both head dims the rule's choice is 3% slower than
+  // the faster way at most.
+  static bool pays(const marble_plan_t* pl, const marble_qkv_t& qkv, int sms) {
+    const int64_t group = qkv.hq / qkv.hkv, one = longest_row(pl);
+    const int64_t share = (pl->nnz * qkv.hq + sms - 1) / sms;
+    auto items = [&](int64_t longest) { return (double)std::max(longest, share + longest / 2); };
+    const double mb = 8e-6 * pl->n * qkv.hq * qkv.d;
+    return (items(one * group) - items(one)) * (qkv.d == 128 ? 2.1 : 1.3) > 6 + 0.65 * mb;
+  }
+
   float* mem = nullptr;
   cudaStream_t stream = nullptr;
   int64_t n = 0;
@@ -1729,13 +1751,11 @@ marble_status_t launch_fused(const marble_plan_t* pl, const marble_qkv_t* qkv,
   const int sms = sm_count();
   const int P = pl->P;
   const int64_t hq = qkv->hq;
-  // Few units and grouped heads: every q head of a group gets a unit of its own, with dK/dV of its
-  // own in a scratch, which are added up in head order at the end (4096 tokens, 8/2 heads of 64:
-  // 64 units, the longest of 128 items, become 256; the backward 310 -> 165 us, and 120
-  // with one launch over every kv block).  Scored calls
-  // only: plain calls keep the order in which their gradients are summed.
+  // Few or long units and grouped heads: every q head of a group gets a unit of its own, with dK/dV
+  // of its own in a scratch, which are added up in head order at the end.  Scored calls only:
+  // plain calls keep the order in which their gradients are summed.
   GroupScratch split;
-  if (MOD != 0 && prm.group > 1 && (int64_t)pl->h_nwork_all[1] * qkv->hkv < sms) {
+  if (MOD != 0 && prm.group > 1 && GroupScratch::pays(pl, *qkv, sms)) {
     rc = split.open(pl, *qkv, &prm, s);
     if (rc != MARBLE_OK) return rc;
   }

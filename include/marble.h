@@ -558,11 +558,10 @@ typedef struct {
  * NULL, or with neither cap nor slopes, is the plain call.  The fused forward of few and long
  * rows works on up to 8 pieces of each at once and joins them (sums in another order than the
  * plain call's); their states, 4 * pieces * N * hq * (d + 2) bytes and at most about 1 GB, are in
- * the library's pool for the call's length.  The fused backward of a small pack with grouped heads
+ * the library's pool for the call's length.  The fused backward of few or long rows with grouped heads
  * takes 8 * N * hq * d bytes there, if they can be had within the scratch cap: the q heads of a
  * group are then worked on side by side.  Scored backward calls take whole rows (and with them
- * nnz * hq * 32 KB of dS tiles, up to the cap) also for rows of at most 4 P^2 tiles that do not
- * balance.  The launches take ticket counters and scratch of the plan: a
+ * nnz * hq * 32 KB of dS tiles, up to the cap) also for rows that do not balance.  The launches take ticket counters and scratch of the plan: a
  * stream that is being captured into a graph is refused (INVALID_ARG).
  */
 marble_status_t marble_attn_steps_scored(const marble_plan_t *plan, const marble_qkv_t *qkv,

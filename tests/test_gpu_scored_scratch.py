@@ -19,26 +19,33 @@ def _capped(monkeypatch, mb):
 
 
 def test_grouped_heads_without_room_for_their_scratch(monkeypatch):
-    """Grouped heads of few units have dK/dV of every q head in a scratch.  Where the cap leaves no
+    """Grouped heads of long units have dK/dV of every q head in a scratch.  Where the cap leaves no
     room for it the backward runs without, as it does where the allocation fails."""
-    n, hq, hkv, d, length = 8192, 32, 1, 128, 128
-    tr = wl.tracks_from_samples([[wl.Span("causal", length)]] * (n // length))
+    hq, hkv, d, length, mb = 32, 1, 128, 1024, 100
+    n = 4 * length
+    tr = wl.tracks_from_samples([[wl.Span("causal", length)]] * 4)
     q, k, v, do = _qkvdo(n, hq, hkv, d, 41)
     slopes = _slopes(hq, "usual")
-    pl = M.Plan(*device_tracks(tr), INF, 1)
-    tiles, group = pl.stats()["nnz"] * hq * 32768, 8 * n * hq * d
-    assert tiles < 100 << 20 < group
+    pl = M.Plan(*device_tracks(tr), INF, 4)
+    group = 8 * n * hq * d
+    assert mb << 20 < group
     score = M.Score(8.0, slopes)
-    _run(pl, q, k, v, do, score, fused=True)  # torch's own buffers, and results with the scratch
-    torch.cuda.synchronize()
-    _capped(monkeypatch, 100)
+
+    def pool():  # what the library holds beside torch; its pool keeps what a call has freed
+        torch.cuda.synchronize()
+        return -torch.cuda.mem_get_info()[0] - torch.cuda.memory_reserved()
+
+    _run(pl, q, k, v, do, score, fused=True)  # the plan's own scratch, kept from here on
     M.release_memory()
-    before = torch.cuda.mem_get_info()[0] + torch.cuda.memory_reserved()
+    start = pool()
+    _run(pl, q, k, v, do, score, fused=True)
+    assert pool() - start >= group
+    _capped(monkeypatch, mb)
+    M.release_memory()
+    start = pool()
     got = _run(pl, q, k, v, do, score, fused=True)
-    torch.cuda.synchronize()
-    held = before - torch.cuda.mem_get_info()[0] - torch.cuda.memory_reserved()
-    assert held < group  # the pool keeps what a call has freed
-    for a in (0, 5 * length, n - length):
+    assert pool() - start < group
+    for a in (0, n - length):
         cut = slice(a, a + length)
         sub = {x: np.asarray(tr[x])[cut] for x in ("sample", "seg", "noise")}
         part = (got[0][cut], got[1][:, cut]) + tuple(x[cut] for x in got[2:])
