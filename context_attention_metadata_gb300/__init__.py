@@ -560,8 +560,9 @@ def _qkv(plan, q, k, v, scale):
 
 class Score:
     """What happens to a score before the softmax (marble_score_t): ``cap`` c > 0 makes it
-    c tanh(score / c), ``slopes`` (fp32 CUDA tensor [hq]) then takes slopes[h] * |pos_q - pos_k|
-    off.  The same Score goes to every call of a pass, forward and backward."""
+    c tanh(score / c), ``slopes`` (fp32 CUDA tensor [hq], 16-byte aligned: a slice of a longer table
+    may need a clone()) then takes slopes[h] * |pos_q - pos_k| off.  The same Score goes to every
+    call of a pass, forward and backward."""
 
     def __init__(self, cap: float = 0.0, slopes=None):
         import torch

@@ -718,7 +718,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           }
         }
         // P = exp2(s - m_run) as bf16, packed into columns [64 half, 64 half + 32) of the S
-        // buffer: inside the fp32 columns this warp has just read
+        // buffer: inside the fp32 columns this warp has just read.  bf16 because the tensor core
+        // wants both operands of one type and V is bf16 (two products for the upper and the lower
+        // bits of P would double PV): against 64 bits O is off by 0.0023 of its norm, where its own
+        // rounding alone makes 0.0017.  The row sum takes P as it was.
         [[maybe_unused]] const float base = m_run == -INFINITY ? 0.f : m_run;
         // v holds scaled scores where keys were masked, raw ones otherwise
         [[maybe_unused]] const float vs = (MOD != 0 || masked) ? 1.f : sl2;

@@ -19,12 +19,12 @@
 //     2^-14 (kWideCap), a score with |y| <= 0.875 takes the polynomial here too, score by score.
 // The bias has no part in this choice: whether it is linear over the tile (the tile off the
 // diagonal block, and no position track) decides only how the distances are had.
-// The special function unit is what these two spare: it gives 16 results a clock on an SM, where
-// multiply-adds have 128, and the softmax's exp2 takes one a score.  A forward over 64K packed
-// tokens (16 heads of 128) takes 1669 us without a cap, 1670 with nearly every tile within the
-// four-term range (cap 50), 1855 within the six-term one (cap 18), 2407 where most tiles go
-// through the exponential (cap 5); the dK/dV kernel 3046, 3645, 3659 and 4287 us.  A polynomial in
-// y instead of x needs one multiplication more a score: 3 to 9% slower.
+// The special function unit is what these two spare: an SM takes 32 exp2 or 16 reciprocals a
+// clock (measured), 125 multiply-adds, and the softmax's exp2 takes one a score.  A forward over
+// 64K packed tokens (16 heads of 128) takes 1667 us without a cap, 1597 with nearly every tile
+// within the four-term range (cap 50), 1770 within the six-term one (cap 18), 2290 where most
+// tiles go through the exponential (cap 5); the dK/dV kernel 3040, 3630, 3610 and 4300 us.  A
+// polynomial in y instead of x needs one multiplication more a score: 3 to 9% slower.
 // Folded coefficients leave fp32's range for caps far from the scores' size; set_cap then lowers
 // the first two ways' limits to where the lost terms do not matter.
 #pragma once
@@ -55,8 +55,8 @@ enum : int { kScoreCap = 1, kScoreBias = 2, kScoreFixed = 4 };
 // weights 2^s can be below fp32's range, and keeps the running maximum.  (A piece of a row
 // without the own key may lose its weights, which beside that key's are below 2^-46.)
 // Saved are the maximum, its exchange between the two warps of a row and the rescaling (forward of
-// 64K packed tokens, 16 heads of 128: cap 50 2000 -> 1670 us, cap 18 2190 -> 1855, cap 50 with a
-// bias 2517 -> 2117).
+// 64K packed tokens, 16 heads of 128: cap 60, which keeps them, 1977 us, cap 50 1597; with a bias
+// 2600 and 2045).
 constexpr float kFixedCap = 80.f;
 
 // cap2 above which a small score must not take the exponential's absolute error, 2^-22 cap2 (at

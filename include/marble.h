@@ -542,9 +542,9 @@ marble_status_t marble_attn_bwd_fused(const marble_plan_t *plan, const marble_qk
  * (keys of a row) in size, or 0: in rows whose scores all are near +cap the sums of larger ones can
  * overflow, and in rows whose scores all are near -cap smaller ones lose bits (with lower caps, or
  * scores away from the cap, the range is wider by as much).  The backward calls give the
- * gradients of q, k and v through cap and bias.  slopes are constants: finite, of any sign, no
- * gradient.  They are read when the kernels run.  Q, K, V and dO have to be finite for masked
- * tokens too, as for the plain calls.
+ * gradients of q, k and v through cap and bias.  slopes are constants: of any sign, their
+ * products with the distances within fp32's range, no gradient.  They are read when the kernels
+ * run.  Q, K, V and dO have to be finite for masked tokens too, as for the plain calls.
  */
 typedef struct {
   float cap;           /* 0, or in [1e-30, 1e30] */
@@ -558,11 +558,12 @@ typedef struct {
  * NULL, or with neither cap nor slopes, is the plain call.  The fused forward of few and long
  * rows works on up to 8 pieces of each at once and joins them (sums in another order than the
  * plain call's); their states, 4 * pieces * N * hq * (d + 2) bytes and at most about 1 GB, are in
- * the library's pool for the call's length.  The fused backward of few or long rows with grouped heads
- * takes 8 * N * hq * d bytes there, if they can be had within the scratch cap: the q heads of a
- * group are then worked on side by side.  Scored backward calls take whole rows (and with them
- * nnz * hq * 32 KB of dS tiles, up to the cap) also for rows that do not balance.  The launches take ticket counters and scratch of the plan: a
- * stream that is being captured into a graph is refused (INVALID_ARG).
+ * the library's pool for the call's length.  The fused backward of few or long rows with grouped
+ * heads takes 8 * N * hq * d bytes there, if they can be had within the scratch cap: the q heads of
+ * a group are then worked on side by side.  Scored backward calls take whole rows (and with them
+ * nnz * hq * 32 KB of dS tiles, up to the cap) also for rows that do not balance.  The launches
+ * take ticket counters and scratch of the plan: a stream that is being captured into a graph is
+ * refused (INVALID_ARG).
  */
 marble_status_t marble_attn_steps_scored(const marble_plan_t *plan, const marble_qkv_t *qkv,
                                          const marble_score_t *score, int32_t n_steps,
