@@ -37,8 +37,8 @@ import time
 # with the digest of the kernel's source files at the time of the capture: a figure is
 # reported only while the source is unchanged, null otherwise.
 KERNEL_DRAM_BYTES_PER_LAUNCH = {
-    "k_bwd_dkdv": (469.3e6, "profiles/k_bwd_dkdv_packed_multimodal.md", "ff573c7ae7e12bdf"),
-    "k_bwd_dq": (12844.1e6, "profiles/k_bwd_dq_packed_multimodal.md", "ff573c7ae7e12bdf"),
+    "k_bwd_dkdv": (469.1e6, "profiles/k_bwd_dkdv_packed_multimodal.md", "5492cf12ef51c313"),
+    "k_bwd_dq": (12880.0e6, "profiles/k_bwd_dq_packed_multimodal.md", "5492cf12ef51c313"),
     "k_attn_fwd": (151.1e6, "profiles/k_attn_fwd_packed_multimodal.md", "d15512e18a5d16d2"),
 }
 KERNEL_SOURCES = {"k_bwd_dkdv": ("attn_bwd.cu", "common.cuh", "score.cuh"),

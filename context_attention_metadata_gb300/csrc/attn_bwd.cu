@@ -1678,7 +1678,7 @@ __global__ void k_group_sum(const float4* __restrict__ src, float4* __restrict__
 // scratch cap's) the heads of a group stay one unit, and `mem` null.
 struct GroupScratch {
   // Is it worth it?  A launch over units of at most L items takes L items' time, or an SM's share
-  // of all items and half a unit more; an item takes 2.1 us (d = 128; 1.3 for d = 64).  Against
+  // of all items and half a unit more; an item takes 2.1 us (d = 128; 1.4 for d = 64).  Against
   // what shorter units save stand two launches and four passes over the scratch, 0.65 us a MB.
   // (A column's length is taken from the longest row: causal and bidirectional samples have rows
   // and columns of the same lengths.)  Fused backward, d = 128, P = 4, split / not (us): 16 tiles a
@@ -1691,7 +1691,7 @@ struct GroupScratch {
     const int64_t share = (pl->nnz * qkv.hq + sms - 1) / sms;
     auto items = [&](int64_t longest) { return (double)std::max(longest, share + longest / 2); };
     const double mb = 8e-6 * pl->n * qkv.hq * qkv.d;
-    return (items(one * group) - items(one)) * (qkv.d == 128 ? 2.1 : 1.3) > 6 + 0.65 * mb;
+    return (items(one * group) - items(one)) * (qkv.d == 128 ? 2.1 : 1.4) > 6 + 0.65 * mb;
   }
 
   float* mem = nullptr;
