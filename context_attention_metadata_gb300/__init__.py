@@ -103,6 +103,34 @@ class _Score(ctypes.Structure):
     _fields_ = [("cap", ctypes.c_float), ("slopes", ctypes.c_void_p)]
 
 
+CACHE_TYPES = {"bfloat16": 0, "float8_e4m3fn": 1, "int8": 2}
+SEQS_TIMEOUT, SEQS_BAD = 1, 2  # bits of Sequences.status
+ATTN_CACHED_WORKSPACE_BYTES = 25165824
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_scale_stride", ctypes.c_int64), ("v_scale_stride", ctypes.c_int64)]
+
+
+class _Seqs(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("table_pages", ctypes.c_int32),
+                ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("start", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
+class _AttnCached(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("o", ctypes.c_void_p),
+                ("o_stride", ctypes.c_int64), ("lse", ctypes.c_void_p), ("hq", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("window", ctypes.c_int32), ("span", ctypes.c_int32),
+                ("new_tokens", ctypes.c_int32), ("workspace", ctypes.c_void_p)]
+
+
 _lib = None
 
 # every symbol the header declares, with its ctypes signature
@@ -167,6 +195,13 @@ _SIGS = {
                                       ctypes.POINTER(_Score), ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                       ctypes.c_void_p, ctypes.c_void_p]),
+    "marble_cache_write": ([ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(_Cache),
+                            ctypes.POINTER(_Seqs), ctypes.POINTER(_Heads), ctypes.c_void_p]),
+    "marble_cache_read": ([ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(_Cache),
+                           ctypes.POINTER(_Seqs), ctypes.POINTER(_Heads), ctypes.c_void_p]),
+    "marble_attn_cached": ([ctypes.c_int64, ctypes.POINTER(_Cache), ctypes.POINTER(_Seqs),
+                            ctypes.POINTER(_AttnCached), ctypes.POINTER(_Score),
+                            ctypes.c_void_p]),
     "marble_cast_bf16": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
     "marble_check": ([ctypes.c_void_p, ctypes.c_void_p]),
     "marble_set_wait_limit_ns": ([ctypes.c_uint64]),
@@ -802,6 +837,215 @@ def backward(plan: Plan, q, k, v, o, do, lse, delta, dq_acc, dk_acc, dv_acc,
     else:
         attn_bwd_steps(plan, q, k, v, do, lse, delta, ring_schedule(plan.num_shards, needed),
                        dq_acc, dk_acc, dv_acc, scale=scale, stream=stream, score=score)
+
+
+class Cache:
+    """A paged key-value cache (marble_cache_t) in the caller's tensors: ``k`` and ``v``
+    [pages, hkv, page_tokens, d] in bfloat16, float8_e4m3fn or int8, and for the 8-bit types
+    ``k_scale`` and ``v_scale``, fp32 [pages, hkv, page_tokens].  Only the first dimension may be
+    strided: one pool [pages, 2, hkv, page_tokens, d] holds both as pool[:, 0] and pool[:, 1].
+    ``empty()`` makes the tensors."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        kind = CACHE_TYPES.get(str(getattr(k, "dtype", "")).replace("torch.", ""))
+        if kind is None or k.dim() != 4 or not k.is_cuda:
+            raise ValueError("k must be a CUDA tensor [pages, hkv, page_tokens, d] of bfloat16, "
+                             "float8_e4m3fn or int8")
+        parts = [(k, "k", k.dtype, k.shape), (v, "v", k.dtype, k.shape)]
+        if kind:
+            parts += [(t, nm, torch.float32, k.shape[:3])
+                      for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale"))]
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        strides = []
+        for t, nm, dtype, shape in parts:
+            if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or \
+                    t.device != k.device:
+                raise ValueError(f"{nm} must be {dtype} {tuple(shape)} on {k.device}")
+            size = t[0].numel() if shape[0] else 0
+            if shape[0] and not t[0].is_contiguous():
+                raise ValueError(f"{nm}: a page must be contiguous")
+            strides.append(t.stride(0) if shape[0] > 1 else size)
+        strides += [0, 0]
+        self._parts = (k, v, k_scale, v_scale)
+        self._index = k.get_device()
+        self._c = _Cache(kind, k.shape[1], k.shape[3], k.shape[2], k.shape[0], k.data_ptr(),
+                         v.data_ptr(), strides[0], strides[1],
+                         k_scale.data_ptr() if kind else None,
+                         v_scale.data_ptr() if kind else None, strides[2], strides[3])
+        self._shape = (k.shape[1], k.shape[3])
+
+    @classmethod
+    def empty(cls, pages, hkv, page_tokens, d, dtype=None, device="cuda"):
+        """A cache in new tensors; ``dtype`` None: bfloat16."""
+        import torch
+        dtype = torch.bfloat16 if dtype is None else dtype
+        pool = torch.empty((pages, 2, hkv, page_tokens, d), dtype=dtype, device=device)
+        if dtype == torch.bfloat16:
+            return cls(pool[:, 0], pool[:, 1])
+        scale = torch.empty((pages, 2, hkv, page_tokens), device=device)
+        return cls(pool[:, 0], pool[:, 1], scale[:, 0], scale[:, 1])
+
+    # (the C descriptor holds these tensors' addresses: they cannot be exchanged, and a copy is
+    # made from its own tensors)
+    k = property(lambda self: self._parts[0])
+    v = property(lambda self: self._parts[1])
+    k_scale = property(lambda self: self._parts[2])
+    v_scale = property(lambda self: self._parts[3])
+
+    def __reduce__(self):
+        return Cache, self._parts
+
+
+class Sequences:
+    """The sequences of a batch and the rows of a call (marble_seqs_t), in the caller's int32 CUDA
+    tensors: ``table`` [n_seqs, table_pages] (rows may be strided), ``lens`` [n_seqs] (the call's
+    tokens counted), ``start`` [n_seqs + 1] or None (one row a sequence).  Their values are read
+    when the kernels run; update them in place from step to step.  ``status`` (int32 [1], zeroed
+    by the caller, or None) collects SEQS_* bits; check() reads it."""
+
+    def __init__(self, table, lens, start=None, status=None):
+        import torch
+        if getattr(table, "dtype", None) is not torch.int32 or table.dim() != 2 or \
+                not table.is_cuda or (table.shape[1] > 1 and table.stride(1) != 1):
+            raise ValueError("table must be an int32 CUDA tensor [n_seqs, table_pages], its rows "
+                             "contiguous")
+        n, width = table.shape
+        _need(lens, torch.int32, "lens", (n,))
+        if start is not None:
+            _need(start, torch.int32, "start", (n + 1,))
+        if status is not None:
+            _need(status, torch.int32, "status", (1,))
+        for t, nm in ((lens, "lens"), (start, "start"), (status, "status")):
+            if t is not None and t.device != table.device:
+                raise ValueError(f"{nm} must be on {table.device}")
+        self._parts = (table, lens, start, status)
+        self._index = table.get_device()
+        self._c = _Seqs(n, width, table.data_ptr(), table.stride(0) if n > 1 else width,
+                        lens.data_ptr(), None if start is None else start.data_ptr(),
+                        None if status is None else status.data_ptr())
+        self._one = start is None
+
+    table = property(lambda self: self._parts[0])
+    lens = property(lambda self: self._parts[1])
+    start = property(lambda self: self._parts[2])
+    status = property(lambda self: self._parts[3])
+
+    def __reduce__(self):
+        return Sequences, self._parts
+
+    def check(self):
+        """Wait for the status word and raise for what it holds."""
+        bits = 0 if self.status is None else int(self.status.item())
+        if bits & SEQS_TIMEOUT:
+            raise MarbleError(ERR_TIMEOUT, "a bounded wait in marble_attn_cached ran out")
+        if bits & SEQS_BAD:
+            raise MarbleError(ERR_INVALID_ARG, "table, lens or start were out of bounds")
+
+
+def _cache_move(name, cache, seqs, parts, plan, stream, what):
+    import torch
+    index = cache._index
+    if seqs._index != index:
+        raise ValueError(f"the sequences must be on cuda:{index}")
+    if plan is not None and plan.handle is None:  # NULL would be "no plan"
+        raise ValueError("the plan is closed")
+    first = parts[0] if parts[0] is not None else parts[1]
+    if first is None:
+        raise ValueError(f"{what}k or {what}v is needed")
+    n = first.shape[0]
+    heads = _heads((None, *parts), n, torch.bfloat16, index, what)
+    if (heads.hkv, heads.d) != cache._shape:
+        raise ValueError(f"{what}k and {what}v must be [n, {cache._shape[0]}, {cache._shape[1]}]")
+    _call(name, None if plan is None else plan.handle, n, ctypes.byref(cache._c),
+          ctypes.byref(seqs._c), ctypes.byref(heads), _raw_stream(torch, stream, index))
+
+
+def cache_write(cache: Cache, seqs: Sequences, k, v=None, plan: Optional[Plan] = None,
+                stream=None):
+    """Write the rows of k and v (bf16 [n, hkv, d], a token's heads contiguous, e.g. what rope()
+    returns; either may be None) into the cache, quantised on the way (marble_cache_write).  With
+    a plan they are in plan order."""
+    _cache_move("marble_cache_write", cache, seqs, (k, v), plan, stream, "")
+
+
+def cache_read(cache: Cache, seqs: Sequences, n: Optional[int] = None,
+               plan: Optional[Plan] = None, out=None, stream=None):
+    """Read rows back (marble_cache_read): (k, v), bf16 [n, hkv, d], ``out`` or new tensors (``n``
+    rows; None: the plan's, or one a sequence).  With a plan they are in plan order; rows of no
+    sequence are left as they are (zeros in new tensors)."""
+    import torch
+    if out is None:
+        if n is None:
+            if plan is None and not seqs._one:
+                raise ValueError("n, the number of rows, is needed")
+            n = plan.n if plan is not None else seqs.lens.shape[0]
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            out = tuple(torch.zeros((n, *cache._shape), dtype=torch.bfloat16,
+                                    device=cache.k.device) for _ in range(2))
+    elif len(out) != 2:
+        raise ValueError("out must hold k and v (either may be None)")
+    elif n is not None and any(t is not None and t.shape[0] != n for t in out):
+        raise ValueError("out must have n rows")
+    _cache_move("marble_cache_read", cache, seqs, tuple(out), plan, stream, "out ")
+    return tuple(out)
+
+
+def attn_cached(cache: Cache, seqs: Sequences, q, scale: float = 0.0, window: int = WINDOW_INF,
+                span: bool = False, score: Optional[Score] = None, new_tokens: int = 0, out=None,
+                workspace=None, stream=None):
+    """Attention of the sequences' last tokens over their cached keys and values
+    (marble_attn_cached): q [n, hq, d] bf16, a token's heads contiguous.  Write the tokens' own
+    keys and values first.  ``window``, ``scale`` and ``score`` as in the packed calls; ``span``:
+    the rows of a sequence all see each other; ``new_tokens``: how many rows a sequence has at
+    most, a hint (0: n over the number of sequences).  ``workspace``: uint8 CUDA tensor of
+    ATTN_CACHED_WORKSPACE_BYTES for this call alone, or None (torch's allocator).
+    Returns (o, lse), bf16 [n, hq, d] and fp32 [hq, n]: ``out`` (its lse may be None) or new
+    tensors; rows of no sequence are left as they are (undefined in new tensors)."""
+    import torch
+    index = cache._index
+    bf16 = torch.bfloat16
+    try:
+        n, hq, d = q.shape
+        sq = q.stride()
+        ok = q.dtype is bf16 and q.get_device() == index and \
+            (n == 0 or (sq[2] == 1 and (hq == 1 or sq[1] == d)))
+    except (AttributeError, ValueError, TypeError):
+        ok = False
+    if not ok or d != cache._shape[1]:
+        raise ValueError(f"q must be a bf16 tensor [n, hq, {cache._shape[1]}] on cuda:{index}, "
+                         "each token's heads contiguous")
+    if seqs._index != index:
+        raise ValueError(f"the sequences must be on cuda:{index}")
+    if out is None or workspace is None:
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            if out is None:
+                out = (torch.empty((n, hq, d), dtype=bf16, device=q.device),
+                       torch.empty((hq, n), dtype=torch.float32, device=q.device))
+            if workspace is None:
+                workspace = torch.empty(ATTN_CACHED_WORKSPACE_BYTES, dtype=torch.uint8,
+                                        device=q.device)
+    o, lse = out
+    so = o.stride()
+    if o.dtype is not bf16 or o.shape != q.shape or o.get_device() != index or \
+            (n > 0 and (so[2] != 1 or (hq > 1 and so[1] != d))):
+        raise ValueError("o must be a bf16 tensor of q's shape and device, each token's heads "
+                         "contiguous")
+    if lse is not None:
+        _need(lse, torch.float32, "lse", (hq, n))
+    if workspace.numel() * workspace.element_size() < ATTN_CACHED_WORKSPACE_BYTES or \
+            workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be {ATTN_CACHED_WORKSPACE_BYTES} bytes on cuda:{index}")
+    width = hq * d
+    if new_tokens <= 0:
+        new_tokens = -(-n // max(1, seqs._c.n_seqs)) or 1
+    c = _AttnCached(q.data_ptr(), sq[0] if n > 1 else width, o.data_ptr(),
+                    so[0] if n > 1 else width, None if lse is None else lse.data_ptr(), hq,
+                    scale, window, 1 if span else 0, new_tokens, workspace.data_ptr())
+    _call("marble_attn_cached", n, ctypes.byref(cache._c), ctypes.byref(seqs._c), ctypes.byref(c),
+          None if score is None else ctypes.byref(score._c(hq)), _raw_stream(torch, stream, index))
+    return o, lse
 
 
 def layout_vision_groups(sample, seg):

@@ -896,6 +896,169 @@ MARBLE_API marble_status_t marble_rope_bwd(const marble_plan_t* p, int64_t n,
   return MARBLE_OK;
 }
 
+// a score descriptor (null: none)
+static marble_status_t check_score(const marble_score_t* score) {
+  if (!score) return MARBLE_OK;
+  if (score->cap != 0.f && !(score->cap >= 1e-30f && score->cap <= 1e30f))
+    return fail(MARBLE_ERR_INVALID_ARG, "score.cap must be 0 (none) or in [1e-30, 1e30]");
+  return score->slopes ? check_here(score->slopes, "score.slopes", 16) : MARBLE_OK;
+}
+
+// ------------------------------------------------------------------------------------
+// the paged cache
+// ------------------------------------------------------------------------------------
+namespace {
+
+// the pages of k and v as rows (and of their scales)
+marble_status_t check_cache(const marble_cache_t* c, const marble_seqs_t* s, int64_t n,
+                            Rows (&pages)[4]) {
+  if (!c || !s) return fail(MARBLE_ERR_INVALID_ARG, "cache and seqs must be non-null");
+  if (n < 0 || n >= (int64_t)INT_MAX)
+    return fail(MARBLE_ERR_INVALID_ARG, "n_tokens must be in [0, 2^31 - 1)");
+  if (c->type != MARBLE_CACHE_BF16 && c->type != MARBLE_CACHE_E4M3 && c->type != MARBLE_CACHE_INT8)
+    return fail(MARBLE_ERR_INVALID_ARG, "unknown cache type");
+  if (c->d != 64 && c->d != 128) return fail(MARBLE_ERR_INVALID_ARG, "head dim d must be 64 or 128");
+  if (c->hkv < 1 || c->hkv > 65536)
+    return fail(MARBLE_ERR_INVALID_ARG, "hkv must be in [1, 65536]");
+  if (c->page_tokens < 16 || c->page_tokens % 16 || c->page_tokens > 65536)
+    return fail(MARBLE_ERR_INVALID_ARG, "page_tokens must be a multiple of 16 in [16, 65536]");
+  if (c->n_pages < 1 || c->n_pages >= (int64_t)INT_MAX)
+    return fail(MARBLE_ERR_INVALID_ARG, "n_pages must be in [1, 2^31 - 1)");
+  const bool quant = c->type != MARBLE_CACHE_BF16;
+  const int es = quant ? 1 : 2;
+  const int64_t heads = (int64_t)c->hkv * c->page_tokens;
+  for (int64_t stride : {c->k_stride, c->v_stride})
+    if (stride < heads * c->d || stride * es % 16 || stride >= ((int64_t)1 << 40) / es)
+      return fail(MARBLE_ERR_INVALID_ARG,
+                  "a page stride must hold the page's heads, be a multiple of 16 bytes and under "
+                  "2^40 bytes");
+  if (quant)
+    for (int64_t stride : {c->k_scale_stride, c->v_scale_stride})
+      if (stride < heads || stride % 4 || stride >= ((int64_t)1 << 38))
+        return fail(MARBLE_ERR_INVALID_ARG,
+                    "a page stride of the scales must hold the page's heads and be a multiple of 4");
+  if (s->n_seqs < 0 || s->n_seqs >= INT_MAX || s->table_pages < 1 ||
+      s->table_stride < s->table_pages || s->table_stride > ((int64_t)1 << 31))
+    return fail(MARBLE_ERR_INVALID_ARG,
+                "n_seqs must be >= 0, table_pages >= 1 and table_stride at least table_pages");
+  if (!s->start && n != s->n_seqs)
+    return fail(MARBLE_ERR_INVALID_ARG, "without start there is one row a sequence");
+  if (n == 0 || s->n_seqs == 0) return MARBLE_OK;
+  marble_status_t st;
+  if ((st = check_here(c->k, "cache.k", 16)) != MARBLE_OK) return st;
+  if ((st = check_here(c->v, "cache.v", 16)) != MARBLE_OK) return st;
+  pages[0] = Rows{static_cast<const char*>(c->k), c->k_stride * es, heads * c->d * es};
+  pages[1] = Rows{static_cast<const char*>(c->v), c->v_stride * es, heads * c->d * es};
+  if (quant) {
+    if ((st = check_here(c->k_scale, "cache.k_scale", 16)) != MARBLE_OK) return st;
+    if ((st = check_here(c->v_scale, "cache.v_scale", 16)) != MARBLE_OK) return st;
+    pages[2] = Rows{reinterpret_cast<const char*>(c->k_scale), c->k_scale_stride * 4, heads * 4};
+    pages[3] = Rows{reinterpret_cast<const char*>(c->v_scale), c->v_scale_stride * 4, heads * 4};
+  }
+  for (int i = 0; i < (quant ? 4 : 2); ++i)
+    for (int j = 0; j < i; ++j)
+      if (rows_meet(pages[i], pages[j], c->n_pages))
+        return fail(MARBLE_ERR_INVALID_ARG, "the tensors of the cache overlap each other");
+  if ((st = check_here(s->table, "seqs.table", 4)) != MARBLE_OK) return st;
+  if ((st = check_here(s->lens, "seqs.lens", 4)) != MARBLE_OK) return st;
+  if (s->start && (st = check_here(s->start, "seqs.start", 4)) != MARBLE_OK) return st;
+  if (s->status && (st = check_here(s->status, "seqs.status", 4)) != MARBLE_OK) return st;
+  return MARBLE_OK;
+}
+
+// do n rows meet the cache's pages?  (by their whole ranges)
+bool meets_cache(const Rows& r, int64_t n, const marble_cache_t* c, const Rows (&pages)[4]) {
+  const char* end = r.base + (n - 1) * r.stride + r.width;
+  for (const Rows& p : pages)
+    if (p.base && r.base < p.base + (c->n_pages - 1) * p.stride + p.width && p.base < end) return true;
+  return false;
+}
+
+marble_status_t cache_move(bool write, const char* name, const marble_plan_t* p, int64_t n,
+                           const marble_cache_t* cache, const marble_seqs_t* seqs,
+                           const marble_heads_t* heads, marble_stream_t stream) {
+  Rows pages[4] = {};
+  marble_status_t st = check_cache(cache, seqs, n, pages);
+  if (st != MARBLE_OK) return st;
+  if (!heads) return fail(MARBLE_ERR_INVALID_ARG, "the heads must be non-null");
+  if (heads->d != cache->d || heads->hkv != cache->hkv)
+    return fail(MARBLE_ERR_INVALID_ARG, "the heads are not the cache's");
+  if (p) {
+    if (n != p->n) return fail(MARBLE_ERR_INVALID_ARG, "n_tokens is not the plan's");
+    if ((st = check_plan_here(p)) != MARBLE_OK) return st;
+  }
+  const int parts = (heads->k ? 2 : 0) | (heads->v ? 4 : 0);
+  if (n == 0 || parts == 0 || seqs->n_seqs == 0) return MARBLE_OK;
+  Rows r[3];
+  if ((st = check_heads(heads, write ? "src" : "dst", 2, parts, n, r)) != MARBLE_OK) return st;
+  for (int i = 1; i < 3; ++i)
+    if ((parts >> i & 1) && meets_cache(r[i], n, cache, pages))
+      return fail(MARBLE_ERR_INVALID_ARG, "the rows overlap the cache");
+  if (!write && parts == 6 && rows_meet(r[1], r[2], n))
+    return fail(MARBLE_ERR_INVALID_ARG, "the tensors written overlap each other");
+  bool cap = false;
+  if ((st = capturing((cudaStream_t)stream, &cap)) != MARBLE_OK) return st;
+  const cudaError_t e = launch_cache(write, p, n, cache, seqs, heads, (cudaStream_t)stream);
+  if (p && !cap) plan_used(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  return MARBLE_OK;
+}
+
+}  // namespace
+
+MARBLE_API marble_status_t marble_cache_write(const marble_plan_t* p, int64_t n,
+                                              const marble_cache_t* cache,
+                                              const marble_seqs_t* seqs, const marble_heads_t* src,
+                                              marble_stream_t stream) {
+  NvtxRange nvtx_("marble_cache_write");
+  return cache_move(true, "marble_cache_write launch", p, n, cache, seqs, src, stream);
+}
+
+MARBLE_API marble_status_t marble_cache_read(const marble_plan_t* p, int64_t n,
+                                             const marble_cache_t* cache, const marble_seqs_t* seqs,
+                                             const marble_heads_t* dst, marble_stream_t stream) {
+  NvtxRange nvtx_("marble_cache_read");
+  return cache_move(false, "marble_cache_read launch", p, n, cache, seqs, dst, stream);
+}
+
+MARBLE_API marble_status_t marble_attn_cached(int64_t n, const marble_cache_t* cache,
+                                              const marble_seqs_t* seqs,
+                                              const marble_attn_cached_t* a,
+                                              const marble_score_t* score,
+                                              marble_stream_t stream) {
+  NvtxRange nvtx_("marble_attn_cached");
+  Rows pages[4] = {};
+  marble_status_t st = check_cache(cache, seqs, n, pages);
+  if (st != MARBLE_OK) return st;
+  if (!a) return fail(MARBLE_ERR_INVALID_ARG, "attn is null");
+  if (a->hq < 1 || a->hq > 65536 || a->hq % cache->hkv)
+    return fail(MARBLE_ERR_INVALID_ARG, "hq must be a positive multiple of hkv, at most 65536");
+  if (n * a->hq >= (int64_t)INT_MAX)
+    return fail(MARBLE_ERR_INVALID_ARG, "n_tokens * hq must be below 2^31 - 1");
+  if (a->window < 0 || a->new_tokens < 1)
+    return fail(MARBLE_ERR_INVALID_ARG, "window must be >= 0 and new_tokens >= 1");
+  if (std::isnan(a->scale) || std::isinf(a->scale))
+    return fail(MARBLE_ERR_INVALID_ARG, "scale must be finite");
+  if ((st = check_score(score)) != MARBLE_OK) return st;
+  if (n == 0 || seqs->n_seqs == 0) return MARBLE_OK;
+  marble_heads_t h = {};
+  h.hq = a->hq;
+  h.hkv = cache->hkv;
+  h.d = cache->d;
+  Rows q[3], o[3];
+  h.q = const_cast<void*>(a->q);
+  h.q_stride = a->q_stride;
+  if ((st = check_heads(&h, "attn", 2, 1, n, q)) != MARBLE_OK) return st;
+  h.q = a->o;
+  h.q_stride = a->o_stride;
+  if ((st = check_heads(&h, "output", 2, 1, n, o)) != MARBLE_OK) return st;
+  if (rows_meet(q[0], o[0], n) || meets_cache(o[0], n, cache, pages))
+    return fail(MARBLE_ERR_INVALID_ARG, "o overlaps q or the cache");
+  if (a->lse && (st = check_here(a->lse, "attn.lse", 4)) != MARBLE_OK) return st;
+  if ((st = check_here(a->workspace, "attn.workspace", 16)) != MARBLE_OK) return st;
+  return run_attn_cached(n, cache, seqs, a, score, (cudaStream_t)stream);
+}
+
 constexpr uint32_t kMergeBits = MARBLE_STEP_BF16_MERGE | MARBLE_STEP_FP32_MERGE;
 
 // known bits only, and at most one merge variant
@@ -938,11 +1101,7 @@ static marble_status_t check_score(const marble_plan_t* p, const marble_score_t*
                                    marble_stream_t stream) {
   if (!p) return fail(MARBLE_ERR_INVALID_ARG, "plan is null");
   marble_status_t st;
-  if (score) {
-    if (score->cap != 0.f && !(score->cap >= 1e-30f && score->cap <= 1e30f))
-      return fail(MARBLE_ERR_INVALID_ARG, "score.cap must be 0 (none) or in [1e-30, 1e30]");
-    if (score->slopes && (st = check_here(score->slopes, "score.slopes", 16)) != MARBLE_OK) return st;
-  }
+  if ((st = check_score(score)) != MARBLE_OK) return st;
   if ((st = check_plan_here(p)) != MARBLE_OK) return st;
   bool cap = false;
   if ((st = capturing((cudaStream_t)stream, &cap)) != MARBLE_OK) return st;

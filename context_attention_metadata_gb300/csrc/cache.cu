@@ -1,0 +1,281 @@
+// The paged key-value cache: rows written into it, quantised on the way, and read back.
+//
+// With `top` the largest |channel| of a token's head, x a channel:
+//   e4m3:  s = 2^e, the smallest with top <= 448 s;   code = x / s rounded to e4m3
+//   int8:  s = top / 127;                             code = x * 127 / top rounded to an integer
+// and back: bf16(code * s).
+//
+// Both kernels are bound by memory: 2 bytes a channel on one side, 2 or 1 on the other.  A thread
+// holds 16 channels of a head, d / 16 lanes a head, so that `top` is a butterfly and a code's
+// store or load is 16 bytes.  A warp resolves where the tokens of a run of rows are cached with a
+// lane for each (the table look-up is a chain of three loads), then moves them one after the
+// other, its group of heads of k and of v side by side.
+#include <algorithm>
+#include <cstring>
+
+#include "seqs.cuh"
+
+namespace marble {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+struct CachePart {
+  char* rows;              // bf16 [n, hkv, d], null: not in the call
+  char* pages;
+  float* scale;
+  long long row_bytes, page_bytes, scale_stride;
+};
+
+struct CacheParams {
+  CachePart part[2];       // k, v
+  SeqsParams seqs;
+  const int32_t* perm;     // plan index -> original index, or null
+  int hkv, groups;         // heads, and warp iterations over them
+  int run, split;          // rows of a warp's run, warps a run
+};
+
+// where the token of row i is: its page (-1: none, -2: the row belongs to no sequence) and slot
+struct Place {
+  int page, slot;
+};
+__device__ __forceinline__ Place place_of(const SeqsParams& s, long long row) {
+  int b = (int)row;
+  if (s.start) {
+    // the sequence whose rows end first behind `row`
+    int lo = 0, hi = s.n_seqs;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(s.start + mid + 1) <= row) lo = mid + 1; else hi = mid;
+    }
+    b = lo;
+  }
+  if (b >= s.n_seqs) return {-2, 0};
+  const Seq q = seq_at<true>(s, b);
+  const long long at = row - q.first;
+  if (at < 0 || at >= q.count) return {-2, 0};
+  const long long pos = (long long)q.len - q.count + at;
+  if (pos < 0) return {-1, 0};
+  const int page = page_at(s, b, (int)pos);
+  if (page < 0) seqs_bad(s);
+  return {page, (int)(pos % s.page)};
+}
+
+__device__ __forceinline__ uint32_t hmax2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// the largest |channel| of a head, as bf16 bits (a NaN's if there is one)
+template <int D>
+__device__ __forceinline__ uint32_t top_bits(const uint32_t (&w)[8]) {
+  uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = hmax2_nan(m, w[i] & 0x7fff7fffu);
+#pragma unroll
+  for (int off = D / 32; off > 0; off >>= 1) m = hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+  return hmax2_nan(m, m >> 16 | m << 16) & 0xffffu;
+}
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// 16 bf16 channels -> 16 codes; the scale of their head
+template <int D, int kType>
+__device__ __forceinline__ uint4 quantise(const uint32_t (&w)[8], float* scale) {
+  const uint32_t top = top_bits<D>(w);
+  uint32_t c[4] = {0, 0, 0, 0};
+  if (top >= 0x7f80u) {
+    *scale = __uint_as_float(0x7fc00000u);
+    return make_uint4(0, 0, 0, 0);
+  }
+  if constexpr (kType == MARBLE_CACHE_E4M3) {
+    // 448 = 1.75 * 2^8; top's mantissa (7 bits) says whether its binade reaches beyond
+    const int e = max((int)(top >> 7) - ((top & 0x7fu) <= 0x60u ? 8 : 7), 1);
+    *scale = top ? __uint_as_float((uint32_t)e << 23) : 0.f;
+    const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint16_t two;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+          : "=h"(two)
+          : "f"(hi_f(w[i]) * inv), "f"(lo_f(w[i]) * inv));
+      c[i >> 1] |= (uint32_t)two << (16 * (i & 1));
+    }
+  } else {
+    *scale = __fdiv_rn(__uint_as_float(top << 16), 127.f);
+    // In units of 2^e, in which top is `at`, in [1, 2) (less for a top below 2^-119), all of this
+    // is exact but the quotient's estimate: y = x * 127 (15 bits), the whole number q next to the
+    // estimate, and y - q at (a whole number of the smaller one's last places, below 2^17 of
+    // them).  The estimate is off by less than 127 * 2^-22, so q is right or, next to a tie, one
+    // off: the remainder tells.
+    const int e = max((int)(top >> 7) - 127, -119);
+    const float one = e < 127 ? __uint_as_float((uint32_t)(127 - e) << 23) : 0x1p-127f;
+    const float at = __uint_as_float(top << 16) * one, r = top ? __frcp_rn(at) : 0.f;
+    const float by = 127.f * one;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float y = (i & 1 ? hi_f(w[i >> 1]) : lo_f(w[i >> 1])) * by;
+      constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer
+      float m = fmaf(y, r, kWhole);
+      const float rest = fmaf(kWhole - m, at, y), twice = 2.f * fabsf(rest);
+      if (twice > at || (twice == at && (__float_as_uint(m) & 1u))) m += rest > 0.f ? 1.f : -1.f;
+      c[i >> 2] |= (__float_as_uint(m) & 0xffu) << (8 * (i & 3));
+    }
+  }
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// 16 codes and their head's scale -> 16 bf16 channels
+template <int kType>
+__device__ __forceinline__ void restore(const uint4& codes, float scale, uint32_t (&w)[8]) {
+  const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float lo, hi;
+    if constexpr (kType == MARBLE_CACHE_E4M3) {
+      const uint32_t h = e4m3_halves(c[i >> 1] >> (16 * (i & 1)));
+      asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\t"
+          "cvt.f32.f16 %1, b;\n\t}"
+          : "=f"(lo), "=f"(hi)
+          : "r"(h));
+    } else {
+      // the byte above 2^23 with its sign bit turned is 2^23 + 128 + code
+      const uint32_t u = c[i >> 1] ^ 0x80808080u;
+      lo = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540 | (2 * (i & 1)))) - 8388736.f;
+      hi = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540 | (2 * (i & 1) + 1))) - 8388736.f;
+    }
+    w[i] = pack_bf16(lo * scale, hi * scale);
+  }
+}
+
+template <int D, int kType, bool kWrite>
+__global__ void __launch_bounds__(kThreads, 4) k_cache(const __grid_constant__ CacheParams p) {
+  constexpr int kTpr = D / 16, kHpi = 32 / kTpr, kEs = kType == MARBLE_CACHE_BF16 ? 2 : 1;
+  const int lane = threadIdx.x & 31, j = lane % kTpr, sub = lane / kTpr;
+  const SeqsParams& s = p.seqs;
+  const long long runs = (s.n + p.run - 1) / p.run, items = runs * p.split;
+  const long long warps = (long long)gridDim.x * kWarps;
+  for (long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); w < items; w += warps) {
+    const long long i0 = w / p.split * p.run;
+    const int g0 = (int)(w % p.split), rows = (int)min((long long)p.run, s.n - i0);
+    Place mine = {-2, 0};
+    if (lane < rows) mine = place_of(s, p.perm ? p.perm[i0 + lane] : i0 + lane);
+    for (int r = 0; r < rows; ++r) {
+      const int page = __shfl_sync(0xffffffffu, mine.page, r);
+      const int slot = __shfl_sync(0xffffffffu, mine.slot, r);
+      if (page == -2 || (kWrite && page < 0)) continue;
+      for (int g = g0; g < p.groups; g += p.split) {
+        const int h = g * kHpi + sub;
+        const bool live = h < p.hkv;
+        uint4 a[2][2];
+        float scale[2];
+        // all loads first
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const CachePart& c = p.part[x];
+          a[x][0] = a[x][1] = make_uint4(0, 0, 0, 0);
+          scale[x] = 0.f;
+          if (!c.rows || !live) continue;
+          const long long at = (long long)h * s.page + slot;
+          if constexpr (kWrite) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                c.rows + (i0 + r) * c.row_bytes + ((long long)h * D + 16 * j) * 2);
+            a[x][0] = __ldcs(src);
+            a[x][1] = __ldcs(src + 1);
+          } else if (page >= 0) {
+            const uint4* src = reinterpret_cast<const uint4*>(c.pages + page * c.page_bytes +
+                                                              (at * D + 16 * j) * kEs);
+            a[x][0] = __ldcs(src);
+            if constexpr (kEs == 2)
+              a[x][1] = __ldcs(src + 1);
+            else
+              scale[x] = c.scale[page * c.scale_stride + at];
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const CachePart& c = p.part[x];
+          if (!c.rows) continue;
+          const long long at = (long long)h * s.page + slot;
+          if constexpr (kWrite) {
+            uint4* dst = reinterpret_cast<uint4*>(c.pages + page * c.page_bytes +
+                                                  (at * D + 16 * j) * kEs);
+            if constexpr (kEs == 2) {
+              if (live) {
+                dst[0] = a[x][0];
+                dst[1] = a[x][1];
+              }
+            } else {
+              const uint32_t v[8] = {a[x][0].x, a[x][0].y, a[x][0].z, a[x][0].w,
+                                     a[x][1].x, a[x][1].y, a[x][1].z, a[x][1].w};
+              float sc;
+              const uint4 codes = quantise<D, kType>(v, &sc);
+              if (live) {
+                *dst = codes;
+                if (j == 0) c.scale[page * c.scale_stride + at] = sc;
+              }
+            }
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(c.rows + (i0 + r) * c.row_bytes +
+                                                  ((long long)h * D + 16 * j) * 2);
+            if constexpr (kEs == 1) {
+              uint32_t v[8];
+              restore<kType>(a[x][0], scale[x], v);
+              a[x][0] = make_uint4(v[0], v[1], v[2], v[3]);
+              a[x][1] = make_uint4(v[4], v[5], v[6], v[7]);
+            }
+            if (live) {
+              dst[0] = a[x][0];
+              dst[1] = a[x][1];
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache(bool write, const marble_plan_t* plan, int64_t n, const marble_cache_t* c,
+                         const marble_seqs_t* seqs, const marble_heads_t* rows, cudaStream_t s) {
+  CacheParams p;
+  memset(&p, 0, sizeof(p));
+  const int es = c->type == MARBLE_CACHE_BF16 ? 2 : 1;
+  p.part[0] = CachePart{static_cast<char*>(rows->k), static_cast<char*>(c->k), c->k_scale,
+                        rows->k_stride * 2, c->k_stride * es, c->k_scale_stride};
+  p.part[1] = CachePart{static_cast<char*>(rows->v), static_cast<char*>(c->v), c->v_scale,
+                        rows->v_stride * 2, c->v_stride * es, c->v_scale_stride};
+  p.seqs = seqs_params(*seqs, *c, n);
+  p.perm = plan ? plan->perm : nullptr;
+  p.hkv = c->hkv;
+  p.groups = (c->hkv * (c->d / 16) + 31) / 32;
+  // Warps: 32 on every SM where there are rows enough, then up to 32 rows a warp; few rows get a
+  // warp for every group of heads.
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t want = (int64_t)sms * 32;
+  p.run = (int)std::max<int64_t>(1, std::min<int64_t>(32, n / want));
+  const int64_t runs = (n + p.run - 1) / p.run;
+  p.split = (int)std::max<int64_t>(1, std::min<int64_t>(p.groups, (want + runs - 1) / runs));
+  const int64_t ctas = (runs * p.split + kWarps - 1) / kWarps;
+  const int grid = (int)std::min<int64_t>(ctas, (int64_t)sms * 4);
+  auto pick = [&](auto dd) {
+    constexpr int D = decltype(dd)::value;
+    if (c->type == MARBLE_CACHE_BF16)
+      return write ? k_cache<D, MARBLE_CACHE_BF16, true> : k_cache<D, MARBLE_CACHE_BF16, false>;
+    if (c->type == MARBLE_CACHE_E4M3)
+      return write ? k_cache<D, MARBLE_CACHE_E4M3, true> : k_cache<D, MARBLE_CACHE_E4M3, false>;
+    return write ? k_cache<D, MARBLE_CACHE_INT8, true> : k_cache<D, MARBLE_CACHE_INT8, false>;
+  };
+  auto kernel = c->d == 128 ? pick(std::integral_constant<int, 128>{})
+                            : pick(std::integral_constant<int, 64>{});
+  kernel<<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace marble

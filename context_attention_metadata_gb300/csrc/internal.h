@@ -191,6 +191,13 @@ cudaError_t launch_rope_bwd(const marble_plan_t* plan, int64_t n, const marble_r
                             const marble_heads_t* x, const marble_heads_t* grad,
                             const marble_heads_t* dx, float* dwq, float* dwk, float* workspace,
                             cudaStream_t s);
+// the paged cache (cache.cu): rows written into it or read back; arguments checked by the caller
+cudaError_t launch_cache(bool write, const marble_plan_t* plan, int64_t n, const marble_cache_t* c,
+                         const marble_seqs_t* seqs, const marble_heads_t* rows, cudaStream_t s);
+// attention over it (attn_cached.cu)
+marble_status_t run_attn_cached(int64_t n, const marble_cache_t* c, const marble_seqs_t* seqs,
+                                const marble_attn_cached_t* a, const marble_score_t* score,
+                                cudaStream_t s);
 cudaError_t launch_debug_wait(unsigned* err, uint64_t limit_ns, cudaStream_t s);
 
 // attention (attn_fwd.cu, attn_bwd.cu): a list of ring steps launched back to back on `s`

@@ -1,0 +1,75 @@
+// What the cache kernels share: the sequences of a batch, and where a row's token is cached.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace marble {
+
+struct SeqsParams {
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* start;  // null: one row a sequence
+  int32_t* status;       // or null
+  long long table_stride, n;
+  int n_seqs, page, n_pages;
+  int top;               // positions that the table reaches, at most INT_MAX
+};
+
+inline SeqsParams seqs_params(const marble_seqs_t& s, const marble_cache_t& c, int64_t n) {
+  SeqsParams p;
+  p.table = s.table;
+  p.lens = s.lens;
+  p.start = s.start;
+  p.status = s.status;
+  p.table_stride = s.table_stride;
+  p.n = n;
+  p.n_seqs = s.n_seqs;
+  p.page = c.page_tokens;
+  p.n_pages = (int)c.n_pages;
+  const int64_t top = (int64_t)s.table_pages * c.page_tokens;
+  p.top = (int)(top < 0x7fffffff ? top : 0x7fffffff);
+  return p;
+}
+
+__device__ __forceinline__ void seqs_bad(const SeqsParams& p) {
+  if (p.status) atomicOr(p.status, MARBLE_SEQS_BAD);
+}
+
+// The rows [first, first + count) and the length of sequence b, cut to what the arrays hold.
+struct Seq {
+  int first, count, len;
+};
+template <bool kTell>
+__device__ __forceinline__ Seq seq_at(const SeqsParams& p, int b) {
+  const int len = p.lens[b];
+  int s0 = b, s1 = b + 1;
+  if (p.start) {
+    s0 = p.start[b];
+    s1 = p.start[b + 1];
+  }
+  const int n = (int)p.n;
+  if (kTell && (len < 0 || len > p.top || s0 < 0 || s1 < s0 || s1 > n)) seqs_bad(p);
+  Seq s;
+  s.first = min(max(s0, 0), n);
+  s.count = min(max(s1, s.first), n) - s.first;
+  s.len = min(max(len, 0), p.top);
+  return s;
+}
+
+// the page that holds position `pos` of sequence b, -1 if the table's entry is none
+__device__ __forceinline__ int page_at(const SeqsParams& p, int b, int pos) {
+  const int g = __ldg(p.table + (int64_t)b * p.table_stride + pos / p.page);
+  return (unsigned)g < (unsigned)p.n_pages ? g : -1;
+}
+
+// e4m3 and int8 codes, two or four at a time, as halves (exact)
+__device__ __forceinline__ uint32_t e4m3_halves(uint32_t two) {  // low 16 bits
+  uint32_t h;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+      : "=r"(h)
+      : "r"(two));
+  return h;
+}
+
+}  // namespace marble

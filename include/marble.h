@@ -586,6 +586,130 @@ marble_status_t marble_attn_bwd_fused_scored(const marble_plan_t *plan, const ma
                                              float *dk_acc, float *dv_acc,
                                              marble_stream_t stream);
 
+/*
+ * A paged key-value cache: what a sequence needs to go on from its prompt token by token.
+ *
+ * The cache is a pool of pages of page_tokens tokens each.  Channel c of kv head h, token t of
+ * page g is element g * k_stride + (h * page_tokens + t) * d + c of k (and v likewise): within a
+ * page a head's tokens are contiguous, and one allocation may hold the pages of many layers, keys
+ * and values side by side.  8-bit types hold a code for every channel and one fp32 scale for
+ * every token and head, element g * k_scale_stride + h * page_tokens + t of k_scale; the code
+ * stands for code * scale.  With `top` the largest |channel| of a token's head:
+ *   MARBLE_CACHE_BF16  the values as they are, no scales;
+ *   MARBLE_CACHE_E4M3  scale = the smallest power of two (at least 2^-126) with top <= 448 scale,
+ *                      the code x / scale rounded to e4m3 (nearest even);
+ *   MARBLE_CACHE_INT8  scale = top / 127 in fp32, the code x * 127 / top rounded to a whole
+ *                      number (ties to even; exact, not subject to fp32's rounding).
+ * A head of zeros has scale 0.  A head with an infinity or NaN has scale NaN, codes 0: it reads
+ * back as NaN.
+ */
+typedef enum {
+  MARBLE_CACHE_BF16 = 0,
+  MARBLE_CACHE_E4M3 = 1,
+  MARBLE_CACHE_INT8 = 2
+} marble_cache_type_t;
+
+typedef struct {
+  int32_t type;           /* marble_cache_type_t */
+  int32_t hkv, d;         /* d = 64 or 128 */
+  int32_t page_tokens;    /* a positive multiple of 16, at most 65536 */
+  int64_t n_pages;        /* >= 1, < 2^31 */
+  void *k, *v;            /* device, 16-byte aligned, pages k_stride / v_stride elements apart */
+  int64_t k_stride, v_stride; /* hkv * page_tokens * d or more, multiples of 16 bytes, under 2^40
+                                 bytes */
+  float *k_scale, *v_scale;   /* device, 16-byte aligned; NULL for MARBLE_CACHE_BF16 */
+  int64_t k_scale_stride, v_scale_stride; /* elements between pages: hkv * page_tokens or more,
+                                             multiples of 4 */
+} marble_cache_t;
+
+/* The sequences of a batch.  Position p of sequence b is in page table[b * table_stride +
+ * p / page_tokens], at p % page_tokens.  A call works on the LAST tokens of every sequence: its
+ * rows are start[b] .. start[b + 1] (non-decreasing from 0; rows from start[n_seqs] on are left
+ * alone), and row start[b + 1] - 1 is position lens[b] - 1, so lens counts the call's tokens
+ * too.  start == NULL: one row a sequence.  Rows that fall before position 0 (an idle place of a
+ * batch: one row, lens 0) have no token: they are not written, read as zeros, and attend to
+ * nothing.  table_pages: entries of a table row that may be read; entries outside the pages that
+ * a call needs may hold anything.  All arrays are read when the kernels run.
+ * What is out of bounds when they run (an entry outside [0, n_pages) where a page is needed, lens
+ * outside [0, table_pages * page_tokens], a start that decreases or passes n_tokens) touches no
+ * memory outside the arrays; the results of that sequence are then unspecified, nothing of a bad
+ * page is written, and *status, if given, gets MARBLE_SEQS_BAD.  The kernels only ever set bits
+ * of *status; a wait in a kernel that runs out of time sets MARBLE_SEQS_TIMEOUT. */
+#define MARBLE_SEQS_TIMEOUT 1
+#define MARBLE_SEQS_BAD 2
+typedef struct {
+  int32_t n_seqs;         /* >= 0 */
+  int32_t table_pages;    /* >= 1 */
+  const int32_t *table;   /* device int32[n_seqs][table_stride] */
+  int64_t table_stride;   /* table_pages or more */
+  const int32_t *lens;    /* device int32[n_seqs] */
+  const int32_t *start;   /* device int32[n_seqs + 1], or NULL */
+  int32_t *status;        /* device int32, or NULL */
+} marble_seqs_t;
+
+/*
+ * Write the keys and values of n_tokens rows into the cache, quantised on the way: src->k and
+ * src->v, bf16 [n_tokens, hkv, d] as marble_rope leaves them (src->q is not looked at; a NULL
+ * tensor is not written).  With a plan, src is in plan order and its n_tokens are the plan's;
+ * rows are counted in original order.  plan == NULL: rows as they are.
+ * A page that a call writes to must be in one sequence's table only: pages that sequences share
+ * (a common prefix) are for reading.  Everything else in the pool keeps its bytes.
+ * May be captured into a graph.  Errors: INVALID_ARG; CUDA.
+ */
+marble_status_t marble_cache_write(const marble_plan_t *plan, int64_t n_tokens,
+                                   const marble_cache_t *cache, const marble_seqs_t *seqs,
+                                   const marble_heads_t *src, marble_stream_t stream);
+
+/*
+ * Read n_tokens rows back, bf16 (code * scale rounded once): dst->k and dst->v [n_tokens, hkv, d].
+ * With a plan dst is in plan order, ready for the attention calls (a chunk of a prompt behind its
+ * cached prefix: one row for each of both).  Rows without a token become zeros; rows that belong
+ * to no sequence stay as they are.  dst may not overlap the cache, nor its tensors each other.
+ * May be captured into a graph.  Errors: INVALID_ARG; CUDA.
+ */
+marble_status_t marble_cache_read(const marble_plan_t *plan, int64_t n_tokens,
+                                  const marble_cache_t *cache, const marble_seqs_t *seqs,
+                                  const marble_heads_t *dst, marble_stream_t stream);
+
+/*
+ * Attention of every sequence's last tokens (one, or a few: drafts to be checked, the tokens of
+ * a short span) over its cached tokens, their own included: write them first.  For the row at
+ * position p and q head h, over the cached positions j < lens with
+ *   0 <= p - j < window   or   (span != 0 and j among the sequence's rows of this call):
+ *   s_j = scale * q . k_j, changed by `score` as in the scored calls (distances p - j),
+ *   o = sum_j softmax(s)_j v_j as bf16,   lse = ln sum_j exp(s_j).
+ * A row that sees nothing gives o = 0, lse = -inf.  Cached values that no row of a sequence sees
+ * may be anything, infinities and NaN too; those that some row of it sees have to be finite.
+ * Sums and the softmax are in fp32.  bf16 caches: the weights enter their product with v as two
+ * bf16 terms (16 bits).  8-bit caches: q enters in fp16 after a power of two for each row (no
+ * bits are lost above 2^-29 of its largest channel), the weights, times v's scale, in fp16.
+ * The keys of all (sequence, kv head, tile of up to 64 rows) are dealt evenly to the SMs, whatever
+ * the lengths; the pieces of one softmax are joined in order, so that results do not depend on
+ * timing.  Rows of a kv head beyond 64 read the cache again.
+ */
+#define MARBLE_ATTN_CACHED_WORKSPACE_BYTES 25165824
+typedef struct {
+  const void *q;     /* device bf16 [n_tokens, hq, d], 16-byte aligned, tokens q_stride apart */
+  int64_t q_stride;  /* elements: hq * d or more, a multiple of 8 */
+  void *o;           /* device bf16 [n_tokens, hq, d]; the same rules; may not overlap q or the
+                        cache */
+  int64_t o_stride;
+  float *lse;        /* device fp32 [hq][n_tokens], or NULL */
+  int32_t hq;        /* a multiple of hkv; q head h reads kv head h / (hq / hkv) */
+  float scale;       /* <= 0 selects 1 / sqrt(d) */
+  int32_t window;    /* >= 0, MARBLE_WINDOW_INF for none */
+  int32_t span;      /* != 0: the rows of a sequence all see each other */
+  int32_t new_tokens; /* how many rows a sequence has at most, as a hint (>= 1): it chooses the
+                         rows of a tile, and results do not depend on it but for rounding */
+  void *workspace;   /* device, 16-byte aligned, MARBLE_ATTN_CACHED_WORKSPACE_BYTES, used by this
+                        call alone until it has completed; no contents expected or kept */
+} marble_attn_cached_t;
+/* n_tokens * hq < 2^31.  May be captured into a graph (one workspace per graph that may run at
+ * the same time).  score: NULL for none.  Errors: INVALID_ARG; CUDA. */
+marble_status_t marble_attn_cached(int64_t n_tokens, const marble_cache_t *cache,
+                                   const marble_seqs_t *seqs, const marble_attn_cached_t *attn,
+                                   const marble_score_t *score, marble_stream_t stream);
+
 /* Cast fp32 -> bf16 (round to nearest even) for n elements, e.g. gradient accumulators;
  * n must be a multiple of 4 and both pointers 16-byte aligned. */
 marble_status_t marble_cast_bf16(const float *src, void *dst, int64_t n,
