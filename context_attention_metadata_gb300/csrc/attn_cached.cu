@@ -16,7 +16,9 @@
 //   table look-ups included) and four that compute; two CTAs share an SM, so that one's item
 //   boundaries hide behind the other's streaming.
 // - A chunk belongs to one warp of every 16 rows: warps have their own m, l and O over their
-//   chunks and meet only at an item's end.  The products are m16n8k16 matrix instructions, whose
+//   chunks and meet only at an item's end.  A place of the ring always belongs to the same warps
+//   (its copies may land before those of an earlier place: whoever waits for a place's next
+//   filling must have seen the one before, or the barrier's parity misleads it).  The products are m16n8k16 matrix instructions, whose
 //   16 rows are what a kv head's group gives; tcgen05's 128 would be mostly padding, and the rate
 //   of the warp-level ones is several times what memory can feed at these sizes.
 // - 8-bit codes become fp16 exactly in registers; k's scales multiply scores, v's scales the
@@ -46,7 +48,8 @@ struct Cfg {
   static constexpr int kHalves = kRow / kPitch;
   static constexpr int kKeys = kRow > 128 ? 32 : 64;         // of a chunk
   static constexpr int kTile = kKeys * kRow;
-  static constexpr int kStages = kTile == 8192 ? 5 : 10;
+  static constexpr int kStages = kTile == 8192 ? 4 : 8;
+  static_assert(kStages % kWorkers == 0, "a place of the ring belongs to the same warps");
   static constexpr int kMerge = 32 * (D / 2 + 4) * 4;        // a warp's O, m, l
   static constexpr int kScales = kQuant ? kStages * 2 * kKeys * 4 : 0;
   static constexpr int kSmem =
@@ -380,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) {
-      // copies in flight write to this CTA's shared memory: wait for them
+    if (lane == 0) {
+      // the last copies write to this CTA's shared memory, whoever still waits for them
       for (int i = max(0, n - kStages); i < n; ++i)
         drain_wait(&full[i % kStages], (i / kStages) & 1, p.limit_ns, p.err);
     }
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    for (int i = kg; i < walk.c1 - walk.c0; i += kgs) {
+    for (int i = (kg - n) & (kgs - 1); i < walk.c1 - walk.c0; i += kgs) {
       const int at = n + i, st = at % kStages, base = (w.chunk0 + walk.c0 + i) * kKeys;
       // (given up: the warps still meet at the items' ends)
       if (!wait_all(&full[st], (at / kStages) & 1, wait)) break;

@@ -94,6 +94,19 @@ def test_many_sequences(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,group,counts", [(128, 2, None), (64, 4, None), (128, 4, [7, 1, 16])])
+def test_the_ring_goes_round(kind, d, group, counts):
+    """Enough keys that every CTA fills its ring many times over."""
+    batch = Batch(kind, [30000, 5, 21003], counts, 6, d, 64, seed=5)
+    q = _q(batch.n, 6 * group, d, 10)
+    o, lse = _run(batch, q)
+    check_attn(batch, q, o, lse)
+    for _ in range(20):
+        again = _run(batch, q)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_strided_rows_and_outputs(kind):
     """q as a slice of a projection, o as a slice, no lse, rows behind the last sequence."""
     batch = Batch(kind, [100, 61], [2, 3], 2, 128, 16)
