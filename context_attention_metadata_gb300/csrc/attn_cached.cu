@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <cstring>
 
+#include "score.cuh"
 #include "seqs.cuh"
 #include "tma_host.h"
 
@@ -39,10 +40,13 @@ constexpr int kThreads = 32 * (kWorkers + 1);
 constexpr int kUnitOver = 1;                    // an item's constant cost, in chunks
 constexpr float kLazy = 8.f;                    // O is rescaled when m grows by more (base 2)
 constexpr float kPUp = 64.f;                    // fp16 weights are raised by this (see below)
+constexpr float kLoUp = 32.f;                   // q's second e4m3 term is raised by this
 
-template <int D, int kType>
+// kNt: tiles of 8 rows that a warp computes
+template <int D, int kType, int kNt>
 struct Cfg {
   static constexpr bool kQuant = kType != MARBLE_CACHE_BF16;
+  static constexpr bool kFp8 = kType == MARBLE_CACHE_E4M3;
   static constexpr int kRow = D * (kQuant ? 1 : 2);          // bytes of a key
   static constexpr int kPitch = kRow > 128 ? 128 : kRow;     // of its rows in shared memory
   static constexpr int kHalves = kRow / kPitch;
@@ -50,10 +54,21 @@ struct Cfg {
   static constexpr int kTile = kKeys * kRow;
   static constexpr int kStages = kTile == 8192 ? 4 : 8;
   static_assert(kStages % kWorkers == 0, "a place of the ring belongs to the same warps");
-  static constexpr int kMerge = 32 * (D / 2 + 4) * 4;        // a warp's O, m, l
   static constexpr int kScales = kQuant ? kStages * 2 * kKeys * 4 : 0;
-  static constexpr int kSmem =
-      1024 + kStages * 2 * kTile + kScales + (kWorkers - 1) * kMerge + 2 * kStages * 8 + 64;
+  // pieces the fetching warp may be ahead, their q, and the warps' O, m and l on their way
+  // together: 4 (2) of 8 (16) rows for each row warp; O of all but the rows' first warp
+  static constexpr int kPieces = kNt == 1 ? 4 : 2;
+  static constexpr int kQPitch = D * 2 + 16;
+  static constexpr int kMerge = 32 * (D / 4 * kNt + 4 * kNt) * 4;
+  static constexpr int most() {
+    int m = 0;
+    for (int r = 1; r <= kWorkers; r *= 2) {
+      const int bytes = kPieces * 8 * kNt * r * kQPitch + (kWorkers - r) * kMerge;
+      if (bytes > m && (kNt > 1 || r == 1)) m = bytes;
+    }
+    return m;
+  }
+  static constexpr int kSmem = 1024 + kStages * 2 * kTile + kScales + most();
 };
 
 struct AttnParams {
@@ -72,11 +87,12 @@ struct AttnParams {
   float cap2;        // cap * log2 e, 0: none
   int hkv, group, hq;
   int window, span;
-  int tiles;         // 16-row tiles of an item: 1, 2 or 4
+  int row_warps;     // warps that an item's rows are split over: 1, 2 or 4
+  int rows;          // of an item: 8 * kNt * row_warps
   int box;           // keys of a TMA box
   int grain;         // units a CTA takes at least
-  float* part_o;     // [2 * CTAs][16 * tiles][D] pieces
-  float2* part_ml;   // [2 * CTAs][16 * tiles]
+  float* part_o;     // [2 * CTAs][rows][D] pieces
+  float2* part_ml;   // [2 * CTAs][rows]
   int4* joins;       // [CTAs]: sequence, item, pieces (0: none)
   unsigned* err;
   uint64_t limit_ns;
@@ -110,7 +126,7 @@ __device__ __forceinline__ Work work_of(const AttnParams& p, int b) {
   w.hi = p.window > 0 || p.span ? w.s.len : w.lo;  // (no window: no keys at all)
   w.chunk0 = w.lo / kKeys;
   w.chunks = w.lo < w.hi ? (w.hi - 1) / kKeys - w.chunk0 + 1 : 0;
-  w.tiles = (int)(((long long)w.s.count * p.group + 16 * p.tiles - 1) / (16 * p.tiles));
+  w.tiles = (int)(((long long)w.s.count * p.group + p.rows - 1) / p.rows);
   w.items = w.tiles * p.hkv;
   w.units = w.items ? w.chunks + kUnitOver : 0;
   return w;
@@ -162,23 +178,37 @@ __device__ __forceinline__ void ldsm4_t(uint32_t at, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(at));
 }
-// c += a b, 16 x 8 x 16
-template <bool kHalf>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (kHalf)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+// the 8 x 8 matrix of 16-bit values turned over
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// c += a b, 16 x 8 x 16 (e4m3: x 32)
+template <int kKind>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  if constexpr (kKind == 0)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+  else if constexpr (kKind == 1)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
+__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -191,17 +221,11 @@ __device__ __forceinline__ uint32_t int8_halves(uint32_t u, uint32_t sel) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
   return r;
 }
-// four codes of consecutive channels of one key: the halves of the first two, and the others
-template <int kType>
+// four int8 codes of consecutive channels of one key: the halves of the first two, and the others
 __device__ __forceinline__ void along(uint32_t c, uint32_t* a, uint32_t* b) {
-  if constexpr (kType == MARBLE_CACHE_E4M3) {
-    *a = e4m3_halves(c);
-    *b = e4m3_halves(c >> 16);
-  } else {
-    const uint32_t u = c ^ 0x80808080u;
-    *a = int8_halves(u, 0x4140);
-    *b = int8_halves(u, 0x4342);
-  }
+  const uint32_t u = c ^ 0x80808080u;
+  *a = int8_halves(u, 0x4140);
+  *b = int8_halves(u, 0x4342);
 }
 // codes (key 0: channels 0, 1; key 1: channels 0, 1): the halves of channel 0, and of channel 1
 template <int kType>
@@ -234,13 +258,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-__device__ __forceinline__ float quad_max(float x) {
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+// over the 8 lanes that hold a row's keys
+__device__ __forceinline__ float row_max(float x) {
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+  return x;
 }
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
 }
 
 // ln of the sum, from a base-2 maximum and a sum
@@ -248,34 +275,44 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
 }
 
-// row `r` of an item: its token's row in the call and its q head
+// row `x` of a kv head's rows (new token by new token, the group's q heads of each): its token's
+// row in the call, its q head and its position
 struct RowAt {
   int token, head, pos;
   bool live;
 };
-__device__ __forceinline__ RowAt row_at(const AttnParams& p, const Work& w, int item, int r) {
-  const int head = item / w.tiles, x = (item - head * w.tiles) * 16 * p.tiles + r;
+__device__ __forceinline__ RowAt row_at(const AttnParams& p, const Seq& s, int head, int x) {
   const int t = x / p.group;
   RowAt a;
-  a.live = t < w.s.count;
-  a.token = w.s.first + t;
+  a.live = t < s.count;
+  a.token = s.first + t;
   a.head = head * p.group + (x - t * p.group);
-  a.pos = w.s.len - w.s.count + t;
+  a.pos = s.len - s.count + t;
   return a;
 }
 
-template <int D, int kType, bool kScored>
+// what the computing warps need of a piece
+struct Piece {
+  Seq s;
+  int lo, hi;           // the item's keys
+  int key0, chunks;     // the piece's first key and chunks; chunks < 0: there are no more pieces
+  int head, row0;       // the item's kv head and first row
+  int place;            // where the piece goes in the workspace, -1: it is the whole item
+};
+
+template <int D, int kType, int kNt, bool kScored>
 __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_constant__ AttnParams p) {
-  using C = Cfg<D, kType>;
+  using C = Cfg<D, kType, kNt>;
   constexpr bool kQuant = C::kQuant;
-  constexpr int kKeys = C::kKeys, kStages = C::kStages, kNt = kKeys / 8;
+  constexpr int kKeys = C::kKeys, kStages = C::kStages, kMt = kKeys / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align1024(smem_raw);
   float* scales = reinterpret_cast<float*>(ring + kStages * 2 * C::kTile);
-  float4* merge = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(scales) + C::kScales);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(merge) +
-                                               (kWorkers - 1) * C::kMerge);
-  uint64_t* empty = full + kStages;
+  uint8_t* qs = reinterpret_cast<uint8_t*>(scales) + C::kScales;
+  float4* merge = reinterpret_cast<float4*>(qs + C::kPieces * p.rows * C::kQPitch);
+  __shared__ uint64_t full[kStages], empty[kStages], piece_full[C::kPieces], piece_empty[C::kPieces];
+  __shared__ uint64_t merge_full[kWorkers], merge_empty[kWorkers];
+  __shared__ Piece pieces[C::kPieces];
   __shared__ int abort_flag, first_b;
   __shared__ long long first_at, range[2], sums[kWorkers + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -298,12 +335,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     upto += lane >= off ? v : 0;
   }
   if (lane == 31) sums[warp] = upto;
+  const int kgs = kWorkers / p.row_warps;
   if (tid == 0) {
     abort_flag = 0;
     p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], p.tiles);
+      mbar_init(&empty[i], p.row_warps);
+    }
+    for (int i = 0; i < C::kPieces; ++i) {
+      mbar_init(&piece_full[i], 1);
+      mbar_init(&piece_empty[i], kWorkers);
+    }
+    for (int i = 0; i < kWorkers; ++i) {
+      mbar_init(&merge_full[i], max(kgs - 1, 1));
+      mbar_init(&merge_empty[i], 1);
     }
     fence_mbar_init();
   }
@@ -331,53 +377,104 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     range[1] = ctas;
   }
   __syncthreads();
-
   const WaitCtx wait = {p.limit_ns, p.err, &abort_flag};
-  Walk<kKeys> walk(p, first_b, first_at, u1 - u0);
-  int n = 0;  // chunks of the CTA so far
 
   if (warp == kWorkers) {
-    // ---- fetch: lane 4 x + j takes box j of part x
-    const int box = lane & 3, part = lane >> 2, boxes = kKeys / p.box;
+    // ---- fetch.  The boxes of the next 32 / boxes chunks are looked up at once, a lane each;
+    // lane 4 x + j then issues box j of part x of a chunk.
+    const int boxes = kKeys / p.box, group = 32 / boxes;
+    const int box = lane & 3, part = lane >> 2;
     constexpr int kParts = kQuant ? 4 : 2 * C::kHalves;
+    Walk<kKeys> walk(p, first_b, first_at, u1 - u0);
+    int n = 0, np = 0;  // chunks and pieces so far
     bool ok = true;
-    while (ok && walk.next()) {
-      const int head = walk.item / walk.w.tiles;
-      for (int c = walk.c0; c < walk.c1; ++c, ++n) {
-        const int st = n % kStages;
-        const int key = (walk.w.chunk0 + c) * kKeys + box * p.box;
-        const bool needed = box < boxes && key < walk.w.hi && key + p.box > walk.w.lo;
-        int page = 0;
-        if (needed && part < kParts) {
-          page = page_at(p.seqs, walk.b, key);
-          if (page < 0 && part == 0) seqs_bad(p.seqs);
+    while (ok) {
+      const bool more = walk.next();
+      const int ps = np % C::kPieces;
+      if (np >= C::kPieces && !warp_wait(&piece_empty[ps], ((np / C::kPieces) & 1) ^ 1, wait)) {
+        ok = false;
+        break;
+      }
+      const Work& w = walk.w;
+      const int head = more ? walk.item / w.tiles : 0;
+      const int row0 = more ? (walk.item - head * w.tiles) * p.rows : 0;
+      const int live = more ? min((int)min((long long)w.s.count * p.group - row0, 64ll), p.rows) : 0;
+      if (lane == 0) {
+        Piece& q = pieces[ps];
+        q.chunks = -1;
+        if (more) {
+          const bool begins = walk.c0 == 0, ends = walk.c1 == w.chunks;
+          q.s = w.s;
+          q.lo = w.lo;
+          q.hi = w.hi;
+          q.key0 = (w.chunk0 + walk.c0) * kKeys;
+          q.chunks = walk.c1 - walk.c0;
+          q.head = head;
+          q.row0 = row0;
+          // a CTA's first place is for an item that another CTA began, its second for one that
+          // another goes on with
+          q.place = begins && ends ? -1 : 2 * (int)blockIdx.x + (begins ? 1 : 0);
+          if (begins && !ends) {
+            // the CTAs that have the rest: the last one holds the item's last unit
+            const long long end = u1 + (w.chunks - walk.c1);
+            const int last = (int)((end * range[1] - 1) / range[0]);
+            p.joins[blockIdx.x] = make_int4(walk.b, walk.item, last - (int)blockIdx.x + 1, 0);
+          }
         }
+        mbar_arrive_expect_tx(&piece_full[ps], live * D * 2);
+      }
+      __syncwarp();
+      for (int r = lane; r < live; r += 32) {
+        const RowAt at = row_at(p, w.s, head, row0 + r);
+        bulk_load(smem_u32(qs + (ps * p.rows + r) * C::kQPitch),
+                  p.q + at.token * p.q_stride + (long long)at.head * D, D * 2, &piece_full[ps]);
+      }
+      ++np;
+      if (!more) break;
+
+      int page = -1, slot = 0;
+      for (int c = walk.c0; c < walk.c1; ++c, ++n) {
+        const int in = (c - walk.c0) % group;
+        if (in == 0) {
+          const int key = (w.chunk0 + c + lane / boxes) * kKeys + lane % boxes * p.box;
+          page = -1;
+          slot = -1;  // not needed
+          if (c + lane / boxes < walk.c1 && key < w.hi && key + p.box > w.lo) {
+            page = page_at(p.seqs, walk.b, key);
+            slot = key % p.seqs.page;
+            if (page < 0) seqs_bad(p.seqs);
+          }
+        }
+        const int st = n % kStages;
+        const int my_page = __shfl_sync(0xffffffffu, page, (in * boxes + box) & 31);
+        const int my_slot = __shfl_sync(0xffffffffu, slot, (in * boxes + box) & 31);
+        const bool needed = box < boxes && my_slot >= 0;
+        const int count = __popc(__ballot_sync(0xffffffffu, needed && part == 0));
         if (n >= kStages && !warp_wait(&empty[st], ((n / kStages) & 1) ^ 1, wait)) {
           ok = false;
           break;
         }
-        const int count = __popc(__ballot_sync(0xffffffffu, needed && part == 0));
         if (lane == 0)
           mbar_arrive_expect_tx(&full[st], count * p.box * (2 * C::kRow + (kQuant ? 8 : 0)));
         __syncwarp();
         if (needed && part < kParts) {
           const uint32_t tile = smem_u32(ring) + st * 2 * C::kTile;
           // (a page that is none lies outside the tensor map: zeros)
-          const int g = page < 0 ? p.seqs.n_pages : page, slot = key % p.seqs.page;
+          const int g = my_page < 0 ? p.seqs.n_pages : my_page;
           if constexpr (kQuant) {
             if (part < 2) {
               tma_load_4d(tile + part * C::kTile + box * p.box * C::kPitch,
-                          part ? &p.vmap : &p.kmap, &full[st], 0, slot, head, g);
+                          part ? &p.vmap : &p.kmap, &full[st], 0, my_slot, head, g);
             } else {
-              const float* src = part == 2 ? p.k_scale + max(page, 0) * p.k_scale_stride
-                                           : p.v_scale + max(page, 0) * p.v_scale_stride;
+              const float* src = part == 2 ? p.k_scale + max(my_page, 0) * p.k_scale_stride
+                                           : p.v_scale + max(my_page, 0) * p.v_scale_stride;
               bulk_load(smem_u32(scales + (2 * st + part - 2) * kKeys + box * p.box),
-                        src + (long long)head * p.seqs.page + slot, p.box * 4, &full[st]);
+                        src + (long long)head * p.seqs.page + my_slot, p.box * 4, &full[st]);
             }
           } else {
             const int which = part / C::kHalves, half = part % C::kHalves;
             tma_load_4d(tile + which * C::kTile + (half * kKeys + box * p.box) * C::kPitch,
-                        which ? &p.vmap : &p.kmap, &full[st], half * 64, slot, head, g);
+                        which ? &p.vmap : &p.kmap, &full[st], half * 64, my_slot, head, g);
           }
         }
         __syncwarp();
@@ -387,169 +484,255 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       // the last copies write to this CTA's shared memory, whoever still waits for them
       for (int i = max(0, n - kStages); i < n; ++i)
         drain_wait(&full[i % kStages], (i / kStages) & 1, p.limit_ns, p.err);
+      for (int i = max(0, np - C::kPieces); i < np; ++i)
+        drain_wait(&piece_full[i % C::kPieces], (i / C::kPieces) & 1, p.limit_ns, p.err);
     }
     return;
   }
 
-  // ---- compute
-  const int tile = warp % p.tiles, kg = warp / p.tiles, kgs = kWorkers / p.tiles;
+  // ---- compute.  Products are taken with the keys as rows: S^T = K Q^T (16 keys x 8 rows), and
+  // O^T = V^T P^T (16 channels x 8 rows), so that a group of up to 8 rows wastes nothing.  Lane 4 n
+  // + t holds keys n and n + 8 of 16, rows 2 t and 2 t + 1 of 8.
+  const int tile = warp % p.row_warps, kg = warp / p.row_warps;
   const int qn = lane >> 2, qt = lane & 3, l7 = lane & 7, lm = lane >> 3;
-  while (walk.next()) {
-    const Work& w = walk.w;
-    const RowAt ra[2] = {row_at(p, w, walk.item, 16 * tile + qn),
-                         row_at(p, w, walk.item, 16 * tile + qn + 8)};
-    // q in registers: bf16, channels (16 s + 2 t, + 1, + 8, + 9) of step s; or fp16, channels
-    // 16 s + 4 t .. + 3, the order in which 8-bit codes come out of the ring
-    uint32_t q[D / 16][4];
-    int lo[2], hi[2];
-    float up[2] = {1.f, 1.f};  // what the row's products have to be multiplied by
+  // where a lane's row of an ldmatrix begins: of keys (lm & 1 or lm >> 1: the second eight), and
+  // the 16-byte chunk in it (the other bit), which the swizzle moves by the row
+  const uint32_t swz = C::kPitch == 128 ? l7 : (l7 >> 1) & 3;
+  const uint32_t k_row = ((lm & 1) * 8 + l7) * C::kPitch, k_x = ((lm >> 1) ^ swz) << 4;
+  const uint32_t v_row = kQuant ? k_row : ((lm >> 1) * 8 + l7) * C::kPitch;
+  const uint32_t v_x = kQuant ? k_x : ((lm & 1) ^ swz) << 4;
+  int n = 0;  // chunks so far
+  for (int np = 0;; ++np) {
+    const int ps = np % C::kPieces;
+    if (!wait_all(&piece_full[ps], (np / C::kPieces) & 1, wait)) return;
+    const Piece pc = pieces[ps];
+    if (pc.chunks < 0) return;
+    const int row0 = pc.row0 + 8 * kNt * tile;  // this warp's first row
+
+    // q: bf16, channels (2 t, + 1, + 8, + 9) of 16; for int8 fp16, channels 4 t .. + 3 of 16 (the
+    // order in which the codes come out of the ring); for e4m3 two terms, channels 4 t .. + 3 and
+    // 16 + 4 t .. + 3 of 32
+    constexpr int kQn = C::kFp8 ? D / 32 : D / 16;
+    uint32_t q[kNt][kQn][2], q2[C::kFp8 ? kNt : 1][kQn][2];
+    F2 mul[kNt];                     // what the rows' products have to be multiplied by
+    int lo[kNt][2], hi[kNt][2], pos[kNt][2];
+    F2 slope2[kNt];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      sees(p, w.s, ra[x].pos, &lo[x], &hi[x]);
-      if (!ra[x].live) lo[x] = hi[x] = 0;
-      const __nv_bfloat16* src =
-          p.q + (ra[x].live ? ra[x].token * p.q_stride + (long long)ra[x].head * D : 0);
+    for (int t = 0; t < kNt; ++t) {
+      const int r = 8 * (kNt * tile + t) + qn;
+      const bool live = row_at(p, pc.s, pc.head, pc.row0 + r).live;
+      const uint8_t* src = qs + (ps * p.rows + r) * C::kQPitch;
+      float up = 1.f;
       if constexpr (!kQuant) {
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t* at = reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * qt);
-          q[s][x] = ra[x].live ? at[0] : 0u;
-          q[s][2 + x] = ra[x].live ? at[4] : 0u;
+        for (int s = 0; s < kQn; ++s) {
+          const uint32_t* at = reinterpret_cast<const uint32_t*>(src + 32 * s + 4 * qt);
+          q[t][s][0] = live ? at[0] : 0u;
+          q[t][s][1] = live ? at[4] : 0u;
         }
       } else {
         uint2 v[D / 16];
         uint32_t top = 0;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          v[s] = ra[x].live ? *reinterpret_cast<const uint2*>(src + 16 * s + 4 * qt)
-                            : make_uint2(0, 0);
+          v[s] = live ? *reinterpret_cast<const uint2*>(src + 32 * s + 8 * qt) : make_uint2(0, 0);
           top = max(top, max(max(v[s].x & 0x7fffu, v[s].x >> 16 & 0x7fffu),
                              max(v[s].y & 0x7fffu, v[s].y >> 16 & 0x7fffu)));
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the largest channel into [2^14, 2^15)
-        const int e = min(max((int)(top >> 7) - 127 - 14, -126), 126);
+        // the largest channel into [2^14, 2^15), for e4m3 into [2^7, 2^8)
+        const int e = min(max((int)(top >> 7) - 127 - (C::kFp8 ? 7 : 14), -126), 126);
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-        up[x] = __uint_as_float((uint32_t)(127 + e) << 23);
+        up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          q[s][x] = pack_half(__uint_as_float(v[s].x << 16) * down,
-                              __uint_as_float(v[s].x & 0xffff0000u) * down);
-          q[s][2 + x] = pack_half(__uint_as_float(v[s].y << 16) * down,
-                                  __uint_as_float(v[s].y & 0xffff0000u) * down);
+          const float f[4] = {__uint_as_float(v[s].x << 16) * down,
+                              __uint_as_float(v[s].x & 0xffff0000u) * down,
+                              __uint_as_float(v[s].y << 16) * down,
+                              __uint_as_float(v[s].y & 0xffff0000u) * down};
+          if constexpr (C::kFp8) {
+            // two e4m3 terms hold bf16's 8 bits: what the first leaves is at most 8 of its last
+            // places' halves.  Channels below 2^-14 of the largest lose bits below 2^-22 of it.
+            q[t][s >> 1][s & 1] = pack_e4m3(f[0], f[1]) | pack_e4m3(f[2], f[3]) << 16;
+            const uint32_t c = q[t][s >> 1][s & 1];
+            float g[4];
+            halves_to_float(e4m3_halves(c), &g[0], &g[1]);
+            halves_to_float(e4m3_halves(c >> 16), &g[2], &g[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[i] = (f[i] - g[i]) * kLoUp;
+            q2[t][s >> 1][s & 1] = pack_e4m3(g[0], g[1]) | pack_e4m3(g[2], g[3]) << 16;
+            // (a NaN's or an infinity's codes would be finite)
+            if (top >= 0x7f80u) q[t][s >> 1][s & 1] = 0x7f7f7f7fu;
+          } else {
+            q[t][s][0] = pack_half(f[0], f[1]);
+            q[t][s][1] = pack_half(f[2], f[3]);
+          }
         }
       }
-    }
-    float mul[2] = {up[0] * p.scale2, up[1] * p.scale2}, slope2[2] = {0.f, 0.f};
-    if constexpr (kScored) {
-      if (p.cap2 > 0.f) {
-        mul[0] = up[0] * p.to_cap;
-        mul[1] = up[1] * p.to_cap;
-      }
+      // from the lanes that read a row to those that hold its products
+      float m2[2], sl[2] = {0.f, 0.f};
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (p.slopes && ra[x].live) slope2[x] = p.slopes[ra[x].head] * 1.4426950408889634f;
+      for (int x = 0; x < 2; ++x) {
+        m2[x] = __shfl_sync(0xffffffffu, up, 4 * (2 * qt + x)) *
+                (kScored && p.cap2 > 0.f ? p.to_cap : p.scale2);
+        const RowAt ra = row_at(p, pc.s, pc.head, row0 + 8 * t + 2 * qt + x);
+        pos[t][x] = ra.pos;
+        sees(p, pc.s, ra.pos, &lo[t][x], &hi[t][x]);
+        if (!ra.live) lo[t][x] = hi[t][x] = 0;
+        if constexpr (kScored)
+          if (p.slopes && ra.live) sl[x] = p.slopes[ra.head] * -1.4426950408889634f;
+      }
+      mul[t] = f2(m2[0], m2[1]);
+      slope2[t] = f2(sl[0], sl[1]);
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&piece_empty[ps]);
     // the keys that all of this warp's rows see
     int all_lo, all_hi, dummy;
     {
-      const RowAt a = row_at(p, w, walk.item, 16 * tile);
-      const RowAt z = row_at(p, w, walk.item, 16 * tile + 15);
-      sees(p, w.s, a.pos, &dummy, &all_hi);
-      sees(p, w.s, min(z.pos, w.s.len - 1), &all_lo, &dummy);
+      const RowAt a = row_at(p, pc.s, pc.head, row0);
+      const RowAt z = row_at(p, pc.s, pc.head, row0 + 8 * kNt - 1);
+      sees(p, pc.s, a.pos, &dummy, &all_hi);
+      sees(p, pc.s, min(z.pos, pc.s.len - 1), &all_lo, &dummy);
     }
 
-    float o[D / 8][4];
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, vref = 0.f;
+    float o[D / 16][kNt][4];
+    float m[kNt][2];
+    F2 l[kNt];
+    float vref = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (int t = 0; t < kNt; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t] = f2(0.f);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.f;
+    }
 
-    for (int i = (kg - n) & (kgs - 1); i < walk.c1 - walk.c0; i += kgs) {
-      const int at = n + i, st = at % kStages, base = (w.chunk0 + walk.c0 + i) * kKeys;
-      // (given up: the warps still meet at the items' ends)
-      if (!wait_all(&full[st], (at / kStages) & 1, wait)) break;
+    for (int i = (kg - n) & (kgs - 1); i < pc.chunks; i += kgs) {
+      const int at = n + i, st = at % kStages, base = pc.key0 + i * kKeys;
+      if (!wait_all(&full[st], (at / kStages) & 1, wait)) return;
       const uint32_t kt = smem_u32(ring) + st * 2 * C::kTile, vt = kt + C::kTile;
       const float* ks = scales + 2 * st * kKeys;
       const float* vs = ks + kKeys;
-      const bool cut_v = base < w.lo || base + kKeys > w.hi;    // keys that no row may see
+      const bool cut_v = base < pc.lo || base + kKeys > pc.hi;  // keys that no row may see
       const bool masked = base < all_lo || base + kKeys > all_hi;
 
-      // scores: keys 8 j + 2 t, + 1 of rows n and n + 8
-      float s[kNt][4];
+      // scores
+      float s[kMt][kNt][4];
 #pragma unroll
-      for (int j = 0; j < kNt; ++j) {
-        s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-        const int row = 8 * j + l7;
+      for (int j = 0; j < kMt; ++j)
 #pragma unroll
-        for (int x = 0; x < C::kRow / 64; ++x) {  // 64 bytes of the keys at a time
-          const int chunk = 4 * x + lm;
-          uint32_t f[4];
-          if constexpr (C::kPitch == 128) {
-            const int half = chunk >> 3;
-            ldsm4(kt + (half * kKeys + row) * 128 + (((chunk & 7) ^ l7) << 4), f);
-          } else {
-            ldsm4(kt + row * 64 + ((chunk ^ ((l7 >> 1) & 3)) << 4), f);
+        for (int t = 0; t < kNt; ++t) s[j][t][0] = s[j][t][1] = s[j][t][2] = s[j][t][3] = 0.f;
+      if constexpr (C::kFp8) {
+        float s2[kMt][kNt][4];
+#pragma unroll
+        for (int j = 0; j < kMt; ++j)
+#pragma unroll
+          for (int t = 0; t < kNt; ++t) s2[j][t][0] = s2[j][t][1] = s2[j][t][2] = s2[j][t][3] = 0.f;
+#pragma unroll
+        for (int x = 0; x < C::kRow / 32; ++x) {
+          const uint32_t row = kt + k_row + (k_x ^ (x << 5));
+#pragma unroll
+          for (int j = 0; j < kMt; ++j) {
+            uint32_t f[4];
+            ldsm4(row + j * 16 * C::kPitch, f);
+#pragma unroll
+            for (int t = 0; t < kNt; ++t) {
+              mma<2>(s[j][t], f, q[t][x]);
+              mma<2>(s2[j][t], f, q2[t][x]);
+            }
           }
-          if constexpr (!kQuant) {
-            mma<false>(s[j], q[2 * x], f[0], f[1]);
-            mma<false>(s[j], q[2 * x + 1], f[2], f[3]);
-          } else {
+        }
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              uint32_t h0, h1;
-              along<kType>(f[y], &h0, &h1);
-              mma<true>(s[j], q[4 * x + y], h0, h1);
+        for (int j = 0; j < kMt; ++j)
+#pragma unroll
+          for (int t = 0; t < kNt; ++t)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) s[j][t][y] = fmaf(s2[j][t][y], 1.f / kLoUp, s[j][t][y]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < C::kRow / 32; ++x) {  // 32 bytes of the keys at a time
+          const uint32_t row = kt + (x >> 2) * kKeys * C::kPitch + k_row + (k_x ^ ((x & 3) << 5));
+#pragma unroll
+          for (int j = 0; j < kMt; ++j) {
+            uint32_t f[4];
+            ldsm4(row + j * 16 * C::kPitch, f);
+            if constexpr (!kQuant) {
+#pragma unroll
+              for (int t = 0; t < kNt; ++t) mma<0>(s[j][t], f, q[t][x]);
+            } else {
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                uint32_t a[4];
+                along(f[2 * y], &a[0], &a[2]);
+                along(f[2 * y + 1], &a[1], &a[3]);
+#pragma unroll
+                for (int t = 0; t < kNt; ++t) mma<1>(s[j][t], a, q[t][2 * x + y]);
+              }
             }
           }
         }
       }
 
-      // scale, cap, bias, mask
-      float top[2] = {-INFINITY, -INFINITY};
+      // scale, cap, bias, mask; s becomes base-2 scores
+      F2 top[kNt];
 #pragma unroll
-      for (int j = 0; j < kNt; ++j) {
-        float2 kscale = make_float2(1.f, 1.f);
-        if constexpr (kQuant) kscale = *reinterpret_cast<const float2*>(ks + 8 * j + 2 * qt);
+      for (int t = 0; t < kNt; ++t) top[t] = f2(-INFINITY);
+      bool grow = false;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int x = y >> 1, key = base + 8 * j + 2 * qt + (y & 1);
-          float v = s[j][y] * mul[x];
-          if constexpr (kQuant) v *= (y & 1) ? kscale.y : kscale.x;
-          if constexpr (kScored) {
-            if (p.cap2 > 0.f) v = p.cap2 * tanhf(v);
-            v = fmaf(-slope2[x], (float)abs(ra[x].pos - key), v);
+      for (int t = 0; t < kNt; ++t) {
+        float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kMt; ++j)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int at_key = 16 * j + 8 * y + qn;
+            F2 by = mul[t];
+            if constexpr (kQuant) by = mul2(by, f2(ks[at_key]));
+            F2 v = mul2(f2(s[j][t][2 * y], s[j][t][2 * y + 1]), by);
+            float v0, v1;
+            if constexpr (kScored) {
+              if (p.cap2 > 0.f) {
+                split(v, &v0, &v1);
+                v = f2(p.cap2 * tanhf(v0), p.cap2 * tanhf(v1));
+              }
+              const int key = base + at_key;
+              v = fma2(slope2[t], f2((float)abs(pos[t][0] - key), (float)abs(pos[t][1] - key)), v);
+            }
+            split(v, &v0, &v1);
+            if (masked) {
+              const int key = base + at_key;
+              if ((unsigned)(key - lo[t][0]) >= (unsigned)(hi[t][0] - lo[t][0])) v0 = -INFINITY;
+              if ((unsigned)(key - lo[t][1]) >= (unsigned)(hi[t][1] - lo[t][1])) v1 = -INFINITY;
+            }
+            s[j][t][2 * y] = v0;
+            s[j][t][2 * y + 1] = v1;
+            top0 = fmaxf(top0, v0);
+            top1 = fmaxf(top1, v1);
           }
-          if (masked && (unsigned)(key - lo[x]) >= (unsigned)(hi[x] - lo[x])) v = -INFINITY;
-          s[j][y] = v;
-          top[x] = fmaxf(top[x], v);
-        }
+        top[t] = f2(top0, top1);
+        grow |= top0 > m[t][0] + kLazy || top1 > m[t][1] + kLazy;
       }
-      top[0] = quad_max(top[0]);
-      top[1] = quad_max(top[1]);
-      if (__any_sync(0xffffffffu, top[0] > m[0] + kLazy || top[1] > m[1] + kLazy)) {
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float to = fmaxf(m[x], top[x]), by = to == m[x] ? 1.f : fast_exp2(m[x] - to);
-          m[x] = to;
-          l[x] *= by;
+        for (int t = 0; t < kNt; ++t) {
+          float tops[2], by[2];
+          split(top[t], &tops[0], &tops[1]);
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d) {
-            o[d][2 * x] *= by;
-            o[d][2 * x + 1] *= by;
+          for (int x = 0; x < 2; ++x) {
+            const float to = fmaxf(m[t][x], row_max(tops[x]));
+            by[x] = to == m[t][x] ? 1.f : fast_exp2(m[t][x] - to);
+            m[t][x] = to;
           }
+          l[t] = mul2(l[t], f2(by[0], by[1]));
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) o[d][t][y] *= by[y & 1];
         }
       }
-      const float at0 = m[0] == -INFINITY ? 0.f : m[0], at1 = m[1] == -INFINITY ? 0.f : m[1];
-#pragma unroll
-      for (int j = 0; j < kNt; ++j) {
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          s[j][y] = fast_exp2(s[j][y] - (y < 2 ? at0 : at1));
-          l[y >> 1] += s[j][y];
-        }
-      }
-
+      float inv = 0.f;
       if constexpr (kQuant) {
         // fp16 weights p * v's scale in units of vref, the power of two at or above the largest
         // scale so far, raised by kPUp: at most 2^(8 + 6 + 1), and nothing is lost above 2^-20
@@ -558,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 #pragma unroll
         for (int x = 0; x < kKeys / 32; ++x) {
           const int key = base + 32 * x + lane;
-          if (key >= w.lo && key < w.hi)
+          if (!cut_v || (key >= pc.lo && key < pc.hi))
             big = max(big, __float_as_uint(vs[32 * x + lane]) & 0x7fffffffu);
         }
         big = __reduce_max_sync(0xffffffffu, big);
@@ -567,84 +750,86 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
           if (to > vref) {
             const float by = vref / to;
 #pragma unroll
-            for (int d = 0; d < D / 8; ++d)
+            for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-              for (int y = 0; y < 4; ++y) o[d][y] *= by;
+              for (int t = 0; t < kNt; ++t)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) o[d][t][y] *= by;
             vref = to;
           }
         }
-        const float inv = vref > 0.f ? kPUp / vref : 0.f;
-#pragma unroll
-        for (int j = 0; j < kNt; ++j) {
-          float2 f = *reinterpret_cast<const float2*>(vs + 8 * j + 2 * qt);
-          if (cut_v) {
-            const int key = base + 8 * j + 2 * qt;
-            if (key < w.lo || key >= w.hi) f.x = 0.f;
-            if (key + 1 < w.lo || key + 1 >= w.hi) f.y = 0.f;
-          }
-          f.x *= inv;
-          f.y *= inv;
-          s[j][0] *= f.x;
-          s[j][1] *= f.y;
-          s[j][2] *= f.x;
-          s[j][3] *= f.y;
-        }
+        inv = vref > 0.f ? kPUp / vref : 0.f;
       }
 
-      // O += P V, 16 keys at a time
+      // weights, as B operands: [row n][keys 2 t, + 1]
+      uint32_t ph[kMt][kNt][2], pl[kQuant ? 1 : kMt][kNt][2];
 #pragma unroll
-      for (int kk = 0; kk < kKeys / 16; ++kk) {
+      for (int t = 0; t < kNt; ++t) {
+        const F2 off = f2(m[t][0] == -INFINITY ? 0.f : -m[t][0], m[t][1] == -INFINITY ? 0.f : -m[t][1]);
+#pragma unroll
+        for (int j = 0; j < kMt; ++j)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float a, b;
+            split(add2(f2(s[j][t][2 * y], s[j][t][2 * y + 1]), off), &a, &b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            l[t] = add2(l[t], f2(a, b));
+            if constexpr (kQuant) {
+              const int key = 16 * j + 8 * y + qn;
+              float f = vs[key] * inv;
+              if (cut_v && (base + key < pc.lo || base + key >= pc.hi)) f = 0.f;
+              ph[j][t][y] = turned(pack_half(a * f, b * f));
+            } else {
+              const uint32_t h = pack_bf16(a, b);
+              ph[j][t][y] = turned(h);
+              pl[j][t][y] = turned(pack_bf16(a - __uint_as_float(h << 16),
+                                             b - __uint_as_float(h & 0xffff0000u)));
+            }
+          }
+      }
+
+      // O^T += V^T P^T, 16 keys at a time
+#pragma unroll
+      for (int j = 0; j < kMt; ++j) {
         uint32_t live[2] = {~0u, ~0u};
         if (cut_v) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int key = base + 16 * kk + 8 * x + 2 * qt;
-            live[x] = (key >= w.lo && key < w.hi ? 0xffffu : 0u) |
-                      (key + 1 >= w.lo && key + 1 < w.hi ? 0xffff0000u : 0u);
+            const int key = base + 16 * j + 8 * x + 2 * qt;
+            live[x] = (key >= pc.lo && key < pc.hi ? 0xffffu : 0u) |
+                      (key + 1 >= pc.lo && key + 1 < pc.hi ? 0xffff0000u : 0u);
           }
         }
-        uint32_t ph[4], pl[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float a = s[2 * kk + (x >> 1)][2 * (x & 1)], b = s[2 * kk + (x >> 1)][2 * (x & 1) + 1];
-          if constexpr (kQuant) {
-            ph[x] = pack_half(a, b);
-          } else {
-            ph[x] = pack_bf16(a, b);
-            pl[x] = pack_bf16(a - __uint_as_float(ph[x] << 16),
-                              b - __uint_as_float(ph[x] & 0xffff0000u));
-          }
-        }
-        const int row = 16 * kk + (lm & 1) * 8 + l7;
 #pragma unroll
         for (int x = 0; x < C::kRow / 32; ++x) {  // 32 bytes of the values at a time
-          const int chunk = 2 * x + (lm >> 1);
           uint32_t f[4];
-          if constexpr (C::kPitch == 128) {
-            const int half = chunk >> 3;
-            ldsm4_t(vt + (half * kKeys + row) * 128 + (((chunk & 7) ^ l7) << 4), f);
-          } else {
-            ldsm4_t(vt + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4), f);
-          }
-          if (cut_v) {
-            f[0] &= live[0];
-            f[1] &= live[1];
-            f[2] &= live[0];
-            f[3] &= live[1];
-          }
+          ldsm4_t(vt + ((x >> 2) * kKeys + 16 * j) * C::kPitch + v_row + (v_x ^ ((x & 3) << 5)), f);
           if constexpr (!kQuant) {
-            mma<false>(o[2 * x], ph, f[0], f[1]);
-            mma<false>(o[2 * x + 1], ph, f[2], f[3]);
-            mma<false>(o[2 * x], pl, f[0], f[1]);
-            mma<false>(o[2 * x + 1], pl, f[2], f[3]);
+            if (cut_v) {
+              f[0] &= live[0];
+              f[1] &= live[0];
+              f[2] &= live[1];
+              f[3] &= live[1];
+            }
+#pragma unroll
+            for (int t = 0; t < kNt; ++t) mma<0>(o[x][t], f, ph[j][t]);
+#pragma unroll
+            for (int t = 0; t < kNt; ++t) mma<0>(o[x][t], f, pl[j][t]);
           } else {
+            if (cut_v) {
+              f[0] &= live[0];
+              f[1] &= live[1];
+              f[2] &= live[0];
+              f[3] &= live[1];
+            }
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              uint32_t a0, a1, c0, c1;
-              across<kType>(f[2 * y], &a0, &c0);
-              across<kType>(f[2 * y + 1], &a1, &c1);
-              mma<true>(o[4 * x + 2 * y], ph, a0, a1);
-              mma<true>(o[4 * x + 2 * y + 1], ph, c0, c1);
+              uint32_t a[4];
+              across<kType>(f[2 * y], &a[0], &a[1]);
+              across<kType>(f[2 * y + 1], &a[2], &a[3]);
+#pragma unroll
+              for (int t = 0; t < kNt; ++t) mma<1>(o[2 * x + y][t], a, ph[j][t]);
             }
           }
         }
@@ -652,101 +837,107 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
     }
-    n += walk.c1 - walk.c0;
+    n += pc.chunks;
 
-    l[0] = quad_sum(l[0]);
-    l[1] = quad_sum(l[1]);
+    float ls[kNt][2];
+#pragma unroll
+    for (int t = 0; t < kNt; ++t) {
+      split(l[t], &ls[t][0], &ls[t][1]);
+      ls[t][0] = row_sum(ls[t][0]);
+      ls[t][1] = row_sum(ls[t][1]);
+    }
     if constexpr (kQuant) {
 #pragma unroll
-      for (int d = 0; d < D / 8; ++d)
+      for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) o[d][y] = o[d][y] * (1.f / kPUp) * vref;
+        for (int t = 0; t < kNt; ++t)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) o[d][t][y] = o[d][t][y] * (1.f / kPUp) * vref;
     }
     // the warps of the same rows: into the first of them
     if (kgs > 1) {
-      const int bar = 1 + tile;
-      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * kgs) : "memory");
+      const uint32_t parity = np & 1;
       if (kg > 0) {
-        float4* to = merge + ((kg - 1) * p.tiles + tile) * (C::kMerge / 16) + lane;
+        if (np > 0 && !wait_all(&merge_empty[tile], parity ^ 1, wait)) return;
+        float4* to = merge + ((kg - 1) * p.row_warps + tile) * (C::kMerge / 16) + lane;
 #pragma unroll
-        for (int d = 0; d < D / 8; ++d) to[32 * d] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
-        to[32 * (D / 8)] = make_float4(m[0], m[1], l[0], l[1]);
+        for (int t = 0; t < kNt; ++t) {
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d, to += 32)
+            *to = make_float4(o[d][t][0], o[d][t][1], o[d][t][2], o[d][t][3]);
+          *to = make_float4(m[t][0], m[t][1], ls[t][0], ls[t][1]);
+          to += 32;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&merge_full[tile]);
+        continue;
       }
-      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * kgs) : "memory");
-      if (kg > 0) continue;
+      if (!wait_all(&merge_full[tile], parity, wait)) return;
       for (int g = 1; g < kgs; ++g) {
-        const float4* from = merge + ((g - 1) * p.tiles + tile) * (C::kMerge / 16) + lane;
-        const float4 ml = from[32 * (D / 8)];
-        float mine[2], other[2];
+        const float4* from = merge + ((g - 1) * p.row_warps + tile) * (C::kMerge / 16) + lane;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float mo = x ? ml.y : ml.x, lother = x ? ml.w : ml.z;
-          const float to = fmaxf(m[x], mo), ref = to == -INFINITY ? 0.f : to;
-          mine[x] = fast_exp2(m[x] - ref);
-          other[x] = fast_exp2(mo - ref);
-          l[x] = l[x] * mine[x] + lother * other[x];
-          m[x] = to;
-        }
+        for (int t = 0; t < kNt; ++t, from += 32 * (D / 16 + 1)) {
+          const float4 ml = from[32 * (D / 16)];
+          float own[2], other[2];
 #pragma unroll
-        for (int d = 0; d < D / 8; ++d) {
-          const float4 v = from[32 * d];
-          o[d][0] = o[d][0] * mine[0] + v.x * other[0];
-          o[d][1] = o[d][1] * mine[0] + v.y * other[0];
-          o[d][2] = o[d][2] * mine[1] + v.z * other[1];
-          o[d][3] = o[d][3] * mine[1] + v.w * other[1];
+          for (int x = 0; x < 2; ++x) {
+            const float mo = x ? ml.y : ml.x, lo_ = x ? ml.w : ml.z;
+            const float to = fmaxf(m[t][x], mo), ref = to == -INFINITY ? 0.f : to;
+            own[x] = fast_exp2(m[t][x] - ref);
+            other[x] = fast_exp2(mo - ref);
+            ls[t][x] = ls[t][x] * own[x] + lo_ * other[x];
+            m[t][x] = to;
+          }
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            const float4 v = from[32 * d];
+            o[d][t][0] = o[d][t][0] * own[0] + v.x * other[0];
+            o[d][t][1] = o[d][t][1] * own[1] + v.y * other[1];
+            o[d][t][2] = o[d][t][2] * own[0] + v.z * other[0];
+            o[d][t][3] = o[d][t][3] * own[1] + v.w * other[1];
+          }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&merge_empty[tile]);
     }
 
-    const bool begins = walk.c0 == 0, ends = walk.c1 == w.chunks;
-    if (begins && ends) {
+    // channels of o[d][t][0 / 2] (row 2 t; [1 / 3]: row 2 t + 1): bf16 16 d + n and 16 d + 8 + n, 8-bit types
+    // 16 d + 2 n and the next
+#pragma unroll
+    for (int t = 0; t < kNt; ++t) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if (!ra[x].live) continue;
-        const float by = l[x] == 0.f ? 0.f : 1.f / l[x];
-        __nv_bfloat16* to = p.o + ra[x].token * p.o_stride + (long long)ra[x].head * D;
-        if constexpr (!kQuant) {
+        const RowAt ra = row_at(p, pc.s, pc.head, row0 + 8 * t + 2 * qt + x);
+        if (!ra.live) continue;
+        if (pc.place < 0) {
+          const float by = ls[t][x] == 0.f ? 0.f : 1.f / ls[t][x];
+          __nv_bfloat16* to = p.o + ra.token * p.o_stride + (long long)ra.head * D;
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d)
-            *reinterpret_cast<uint32_t*>(to + 8 * d + 2 * qt) =
-                pack_bf16(o[d][2 * x] * by, o[d][2 * x + 1] * by);
+          for (int d = 0; d < D / 16; ++d) {
+            const uint32_t two = pack_bf16(o[d][t][x] * by, o[d][t][2 + x] * by);
+            if constexpr (kQuant) {
+              *reinterpret_cast<uint32_t*>(to + 16 * d + 2 * qn) = two;
+            } else {
+              reinterpret_cast<uint16_t*>(to)[16 * d + qn] = (uint16_t)two;
+              reinterpret_cast<uint16_t*>(to)[16 * d + 8 + qn] = (uint16_t)(two >> 16);
+            }
+          }
+          if (p.lse && qn == 0) p.lse[ra.head * p.seqs.n + ra.token] = lse_of(m[t][x], ls[t][x]);
         } else {
+          const long long row = (long long)pc.place * p.rows + 8 * (kNt * tile + t) + 2 * qt + x;
+          float* to = p.part_o + row * D;
 #pragma unroll
-          for (int d = 0; d < D / 16; ++d)
-            *reinterpret_cast<uint2*>(to + 16 * d + 4 * qt) =
-                make_uint2(pack_bf16(o[2 * d][2 * x] * by, o[2 * d + 1][2 * x] * by),
-                           pack_bf16(o[2 * d][2 * x + 1] * by, o[2 * d + 1][2 * x + 1] * by));
+          for (int d = 0; d < D / 16; ++d) {
+            if constexpr (kQuant) {
+              *reinterpret_cast<float2*>(to + 16 * d + 2 * qn) = make_float2(o[d][t][x], o[d][t][2 + x]);
+            } else {
+              to[16 * d + qn] = o[d][t][x];
+              to[16 * d + 8 + qn] = o[d][t][2 + x];
+            }
+          }
+          if (qn == 0) p.part_ml[row] = make_float2(m[t][x], ls[t][x]);
         }
-        if (p.lse && qt == 0) p.lse[ra[x].head * p.seqs.n + ra[x].token] = lse_of(m[x], l[x]);
-      }
-    } else {
-      // a piece: the CTA's first place for one that another CTA began, its second otherwise
-      const int place = 2 * blockIdx.x + (begins ? 1 : 0), rows = 16 * p.tiles;
-      if (begins && tile == 0 && lane == 0) {
-        // the CTAs that have the rest: the last one holds the item's last unit
-        const long long rest = (long long)w.chunks - walk.c1;  // units behind this range
-        const long long end = u1 + rest;
-        const int last = (int)((end * range[1] - 1) / range[0]);
-        p.joins[blockIdx.x] = make_int4(walk.b, walk.item, last - (int)blockIdx.x + 1, 0);
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (!ra[x].live) continue;
-        const long long row = (long long)place * rows + 16 * tile + qn + 8 * x;
-        float* to = p.part_o + row * D;
-        if constexpr (!kQuant) {
-#pragma unroll
-          for (int d = 0; d < D / 8; ++d)
-            *reinterpret_cast<float2*>(to + 8 * d + 2 * qt) =
-                make_float2(o[d][2 * x], o[d][2 * x + 1]);
-        } else {
-#pragma unroll
-          for (int d = 0; d < D / 16; ++d)
-            *reinterpret_cast<float4*>(to + 16 * d + 4 * qt) =
-                make_float4(o[2 * d][2 * x], o[2 * d + 1][2 * x], o[2 * d][2 * x + 1],
-                            o[2 * d + 1][2 * x + 1]);
-        }
-        if (qt == 0) p.part_ml[row] = make_float2(m[x], l[x]);
       }
     }
   }
@@ -762,10 +953,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
   const int4 join = p.joins[blockIdx.x];
   if (join.z == 0) return;
   __shared__ float so[kJoinWarps][D], sm[kJoinWarps], sl[kJoinWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = 16 * p.tiles;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = p.rows;
   const Work w = work_of<kKeys, false>(p, join.x);
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    const RowAt at = row_at(p, w, join.y, r);
+    const int head = join.y / w.tiles;
+    const RowAt at = row_at(p, w.s, head, (join.y - head * w.tiles) * rows + r);
     if (!at.live) break;  // rows are live up to the last token's
     float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
@@ -831,15 +1023,16 @@ bool pages_map(CUtensorMap* map, const void* base, int type, int64_t stride, con
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int kType, bool kScored>
+template <int D, int kType, int kNt, bool kScored>
 marble_status_t launch(AttnParams& p, int grid, int join_rows, cudaStream_t s) {
-  using C = Cfg<D, kType>;
-  if (once_per_device(64 + (D == 128 ? 0 : 1) + 2 * kType + (kScored ? 8 : 0))) {
-    const cudaError_t e = cudaFuncSetAttribute(k_attn_cached<D, kType, kScored>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  using C = Cfg<D, kType, kNt>;
+  auto kernel = k_attn_cached<D, kType, kNt, kScored>;
+  if (once_per_device(64 + (D == 128 ? 0 : 1) + 2 * kType + (kScored ? 8 : 0) + 16 * kNt)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(k_attn_cached)");
   }
-  k_attn_cached<D, kType, kScored><<<grid, kThreads, C::kSmem, s>>>(p);
+  kernel<<<grid, kThreads, C::kSmem, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "marble_attn_cached launch");
   cudaLaunchAttribute early;
@@ -896,34 +1089,40 @@ marble_status_t run_attn_cached(int64_t n, const marble_cache_t* c, const marble
   p.window = a->window;
   p.span = a->span ? 1 : 0;
   const int64_t rows = std::min<int64_t>(64, (int64_t)p.group * std::max(1, a->new_tokens));
-  p.tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  const int nt = rows <= 8 ? 1 : 2;
+  p.row_warps = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  p.rows = 8 * nt * p.row_warps;
   p.grain = 2;
   p.limit_ns = wait_limit_ns();
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // workspace: a word for timeouts without a status, the joins, the pieces
-  const int64_t piece = 16 * p.tiles * (int64_t)(c->d + 2) * 4;
+  const int64_t piece = p.rows * (int64_t)(c->d + 2) * 4;
   const int64_t most = (MARBLE_ATTN_CACHED_WORKSPACE_BYTES - 65536) / (2 * piece);
   const int grid = (int)std::min<int64_t>(std::min<int64_t>(2 * sms, most), 4000);
   char* ws = static_cast<char*>(a->workspace);
   p.err = seqs->status ? reinterpret_cast<unsigned*>(seqs->status) : reinterpret_cast<unsigned*>(ws);
   p.joins = reinterpret_cast<int4*>(ws + 256);
   p.part_ml = reinterpret_cast<float2*>(ws + 65536);
-  p.part_o = reinterpret_cast<float*>(ws + 65536 + 2 * (int64_t)grid * 16 * p.tiles * 8);
-  auto at_d = [&](auto dd) {
-    constexpr int D = decltype(dd)::value;
+  p.part_o = reinterpret_cast<float*>(ws + 65536 + 2 * (int64_t)grid * p.rows * 8);
+  auto at_d = [&](auto dd, auto tt) {
+    constexpr int D = decltype(dd)::value, T = decltype(tt)::value;
     switch (c->type * 2 + (scored ? 1 : 0)) {
-      case 0: return launch<D, MARBLE_CACHE_BF16, false>(p, grid, (int)rows, s);
-      case 1: return launch<D, MARBLE_CACHE_BF16, true>(p, grid, (int)rows, s);
-      case 2: return launch<D, MARBLE_CACHE_E4M3, false>(p, grid, (int)rows, s);
-      case 3: return launch<D, MARBLE_CACHE_E4M3, true>(p, grid, (int)rows, s);
-      case 4: return launch<D, MARBLE_CACHE_INT8, false>(p, grid, (int)rows, s);
-      default: return launch<D, MARBLE_CACHE_INT8, true>(p, grid, (int)rows, s);
+      case 0: return launch<D, MARBLE_CACHE_BF16, T, false>(p, grid, (int)rows, s);
+      case 1: return launch<D, MARBLE_CACHE_BF16, T, true>(p, grid, (int)rows, s);
+      case 2: return launch<D, MARBLE_CACHE_E4M3, T, false>(p, grid, (int)rows, s);
+      case 3: return launch<D, MARBLE_CACHE_E4M3, T, true>(p, grid, (int)rows, s);
+      case 4: return launch<D, MARBLE_CACHE_INT8, T, false>(p, grid, (int)rows, s);
+      default: return launch<D, MARBLE_CACHE_INT8, T, true>(p, grid, (int)rows, s);
     }
   };
-  return c->d == 128 ? at_d(std::integral_constant<int, 128>{})
-                     : at_d(std::integral_constant<int, 64>{});
+  const std::integral_constant<int, 128> d128;
+  const std::integral_constant<int, 64> d64;
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 2> two;
+  return c->d == 128 ? (nt == 1 ? at_d(d128, one) : at_d(d128, two))
+                     : (nt == 1 ? at_d(d64, one) : at_d(d64, two));
 }
 
 }  // namespace marble

@@ -136,11 +136,7 @@ __device__ __forceinline__ void restore(const uint4& codes, float scale, uint32_
   for (int i = 0; i < 8; ++i) {
     float lo, hi;
     if constexpr (kType == MARBLE_CACHE_E4M3) {
-      const uint32_t h = e4m3_halves(c[i >> 1] >> (16 * (i & 1)));
-      asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\t"
-          "cvt.f32.f16 %1, b;\n\t}"
-          : "=f"(lo), "=f"(hi)
-          : "r"(h));
+      halves_to_float(e4m3_halves(c[i >> 1] >> (16 * (i & 1))), &lo, &hi);
     } else {
       // the byte above 2^23 with its sign bit turned is 2^23 + 128 + code
       const uint32_t u = c[i >> 1] ^ 0x80808080u;

@@ -63,13 +63,20 @@ __device__ __forceinline__ int page_at(const SeqsParams& p, int b, int pos) {
   return (unsigned)g < (unsigned)p.n_pages ? g : -1;
 }
 
-// e4m3 and int8 codes, two or four at a time, as halves (exact)
+// two e4m3 codes as halves, and those as fp32 (all exact)
 __device__ __forceinline__ uint32_t e4m3_halves(uint32_t two) {  // low 16 bits
   uint32_t h;
   asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
       : "=r"(h)
       : "r"(two));
   return h;
+}
+
+__device__ __forceinline__ void halves_to_float(uint32_t h, float* lo, float* hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\t"
+      "cvt.f32.f16 %1, b;\n\t}"
+      : "=f"(*lo), "=f"(*hi)
+      : "r"(h));
 }
 
 }  // namespace marble
