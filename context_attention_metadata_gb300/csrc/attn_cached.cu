@@ -40,17 +40,17 @@ constexpr int kThreads = 32 * (kWorkers + 1);
 constexpr int kUnitOver = 1;                    // an item's constant cost, in chunks
 constexpr float kLazy = 8.f;                    // O is rescaled when m grows by more (base 2)
 constexpr float kPUp = 64.f;                    // fp16 weights are raised by this (see below)
-constexpr float kLoUp = 32.f;                   // q's second e4m3 term is raised by this
 
 // kNt: tiles of 8 rows that a warp computes
 template <int D, int kType, int kNt>
 struct Cfg {
   static constexpr bool kQuant = kType != MARBLE_CACHE_BF16;
-  static constexpr bool kFp8 = kType == MARBLE_CACHE_E4M3;
   static constexpr int kRow = D * (kQuant ? 1 : 2);          // bytes of a key
   static constexpr int kPitch = kRow > 128 ? 128 : kRow;     // of its rows in shared memory
   static constexpr int kHalves = kRow / kPitch;
   static constexpr int kKeys = kRow > 128 ? 32 : 64;         // of a chunk
+  // keys that a warp works on at once: what its registers hold beside O and q
+  static constexpr int kSub = kNt == 2 && kQuant && D == 128 ? 32 : kKeys;
   static constexpr int kTile = kKeys * kRow;
   static constexpr int kStages = kTile == 8192 ? 4 : 8;
   static_assert(kStages % kWorkers == 0, "a place of the ring belongs to the same warps");
@@ -88,7 +88,7 @@ struct AttnParams {
   int hkv, group, hq;
   int window, span;
   int row_warps;     // warps that an item's rows are split over: 1, 2 or 4
-  int rows;          // of an item: 8 * kNt * row_warps
+  int rows, rows_log;  // of an item: 8 * kNt * row_warps
   int box;           // keys of a TMA box
   int grain;         // units a CTA takes at least
   float* part_o;     // [2 * CTAs][rows][D] pieces
@@ -126,7 +126,7 @@ __device__ __forceinline__ Work work_of(const AttnParams& p, int b) {
   w.hi = p.window > 0 || p.span ? w.s.len : w.lo;  // (no window: no keys at all)
   w.chunk0 = w.lo / kKeys;
   w.chunks = w.lo < w.hi ? (w.hi - 1) / kKeys - w.chunk0 + 1 : 0;
-  w.tiles = (int)(((long long)w.s.count * p.group + p.rows - 1) / p.rows);
+  w.tiles = (int)(((long long)w.s.count * p.group + p.rows - 1) >> p.rows_log);
   w.items = w.tiles * p.hkv;
   w.units = w.items ? w.chunks + kUnitOver : 0;
   return w;
@@ -139,33 +139,41 @@ __device__ __forceinline__ int cut(long long x) { return (int)max(x - kUnitOver,
 template <int kKeys>
 struct Walk {
   const AttnParams& p;
-  long long left, at;  // units left, offset in the sequence's units
+  long long left, off;  // units left, those of the present item that are behind
   int b;
   Work w;
   // of the present piece
   int item, c0, c1;
-  __device__ __forceinline__ Walk(const AttnParams& p_, int b_, long long at_, long long left_)
-      : p(p_), left(left_), at(at_), b(b_) {
+  // from unit `at` of sequence b_ on
+  __device__ __forceinline__ Walk(const AttnParams& p_, int b_, long long at, long long left_)
+      : p(p_), left(left_), b(b_) {
     w = work_of<kKeys, false>(p, b);
+    next_item = (int)(at / w.units);
+    off = at - next_item * w.units;
   }
   __device__ __forceinline__ bool next() {
     while (left > 0) {
-      if (at >= w.units * w.items) {
-        at -= w.units * w.items;
+      if (next_item >= w.items) {
         if (++b >= p.seqs.n_seqs) return false;
         w = work_of<kKeys, false>(p, b);
+        next_item = 0;
         continue;
       }
-      item = (int)(at / w.units);
-      const long long from = at - item * w.units, to = min(w.units, from + left);
-      at += to - from;
+      item = next_item;
+      const long long from = off, to = min(w.units, from + left);
       left -= to - from;
+      const bool ends = to == w.units;
+      next_item += ends ? 1 : 0;
+      off = ends ? 0 : to;
       c0 = cut(from);
       c1 = cut(to);
       if (c1 > c0 || (w.chunks == 0 && from == 0)) return true;
     }
     return false;
   }
+
+ private:
+  int next_item;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t at, uint32_t (&r)[4]) {
@@ -184,31 +192,21 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-// c += a b, 16 x 8 x 16 (e4m3: x 32)
-template <int kKind>
+// c += a b, 16 x 8 x 16, of halves or bf16
+template <bool kHalf>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  if constexpr (kKind == 0)
+  if constexpr (!kHalf)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-  else if constexpr (kKind == 1)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
   else
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-__device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -221,11 +219,17 @@ __device__ __forceinline__ uint32_t int8_halves(uint32_t u, uint32_t sel) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
   return r;
 }
-// four int8 codes of consecutive channels of one key: the halves of the first two, and the others
+// four codes of consecutive channels of one key: the halves of the first two, and the others
+template <int kType>
 __device__ __forceinline__ void along(uint32_t c, uint32_t* a, uint32_t* b) {
-  const uint32_t u = c ^ 0x80808080u;
-  *a = int8_halves(u, 0x4140);
-  *b = int8_halves(u, 0x4342);
+  if constexpr (kType == MARBLE_CACHE_E4M3) {
+    *a = e4m3_halves(c);
+    *b = e4m3_halves(c >> 16);
+  } else {
+    const uint32_t u = c ^ 0x80808080u;
+    *a = int8_halves(u, 0x4140);
+    *b = int8_halves(u, 0x4342);
+  }
 }
 // codes (key 0: channels 0, 1; key 1: channels 0, 1): the halves of channel 0, and of channel 1
 template <int kType>
@@ -304,7 +308,7 @@ template <int D, int kType, int kNt, bool kScored>
 __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_constant__ AttnParams p) {
   using C = Cfg<D, kType, kNt>;
   constexpr bool kQuant = C::kQuant;
-  constexpr int kKeys = C::kKeys, kStages = C::kStages, kMt = kKeys / 16;
+  constexpr int kKeys = C::kKeys, kStages = C::kStages, kMt = C::kSub / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align1024(smem_raw);
   float* scales = reinterpret_cast<float*>(ring + kStages * 2 * C::kTile);
@@ -313,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   __shared__ uint64_t full[kStages], empty[kStages], piece_full[C::kPieces], piece_empty[C::kPieces];
   __shared__ uint64_t merge_full[kWorkers], merge_empty[kWorkers];
   __shared__ Piece pieces[C::kPieces];
+  __shared__ int2 looked[32];
   __shared__ int abort_flag, first_b;
   __shared__ long long first_at, range[2], sums[kWorkers + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -381,12 +386,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 
   if (warp == kWorkers) {
     // ---- fetch.  The boxes of the next 32 / boxes chunks are looked up at once, a lane each;
-    // lane 4 x + j then issues box j of part x of a chunk.
+    // one thread then issues all copies (its operands are uniform; lanes side by side would be
+    // taken one by one, at twice the cost).
     const int boxes = kKeys / p.box, group = 32 / boxes;
-    const int box = lane & 3, part = lane >> 2;
-    constexpr int kParts = kQuant ? 4 : 2 * C::kHalves;
+    const bool leader = elect_one();
     Walk<kKeys> walk(p, first_b, first_at, u1 - u0);
-    int n = 0, np = 0;  // chunks and pieces so far
+    int n = 0, np = 0, issued = 0;  // chunks and pieces so far
     bool ok = true;
     while (ok) {
       const bool more = walk.next();
@@ -432,58 +437,63 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       ++np;
       if (!more) break;
 
-      int page = -1, slot = 0;
-      for (int c = walk.c0; c < walk.c1; ++c, ++n) {
-        const int in = (c - walk.c0) % group;
-        if (in == 0) {
-          const int key = (w.chunk0 + c + lane / boxes) * kKeys + lane % boxes * p.box;
-          page = -1;
-          slot = -1;  // not needed
-          if (c + lane / boxes < walk.c1 && key < w.hi && key + p.box > w.lo) {
-            page = page_at(p.seqs, walk.b, key);
-            slot = key % p.seqs.page;
-            if (page < 0) seqs_bad(p.seqs);
-          }
+      for (int c = walk.c0; ok && c < walk.c1; c += group) {
+        const int key = (w.chunk0 + c + lane / boxes) * kKeys + lane % boxes * p.box;
+        int2 at = make_int2(-1, -1);  // page, slot; no slot: not needed
+        if (c + lane / boxes < walk.c1 && key < w.hi && key + p.box > w.lo) {
+          at.x = page_at(p.seqs, walk.b, key);
+          at.y = key % p.seqs.page;
+          if (at.x < 0) seqs_bad(p.seqs);
         }
-        const int st = n % kStages;
-        const int my_page = __shfl_sync(0xffffffffu, page, (in * boxes + box) & 31);
-        const int my_slot = __shfl_sync(0xffffffffu, slot, (in * boxes + box) & 31);
-        const bool needed = box < boxes && my_slot >= 0;
-        const int count = __popc(__ballot_sync(0xffffffffu, needed && part == 0));
-        if (n >= kStages && !warp_wait(&empty[st], ((n / kStages) & 1) ^ 1, wait)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0)
-          mbar_arrive_expect_tx(&full[st], count * p.box * (2 * C::kRow + (kQuant ? 8 : 0)));
+        looked[lane] = at;
+        const unsigned needed = __ballot_sync(0xffffffffu, at.y >= 0);
         __syncwarp();
-        if (needed && part < kParts) {
-          const uint32_t tile = smem_u32(ring) + st * 2 * C::kTile;
-          // (a page that is none lies outside the tensor map: zeros)
-          const int g = my_page < 0 ? p.seqs.n_pages : my_page;
-          if constexpr (kQuant) {
-            if (part < 2) {
-              tma_load_4d(tile + part * C::kTile + box * p.box * C::kPitch,
-                          part ? &p.vmap : &p.kmap, &full[st], 0, my_slot, head, g);
-            } else {
-              const float* src = part == 2 ? p.k_scale + max(my_page, 0) * p.k_scale_stride
-                                           : p.v_scale + max(my_page, 0) * p.v_scale_stride;
-              bulk_load(smem_u32(scales + (2 * st + part - 2) * kKeys + box * p.box),
-                        src + (long long)head * p.seqs.page + my_slot, p.box * 4, &full[st]);
+        const int last = min(group, walk.c1 - c);
+        if (leader) {
+          for (int i = 0; i < last; ++i) {
+            const int at_n = n + i, st = at_n % kStages;
+            if (at_n >= kStages && !mbar_wait(&empty[st], ((at_n / kStages) & 1) ^ 1, wait)) {
+              ok = false;
+              break;
             }
-          } else {
-            const int which = part / C::kHalves, half = part % C::kHalves;
-            tma_load_4d(tile + which * C::kTile + (half * kKeys + box * p.box) * C::kPitch,
-                        which ? &p.vmap : &p.kmap, &full[st], half * 64, my_slot, head, g);
+            issued = at_n + 1;
+            const unsigned want = needed >> (i * boxes) & ((1u << boxes) - 1);
+            mbar_arrive_expect_tx(&full[st],
+                                  __popc(want) * p.box * (2 * C::kRow + (kQuant ? 8 : 0)));
+            const uint32_t tile = smem_u32(ring) + st * 2 * C::kTile;
+            for (int j = 0; j < boxes; ++j) {
+              if (!(want >> j & 1)) continue;
+              const int2 place = looked[i * boxes + j];
+              // (a page that is none lies outside the tensor map: zeros)
+              const int g = place.x < 0 ? p.seqs.n_pages : place.x;
+              const uint32_t to = tile + j * p.box * C::kPitch;
+#pragma unroll
+              for (int h = 0; h < C::kHalves; ++h) {
+                tma_load_4d(to + h * kKeys * C::kPitch, &p.kmap, &full[st], h * 64, place.y, head, g);
+                tma_load_4d(to + C::kTile + h * kKeys * C::kPitch, &p.vmap, &full[st], h * 64, place.y,
+                            head, g);
+              }
+              if constexpr (kQuant) {
+                const long long row = (long long)head * p.seqs.page + place.y;
+                const uint32_t s_to = smem_u32(scales + 2 * st * kKeys + j * p.box);
+                bulk_load(s_to, p.k_scale + max(place.x, 0) * p.k_scale_stride + row, p.box * 4,
+                          &full[st]);
+                bulk_load(s_to + kKeys * 4, p.v_scale + max(place.x, 0) * p.v_scale_stride + row,
+                          p.box * 4, &full[st]);
+              }
+            }
           }
         }
-        __syncwarp();
+        n += last;
+        ok = __all_sync(0xffffffffu, ok);
       }
     }
-    if (lane == 0) {
+    if (leader) {
       // the last copies write to this CTA's shared memory, whoever still waits for them
-      for (int i = max(0, n - kStages); i < n; ++i)
+      for (int i = max(0, issued - kStages); i < issued; ++i)
         drain_wait(&full[i % kStages], (i / kStages) & 1, p.limit_ns, p.err);
+    }
+    if (lane == 0) {
       for (int i = max(0, np - C::kPieces); i < np; ++i)
         drain_wait(&piece_full[i % C::kPieces], (i / C::kPieces) & 1, p.limit_ns, p.err);
     }
@@ -509,13 +519,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     if (pc.chunks < 0) return;
     const int row0 = pc.row0 + 8 * kNt * tile;  // this warp's first row
 
-    // q: bf16, channels (2 t, + 1, + 8, + 9) of 16; for int8 fp16, channels 4 t .. + 3 of 16 (the
-    // order in which the codes come out of the ring); for e4m3 two terms, channels 4 t .. + 3 and
-    // 16 + 4 t .. + 3 of 32
-    constexpr int kQn = C::kFp8 ? D / 32 : D / 16;
-    uint32_t q[kNt][kQn][2], q2[C::kFp8 ? kNt : 1][kQn][2];
+    // q: bf16, channels (2 t, + 1, + 8, + 9) of 16; or fp16, channels 4 t .. + 3 of 16, the order in
+    // which 8-bit codes come out of the ring
+    uint32_t q[kNt][D / 16][2];
     F2 mul[kNt];                     // what the rows' products have to be multiplied by
-    int lo[kNt][2], hi[kNt][2], pos[kNt][2];
+    int pos[kNt][2];                 // -1: no row
     F2 slope2[kNt];
 #pragma unroll
     for (int t = 0; t < kNt; ++t) {
@@ -525,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       float up = 1.f;
       if constexpr (!kQuant) {
 #pragma unroll
-        for (int s = 0; s < kQn; ++s) {
+        for (int s = 0; s < D / 16; ++s) {
           const uint32_t* at = reinterpret_cast<const uint32_t*>(src + 32 * s + 4 * qt);
           q[t][s][0] = live ? at[0] : 0u;
           q[t][s][1] = live ? at[4] : 0u;
@@ -541,33 +549,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the largest channel into [2^14, 2^15), for e4m3 into [2^7, 2^8)
-        const int e = min(max((int)(top >> 7) - 127 - (C::kFp8 ? 7 : 14), -126), 126);
+        // the largest channel into [2^14, 2^15)
+        const int e = min(max((int)(top >> 7) - 127 - 14, -126), 126);
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
         up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          const float f[4] = {__uint_as_float(v[s].x << 16) * down,
-                              __uint_as_float(v[s].x & 0xffff0000u) * down,
-                              __uint_as_float(v[s].y << 16) * down,
-                              __uint_as_float(v[s].y & 0xffff0000u) * down};
-          if constexpr (C::kFp8) {
-            // two e4m3 terms hold bf16's 8 bits: what the first leaves is at most 8 of its last
-            // places' halves.  Channels below 2^-14 of the largest lose bits below 2^-22 of it.
-            q[t][s >> 1][s & 1] = pack_e4m3(f[0], f[1]) | pack_e4m3(f[2], f[3]) << 16;
-            const uint32_t c = q[t][s >> 1][s & 1];
-            float g[4];
-            halves_to_float(e4m3_halves(c), &g[0], &g[1]);
-            halves_to_float(e4m3_halves(c >> 16), &g[2], &g[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = (f[i] - g[i]) * kLoUp;
-            q2[t][s >> 1][s & 1] = pack_e4m3(g[0], g[1]) | pack_e4m3(g[2], g[3]) << 16;
-            // (a NaN's or an infinity's codes would be finite)
-            if (top >= 0x7f80u) q[t][s >> 1][s & 1] = 0x7f7f7f7fu;
-          } else {
-            q[t][s][0] = pack_half(f[0], f[1]);
-            q[t][s][1] = pack_half(f[2], f[3]);
-          }
+          q[t][s][0] = pack_half(__uint_as_float(v[s].x << 16) * down,
+                                 __uint_as_float(v[s].x & 0xffff0000u) * down);
+          q[t][s][1] = pack_half(__uint_as_float(v[s].y << 16) * down,
+                                 __uint_as_float(v[s].y & 0xffff0000u) * down);
         }
       }
       // from the lanes that read a row to those that hold its products
@@ -577,9 +568,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         m2[x] = __shfl_sync(0xffffffffu, up, 4 * (2 * qt + x)) *
                 (kScored && p.cap2 > 0.f ? p.to_cap : p.scale2);
         const RowAt ra = row_at(p, pc.s, pc.head, row0 + 8 * t + 2 * qt + x);
-        pos[t][x] = ra.pos;
-        sees(p, pc.s, ra.pos, &lo[t][x], &hi[t][x]);
-        if (!ra.live) lo[t][x] = hi[t][x] = 0;
+        pos[t][x] = ra.live ? ra.pos : -1;
         if constexpr (kScored)
           if (p.slopes && ra.live) sl[x] = p.slopes[ra.head] * -1.4426950408889634f;
       }
@@ -610,13 +599,45 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     }
 
     for (int i = (kg - n) & (kgs - 1); i < pc.chunks; i += kgs) {
-      const int at = n + i, st = at % kStages, base = pc.key0 + i * kKeys;
+      const int at = n + i, st = at % kStages, chunk_base = pc.key0 + i * kKeys;
       if (!wait_all(&full[st], (at / kStages) & 1, wait)) return;
-      const uint32_t kt = smem_u32(ring) + st * 2 * C::kTile, vt = kt + C::kTile;
-      const float* ks = scales + 2 * st * kKeys;
+      const bool cut_v = chunk_base < pc.lo || chunk_base + kKeys > pc.hi;  // keys that no row may see
+      const bool masked = chunk_base < all_lo || chunk_base + kKeys > all_hi;
+      float inv = 0.f;
+      if constexpr (kQuant) {
+        const float* vs_all = scales + (2 * st + 1) * kKeys;
+        // fp16 weights p * v's scale in units of vref, the power of two at or above the largest
+        // scale so far, raised by kPUp: at most 2^(8 + 6 + 1), and nothing is lost above 2^-20
+        // of the largest.
+        uint32_t big = 0;
+#pragma unroll
+        for (int x = 0; x < kKeys / 32; ++x) {
+          const int key = chunk_base + 32 * x + lane;
+          if (!cut_v || (key >= pc.lo && key < pc.hi))
+            big = max(big, __float_as_uint(vs_all[32 * x + lane]) & 0x7fffffffu);
+        }
+        big = __reduce_max_sync(0xffffffffu, big);
+        if (big > __float_as_uint(vref)) {
+          const float to = __uint_as_float(min((big + 0x7fffffu) & 0xff800000u, 0x7f000000u));
+          if (to > vref) {
+            const float by = vref / to;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+              for (int t = 0; t < kNt; ++t)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) o[d][t][y] *= by;
+            vref = to;
+          }
+        }
+        inv = vref > 0.f ? kPUp / vref : 0.f;
+      }
+#pragma unroll 1
+      for (int sub = 0; sub < kKeys; sub += C::kSub) {
+      const int base = chunk_base + sub;
+      const uint32_t kt = smem_u32(ring) + st * 2 * C::kTile + sub * C::kPitch, vt = kt + C::kTile;
+      const float* ks = scales + 2 * st * kKeys + sub;
       const float* vs = ks + kKeys;
-      const bool cut_v = base < pc.lo || base + kKeys > pc.hi;  // keys that no row may see
-      const bool masked = base < all_lo || base + kKeys > all_hi;
 
       // scores
       float s[kMt][kNt][4];
@@ -624,52 +645,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       for (int j = 0; j < kMt; ++j)
 #pragma unroll
         for (int t = 0; t < kNt; ++t) s[j][t][0] = s[j][t][1] = s[j][t][2] = s[j][t][3] = 0.f;
-      if constexpr (C::kFp8) {
-        float s2[kMt][kNt][4];
 #pragma unroll
-        for (int j = 0; j < kMt; ++j)
+      for (int x = 0; x < C::kRow / 32; ++x) {  // 32 bytes of the keys at a time
+        const uint32_t row = kt + (x >> 2) * kKeys * C::kPitch + k_row + (k_x ^ ((x & 3) << 5));
 #pragma unroll
-          for (int t = 0; t < kNt; ++t) s2[j][t][0] = s2[j][t][1] = s2[j][t][2] = s2[j][t][3] = 0.f;
+        for (int j = 0; j < kMt; ++j) {
+          uint32_t f[4];
+          ldsm4(row + j * 16 * C::kPitch, f);
+          if constexpr (!kQuant) {
 #pragma unroll
-        for (int x = 0; x < C::kRow / 32; ++x) {
-          const uint32_t row = kt + k_row + (k_x ^ (x << 5));
+            for (int t = 0; t < kNt; ++t) mma<false>(s[j][t], f, q[t][x]);
+          } else {
 #pragma unroll
-          for (int j = 0; j < kMt; ++j) {
-            uint32_t f[4];
-            ldsm4(row + j * 16 * C::kPitch, f);
+            for (int y = 0; y < 2; ++y) {
+              uint32_t a[4];
+              along<kType>(f[2 * y], &a[0], &a[2]);
+              along<kType>(f[2 * y + 1], &a[1], &a[3]);
 #pragma unroll
-            for (int t = 0; t < kNt; ++t) {
-              mma<2>(s[j][t], f, q[t][x]);
-              mma<2>(s2[j][t], f, q2[t][x]);
-            }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kMt; ++j)
-#pragma unroll
-          for (int t = 0; t < kNt; ++t)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) s[j][t][y] = fmaf(s2[j][t][y], 1.f / kLoUp, s[j][t][y]);
-      } else {
-#pragma unroll
-        for (int x = 0; x < C::kRow / 32; ++x) {  // 32 bytes of the keys at a time
-          const uint32_t row = kt + (x >> 2) * kKeys * C::kPitch + k_row + (k_x ^ ((x & 3) << 5));
-#pragma unroll
-          for (int j = 0; j < kMt; ++j) {
-            uint32_t f[4];
-            ldsm4(row + j * 16 * C::kPitch, f);
-            if constexpr (!kQuant) {
-#pragma unroll
-              for (int t = 0; t < kNt; ++t) mma<0>(s[j][t], f, q[t][x]);
-            } else {
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                uint32_t a[4];
-                along(f[2 * y], &a[0], &a[2]);
-                along(f[2 * y + 1], &a[1], &a[3]);
-#pragma unroll
-                for (int t = 0; t < kNt; ++t) mma<1>(s[j][t], a, q[t][2 * x + y]);
-              }
+              for (int t = 0; t < kNt; ++t) mma<true>(s[j][t], a, q[t][2 * x + y]);
             }
           }
         }
@@ -683,6 +676,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 #pragma unroll
       for (int t = 0; t < kNt; ++t) {
         float top0 = -INFINITY, top1 = -INFINITY;
+        int lo[2] = {0, 0}, hi[2] = {0, 0};
+        if (masked) {
+          sees(p, pc.s, pos[t][0], &lo[0], &hi[0]);
+          sees(p, pc.s, pos[t][1], &lo[1], &hi[1]);
+        }
 #pragma unroll
         for (int j = 0; j < kMt; ++j)
 #pragma unroll
@@ -703,8 +701,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
             split(v, &v0, &v1);
             if (masked) {
               const int key = base + at_key;
-              if ((unsigned)(key - lo[t][0]) >= (unsigned)(hi[t][0] - lo[t][0])) v0 = -INFINITY;
-              if ((unsigned)(key - lo[t][1]) >= (unsigned)(hi[t][1] - lo[t][1])) v1 = -INFINITY;
+              if ((unsigned)(key - lo[0]) >= (unsigned)(hi[0] - lo[0])) v0 = -INFINITY;
+              if ((unsigned)(key - lo[1]) >= (unsigned)(hi[1] - lo[1])) v1 = -INFINITY;
             }
             s[j][t][2 * y] = v0;
             s[j][t][2 * y + 1] = v1;
@@ -732,35 +730,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
             for (int y = 0; y < 4; ++y) o[d][t][y] *= by[y & 1];
         }
       }
-      float inv = 0.f;
-      if constexpr (kQuant) {
-        // fp16 weights p * v's scale in units of vref, the power of two at or above the largest
-        // scale so far, raised by kPUp: at most 2^(8 + 6 + 1), and nothing is lost above 2^-20
-        // of the largest.
-        uint32_t big = 0;
-#pragma unroll
-        for (int x = 0; x < kKeys / 32; ++x) {
-          const int key = base + 32 * x + lane;
-          if (!cut_v || (key >= pc.lo && key < pc.hi))
-            big = max(big, __float_as_uint(vs[32 * x + lane]) & 0x7fffffffu);
-        }
-        big = __reduce_max_sync(0xffffffffu, big);
-        if (big > __float_as_uint(vref)) {
-          const float to = __uint_as_float(min((big + 0x7fffffu) & 0xff800000u, 0x7f000000u));
-          if (to > vref) {
-            const float by = vref / to;
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-              for (int t = 0; t < kNt; ++t)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) o[d][t][y] *= by;
-            vref = to;
-          }
-        }
-        inv = vref > 0.f ? kPUp / vref : 0.f;
-      }
-
       // weights, as B operands: [row n][keys 2 t, + 1]
       uint32_t ph[kMt][kNt][2], pl[kQuant ? 1 : kMt][kNt][2];
 #pragma unroll
@@ -813,9 +782,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
               f[3] &= live[1];
             }
 #pragma unroll
-            for (int t = 0; t < kNt; ++t) mma<0>(o[x][t], f, ph[j][t]);
+            for (int t = 0; t < kNt; ++t) mma<false>(o[x][t], f, ph[j][t]);
 #pragma unroll
-            for (int t = 0; t < kNt; ++t) mma<0>(o[x][t], f, pl[j][t]);
+            for (int t = 0; t < kNt; ++t) mma<false>(o[x][t], f, pl[j][t]);
           } else {
             if (cut_v) {
               f[0] &= live[0];
@@ -829,10 +798,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
               across<kType>(f[2 * y], &a[0], &a[1]);
               across<kType>(f[2 * y + 1], &a[2], &a[3]);
 #pragma unroll
-              for (int t = 0; t < kNt; ++t) mma<1>(o[2 * x + y][t], a, ph[j][t]);
+              for (int t = 0; t < kNt; ++t) mma<true>(o[2 * x + y][t], a, ph[j][t]);
             }
           }
         }
+      }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
@@ -1092,6 +1062,7 @@ marble_status_t run_attn_cached(int64_t n, const marble_cache_t* c, const marble
   const int nt = rows <= 8 ? 1 : 2;
   p.row_warps = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   p.rows = 8 * nt * p.row_warps;
+  while ((1 << p.rows_log) < p.rows) ++p.rows_log;
   p.grain = 2;
   p.limit_ns = wait_limit_ns();
   int dev = 0, sms = 148;
