@@ -874,6 +874,7 @@ class Cache:
                          v.data_ptr(), strides[0], strides[1],
                          k_scale.data_ptr() if kind else None,
                          v_scale.data_ptr() if kind else None, strides[2], strides[3])
+        self._ref = ctypes.byref(self._c)
         self._shape = (k.shape[1], k.shape[3])
 
     @classmethod
@@ -925,7 +926,9 @@ class Sequences:
         self._c = _Seqs(n, width, table.data_ptr(), table.stride(0) if n > 1 else width,
                         lens.data_ptr(), None if start is None else start.data_ptr(),
                         None if status is None else status.data_ptr())
-        self._one = start is None
+        self._ref = ctypes.byref(self._c)
+        self._n = n
+        self._work = {}  # attn_cached's workspaces, one for every stream it has run on
 
     table = property(lambda self: self._parts[0])
     lens = property(lambda self: self._parts[1])
@@ -958,8 +961,8 @@ def _cache_move(name, cache, seqs, parts, plan, stream, what):
     heads = _heads((None, *parts), n, torch.bfloat16, index, what)
     if (heads.hkv, heads.d) != cache._shape:
         raise ValueError(f"{what}k and {what}v must be [n, {cache._shape[0]}, {cache._shape[1]}]")
-    _call(name, None if plan is None else plan.handle, n, ctypes.byref(cache._c),
-          ctypes.byref(seqs._c), ctypes.byref(heads), _raw_stream(torch, stream, index))
+    _call(name, None if plan is None else plan.handle, n, cache._ref, seqs._ref,
+          ctypes.byref(heads), _raw_stream(torch, stream, index))
 
 
 def cache_write(cache: Cache, seqs: Sequences, k, v=None, plan: Optional[Plan] = None,
@@ -978,7 +981,7 @@ def cache_read(cache: Cache, seqs: Sequences, n: Optional[int] = None,
     import torch
     if out is None:
         if n is None:
-            if plan is None and not seqs._one:
+            if plan is None and seqs.start is not None:
                 raise ValueError("n, the number of rows, is needed")
             n = plan.n if plan is not None else seqs.lens.shape[0]
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
@@ -992,6 +995,23 @@ def cache_read(cache: Cache, seqs: Sequences, n: Optional[int] = None,
     return tuple(out)
 
 
+def _attn_workspace(torch, seqs, stream, raw):
+    """The workspace of a call on a stream (its handle: raw; ``stream`` None: the current one).  The
+    sequences keep one for each stream, whose calls run one after the other; a call that is being
+    captured gets one from torch's allocator, which keeps it for its graph alone."""
+    if stream is not None and stream.cuda_stream != _raw_stream(torch, None, seqs._index):
+        with torch.cuda.stream(stream):
+            return _attn_workspace(torch, seqs, None, raw)
+    alone = torch.cuda.is_current_stream_capturing()
+    kept = None if alone else seqs._work.get(raw)
+    if kept is None:
+        kept = torch.empty(ATTN_CACHED_WORKSPACE_BYTES, dtype=torch.uint8,
+                           device=seqs.table.device)
+        if not alone:
+            seqs._work[raw] = kept
+    return kept
+
+
 def attn_cached(cache: Cache, seqs: Sequences, q, scale: float = 0.0, window: int = WINDOW_INF,
                 span: bool = False, score: Optional[Score] = None, new_tokens: int = 0, out=None,
                 workspace=None, stream=None):
@@ -1000,7 +1020,8 @@ def attn_cached(cache: Cache, seqs: Sequences, q, scale: float = 0.0, window: in
     keys and values first.  ``window``, ``scale`` and ``score`` as in the packed calls; ``span``:
     the rows of a sequence all see each other; ``new_tokens``: how many rows a sequence has at
     most, a hint (0: n over the number of sequences).  ``workspace``: uint8 CUDA tensor of
-    ATTN_CACHED_WORKSPACE_BYTES for this call alone, or None (torch's allocator).
+    ATTN_CACHED_WORKSPACE_BYTES for this call alone, or None (the sequences keep one for every
+    stream; a captured call gets its own).
     Returns (o, lse), bf16 [n, hq, d] and fp32 [hq, n]: ``out`` (its lse may be None) or new
     tensors; rows of no sequence are left as they are (undefined in new tensors)."""
     import torch
@@ -1018,14 +1039,16 @@ def attn_cached(cache: Cache, seqs: Sequences, q, scale: float = 0.0, window: in
                          "each token's heads contiguous")
     if seqs._index != index:
         raise ValueError(f"the sequences must be on cuda:{index}")
-    if out is None or workspace is None:
+    raw = _raw_stream(torch, stream, index)
+    if out is None:
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            if out is None:
-                out = (torch.empty((n, hq, d), dtype=bf16, device=q.device),
-                       torch.empty((hq, n), dtype=torch.float32, device=q.device))
-            if workspace is None:
-                workspace = torch.empty(ATTN_CACHED_WORKSPACE_BYTES, dtype=torch.uint8,
-                                        device=q.device)
+            out = (torch.empty((n, hq, d), dtype=bf16, device=q.device),
+                   torch.empty((hq, n), dtype=torch.float32, device=q.device))
+    if workspace is None:
+        workspace = _attn_workspace(torch, seqs, stream, raw)
+    elif workspace.numel() * workspace.element_size() < ATTN_CACHED_WORKSPACE_BYTES or \
+            workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be {ATTN_CACHED_WORKSPACE_BYTES} bytes on cuda:{index}")
     o, lse = out
     so = o.stride()
     if o.dtype is not bf16 or o.shape != q.shape or o.get_device() != index or \
@@ -1034,17 +1057,14 @@ def attn_cached(cache: Cache, seqs: Sequences, q, scale: float = 0.0, window: in
                          "contiguous")
     if lse is not None:
         _need(lse, torch.float32, "lse", (hq, n))
-    if workspace.numel() * workspace.element_size() < ATTN_CACHED_WORKSPACE_BYTES or \
-            workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be {ATTN_CACHED_WORKSPACE_BYTES} bytes on cuda:{index}")
     width = hq * d
     if new_tokens <= 0:
-        new_tokens = -(-n // max(1, seqs._c.n_seqs)) or 1
+        new_tokens = -(-n // max(1, seqs._n)) or 1
     c = _AttnCached(q.data_ptr(), sq[0] if n > 1 else width, o.data_ptr(),
                     so[0] if n > 1 else width, None if lse is None else lse.data_ptr(), hq,
                     scale, window, 1 if span else 0, new_tokens, workspace.data_ptr())
-    _call("marble_attn_cached", n, ctypes.byref(cache._c), ctypes.byref(seqs._c), ctypes.byref(c),
-          None if score is None else ctypes.byref(score._c(hq)), _raw_stream(torch, stream, index))
+    _call("marble_attn_cached", n, cache._ref, seqs._ref, ctypes.byref(c),
+          None if score is None else ctypes.byref(score._c(hq)), raw)
     return o, lse
 
 

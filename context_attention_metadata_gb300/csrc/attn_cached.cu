@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kWorkers = 4;                     // computing warps
 constexpr int kThreads = 32 * (kWorkers + 1);
-constexpr int kUnitOver = 1;                    // an item's constant cost, in chunks
+constexpr int kUnitOver = 3;                    // an item's constant cost, in chunks (measured)
 constexpr float kLazy = 8.f;                    // O is rescaled when m grows by more (base 2)
 constexpr float kPUp = 64.f;                    // fp16 weights are raised by this (see below)
 
@@ -60,10 +60,11 @@ struct Cfg {
   static constexpr int kPieces = kNt == 1 ? 4 : 2;
   static constexpr int kQPitch = D * 2 + 16;
   static constexpr int kMerge = 32 * (D / 4 * kNt + 4 * kNt) * 4;
+  static constexpr int kMergeBufs = kNt == 1 ? 2 : 1;
   static constexpr int most() {
     int m = 0;
     for (int r = 1; r <= kWorkers; r *= 2) {
-      const int bytes = kPieces * 8 * kNt * r * kQPitch + (kWorkers - r) * kMerge;
+      const int bytes = kPieces * 8 * kNt * r * kQPitch + kMergeBufs * (kWorkers - r) * kMerge;
       if (bytes > m && (kNt > 1 || r == 1)) m = bytes;
     }
     return m;
@@ -93,7 +94,7 @@ struct AttnParams {
   int grain;         // units a CTA takes at least
   float* part_o;     // [2 * CTAs][rows][D] pieces
   float2* part_ml;   // [2 * CTAs][rows]
-  int4* joins;       // [CTAs]: sequence, item, pieces (0: none)
+  int4* joins;       // [CTAs][2]: pieces (0: none), the sequence's first row and rows; kv head, first row
   unsigned* err;
   uint64_t limit_ns;
 };
@@ -132,6 +133,11 @@ __device__ __forceinline__ Work work_of(const AttnParams& p, int b) {
   return w;
 }
 
+// a / b of non-negative numbers; most fit 32 bits, whose quotient takes a fifth of the time
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 // chunks before offset x of an item
 __device__ __forceinline__ int cut(long long x) { return (int)max(x - kUnitOver, 0ll); }
 
@@ -148,7 +154,7 @@ struct Walk {
   __device__ __forceinline__ Walk(const AttnParams& p_, int b_, long long at, long long left_)
       : p(p_), left(left_), b(b_) {
     w = work_of<kKeys, false>(p, b);
-    next_item = (int)(at / w.units);
+    next_item = (int)quotient(at, w.units);
     off = at - next_item * w.units;
   }
   __device__ __forceinline__ bool next() {
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   uint8_t* qs = reinterpret_cast<uint8_t*>(scales) + C::kScales;
   float4* merge = reinterpret_cast<float4*>(qs + C::kPieces * p.rows * C::kQPitch);
   __shared__ uint64_t full[kStages], empty[kStages], piece_full[C::kPieces], piece_empty[C::kPieces];
-  __shared__ uint64_t merge_full[kWorkers], merge_empty[kWorkers];
+  __shared__ uint64_t merge_full[kWorkers][C::kMergeBufs], merge_empty[kWorkers][C::kMergeBufs];
   __shared__ Piece pieces[C::kPieces];
   __shared__ int2 looked[32];
   __shared__ int abort_flag, first_b;
@@ -343,7 +349,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   const int kgs = kWorkers / p.row_warps;
   if (tid == 0) {
     abort_flag = 0;
-    p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+    p.joins[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    tma_prefetch_desc(&p.kmap);
+    tma_prefetch_desc(&p.vmap);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], p.row_warps);
@@ -353,8 +361,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       mbar_init(&piece_empty[i], kWorkers);
     }
     for (int i = 0; i < kWorkers; ++i) {
-      mbar_init(&merge_full[i], max(kgs - 1, 1));
-      mbar_init(&merge_empty[i], 1);
+      for (int j = 0; j < C::kMergeBufs; ++j) {
+        mbar_init(&merge_full[i][j], max(kgs - 1, 1));
+        mbar_init(&merge_empty[i][j], 1);
+      }
     }
     fence_mbar_init();
   }
@@ -365,9 +375,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     before += i < warp ? sums[i] : 0;
     total += sums[i];
   }
-  const long long ctas = min((long long)gridDim.x, (total + p.grain - 1) / p.grain);
+  const long long ctas = min((long long)gridDim.x, quotient(total + p.grain - 1, p.grain));
   if (blockIdx.x >= ctas) return;
-  const long long u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
+  const long long u0 = quotient(total * blockIdx.x, ctas), u1 = quotient(total * (blockIdx.x + 1), ctas);
   if (before <= u0 && u0 < before + mine) {
     long long at = u0 - before;
     int b = b0;
@@ -390,6 +400,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     // taken one by one, at twice the cost).
     const int boxes = kKeys / p.box, group = 32 / boxes;
     const bool leader = elect_one();
+    // page and slot of box j of the chunk i behind chunk c of a piece; no slot: not needed
+    auto look = [&](int c, const Walk<kKeys>& walk, int i, int j) {
+      int2 at = make_int2(-1, -1);
+      const int key = (walk.w.chunk0 + c + i) * kKeys + j * p.box;
+      if (c + i < walk.c1 && key < walk.w.hi && key + p.box > walk.w.lo) {
+        at.x = page_at(p.seqs, walk.b, key);
+        at.y = key % p.seqs.page;
+      }
+      return at;
+    };
     Walk<kKeys> walk(p, first_b, first_at, u1 - u0);
     int n = 0, np = 0, issued = 0;  // chunks and pieces so far
     bool ok = true;
@@ -403,6 +423,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       const Work& w = walk.w;
       const int head = more ? walk.item / w.tiles : 0;
       const int row0 = more ? (walk.item - head * w.tiles) * p.rows : 0;
+      // the first look-ups are under way while the piece is described
+      int2 at = more ? look(walk.c0, walk, lane / boxes, lane % boxes) : make_int2(-1, -1);
       const int live = more ? min((int)min((long long)w.s.count * p.group - row0, 64ll), p.rows) : 0;
       if (lane == 0) {
         Piece& q = pieces[ps];
@@ -422,8 +444,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
           if (begins && !ends) {
             // the CTAs that have the rest: the last one holds the item's last unit
             const long long end = u1 + (w.chunks - walk.c1);
-            const int last = (int)((end * range[1] - 1) / range[0]);
-            p.joins[blockIdx.x] = make_int4(walk.b, walk.item, last - (int)blockIdx.x + 1, 0);
+            const int last = (int)quotient(end * range[1] - 1, range[0]);
+            p.joins[2 * blockIdx.x] = make_int4(last - (int)blockIdx.x + 1, w.s.first, w.s.count, head);
+            p.joins[2 * blockIdx.x + 1] = make_int4(row0, 0, 0, 0);
           }
         }
         mbar_arrive_expect_tx(&piece_full[ps], live * D * 2);
@@ -438,13 +461,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       if (!more) break;
 
       for (int c = walk.c0; ok && c < walk.c1; c += group) {
-        const int key = (w.chunk0 + c + lane / boxes) * kKeys + lane % boxes * p.box;
-        int2 at = make_int2(-1, -1);  // page, slot; no slot: not needed
-        if (c + lane / boxes < walk.c1 && key < w.hi && key + p.box > w.lo) {
-          at.x = page_at(p.seqs, walk.b, key);
-          at.y = key % p.seqs.page;
-          if (at.x < 0) seqs_bad(p.seqs);
-        }
+        if (c > walk.c0) at = look(c, walk, lane / boxes, lane % boxes);
+        if (at.y >= 0 && at.x < 0) seqs_bad(p.seqs);
         looked[lane] = at;
         const unsigned needed = __ballot_sync(0xffffffffu, at.y >= 0);
         __syncwarp();
@@ -824,12 +842,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 #pragma unroll
           for (int y = 0; y < 4; ++y) o[d][t][y] = o[d][t][y] * (1.f / kPUp) * vref;
     }
-    // the warps of the same rows: into the first of them
+    // the warps of the same rows: into one of them, which takes turns
     if (kgs > 1) {
-      const uint32_t parity = np & 1;
-      if (kg > 0) {
-        if (np > 0 && !wait_all(&merge_empty[tile], parity ^ 1, wait)) return;
-        float4* to = merge + ((kg - 1) * p.row_warps + tile) * (C::kMerge / 16) + lane;
+      const int buf = np % C::kMergeBufs, parity = (np / C::kMergeBufs) & 1;
+      const int from_one = (kg - np) & (kgs - 1);  // 0: this warp's turn
+      float4* bufs = merge + buf * (kWorkers - p.row_warps) * (C::kMerge / 16) + lane;
+      // (every warp sees every phase of these barriers, one after the other)
+      if (np >= C::kMergeBufs && !wait_all(&merge_empty[tile][buf], parity ^ 1, wait)) return;
+      if (from_one > 0) {
+        float4* to = bufs + ((from_one - 1) * p.row_warps + tile) * (C::kMerge / 16);
 #pragma unroll
         for (int t = 0; t < kNt; ++t) {
 #pragma unroll
@@ -839,12 +860,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
           to += 32;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&merge_full[tile]);
+        if (lane == 0) mbar_arrive(&merge_full[tile][buf]);
         continue;
       }
-      if (!wait_all(&merge_full[tile], parity, wait)) return;
+      if (!wait_all(&merge_full[tile][buf], parity, wait)) return;
       for (int g = 1; g < kgs; ++g) {
-        const float4* from = merge + ((g - 1) * p.row_warps + tile) * (C::kMerge / 16) + lane;
+        const float4* from = bufs + ((g - 1) * p.row_warps + tile) * (C::kMerge / 16);
 #pragma unroll
         for (int t = 0; t < kNt; ++t, from += 32 * (D / 16 + 1)) {
           const float4 ml = from[32 * (D / 16)];
@@ -869,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&merge_empty[tile]);
+      if (lane == 0) mbar_arrive(&merge_empty[tile][buf]);
     }
 
     // channels of o[d][t][0 / 2] (row 2 t; [1 / 3]: row 2 t + 1): bf16 16 d + n and 16 d + 8 + n, 8-bit types
@@ -916,23 +937,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 // Joins the pieces of the item that CTA blockIdx.x of the first kernel began, a row a block (and
 // every gridDim.y-th row after it), a quarter of the pieces a warp.
 constexpr int kJoinWarps = 4;
-template <int D, int kKeys>
+template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ AttnParams p) {
   constexpr int kPer = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 join = p.joins[blockIdx.x];
-  if (join.z == 0) return;
+  const int4 join = p.joins[2 * blockIdx.x];
+  const int row0 = p.joins[2 * blockIdx.x + 1].x;
+  if (join.x == 0) return;
   __shared__ float so[kJoinWarps][D], sm[kJoinWarps], sl[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = p.rows;
-  const Work w = work_of<kKeys, false>(p, join.x);
+  const Seq seq = {join.y, join.z, 0};
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    const int head = join.y / w.tiles;
-    const RowAt at = row_at(p, w.s, head, (join.y - head * w.tiles) * rows + r);
+    const RowAt at = row_at(p, seq, join.w, row0 + r);
     if (!at.live) break;  // rows are live up to the last token's
     float m = -INFINITY, l = 0.f, o[kPer];
 #pragma unroll
     for (int x = 0; x < kPer; ++x) o[x] = 0.f;
-    for (int i = warp; i < join.z; i += kJoinWarps) {
+    for (int i = warp; i < join.x; i += kJoinWarps) {
       const int place = 2 * (blockIdx.x + i) + (i == 0 ? 1 : 0);
       const long long row = (long long)place * rows + r;
       const float2 ml = p.part_ml[row];
@@ -1014,7 +1035,7 @@ marble_status_t launch(AttnParams& p, int grid, int join_rows, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k_join<D, C::kKeys>, p);
+  e = cudaLaunchKernelEx(&cfg, k_join<D>, p);
   if (e != cudaSuccess) return cuda_fail(e, "marble_attn_cached join launch");
   return MARBLE_OK;
 }
@@ -1063,7 +1084,7 @@ marble_status_t run_attn_cached(int64_t n, const marble_cache_t* c, const marble
   p.row_warps = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   p.rows = 8 * nt * p.row_warps;
   while ((1 << p.rows_log) < p.rows) ++p.rows_log;
-  p.grain = 2;
+  p.grain = 5;  // four chunks: one for each computing warp, which takes no longer than fewer
   p.limit_ns = wait_limit_ns();
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
@@ -1071,7 +1092,7 @@ marble_status_t run_attn_cached(int64_t n, const marble_cache_t* c, const marble
   // workspace: a word for timeouts without a status, the joins, the pieces
   const int64_t piece = p.rows * (int64_t)(c->d + 2) * 4;
   const int64_t most = (MARBLE_ATTN_CACHED_WORKSPACE_BYTES - 65536) / (2 * piece);
-  const int grid = (int)std::min<int64_t>(std::min<int64_t>(2 * sms, most), 4000);
+  const int grid = (int)std::min<int64_t>(std::min<int64_t>(2 * sms, most), 2000);
   char* ws = static_cast<char*>(a->workspace);
   p.err = seqs->status ? reinterpret_cast<unsigned*>(seqs->status) : reinterpret_cast<unsigned*>(ws);
   p.joins = reinterpret_cast<int4*>(ws + 256);
