@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kRun = 16;  // rows of a CTA's tile, at most
 
 struct CachePart {
   char* rows;              // bf16 [n, hkv, d], null: not in the call
@@ -32,8 +33,8 @@ struct CacheParams {
   CachePart part[2];       // k, v
   SeqsParams seqs;
   const int32_t* perm;     // plan index -> original index, or null
-  int hkv, groups;         // heads, and warp iterations over them
-  int run, split;          // rows of a warp's run, warps a run
+  int hkv;
+  int run;                 // rows of a tile
 };
 
 // where the token of row i is: its page (-1: none, -2: the row belongs to no sequence) and slot
@@ -109,21 +110,35 @@ __device__ __forceinline__ uint4 quantise(const uint32_t (&w)[8], float* scale) 
     // In units of 2^e, in which top is `at`, in [1, 2) (less for a top below 2^-119), all of this
     // is exact but the quotient's estimate: y = x * 127 (15 bits), the whole number q next to the
     // estimate, and y - q at (a whole number of the smaller one's last places, below 2^17 of
-    // them).  The estimate is off by less than 127 * 2^-22, so q is right or, next to a tie, one
-    // off: the remainder tells.
+    // them).  The estimate is off by less than 127 * 2^-22 < 2^-15, so q is right unless what is
+    // left is that close to a half; then the exact remainder tells.
     const int e = max((int)(top >> 7) - 127, -119);
     const float one = e < 127 ? __uint_as_float((uint32_t)(127 - e) << 23) : 0x1p-127f;
     const float at = __uint_as_float(top << 16) * one, r = top ? __frcp_rn(at) : 0.f;
     const float by = 127.f * one;
+    constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer
+    float m[16], far = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float y = (i & 1 ? hi_f(w[i >> 1]) : lo_f(w[i >> 1])) * by;
-      constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer
-      float m = fmaf(y, r, kWhole);
-      const float rest = fmaf(kWhole - m, at, y), twice = 2.f * fabsf(rest);
-      if (twice > at || (twice == at && (__float_as_uint(m) & 1u))) m += rest > 0.f ? 1.f : -1.f;
-      c[i >> 2] |= (__float_as_uint(m) & 0xffu) << (8 * (i & 3));
+      m[i] = fmaf(y, r, kWhole);
+      far = fmaxf(far, fabsf(fmaf(y, r, kWhole - m[i])));
     }
+    if (far > 0.5f - 0x1p-14f) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float y = (i & 1 ? hi_f(w[i >> 1]) : lo_f(w[i >> 1])) * by;
+        const float rest = fmaf(kWhole - m[i], at, y), twice = 2.f * fabsf(rest);
+        if (twice > at || (twice == at && (__float_as_uint(m[i]) & 1u)))
+          m[i] += rest > 0.f ? 1.f : -1.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c[i] = __byte_perm(__byte_perm(__float_as_uint(m[4 * i]), __float_as_uint(m[4 * i + 1]), 0x0040),
+                         __byte_perm(__float_as_uint(m[4 * i + 2]), __float_as_uint(m[4 * i + 3]),
+                                     0x0040),
+                         0x5410);
   }
   return make_uint4(c[0], c[1], c[2], c[3]);
 }
@@ -149,84 +164,84 @@ __device__ __forceinline__ void restore(const uint4& codes, float scale, uint32_
 
 template <int D, int kType, bool kWrite>
 __global__ void __launch_bounds__(kThreads, 4) k_cache(const __grid_constant__ CacheParams p) {
-  constexpr int kTpr = D / 16, kHpi = 32 / kTpr, kEs = kType == MARBLE_CACHE_BF16 ? 2 : 1;
-  const int lane = threadIdx.x & 31, j = lane % kTpr, sub = lane / kTpr;
+  constexpr int kTpr = D / 16, kRows = 32 / kTpr, kEs = kType == MARBLE_CACHE_BF16 ? 2 : 1;
+  // passes of kRows rows whose loads are under way together (of 1, 2 and 4, by time: more loads do
+  // not help, where the accesses of a CTA lie close together does)
+  constexpr int kPasses = kWrite ? (kEs == 2 ? 2 : 4) : (kEs == 2 ? 1 : 2);
+  __shared__ Place places[2][kRun];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % kTpr, sub = lane / kTpr;
   const SeqsParams& s = p.seqs;
-  const long long runs = (s.n + p.run - 1) / p.run, items = runs * p.split;
-  const long long warps = (long long)gridDim.x * kWarps;
-  for (long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); w < items; w += warps) {
-    const long long i0 = w / p.split * p.run;
-    const int g0 = (int)(w % p.split), rows = (int)min((long long)p.run, s.n - i0);
-    Place mine = {-2, 0};
-    if (lane < rows) mine = place_of(s, p.perm ? p.perm[i0 + lane] : i0 + lane);
-    for (int r = 0; r < rows; ++r) {
-      const int page = __shfl_sync(0xffffffffu, mine.page, r);
-      const int slot = __shfl_sync(0xffffffffu, mine.slot, r);
-      if (page == -2 || (kWrite && page < 0)) continue;
-      for (int g = g0; g < p.groups; g += p.split) {
-        const int h = g * kHpi + sub;
-        const bool live = h < p.hkv;
-        uint4 a[2][2];
-        float scale[2];
-        // all loads first
+  const int tiles = (int)((s.n + p.run - 1) / p.run);
+  const int steps = (p.run + kRows * kPasses - 1) / (kRows * kPasses);  // of a head's rows
+  auto look = [&](int tile, int buf) {
+    const long long i = (long long)tile * p.run + lane;
+    if (tile < tiles && lane < p.run)
+      places[buf][lane] = i < s.n ? place_of(s, p.perm ? p.perm[i] : i) : Place{-2, 0};
+  };
+  if (warp == 0) look(blockIdx.x, 0);
+  int buf = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    __syncthreads();
+    if (warp == 0) look(tile + gridDim.x, buf ^ 1);
+    const long long i0 = (long long)tile * p.run;
+    for (int unit = warp; unit < steps * 2 * p.hkv; unit += kWarps) {
+      const int step = unit % steps, x = unit / steps & 1, h = unit / steps >> 1;
+      const CachePart& c = p.part[x];
+      if (!c.rows) continue;
+      const int r0 = step * kRows * kPasses + sub;
+      char* const row = c.rows + (i0 + r0) * c.row_bytes + ((long long)h * D + 16 * j) * 2;
+      uint4 a[kPasses][kEs == 2 || kWrite ? 2 : 1];
+      float scale[kPasses];
+      Place at[kPasses];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const CachePart& c = p.part[x];
-          a[x][0] = a[x][1] = make_uint4(0, 0, 0, 0);
-          scale[x] = 0.f;
-          if (!c.rows || !live) continue;
-          const long long at = (long long)h * s.page + slot;
-          if constexpr (kWrite) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                c.rows + (i0 + r) * c.row_bytes + ((long long)h * D + 16 * j) * 2);
-            a[x][0] = __ldcs(src);
-            a[x][1] = __ldcs(src + 1);
-          } else if (page >= 0) {
-            const uint4* src = reinterpret_cast<const uint4*>(c.pages + page * c.page_bytes +
-                                                              (at * D + 16 * j) * kEs);
-            a[x][0] = __ldcs(src);
-            if constexpr (kEs == 2)
-              a[x][1] = __ldcs(src + 1);
-            else
-              scale[x] = c.scale[page * c.scale_stride + at];
-          }
+      for (int u = 0; u < kPasses; ++u) {
+        const int r = r0 + u * kRows;
+        at[u] = r < p.run ? places[buf][r] : Place{-2, 0};
+        const bool there = at[u].page >= 0;
+        if constexpr (kWrite) {
+          const uint4* src = reinterpret_cast<const uint4*>(row + (long long)u * kRows * c.row_bytes);
+          a[u][0] = there ? __ldg(src) : make_uint4(0, 0, 0, 0);
+          a[u][1] = there ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+        } else {
+          const long long slot = (long long)h * s.page + at[u].slot;
+          const uint4* src = reinterpret_cast<const uint4*>(c.pages + at[u].page * c.page_bytes +
+                                                            (slot * D + 16 * j) * kEs);
+          a[u][0] = there ? __ldg(src) : make_uint4(0, 0, 0, 0);
+          if constexpr (kEs == 2) a[u][1] = there ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+          if constexpr (kEs == 1) scale[u] = there ? c.scale[at[u].page * c.scale_stride + slot] : 0.f;
         }
+      }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const CachePart& c = p.part[x];
-          if (!c.rows) continue;
-          const long long at = (long long)h * s.page + slot;
-          if constexpr (kWrite) {
-            uint4* dst = reinterpret_cast<uint4*>(c.pages + page * c.page_bytes +
-                                                  (at * D + 16 * j) * kEs);
-            if constexpr (kEs == 2) {
-              if (live) {
-                dst[0] = a[x][0];
-                dst[1] = a[x][1];
-              }
-            } else {
-              const uint32_t v[8] = {a[x][0].x, a[x][0].y, a[x][0].z, a[x][0].w,
-                                     a[x][1].x, a[x][1].y, a[x][1].z, a[x][1].w};
-              float sc;
-              const uint4 codes = quantise<D, kType>(v, &sc);
-              if (live) {
-                *dst = codes;
-                if (j == 0) c.scale[page * c.scale_stride + at] = sc;
-              }
+      for (int u = 0; u < kPasses; ++u) {
+        if constexpr (kWrite) {
+          const long long slot = (long long)h * s.page + at[u].slot;
+          uint4* dst = reinterpret_cast<uint4*>(c.pages + at[u].page * c.page_bytes +
+                                                (slot * D + 16 * j) * kEs);
+          if constexpr (kEs == 2) {
+            if (at[u].page >= 0) {
+              dst[0] = a[u][0];
+              dst[1] = a[u][1];
             }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(c.rows + (i0 + r) * c.row_bytes +
-                                                  ((long long)h * D + 16 * j) * 2);
-            if constexpr (kEs == 1) {
-              uint32_t v[8];
-              restore<kType>(a[x][0], scale[x], v);
-              a[x][0] = make_uint4(v[0], v[1], v[2], v[3]);
-              a[x][1] = make_uint4(v[4], v[5], v[6], v[7]);
+            const uint32_t v[8] = {a[u][0].x, a[u][0].y, a[u][0].z, a[u][0].w,
+                                   a[u][1].x, a[u][1].y, a[u][1].z, a[u][1].w};
+            float sc;
+            const uint4 codes = quantise<D, kType>(v, &sc);
+            if (at[u].page >= 0) {
+              *dst = codes;
+              if (j == 0) c.scale[at[u].page * c.scale_stride + slot] = sc;
             }
-            if (live) {
-              dst[0] = a[x][0];
-              dst[1] = a[x][1];
-            }
+          }
+        } else if (at[u].page != -2) {
+          uint4* dst = reinterpret_cast<uint4*>(row + (long long)u * kRows * c.row_bytes);
+          if constexpr (kEs == 1) {
+            uint32_t o[8];
+            restore<kType>(a[u][0], scale[u], o);
+            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+          } else {
+            dst[0] = a[u][0];
+            dst[1] = a[u][1];
           }
         }
       }
@@ -248,18 +263,16 @@ cudaError_t launch_cache(bool write, const marble_plan_t* plan, int64_t n, const
   p.seqs = seqs_params(*seqs, *c, n);
   p.perm = plan ? plan->perm : nullptr;
   p.hkv = c->hkv;
-  p.groups = (c->hkv * (c->d / 16) + 31) / 32;
-  // Warps: 32 on every SM where there are rows enough, then up to 32 rows a warp; few rows get a
-  // warp for every group of heads.
+  // Tiles of up to 32 rows, fewer where that leaves SMs without work; as many CTAs as run at once,
+  // or fewer that take the same number of rounds.
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t want = (int64_t)sms * 32;
-  p.run = (int)std::max<int64_t>(1, std::min<int64_t>(32, n / want));
-  const int64_t runs = (n + p.run - 1) / p.run;
-  p.split = (int)std::max<int64_t>(1, std::min<int64_t>(p.groups, (want + runs - 1) / runs));
-  const int64_t ctas = (runs * p.split + kWarps - 1) / kWarps;
-  const int grid = (int)std::min<int64_t>(ctas, (int64_t)sms * 4);
+  p.run = kRun;
+  while (p.run > 512 / c->d && n < (int64_t)p.run * sms * 4) p.run /= 2;
+  const int64_t tiles = (n + p.run - 1) / p.run, most = (int64_t)sms * 4;
+  const int64_t rounds = (tiles + most - 1) / most;
+  const int grid = (int)((tiles + rounds - 1) / rounds);
   auto pick = [&](auto dd) {
     constexpr int D = decltype(dd)::value;
     if (c->type == MARBLE_CACHE_BF16)
