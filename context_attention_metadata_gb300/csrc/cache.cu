@@ -107,38 +107,29 @@ __device__ __forceinline__ uint4 quantise(const uint32_t (&w)[8], float* scale) 
     }
   } else {
     *scale = __fdiv_rn(__uint_as_float(top << 16), 127.f);
-    // In units of 2^e, in which top is `at`, in [1, 2) (less for a top below 2^-119), all of this
-    // is exact but the quotient's estimate: y = x * 127 (15 bits), the whole number q next to the
-    // estimate, and y - q at (a whole number of the smaller one's last places, below 2^17 of
-    // them).  The estimate is off by less than 127 * 2^-22 < 2^-15, so q is right unless what is
-    // left is that close to a half; then the exact remainder tells.
+    // In units of 2^e, in which top is `at`, in [1, 2) (less for a top below 2^-119), y = x * 127
+    // has 15 bits, at 8.  The quotient is estimated and put right by one Newton step: what the
+    // estimate leaves, rest, is exact (two of the estimate's last places times at), so the step is
+    // off by 2^-22 of a last place before it is rounded.  A quotient halfway between whole
+    // numbers is therefore met exactly, and the others lie 2^-17 or more away from halfway, where a
+    // last place is 2^-17 at most: the sum below rounds every one as the exact quotient.
     const int e = max((int)(top >> 7) - 127, -119);
     const float one = e < 127 ? __uint_as_float((uint32_t)(127 - e) << 23) : 0x1p-127f;
     const float at = __uint_as_float(top << 16) * one, r = top ? __frcp_rn(at) : 0.f;
     const float by = 127.f * one;
     constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it leaves the nearest integer
-    float m[16], far = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float y = (i & 1 ? hi_f(w[i >> 1]) : lo_f(w[i >> 1])) * by;
-      m[i] = fmaf(y, r, kWhole);
-      far = fmaxf(far, fabsf(fmaf(y, r, kWhole - m[i])));
-    }
-    if (far > 0.5f - 0x1p-14f) {
+    for (int i = 0; i < 16; i += 4) {
+      uint32_t m[4];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float y = (i & 1 ? hi_f(w[i >> 1]) : lo_f(w[i >> 1])) * by;
-        const float rest = fmaf(kWhole - m[i], at, y), twice = 2.f * fabsf(rest);
-        if (twice > at || (twice == at && (__float_as_uint(m[i]) & 1u)))
-          m[i] += rest > 0.f ? 1.f : -1.f;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t two = w[(i + k) >> 1];
+        const float y = (k & 1 ? hi_f(two) : lo_f(two)) * by, q = y * r;
+        const float rest = fmaf(-q, at, y);
+        m[k] = __float_as_uint(fmaf(rest, r, q) + kWhole);
       }
+      c[i >> 2] = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c[i] = __byte_perm(__byte_perm(__float_as_uint(m[4 * i]), __float_as_uint(m[4 * i + 1]), 0x0040),
-                         __byte_perm(__float_as_uint(m[4 * i + 2]), __float_as_uint(m[4 * i + 3]),
-                                     0x0040),
-                         0x5410);
   }
   return make_uint4(c[0], c[1], c[2], c[3]);
 }
