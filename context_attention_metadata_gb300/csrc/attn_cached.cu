@@ -616,24 +616,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       for (int i = 0; i < D / 16; ++i) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.f;
     }
 
-    for (int i = (kg - n) & (kgs - 1); i < pc.chunks; i += kgs) {
-      const int at = n + i, st = at % kStages, chunk_base = pc.key0 + i * kKeys;
-      if (!wait_all(&full[st], (at / kStages) & 1, wait)) return;
-      const bool cut_v = chunk_base < pc.lo || chunk_base + kKeys > pc.hi;  // keys that no row may see
-      const bool masked = chunk_base < all_lo || chunk_base + kKeys > all_hi;
+    // One chunk: S^T, the softmax's step, O^T += V^T P^T, with kT of the warp's tiles of rows.
+    auto chunk_step = [&](auto tiles_, int st, int base, bool masked) {
+      constexpr int kT = decltype(tiles_)::value;
+      const uint32_t kt = smem_u32(ring) + st * 2 * C::kTile, vt = kt + C::kTile;
+      const float* ks = scales + 2 * st * kKeys;
+      const float* vs = ks + kKeys;
       float inv = 0.f;
       if constexpr (kQuant) {
-        const float* vs_all = scales + (2 * st + 1) * kKeys;
         // fp16 weights p * v's scale in units of vref, the power of two at or above the largest
         // scale so far, raised by kPUp: at most 2^(8 + 6 + 1), and nothing is lost above 2^-20
         // of the largest.
         uint32_t big = 0;
 #pragma unroll
-        for (int x = 0; x < kKeys / 32; ++x) {
-          const int key = chunk_base + 32 * x + lane;
-          if (!cut_v || (key >= pc.lo && key < pc.hi))
-            big = max(big, __float_as_uint(vs_all[32 * x + lane]) & 0x7fffffffu);
-        }
+        for (int x = 0; x < kKeys / 32; ++x)
+          big = max(big, __float_as_uint(vs[32 * x + lane]) & 0x7fffffffu);
         big = __reduce_max_sync(0xffffffffu, big);
         if (big > __float_as_uint(vref)) {
           const float to = __uint_as_float(min((big + 0x7fffffu) & 0xff800000u, 0x7f000000u));
@@ -642,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 #pragma unroll
             for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-              for (int t = 0; t < kNt; ++t)
+              for (int t = 0; t < kT; ++t)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) o[d][t][y] *= by;
             vref = to;
@@ -652,175 +649,182 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       }
 #pragma unroll 1
       for (int sub = 0; sub < kKeys; sub += C::kSub) {
-      const int base = chunk_base + sub;
-      const uint32_t kt = smem_u32(ring) + st * 2 * C::kTile + sub * C::kPitch, vt = kt + C::kTile;
-      const float* ks = scales + 2 * st * kKeys + sub;
-      const float* vs = ks + kKeys;
+        // scores
+        float s[kMt][kT][4];
+#pragma unroll
+        for (int j = 0; j < kMt; ++j)
+#pragma unroll
+          for (int t = 0; t < kT; ++t) s[j][t][0] = s[j][t][1] = s[j][t][2] = s[j][t][3] = 0.f;
+#pragma unroll
+        for (int x = 0; x < C::kRow / 32; ++x) {  // 32 bytes of the keys at a time
+          const uint32_t row = kt + (x >> 2) * kKeys * C::kPitch + sub * C::kPitch + k_row +
+                               (k_x ^ ((x & 3) << 5));
+#pragma unroll
+          for (int j = 0; j < kMt; ++j) {
+            uint32_t f[4];
+            ldsm4(row + j * 16 * C::kPitch, f);
+            if constexpr (!kQuant) {
+#pragma unroll
+              for (int t = 0; t < kT; ++t) mma<false>(s[j][t], f, q[t][x]);
+            } else {
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                uint32_t a[4];
+                along<kType>(f[2 * y], &a[0], &a[2]);
+                along<kType>(f[2 * y + 1], &a[1], &a[3]);
+#pragma unroll
+                for (int t = 0; t < kT; ++t) mma<true>(s[j][t], a, q[t][2 * x + y]);
+              }
+            }
+          }
+        }
 
-      // scores
-      float s[kMt][kNt][4];
+        // scale, cap, bias, mask: s becomes base-2 scores
 #pragma unroll
-      for (int j = 0; j < kMt; ++j)
+        for (int j = 0; j < kMt; ++j)
 #pragma unroll
-        for (int t = 0; t < kNt; ++t) s[j][t][0] = s[j][t][1] = s[j][t][2] = s[j][t][3] = 0.f;
+          for (int y = 0; y < 2; ++y) {
+            const int key = sub + 16 * j + 8 * y + qn;
+            F2 k2 = f2(1.f);
+            if constexpr (kQuant) k2 = f2(ks[key]);
 #pragma unroll
-      for (int x = 0; x < C::kRow / 32; ++x) {  // 32 bytes of the keys at a time
-        const uint32_t row = kt + (x >> 2) * kKeys * C::kPitch + k_row + (k_x ^ ((x & 3) << 5));
+            for (int t = 0; t < kT; ++t) {
+              F2 v = mul2(f2(s[j][t][2 * y], s[j][t][2 * y + 1]), kQuant ? mul2(mul[t], k2) : mul[t]);
+              if constexpr (kScored) {
+                float v0, v1;
+                if (p.cap2 > 0.f) {
+                  split(v, &v0, &v1);
+                  v = f2(p.cap2 * tanhf(v0), p.cap2 * tanhf(v1));
+                }
+                v = fma2(slope2[t], f2((float)abs(pos[t][0] - base - key),
+                                       (float)abs(pos[t][1] - base - key)), v);
+              }
+              split(v, &s[j][t][2 * y], &s[j][t][2 * y + 1]);
+            }
+          }
+        if (masked) {
+#pragma unroll
+          for (int t = 0; t < kT; ++t) {
+            int lo[2], hi[2];
+            sees(p, pc.s, pos[t][0], &lo[0], &hi[0]);
+            sees(p, pc.s, pos[t][1], &lo[1], &hi[1]);
+#pragma unroll
+            for (int j = 0; j < kMt; ++j)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int key = base + sub + 16 * j + 8 * (y >> 1) + qn;
+                if ((unsigned)(key - lo[y & 1]) >= (unsigned)(hi[y & 1] - lo[y & 1]))
+                  s[j][t][y] = -INFINITY;
+              }
+          }
+        }
+        bool grow = false;
+        float top[kT][2];
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          top[t][0] = top[t][1] = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < kMt; ++j)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) top[t][y & 1] = fmaxf(top[t][y & 1], s[j][t][y]);
+          grow |= top[t][0] > m[t][0] + kLazy || top[t][1] > m[t][1] + kLazy;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int t = 0; t < kT; ++t) {
+            float by[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float to = fmaxf(m[t][x], row_max(top[t][x]));
+              by[x] = to == m[t][x] ? 1.f : fast_exp2(m[t][x] - to);
+              m[t][x] = to;
+            }
+            l[t] = mul2(l[t], f2(by[0], by[1]));
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) o[d][t][y] *= by[y & 1];
+          }
+        }
+
+        // weights, as B operands: [row n][keys 2 t, + 1]
+        uint32_t ph[kMt][kT][2], pl[kQuant ? 1 : kMt][kT][2];
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          const F2 off = f2(m[t][0] == -INFINITY ? 0.f : -m[t][0], m[t][1] == -INFINITY ? 0.f : -m[t][1]);
+#pragma unroll
+          for (int j = 0; j < kMt; ++j)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              float a, b;
+              split(add2(f2(s[j][t][2 * y], s[j][t][2 * y + 1]), off), &a, &b);
+              a = fast_exp2(a);
+              b = fast_exp2(b);
+              l[t] = add2(l[t], f2(a, b));
+              if constexpr (kQuant) {
+                const float f = vs[sub + 16 * j + 8 * y + qn] * inv;
+                ph[j][t][y] = turned(pack_half(a * f, b * f));
+              } else {
+                const uint32_t h = pack_bf16(a, b);
+                ph[j][t][y] = turned(h);
+                pl[j][t][y] = turned(pack_bf16(a - __uint_as_float(h << 16),
+                                               b - __uint_as_float(h & 0xffff0000u)));
+              }
+            }
+        }
+
+        // O^T += V^T P^T, 16 keys at a time
 #pragma unroll
         for (int j = 0; j < kMt; ++j) {
-          uint32_t f[4];
-          ldsm4(row + j * 16 * C::kPitch, f);
-          if constexpr (!kQuant) {
 #pragma unroll
-            for (int t = 0; t < kNt; ++t) mma<false>(s[j][t], f, q[t][x]);
-          } else {
+          for (int x = 0; x < C::kRow / 32; ++x) {  // 32 bytes of the values at a time
+            uint32_t f[4];
+            ldsm4_t(vt + ((x >> 2) * kKeys + sub + 16 * j) * C::kPitch + v_row + (v_x ^ ((x & 3) << 5)),
+                    f);
+            if constexpr (!kQuant) {
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              uint32_t a[4];
-              along<kType>(f[2 * y], &a[0], &a[2]);
-              along<kType>(f[2 * y + 1], &a[1], &a[3]);
+              for (int t = 0; t < kT; ++t) mma<false>(o[x][t], f, ph[j][t]);
 #pragma unroll
-              for (int t = 0; t < kNt; ++t) mma<true>(s[j][t], a, q[t][2 * x + y]);
-            }
-          }
-        }
-      }
-
-      // scale, cap, bias, mask; s becomes base-2 scores
-      F2 top[kNt];
-#pragma unroll
-      for (int t = 0; t < kNt; ++t) top[t] = f2(-INFINITY);
-      bool grow = false;
-#pragma unroll
-      for (int t = 0; t < kNt; ++t) {
-        float top0 = -INFINITY, top1 = -INFINITY;
-        int lo[2] = {0, 0}, hi[2] = {0, 0};
-        if (masked) {
-          sees(p, pc.s, pos[t][0], &lo[0], &hi[0]);
-          sees(p, pc.s, pos[t][1], &lo[1], &hi[1]);
-        }
-#pragma unroll
-        for (int j = 0; j < kMt; ++j)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int at_key = 16 * j + 8 * y + qn;
-            F2 by = mul[t];
-            if constexpr (kQuant) by = mul2(by, f2(ks[at_key]));
-            F2 v = mul2(f2(s[j][t][2 * y], s[j][t][2 * y + 1]), by);
-            float v0, v1;
-            if constexpr (kScored) {
-              if (p.cap2 > 0.f) {
-                split(v, &v0, &v1);
-                v = f2(p.cap2 * tanhf(v0), p.cap2 * tanhf(v1));
-              }
-              const int key = base + at_key;
-              v = fma2(slope2[t], f2((float)abs(pos[t][0] - key), (float)abs(pos[t][1] - key)), v);
-            }
-            split(v, &v0, &v1);
-            if (masked) {
-              const int key = base + at_key;
-              if ((unsigned)(key - lo[0]) >= (unsigned)(hi[0] - lo[0])) v0 = -INFINITY;
-              if ((unsigned)(key - lo[1]) >= (unsigned)(hi[1] - lo[1])) v1 = -INFINITY;
-            }
-            s[j][t][2 * y] = v0;
-            s[j][t][2 * y + 1] = v1;
-            top0 = fmaxf(top0, v0);
-            top1 = fmaxf(top1, v1);
-          }
-        top[t] = f2(top0, top1);
-        grow |= top0 > m[t][0] + kLazy || top1 > m[t][1] + kLazy;
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int t = 0; t < kNt; ++t) {
-          float tops[2], by[2];
-          split(top[t], &tops[0], &tops[1]);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float to = fmaxf(m[t][x], row_max(tops[x]));
-            by[x] = to == m[t][x] ? 1.f : fast_exp2(m[t][x] - to);
-            m[t][x] = to;
-          }
-          l[t] = mul2(l[t], f2(by[0], by[1]));
-#pragma unroll
-          for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) o[d][t][y] *= by[y & 1];
-        }
-      }
-      // weights, as B operands: [row n][keys 2 t, + 1]
-      uint32_t ph[kMt][kNt][2], pl[kQuant ? 1 : kMt][kNt][2];
-#pragma unroll
-      for (int t = 0; t < kNt; ++t) {
-        const F2 off = f2(m[t][0] == -INFINITY ? 0.f : -m[t][0], m[t][1] == -INFINITY ? 0.f : -m[t][1]);
-#pragma unroll
-        for (int j = 0; j < kMt; ++j)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            float a, b;
-            split(add2(f2(s[j][t][2 * y], s[j][t][2 * y + 1]), off), &a, &b);
-            a = fast_exp2(a);
-            b = fast_exp2(b);
-            l[t] = add2(l[t], f2(a, b));
-            if constexpr (kQuant) {
-              const int key = 16 * j + 8 * y + qn;
-              float f = vs[key] * inv;
-              if (cut_v && (base + key < pc.lo || base + key >= pc.hi)) f = 0.f;
-              ph[j][t][y] = turned(pack_half(a * f, b * f));
+              for (int t = 0; t < kT; ++t) mma<false>(o[x][t], f, pl[j][t]);
             } else {
-              const uint32_t h = pack_bf16(a, b);
-              ph[j][t][y] = turned(h);
-              pl[j][t][y] = turned(pack_bf16(a - __uint_as_float(h << 16),
-                                             b - __uint_as_float(h & 0xffff0000u)));
-            }
-          }
-      }
-
-      // O^T += V^T P^T, 16 keys at a time
 #pragma unroll
-      for (int j = 0; j < kMt; ++j) {
-        uint32_t live[2] = {~0u, ~0u};
-        if (cut_v) {
+              for (int y = 0; y < 2; ++y) {
+                uint32_t a[4];
+                across<kType>(f[2 * y], &a[0], &a[1]);
+                across<kType>(f[2 * y + 1], &a[2], &a[3]);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int key = base + 16 * j + 8 * x + 2 * qt;
-            live[x] = (key >= pc.lo && key < pc.hi ? 0xffffu : 0u) |
-                      (key + 1 >= pc.lo && key + 1 < pc.hi ? 0xffff0000u : 0u);
-          }
-        }
-#pragma unroll
-        for (int x = 0; x < C::kRow / 32; ++x) {  // 32 bytes of the values at a time
-          uint32_t f[4];
-          ldsm4_t(vt + ((x >> 2) * kKeys + 16 * j) * C::kPitch + v_row + (v_x ^ ((x & 3) << 5)), f);
-          if constexpr (!kQuant) {
-            if (cut_v) {
-              f[0] &= live[0];
-              f[1] &= live[0];
-              f[2] &= live[1];
-              f[3] &= live[1];
-            }
-#pragma unroll
-            for (int t = 0; t < kNt; ++t) mma<false>(o[x][t], f, ph[j][t]);
-#pragma unroll
-            for (int t = 0; t < kNt; ++t) mma<false>(o[x][t], f, pl[j][t]);
-          } else {
-            if (cut_v) {
-              f[0] &= live[0];
-              f[1] &= live[1];
-              f[2] &= live[0];
-              f[3] &= live[1];
-            }
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              uint32_t a[4];
-              across<kType>(f[2 * y], &a[0], &a[1]);
-              across<kType>(f[2 * y + 1], &a[2], &a[3]);
-#pragma unroll
-              for (int t = 0; t < kNt; ++t) mma<true>(o[2 * x + y][t], a, ph[j][t]);
+                for (int t = 0; t < kT; ++t) mma<true>(o[2 * x + y][t], a, ph[j][t]);
+              }
             }
           }
         }
       }
+    };
+    // tiles of rows that hold any
+    const int row_tiles = (int)min(((long long)pc.s.count * p.group - row0 + 7) >> 3, (long long)kNt);
+    for (int i = (kg - n) & (kgs - 1); i < pc.chunks; i += kgs) {
+      const int at = n + i, st = at % kStages, base = pc.key0 + i * kKeys;
+      if (!wait_all(&full[st], (at / kStages) & 1, wait)) return;
+      const bool masked = base < all_lo || base + kKeys > all_hi;
+      if (base < pc.lo || base + kKeys > pc.hi) {
+        // Keys outside the item: their weights are 0, and what the ring holds for their values
+        // and scales becomes 0 too (another warp of the chunk writes the same).
+        uint4* v = reinterpret_cast<uint4*>(ring + (2 * st + 1) * C::kTile);
+        for (int x = lane; x < C::kTile / 16; x += 32) {
+          const int key = base + x / (C::kPitch / 16) % kKeys;
+          if (key < pc.lo || key >= pc.hi) v[x] = make_uint4(0, 0, 0, 0);
+        }
+        if constexpr (kQuant)
+          for (int x = lane; x < kKeys; x += 32)
+            if (base + x < pc.lo || base + x >= pc.hi) scales[(2 * st + 1) * kKeys + x] = 0.f;
+        fence_proxy_async_smem();  // before the copies that follow these writes
+        __syncwarp();
+      }
+      if (row_tiles > 0) {
+        if (kNt == 1 || row_tiles > 1)
+          chunk_step(std::integral_constant<int, kNt>{}, st, base, masked);
+        else
+          chunk_step(std::integral_constant<int, 1>{}, st, base, masked);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
