@@ -36,7 +36,11 @@ namespace marble {
 namespace {
 
 constexpr int kWorkers = 4;                     // computing warps
-constexpr int kThreads = 32 * (kWorkers + 1);
+// One more warp fetches; it has three idle ones beside it, so that registers can be moved between
+// two groups of four warps: of the 128 a thread that two CTAs on an SM leave, the computing warps
+// get 200 (five warps alone could have no more than 168, which 16 rows of 128 channels spill).
+constexpr int kThreads = 64 * kWorkers;
+constexpr int kFetchRegs = 56, kWorkRegs = 200;
 constexpr int kUnitOver = 3;                    // an item's constant cost, in chunks (measured)
 constexpr float kLazy = 8.f;                    // O is rescaled when m grows by more (base 2)
 constexpr float kPUp = 64.f;                    // fp16 weights are raised by this (see below)
@@ -325,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   __shared__ Piece pieces[C::kPieces];
   __shared__ int2 looked[32];
   __shared__ int abort_flag, first_b;
-  __shared__ long long first_at, range[2], sums[kWorkers + 1];
+  __shared__ long long first_at, range[2], sums[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // let the joining kernel's CTAs come up beside this one's
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   __syncthreads();
   long long before = upto - mine, total = 0;
 #pragma unroll
-  for (int i = 0; i <= kWorkers; ++i) {
+  for (int i = 0; i < kThreads / 32; ++i) {
     before += i < warp ? sums[i] : 0;
     total += sums[i];
   }
@@ -394,7 +398,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   __syncthreads();
   const WaitCtx wait = {p.limit_ns, p.err, &abort_flag};
 
-  if (warp == kWorkers) {
+  if (warp >= kWorkers) {
+    regs_shrink<kFetchRegs>();
+    if (warp > kWorkers) return;
     // ---- fetch.  The boxes of the next 32 / boxes chunks are looked up at once, a lane each;
     // one thread then issues all copies (its operands are uniform; lanes side by side would be
     // taken one by one, at twice the cost).
@@ -521,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   // ---- compute.  Products are taken with the keys as rows: S^T = K Q^T (16 keys x 8 rows), and
   // O^T = V^T P^T (16 channels x 8 rows), so that a group of up to 8 rows wastes nothing.  Lane 4 n
   // + t holds keys n and n + 8 of 16, rows 2 t and 2 t + 1 of 8.
+  regs_grow<kWorkRegs>();
   const int tile = warp % p.row_warps, kg = warp / p.row_warps;
   const int qn = lane >> 2, qt = lane & 3, l7 = lane & 7, lm = lane >> 3;
   // where a lane's row of an ldmatrix begins: of keys (lm & 1 or lm >> 1: the second eight), and
@@ -542,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     uint32_t q[kNt][D / 16][2];
     F2 mul[kNt];                     // what the rows' products have to be multiplied by
     int pos[kNt][2];                 // -1: no row
-    F2 slope2[kNt];
+    float slope[kNt][2];             // - slope * log2 e
 #pragma unroll
     for (int t = 0; t < kNt; ++t) {
       const int r = 8 * (kNt * tile + t) + qn;
@@ -580,18 +587,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         }
       }
       // from the lanes that read a row to those that hold its products
-      float m2[2], sl[2] = {0.f, 0.f};
+      float m2[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         m2[x] = __shfl_sync(0xffffffffu, up, 4 * (2 * qt + x)) *
                 (kScored && p.cap2 > 0.f ? p.to_cap : p.scale2);
         const RowAt ra = row_at(p, pc.s, pc.head, row0 + 8 * t + 2 * qt + x);
         pos[t][x] = ra.live ? ra.pos : -1;
+        slope[t][x] = 0.f;
         if constexpr (kScored)
-          if (p.slopes && ra.live) sl[x] = p.slopes[ra.head] * -1.4426950408889634f;
+          if (p.slopes && ra.live) slope[t][x] = p.slopes[ra.head] * -1.4426950408889634f;
       }
       mul[t] = f2(m2[0], m2[1]);
-      slope2[t] = f2(sl[0], sl[1]);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&piece_empty[ps]);
@@ -680,6 +687,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         }
 
         // scale, cap, bias, mask: s becomes base-2 scores
+        float far[kT][2];  // distances of this lane's first key
+        if constexpr (kScored) {
+#pragma unroll
+          for (int t = 0; t < kT; ++t) {
+            far[t][0] = (float)(pos[t][0] - base - sub - qn);
+            far[t][1] = (float)(pos[t][1] - base - sub - qn);
+          }
+        }
 #pragma unroll
         for (int j = 0; j < kMt; ++j)
 #pragma unroll
@@ -696,8 +711,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
                   split(v, &v0, &v1);
                   v = f2(p.cap2 * tanhf(v0), p.cap2 * tanhf(v1));
                 }
-                v = fma2(slope2[t], f2((float)abs(pos[t][0] - base - key),
-                                       (float)abs(pos[t][1] - base - key)), v);
+                split(v, &v0, &v1);
+                v = f2(fmaf(slope[t][0], fabsf(far[t][0] - (float)(16 * j + 8 * y)), v0),
+                       fmaf(slope[t][1], fabsf(far[t][1] - (float)(16 * j + 8 * y)), v1));
               }
               split(v, &s[j][t][2 * y], &s[j][t][2 * y + 1]);
             }
