@@ -406,12 +406,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     // taken one by one, at twice the cost).
     const int boxes = kKeys / p.box, group = 32 / boxes;
     const bool leader = elect_one();
-    // page and slot of box j of the chunk i behind chunk c of a piece; no slot: not needed
+    // table entry and slot of box j of the chunk i behind chunk c of a piece; no slot: not needed
     auto look = [&](int c, const Walk<kKeys>& walk, int i, int j) {
       int2 at = make_int2(-1, -1);
       const int key = (walk.w.chunk0 + c + i) * kKeys + j * p.box;
       if (c + i < walk.c1 && key < walk.w.hi && key + p.box > walk.w.lo) {
-        at.x = page_at(p.seqs, walk.b, key);
+        at.x = table_at(p.seqs, walk.b, key);
         at.y = key % p.seqs.page;
       }
       return at;
@@ -468,7 +468,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 
       for (int c = walk.c0; ok && c < walk.c1; c += group) {
         if (c > walk.c0) at = look(c, walk, lane / boxes, lane % boxes);
-        if (at.y >= 0 && at.x < 0) seqs_bad(p.seqs);
+        if (at.y >= 0 && (unsigned)at.x >= (unsigned)p.seqs.n_pages) {
+          seqs_bad(p.seqs);
+          at.x = -1;
+        }
         looked[lane] = at;
         const unsigned needed = __ballot_sync(0xffffffffu, at.y >= 0);
         __syncwarp();
@@ -954,8 +957,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   }
 }
 
-// Joins the pieces of the item that CTA blockIdx.x of the first kernel began, a row a block (and
-// every gridDim.y-th row after it), a quarter of the pieces a warp.
+// Joins the pieces of the item that CTA blockIdx.x of the first kernel began.  A few pieces: a row a
+// warp; more: a row a block, a quarter of the pieces a warp.
 constexpr int kJoinWarps = 4;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ AttnParams p) {
@@ -964,9 +967,45 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
   const int4 join = p.joins[2 * blockIdx.x];
   const int row0 = p.joins[2 * blockIdx.x + 1].x;
   if (join.x == 0) return;
-  __shared__ float so[kJoinWarps][D], sm[kJoinWarps], sl[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = p.rows;
   const Seq seq = {join.y, join.z, 0};
+  auto place = [&](int i) { return 2 * ((int)blockIdx.x + i) + (i == 0 ? 1 : 0); };
+  if (join.x <= 4) {
+    for (int r = blockIdx.y * kJoinWarps + warp; r < rows; r += gridDim.y * kJoinWarps) {
+      const RowAt at = row_at(p, seq, join.w, row0 + r);
+      if (!at.live) break;  // rows are live up to the last token's
+      float2 ml[4];
+      float v[4][kPer], m = -INFINITY, l = 0.f, o[kPer];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long row = (long long)place(min(i, join.x - 1)) * rows + r;
+        ml[i] = i < join.x ? p.part_ml[row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) v[i][x] = p.part_o[row * D + kPer * lane + x];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = fmaxf(m, ml[i].x);
+      const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) o[x] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= join.x) break;
+        const float by = fast_exp2(ml[i].x - ref);
+        l = fmaf(ml[i].y, by, l);
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) o[x] = fmaf(v[i][x], by, o[x]);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint32_t* to = reinterpret_cast<uint32_t*>(p.o + at.token * p.o_stride + (long long)at.head * D) +
+                     kPer / 2 * lane;
+#pragma unroll
+      for (int x = 0; x < kPer / 2; ++x) to[x] = pack_bf16(o[2 * x] * inv, o[2 * x + 1] * inv);
+      if (p.lse && lane == 0) p.lse[at.head * p.seqs.n + at.token] = lse_of(m, l);
+    }
+    return;
+  }
+  __shared__ float so[kJoinWarps][D], sm[kJoinWarps], sl[kJoinWarps];
   for (int r = blockIdx.y; r < rows; r += gridDim.y) {
     const RowAt at = row_at(p, seq, join.w, row0 + r);
     if (!at.live) break;  // rows are live up to the last token's
@@ -974,8 +1013,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
 #pragma unroll
     for (int x = 0; x < kPer; ++x) o[x] = 0.f;
     for (int i = warp; i < join.x; i += kJoinWarps) {
-      const int place = 2 * (blockIdx.x + i) + (i == 0 ? 1 : 0);
-      const long long row = (long long)place * rows + r;
+      const long long row = (long long)place(i) * rows + r;
       const float2 ml = p.part_ml[row];
       float v[kPer];
 #pragma unroll
@@ -1050,7 +1088,7 @@ marble_status_t launch(AttnParams& p, int grid, int join_rows, cudaStream_t s) {
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, join_rows);
+  cfg.gridDim = dim3(grid, join_rows <= 8 ? join_rows : (join_rows + kJoinWarps - 1) / kJoinWarps);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cfg.attrs = &early;

@@ -57,9 +57,12 @@ __device__ __forceinline__ Seq seq_at(const SeqsParams& p, int b) {
   return s;
 }
 
-// the page that holds position `pos` of sequence b, -1 if the table's entry is none
+// the table's entry for position `pos` of sequence b, and the page that it is (-1: none)
+__device__ __forceinline__ int table_at(const SeqsParams& p, int b, int pos) {
+  return __ldg(p.table + (int64_t)b * p.table_stride + pos / p.page);
+}
 __device__ __forceinline__ int page_at(const SeqsParams& p, int b, int pos) {
-  const int g = __ldg(p.table + (int64_t)b * p.table_stride + pos / p.page);
+  const int g = table_at(p, b, pos);
   return (unsigned)g < (unsigned)p.n_pages ? g : -1;
 }
 
