@@ -690,37 +690,64 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         }
 
         // scale, cap, bias, mask: s becomes base-2 scores
-        float far[kT][2];  // distances of this lane's first key
-        if constexpr (kScored) {
+        auto each = [&](auto f) {
+#pragma unroll
+          for (int j = 0; j < kMt; ++j)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int t = 0; t < kT; ++t)
+                split(f(f2(s[j][t][2 * y], s[j][t][2 * y + 1]), 16 * j + 8 * y, t), &s[j][t][2 * y],
+                      &s[j][t][2 * y + 1]);
+        };
+        auto scaled = [&](F2 v, int key, int t) {
+          return mul2(v, kQuant ? mul2(mul[t], f2(ks[sub + key + qn])) : mul[t]);
+        };
+        if constexpr (!kScored) {
+          each(scaled);
+        } else {
+          float far[kT][2];  // distances of this lane's first key
 #pragma unroll
           for (int t = 0; t < kT; ++t) {
             far[t][0] = (float)(pos[t][0] - base - sub - qn);
             far[t][1] = (float)(pos[t][1] - base - sub - qn);
           }
-        }
-#pragma unroll
-        for (int j = 0; j < kMt; ++j)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int key = sub + 16 * j + 8 * y + qn;
-            F2 k2 = f2(1.f);
-            if constexpr (kQuant) k2 = f2(ks[key]);
-#pragma unroll
-            for (int t = 0; t < kT; ++t) {
-              F2 v = mul2(f2(s[j][t][2 * y], s[j][t][2 * y + 1]), kQuant ? mul2(mul[t], k2) : mul[t]);
-              if constexpr (kScored) {
+          auto biased = [&](F2 v, int key, int t) {
+            float v0, v1;
+            split(v, &v0, &v1);
+            return f2(fmaf(slope[t][0], fabsf(far[t][0] - (float)key), v0),
+                      fmaf(slope[t][1], fabsf(far[t][1] - (float)key), v1));
+          };
+          if (p.cap2 > 0.f) {
+            each(scaled);
+            // tanh by its polynomial where all of the warp's scores are within its reach (score.cuh)
+            float top = 0.f;
+            each([&](F2 v, int, int) {
+              float v0, v1;
+              split(v, &v0, &v1);
+              top = fmaxf(top, fmaxf(fabsf(v0), fabsf(v1)));
+              return v;
+            });
+            if (__any_sync(0xffffffffu, top > 0.875f)) {
+              each([&](F2 v, int, int) {
                 float v0, v1;
-                if (p.cap2 > 0.f) {
-                  split(v, &v0, &v1);
-                  v = f2(p.cap2 * tanhf(v0), p.cap2 * tanhf(v1));
-                }
                 split(v, &v0, &v1);
-                v = f2(fmaf(slope[t][0], fabsf(far[t][0] - (float)(16 * j + 8 * y)), v0),
-                       fmaf(slope[t][1], fabsf(far[t][1] - (float)(16 * j + 8 * y)), v1));
-              }
-              split(v, &s[j][t][2 * y], &s[j][t][2 * y + 1]);
+                return f2(p.cap2 * tanhf(v0), p.cap2 * tanhf(v1));
+              });
+            } else {  // (a NaN's way too)
+              each([&](F2 v, int, int) {
+                const F2 u = mul2(v, v);
+                F2 r = f2((float)tanh_coef(5));
+#pragma unroll
+                for (int i = 4; i >= 0; --i) r = fma2(r, u, f2((float)tanh_coef(i)));
+                return mul2(mul2(r, v), f2(p.cap2));
+              });
             }
+            if (p.slopes) each(biased);
+          } else {
+            each([&](F2 v, int key, int t) { return biased(scaled(v, key, t), key, t); });
           }
+        }
         if (masked) {
 #pragma unroll
           for (int t = 0; t < kT; ++t) {
