@@ -328,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   __shared__ uint64_t merge_full[kWorkers][C::kMergeBufs], merge_empty[kWorkers][C::kMergeBufs];
   __shared__ Piece pieces[C::kPieces];
   __shared__ int2 looked[32];
+  __shared__ longlong2 looked_scales[kQuant ? 32 : 1];
   __shared__ int abort_flag, first_b;
   __shared__ long long first_at, range[2], sums[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -468,10 +469,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 
       for (int c = walk.c0; ok && c < walk.c1; c += group) {
         if (c > walk.c0) at = look(c, walk, lane / boxes, lane % boxes);
-        if (at.y >= 0 && (unsigned)at.x >= (unsigned)p.seqs.n_pages) {
-          seqs_bad(p.seqs);
-          at.x = -1;
+        const bool bad = at.y >= 0 && (unsigned)at.x >= (unsigned)p.seqs.n_pages;
+        if (bad) seqs_bad(p.seqs);
+        if constexpr (kQuant) {
+          const long long page = bad || at.y < 0 ? 0 : at.x, row = (long long)head * p.seqs.page + max(at.y, 0);
+          looked_scales[lane] = make_longlong2(
+              reinterpret_cast<long long>(p.k_scale + page * p.k_scale_stride + row),
+              reinterpret_cast<long long>(p.v_scale + page * p.v_scale_stride + row));
         }
+        // (a page that is none lies outside the tensor map: zeros)
+        if (bad) at.x = p.seqs.n_pages;
         looked[lane] = at;
         const unsigned needed = __ballot_sync(0xffffffffu, at.y >= 0);
         __syncwarp();
@@ -488,26 +495,35 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
             mbar_arrive_expect_tx(&full[st],
                                   __popc(want) * p.box * (2 * C::kRow + (kQuant ? 8 : 0)));
             const uint32_t tile = smem_u32(ring) + st * 2 * C::kTile;
-            for (int j = 0; j < boxes; ++j) {
-              if (!(want >> j & 1)) continue;
-              const int2 place = looked[i * boxes + j];
-              // (a page that is none lies outside the tensor map: zeros)
-              const int g = place.x < 0 ? p.seqs.n_pages : place.x;
+            auto issue = [&](int j, int2 place, longlong2 from) {
               const uint32_t to = tile + j * p.box * C::kPitch;
 #pragma unroll
               for (int h = 0; h < C::kHalves; ++h) {
-                tma_load_4d(to + h * kKeys * C::kPitch, &p.kmap, &full[st], h * 64, place.y, head, g);
+                tma_load_4d(to + h * kKeys * C::kPitch, &p.kmap, &full[st], h * 64, place.y, head,
+                            place.x);
                 tma_load_4d(to + C::kTile + h * kKeys * C::kPitch, &p.vmap, &full[st], h * 64, place.y,
-                            head, g);
+                            head, place.x);
               }
               if constexpr (kQuant) {
-                const long long row = (long long)head * p.seqs.page + place.y;
                 const uint32_t s_to = smem_u32(scales + 2 * st * kKeys + j * p.box);
-                bulk_load(s_to, p.k_scale + max(place.x, 0) * p.k_scale_stride + row, p.box * 4,
+                bulk_load(s_to, reinterpret_cast<const void*>(from.x), p.box * 4, &full[st]);
+                bulk_load(s_to + kKeys * 4, reinterpret_cast<const void*>(from.y), p.box * 4,
                           &full[st]);
-                bulk_load(s_to + kKeys * 4, p.v_scale + max(place.x, 0) * p.v_scale_stride + row,
-                          p.box * 4, &full[st]);
               }
+            };
+            if (boxes == 1) {
+              issue(0, looked[i], looked_scales[kQuant ? i : 0]);
+            } else {  // the boxes' operands first: reading them one by one takes longer than a copy
+              int2 place[4];
+              longlong2 from[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                place[j] = looked[(i * boxes + j) & 31];
+                from[j] = looked_scales[kQuant ? (i * boxes + j) & 31 : 0];
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (want >> j & 1) issue(j, place[j], from[j]);
             }
           }
         }
