@@ -1,6 +1,8 @@
 // What the cache kernels share: the sequences of a batch, and where a row's token is cached.
 #pragma once
 
+#include <climits>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -13,7 +15,7 @@ struct SeqsParams {
   int32_t* status;       // or null
   long long table_stride, n;
   int n_seqs, page, n_pages;
-  int top;               // positions that the table reaches, at most INT_MAX
+  int top;               // positions that the table reaches
 };
 
 inline SeqsParams seqs_params(const marble_seqs_t& s, const marble_cache_t& c, int64_t n) {
@@ -27,8 +29,9 @@ inline SeqsParams seqs_params(const marble_seqs_t& s, const marble_cache_t& c, i
   p.n_seqs = s.n_seqs;
   p.page = c.page_tokens;
   p.n_pages = (int)c.n_pages;
-  const int64_t top = (int64_t)s.table_pages * c.page_tokens;
-  p.top = (int)(top < 0x7fffffff ? top : 0x7fffffff);
+  // (so far below 2^31 that a chunk's last position still is)
+  const int64_t top = (int64_t)s.table_pages * c.page_tokens, most = INT_MAX - 65535;
+  p.top = (int)(top < most ? top : most);
   return p;
 }
 

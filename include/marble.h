@@ -631,10 +631,11 @@ typedef struct {
  * nothing.  table_pages: entries of a table row that may be read; entries outside the pages that
  * a call needs may hold anything.  All arrays are read when the kernels run.
  * What is out of bounds when they run (an entry outside [0, n_pages) where a page is needed, lens
- * outside [0, table_pages * page_tokens], a start that decreases or passes n_tokens) touches no
- * memory outside the arrays; the results of that sequence are then unspecified, nothing of a bad
+ * outside [0, table_pages * page_tokens] or above 2^31 - 65536, a start that decreases or passes
+ * n_tokens) touches no memory outside the arrays; the results of that sequence are then unspecified, nothing of a bad
  * page is written, and *status, if given, gets MARBLE_SEQS_BAD.  The kernels only ever set bits
- * of *status; a wait in a kernel that runs out of time sets MARBLE_SEQS_TIMEOUT. */
+ * of *status; a wait in a kernel that runs out of time (marble_set_wait_limit_ns) sets
+ * MARBLE_SEQS_TIMEOUT, and the call's results are then unspecified. */
 #define MARBLE_SEQS_TIMEOUT 1
 #define MARBLE_SEQS_BAD 2
 typedef struct {

@@ -232,6 +232,62 @@ def test_streams_and_graphs(kind):
     check_attn(batches[1], qs[1], o, lse)
 
 
+def test_positions_up_to_the_last():
+    """A table that names one page 32,767 times: as many positions as there may be.  Every key counts
+    32,767 times, so o is the page's own and lse ln 32,767 more.  Sums of fp32 lose up to 2^-24 a
+    term: a thread adds 2^31 / (2 CTAs x 148 SMs x 4 warps x 8 lanes) weights, 1.4%, and the
+    matrix unit as many products of 16 keys, twice that; both enter o."""
+    page = 65536
+    batch = Batch("int8", [page], None, 1, 64, page, spare=0)
+    q = _q(1, 4, 64, 12)
+    o1, l1 = _run(batch, q)
+    check_attn(batch, q, o1, l1)
+    reps = (2 ** 31 - 65536) // page
+    assert reps == 32767
+    table = torch.zeros((1, reps), dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    seqs = M.Sequences(table, torch.tensor([reps * page], dtype=torch.int32).cuda(), None, status)
+    o, lse = M.attn_cached(batch.cache, seqs, q)
+    seqs.check()
+    size = np64(o1).__abs__() + np.abs(batch.v[0]).max() * 0.043
+    assert (np.abs(np64(o) - np64(o1)) <= 0.043 * size + 2 * 2.0 ** -8 * size).all()
+    assert (np.abs(np64(lse) - np64(l1) - np.log(reps)) < 0.015).all()
+    # the end of it alone, in a window
+    ow, lw = M.attn_cached(batch.cache, seqs, q, window=page)
+    torch.testing.assert_close(ow, o1, rtol=2 ** -6, atol=2 ** -8)
+    torch.testing.assert_close(lw, l1, rtol=0, atol=1e-4)
+    seqs.lens.add_(1)  # one more is refused by the kernel
+    M.attn_cached(batch.cache, seqs, q)
+    assert int(status) == M.SEQS_BAD
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_one_table_on_two_streams_and_threads(kind):
+    """Calls on the same sequences at the same time, from two threads on two streams, have
+    workspaces of their own."""
+    import threading
+    batch = Batch(kind, [9000, 77], None, 2, 64, 64)
+    qs = [_q(2, 8, 64, s) for s in (20, 21)]
+    want = [_run(batch, q) for q in qs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(q, w):
+        stream = torch.cuda.Stream()
+        for _ in range(50):
+            o, lse = _run(batch, q, stream=stream)
+            stream.synchronize()
+            if not (torch.equal(o, w[0]) and torch.equal(lse, w[1])):
+                bad.append(1)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(qs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_prompt_then_tokens(kind):
     """The calls as they are used: a packed prompt through rope, the cache and the packed
