@@ -7,10 +7,10 @@
 // value is read once, at 2 or 1 bytes a channel.  One sequence of 1,048,576 tokens, 8 kv heads of
 // 128, microseconds, and the time that a plain copy's rate gives:
 //   rows        4       12      20      64     copy
-//   bf16       594     602     608    1023      642
-//   e4m3       331     375     518    1052      331
-//   int8       337     390     584    1210      331
-// and with heads of 64, 4 rows: bf16 306 (321), e4m3 180 (171).  Above 16 rows the computing
+//   bf16       584     607     606    1054      642
+//   e4m3       332     380     548    1058      331
+//   int8       336     397     581    1133      331
+// and with heads of 64, 4 rows: bf16 301 (321), e4m3 180 (171).  Above 16 rows the computing
 // warps' instructions are the bound (of bf16 above 32).
 //
 // - An item is a (sequence, kv head, tile of 8, 16, 32 or 64 rows); its cost is its chunks of keys
@@ -655,9 +655,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       for (int i = 0; i < D / 16; ++i) o[i][t][0] = o[i][t][1] = o[i][t][2] = o[i][t][3] = 0.f;
     }
 
-    // One chunk: S^T, the softmax's step, O^T += V^T P^T, with kT of the warp's tiles of rows.
-    auto chunk_step = [&](auto tiles_, int st, int base, bool masked) {
-      constexpr int kT = decltype(tiles_)::value;
+    // One chunk: S^T, the softmax's step, O^T += V^T P^T.  (Leaving out a second tile without rows, by a
+    // second copy of this code, costs more in instruction fetches than it saves.)
+    auto chunk_step = [&](int st, int base, bool masked) {
       const uint32_t kt = smem_u32(ring) + st * 2 * C::kTile, vt = kt + C::kTile;
       const float* ks = scales + 2 * st * kKeys;
       const float* vs = ks + kKeys;
@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 #pragma unroll
             for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-              for (int t = 0; t < kT; ++t)
+              for (int t = 0; t < kNt; ++t)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) o[d][t][y] *= by;
             vref = to;
@@ -689,11 +689,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 #pragma unroll 1
       for (int sub = 0; sub < kKeys; sub += C::kSub) {
         // scores
-        float s[kMt][kT][4];
+        float s[kMt][kNt][4];
 #pragma unroll
         for (int j = 0; j < kMt; ++j)
 #pragma unroll
-          for (int t = 0; t < kT; ++t) s[j][t][0] = s[j][t][1] = s[j][t][2] = s[j][t][3] = 0.f;
+          for (int t = 0; t < kNt; ++t) s[j][t][0] = s[j][t][1] = s[j][t][2] = s[j][t][3] = 0.f;
 #pragma unroll
         for (int x = 0; x < C::kRow / 32; ++x) {  // 32 bytes of the keys at a time
           const uint32_t row = kt + (x >> 2) * kKeys * C::kPitch + sub * C::kPitch + k_row +
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
             ldsm4(row + j * 16 * C::kPitch, f);
             if constexpr (!kQuant) {
 #pragma unroll
-              for (int t = 0; t < kT; ++t) mma<false>(s[j][t], f, q[t][x]);
+              for (int t = 0; t < kNt; ++t) mma<false>(s[j][t], f, q[t][x]);
             } else {
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
                 along<kType>(f[2 * y], &a[0], &a[2]);
                 along<kType>(f[2 * y + 1], &a[1], &a[3]);
 #pragma unroll
-                for (int t = 0; t < kT; ++t) mma<true>(s[j][t], a, q[t][2 * x + y]);
+                for (int t = 0; t < kNt; ++t) mma<true>(s[j][t], a, q[t][2 * x + y]);
               }
             }
           }
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
-              for (int t = 0; t < kT; ++t)
+              for (int t = 0; t < kNt; ++t)
                 split(f(f2(s[j][t][2 * y], s[j][t][2 * y + 1]), 16 * j + 8 * y, t), &s[j][t][2 * y],
                       &s[j][t][2 * y + 1]);
         };
@@ -735,9 +735,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         if constexpr (!kScored) {
           each(scaled);
         } else {
-          float far[kT][2];  // distances of this lane's first key
+          float far[kNt][2];  // distances of this lane's first key
 #pragma unroll
-          for (int t = 0; t < kT; ++t) {
+          for (int t = 0; t < kNt; ++t) {
             far[t][0] = (float)(pos[t][0] - base - sub - qn);
             far[t][1] = (float)(pos[t][1] - base - sub - qn);
           }
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         }
         if (masked) {
 #pragma unroll
-          for (int t = 0; t < kT; ++t) {
+          for (int t = 0; t < kNt; ++t) {
             int lo[2], hi[2];
             sees(p, pc.s, pos[t][0], &lo[0], &hi[0]);
             sees(p, pc.s, pos[t][1], &lo[1], &hi[1]);
@@ -794,9 +794,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
           }
         }
         bool grow = false;
-        float top[kT][2];
+        float top[kNt][2];
 #pragma unroll
-        for (int t = 0; t < kT; ++t) {
+        for (int t = 0; t < kNt; ++t) {
           top[t][0] = top[t][1] = -INFINITY;
 #pragma unroll
           for (int j = 0; j < kMt; ++j)
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-          for (int t = 0; t < kT; ++t) {
+          for (int t = 0; t < kNt; ++t) {
             float by[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -823,9 +823,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         }
 
         // weights, as B operands: [row n][keys 2 t, + 1]
-        uint32_t ph[kMt][kT][2], pl[kQuant ? 1 : kMt][kT][2];
+        uint32_t ph[kMt][kNt][2], pl[kQuant ? 1 : kMt][kNt][2];
 #pragma unroll
-        for (int t = 0; t < kT; ++t) {
+        for (int t = 0; t < kNt; ++t) {
           const F2 off = f2(m[t][0] == -INFINITY ? 0.f : -m[t][0], m[t][1] == -INFINITY ? 0.f : -m[t][1]);
 #pragma unroll
           for (int j = 0; j < kMt; ++j)
@@ -858,9 +858,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
                     f);
             if constexpr (!kQuant) {
 #pragma unroll
-              for (int t = 0; t < kT; ++t) mma<false>(o[x][t], f, ph[j][t]);
+              for (int t = 0; t < kNt; ++t) mma<false>(o[x][t], f, ph[j][t]);
 #pragma unroll
-              for (int t = 0; t < kT; ++t) mma<false>(o[x][t], f, pl[j][t]);
+              for (int t = 0; t < kNt; ++t) mma<false>(o[x][t], f, pl[j][t]);
             } else {
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
@@ -868,15 +868,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
                 across<kType>(f[2 * y], &a[0], &a[1]);
                 across<kType>(f[2 * y + 1], &a[2], &a[3]);
 #pragma unroll
-                for (int t = 0; t < kT; ++t) mma<true>(o[2 * x + y][t], a, ph[j][t]);
+                for (int t = 0; t < kNt; ++t) mma<true>(o[2 * x + y][t], a, ph[j][t]);
               }
             }
           }
         }
       }
     };
-    // tiles of rows that hold any
-    const int row_tiles = (int)min(((long long)pc.s.count * p.group - row0 + 7) >> 3, (long long)kNt);
+    const bool any_rows = (long long)pc.s.count * p.group > row0;
     for (int i = (kg - n) & (kgs - 1); i < pc.chunks; i += kgs) {
       const int at = n + i, st = at % kStages, base = pc.key0 + i * kKeys;
       if (!wait_all(&full[st], (at / kStages) & 1, wait)) return;
@@ -895,12 +894,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         fence_proxy_async_smem();  // before the copies that follow these writes
         __syncwarp();
       }
-      if (row_tiles > 0) {
-        if (kNt == 1 || row_tiles > 1)
-          chunk_step(std::integral_constant<int, kNt>{}, st, base, masked);
-        else
-          chunk_step(std::integral_constant<int, 1>{}, st, base, masked);
-      }
+      if (any_rows) chunk_step(st, base, masked);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
     }
