@@ -54,7 +54,7 @@ marble_status_t run_attn_cached(int64_t n, const marble_cache_t* c, const marble
   p.rows = 8 * nt * p.row_warps;
   while ((1 << p.rows_log) < p.rows) ++p.rows_log;
   // (the computing warps do four chunks side by side in the time of one; 3 to 9 differ by 2%)
-  p.grain = 5;
+  p.grain = nt == 1 ? 5 : 4 * 5;
   p.limit_ns = wait_limit_ns();
   p.drain_ns = std::max<uint64_t>(p.limit_ns, 1000000000ull);  // copies under way always land
   int dev = 0, sms = 148;

@@ -23,10 +23,11 @@
 //   q) and four that compute; two CTAs share an SM, so that one's item boundaries hide behind
 //   the other's streaming.
 // - A chunk belongs to one warp of the item's 8 or 16 rows (two or four where there are more rows):
-//   warps have their own m, l and O over their chunks and meet only at an item's end.  A place of
-//   the ring always belongs to the same warps (its copies may land before those of an earlier
-//   place: whoever waits for a place's next filling must have seen the one before, or the
-//   barrier's parity misleads it).
+//   warps have their own m, l and O over their chunks and meet only at an item's end.  Where the
+//   batch has items of more than 16 rows, those of fewer still have their keys dealt to all four
+//   warps.  A place of the ring then passes between warps, and one that waits for its next
+//   filling has to know that the one before is over, or the barrier's parity misleads it: the
+//   fetching warp tells how many chunks it has issued.
 // - The products are m16n8k16 matrix instructions with the keys (channels) as the 16 rows and the q
 //   rows as the 8 columns: tcgen05's 128 x 8 would have the same shape, but its operands come from
 //   shared memory, where 8-bit codes would have to be written as fp16 first, and what memory
@@ -56,6 +57,7 @@ constexpr int kWorkers = 4;   // computing warps
 constexpr int kThreads = 64 * kWorkers;
 constexpr int kFetchRegs = 56, kWorkRegs = 200;
 constexpr int kUnitOver = 3;  // an item's constant cost, in chunks (1 to 6: 3 and 4 are the fastest)
+constexpr int kMergeArrivals = 6;  // of the warps whose O is handed over: 3 or 2
 constexpr float kLazy = 8.f;  // O is rescaled when m grows by more (base 2)
 constexpr float kPUp = 64.f;  // fp16 weights are raised by this (see below)
 
@@ -78,15 +80,11 @@ struct Cfg {
   static constexpr int kQPitch = D * 2 + 16;
   static constexpr int kMerge = 32 * (D / 4 * kNt + 4 * kNt) * 4;
   static constexpr int kMergeBufs = kNt == 1 ? 2 : 1;
-  static constexpr int most() {
-    int m = 0;
-    for (int r = 1; r <= kWorkers; r *= 2) {
-      const int bytes = kPieces * 8 * kNt * r * kQPitch + kMergeBufs * (kWorkers - r) * kMerge;
-      if (bytes > m && (kNt > 1 || r == 1)) m = bytes;
-    }
-    return m;
+  static constexpr int smem(int row_warps) {
+    const int writers = row_warps == kWorkers ? 0 : kWorkers - 1;
+    return 1024 + kStages * 2 * kTile + kScales + kPieces * 8 * kNt * row_warps * kQPitch +
+           kMergeBufs * writers * kMerge;
   }
-  static constexpr int kSmem = 1024 + kStages * 2 * kTile + kScales + most();
 };
 
 struct AttnParams {
@@ -105,7 +103,7 @@ struct AttnParams {
   float cap2;        // cap * log2 e, 0: none
   int hkv, group, hq;
   int window, span;
-  int row_warps;     // warps that an item's rows are split over: 1, 2 or 4
+  int row_warps;     // warps that an item's rows are split over, at most: 1, 2 or 4
   int rows, rows_log;  // of an item: 8 * kNt * row_warps
   int box;           // keys of a TMA box
   int grain;         // units a CTA takes at least
@@ -121,8 +119,16 @@ struct AttnParams {
 struct Work {
   Seq s;
   int lo, hi, chunk0, chunks, tiles, items;
+  int weight;  // units of a chunk
   long long units;
 };
+
+// The time of a chunk by the rows of its item, in quarters: 8-bit items whose keys go to two warps at
+// a time, among others whose keys go to four, take longer.
+__device__ __forceinline__ int weight_of(const AttnParams& p, int count) {
+  const long long rows = min((long long)count * p.group, (long long)p.rows);
+  return !p.k_scale || p.row_warps == kWorkers || rows <= 16 ? 4 : 6;
+}
 
 // the positions that the row at `pos` sees: [lo, hi)
 __device__ __forceinline__ void sees(const AttnParams& p, const Seq& s, int pos, int* lo, int* hi) {
@@ -135,7 +141,7 @@ __device__ __forceinline__ void sees(const AttnParams& p, const Seq& s, int pos,
   if (pos < 0) *lo = *hi = 0;
 }
 
-template <int kKeys, bool kTell>
+template <int kKeys, int kNt, bool kTell>
 __device__ __forceinline__ Work work_of(const AttnParams& p, int b) {
   Work w;
   w.s = seq_at<kTell>(p.seqs, b);
@@ -146,7 +152,8 @@ __device__ __forceinline__ Work work_of(const AttnParams& p, int b) {
   w.chunks = w.lo < w.hi ? (w.hi - 1) / kKeys - w.chunk0 + 1 : 0;
   w.tiles = (int)(((long long)w.s.count * p.group + p.rows - 1) >> p.rows_log);
   w.items = w.tiles * p.hkv;
-  w.units = w.items ? w.chunks + kUnitOver : 0;
+  w.weight = kNt == 1 ? 1 : weight_of(p, w.s.count);
+  w.units = w.items ? (long long)(w.chunks + kUnitOver) * w.weight : 0;
   return w;
 }
 
@@ -156,10 +163,13 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 }
 
 // chunks before offset x of an item
-__device__ __forceinline__ int cut(long long x) { return (int)max(x - kUnitOver, 0ll); }
+template <int kNt>
+__device__ __forceinline__ int cut(const Work& w, long long x) {
+  return (int)max((kNt == 1 ? x : quotient(x, w.weight)) - kUnitOver, 0ll);
+}
 
 // the walk over a CTA's range of units, piece by piece
-template <int kKeys>
+template <int kKeys, int kNt>
 struct Walk {
   const AttnParams& p;
   long long left, off;  // units left, those of the present item that are behind
@@ -167,10 +177,11 @@ struct Walk {
   Work w;
   // of the present piece
   int item, c0, c1;
+  long long rest;       // units of its item behind it
   // from unit `at` of sequence b_ on
   __device__ __forceinline__ Walk(const AttnParams& p_, int b_, long long at, long long left_)
       : p(p_), left(left_), b(b_) {
-    w = work_of<kKeys, false>(p, b);
+    w = work_of<kKeys, kNt, false>(p, b);
     next_item = (int)quotient(at, w.units);
     off = at - next_item * w.units;
   }
@@ -178,7 +189,7 @@ struct Walk {
     while (left > 0) {
       if (next_item >= w.items) {
         if (++b >= p.seqs.n_seqs) return false;
-        w = work_of<kKeys, false>(p, b);
+        w = work_of<kKeys, kNt, false>(p, b);
         next_item = 0;
         continue;
       }
@@ -188,8 +199,9 @@ struct Walk {
       const bool ends = to == w.units;
       next_item += ends ? 1 : 0;
       off = ends ? 0 : to;
-      c0 = cut(from);
-      c1 = cut(to);
+      rest = w.units - to;
+      c0 = cut<kNt>(w, from);
+      c1 = cut<kNt>(w, to);
       if (c1 > c0 || (w.chunks == 0 && from == 0)) return true;
     }
     return false;
@@ -276,6 +288,37 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint6
       "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
+// arrive `n` times
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, int n) {
+  asm volatile(
+      "{\n\t.reg .b64 st;\n\t"
+      "mbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(n)
+      : "memory");
+}
+__device__ __forceinline__ void store_release(int* at, int v) {
+  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(at)), "r"(v) : "memory");
+}
+__device__ __forceinline__ int load_acquire(const int* at) {
+  int v;
+  asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(at)) : "memory");
+  return v;
+}
+// whole warp: until chunk `n` has been issued (bounded like the barriers' waits)
+__device__ __forceinline__ bool wait_issued(const int* issued, int n, const WaitCtx& w) {
+  if (__all_sync(0xffffffffu, load_acquire(issued) > n)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  bool ok = true;
+  while (ok && load_acquire(issued) <= n) {
+    if (*w.abort) ok = false;
+    if (globaltimer_ns() - t0 > w.limit_ns) {
+      atomicOr(w.err, kErrTimeout);
+      *w.abort = 1;
+      ok = false;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
@@ -324,6 +367,7 @@ struct Piece {
   int lo, hi;           // the item's keys
   int key0, chunks;     // the piece's first key and chunks; chunks < 0: there are no more pieces
   int head, row0;       // the item's kv head and first row
+  int row_warps;        // warps that the item's rows are split over
   int place;            // where the piece goes in the workspace, -1: it is the whole item
 };
 
@@ -338,11 +382,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   uint8_t* qs = reinterpret_cast<uint8_t*>(scales) + C::kScales;
   float4* merge = reinterpret_cast<float4*>(qs + C::kPieces * p.rows * C::kQPitch);
   __shared__ uint64_t full[kStages], empty[kStages], piece_full[C::kPieces], piece_empty[C::kPieces];
-  __shared__ uint64_t merge_full[kWorkers][C::kMergeBufs], merge_empty[kWorkers][C::kMergeBufs];
+  __shared__ uint64_t merge_full[C::kMergeBufs], merge_empty[C::kMergeBufs];
   __shared__ Piece pieces[C::kPieces];
   __shared__ int2 looked[32];
   __shared__ longlong2 looked_scales[kQuant ? 32 : 1];
-  __shared__ int abort_flag, first_b;
+  __shared__ int abort_flag, first_b, told;
   __shared__ long long first_at, range[2], sums[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -354,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   const int b0 = min(tid * share, ns), b1 = min(b0 + share, ns);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
-    const Work w = blockIdx.x == 0 ? work_of<kKeys, true>(p, b) : work_of<kKeys, false>(p, b);
+    const Work w = blockIdx.x == 0 ? work_of<kKeys, kNt, true>(p, b) : work_of<kKeys, kNt, false>(p, b);
     mine += w.units * w.items;
   }
   long long upto = mine;  // of this warp's threads up to this one
@@ -364,9 +408,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     upto += lane >= off ? v : 0;
   }
   if (lane == 31) sums[warp] = upto;
-  const int kgs = kWorkers / p.row_warps;
   if (tid == 0) {
     abort_flag = 0;
+    told = 0;
     p.joins[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     tma_prefetch_desc(&p.kmap);
     tma_prefetch_desc(&p.vmap);
@@ -378,11 +422,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       mbar_init(&piece_full[i], 1);
       mbar_init(&piece_empty[i], kWorkers);
     }
-    for (int i = 0; i < kWorkers; ++i) {
-      for (int j = 0; j < C::kMergeBufs; ++j) {
-        mbar_init(&merge_full[i][j], max(kgs - 1, 1));
-        mbar_init(&merge_empty[i][j], 1);
-      }
+    for (int i = 0; i < C::kMergeBufs; ++i) {
+      mbar_init(&merge_full[i], kMergeArrivals);
+      mbar_init(&merge_empty[i], kWorkers);
     }
     fence_mbar_init();
   }
@@ -400,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     long long at = u0 - before;
     int b = b0;
     for (; b < b1; ++b) {
-      const Work w = work_of<kKeys, false>(p, b);
+      const Work w = work_of<kKeys, kNt, false>(p, b);
       if (at < w.units * w.items) break;
       at -= w.units * w.items;
     }
@@ -421,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     const int boxes = kKeys / p.box, group = 32 / boxes;
     const bool leader = elect_one();
     // table entry and slot of box j of the chunk i behind chunk c of a piece; no slot: not needed
-    auto look = [&](int c, const Walk<kKeys>& walk, int i, int j) {
+    auto look = [&](int c, const Walk<kKeys, kNt>& walk, int i, int j) {
       int2 at = make_int2(-1, -1);
       const int key = (walk.w.chunk0 + c + i) * kKeys + j * p.box;
       if (c + i < walk.c1 && key < walk.w.hi && key + p.box > walk.w.lo) {
@@ -430,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       }
       return at;
     };
-    Walk<kKeys> walk(p, first_b, first_at, u1 - u0);
+    Walk<kKeys, kNt> walk(p, first_b, first_at, u1 - u0);
     int n = 0, np = 0, issued = 0;  // chunks and pieces so far
     bool ok = true;
     while (ok) {
@@ -458,12 +500,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
           q.chunks = walk.c1 - walk.c0;
           q.head = head;
           q.row0 = row0;
+          // (four row warps leave no room for merging)
+          q.row_warps = p.row_warps == kWorkers || live > 8 * kNt ? p.row_warps : 1;
           // a CTA's first place is for an item that another CTA began, its second for one that
           // another goes on with
           q.place = begins && ends ? -1 : 2 * (int)blockIdx.x + (begins ? 1 : 0);
           if (begins && !ends) {
             // the CTAs that have the rest: the last one holds the item's last unit
-            const long long end = u1 + (w.chunks - walk.c1);
+            const long long end = u1 + walk.rest;
             const int last = (int)quotient(end * range[1] - 1, range[0]);
             p.joins[2 * blockIdx.x] = make_int4(last - (int)blockIdx.x + 1, w.s.first, w.s.count, head);
             p.joins[2 * blockIdx.x + 1] = make_int4(row0, 0, 0, 0);
@@ -524,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
                           &full[st]);
               }
             };
+            if constexpr (kNt > 1) store_release(&told, at_n + 1);
             if (boxes == 1) {
               issue(0, looked[i], looked_scales[kQuant ? i : 0]);
             } else {  // the boxes' operands first: reading them one by one takes longer than a copy
@@ -560,7 +605,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   // O^T = V^T P^T (16 channels x 8 rows), so that a group of up to 8 rows wastes nothing.  Lane 4 n
   // + t holds keys n and n + 8 of 16, rows 2 t and 2 t + 1 of 8.
   regs_grow<kWorkRegs>();
-  const int tile = warp % p.row_warps, kg = warp / p.row_warps;
   const int qn = lane >> 2, qt = lane & 3, l7 = lane & 7, lm = lane >> 3;
   // where a lane's row of an ldmatrix begins: of keys (lm & 1 or lm >> 1: the second eight), and
   // the 16-byte chunk in it (the other bit), which the swizzle moves by the row
@@ -568,12 +612,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   const uint32_t k_row = ((lm & 1) * 8 + l7) * C::kPitch, k_x = ((lm >> 1) ^ swz) << 4;
   const uint32_t v_row = kQuant ? k_row : ((lm >> 1) * 8 + l7) * C::kPitch;
   const uint32_t v_x = kQuant ? k_x : ((lm & 1) ^ swz) << 4;
-  int n = 0;  // chunks so far
+  int n = 0, nm = 0;  // chunks and merged pieces so far
+  int dealt = 0, unsure = 0;  // row warps of the last piece; chunks whose places had other warps
   for (int np = 0;; ++np) {
     const int ps = np % C::kPieces;
     if (!wait_all(&piece_full[ps], (np / C::kPieces) & 1, wait)) return;
     const Piece pc = pieces[ps];
     if (pc.chunks < 0) return;
+    if (kNt > 1 && pc.row_warps != dealt) {
+      unsure = dealt ? n + kStages : 0;
+      dealt = pc.row_warps;
+    }
+    const int row_warps = kNt == 1 ? 1 : pc.row_warps, kgs = kWorkers / row_warps;
+    const int tile = warp % row_warps, kg = warp / row_warps;
     const int row0 = pc.row0 + 8 * kNt * tile;  // this warp's first row
 
     // q: bf16, channels (2 t, + 1, + 8, + 9) of 16; or fp16, channels 4 t .. + 3 of 16, the order in
@@ -878,7 +929,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     const bool any_rows = (long long)pc.s.count * p.group > row0;
     for (int i = (kg - n) & (kgs - 1); i < pc.chunks; i += kgs) {
       const int at = n + i, st = at % kStages, base = pc.key0 + i * kKeys;
-      if (!wait_all(&full[st], (at / kStages) & 1, wait)) return;
+      if ((kNt > 1 && at < unsure && !wait_issued(&told, at, wait)) ||
+          !wait_all(&full[st], (at / kStages) & 1, wait))
+        return;
       const bool masked = base < all_lo || base + kKeys > all_hi;
       if (base < pc.lo || base + kKeys > pc.hi) {
         // Keys outside the item: their weights are 0, and what the ring holds for their values
@@ -896,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       }
       if (any_rows) chunk_step(st, base, masked);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      if (lane == 0) mbar_arrive_n(&empty[st], kNt == 1 ? 1 : p.row_warps / row_warps);
     }
     n += pc.chunks;
 
@@ -917,13 +970,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
     }
     // the warps of the same rows: into one of them, which takes turns
     if (kgs > 1) {
-      const int buf = np % C::kMergeBufs, parity = (np / C::kMergeBufs) & 1;
-      const int from_one = (kg - np) & (kgs - 1);  // 0: this warp's turn
-      float4* bufs = merge + buf * (kWorkers - p.row_warps) * (C::kMerge / 16) + lane;
+      const int buf = nm % C::kMergeBufs, parity = (nm / C::kMergeBufs) & 1;
+      const int from_one = (kg - nm) & (kgs - 1);  // 0: this warp's turn
+      float4* bufs = merge + buf * (kWorkers - 1) * (C::kMerge / 16) + lane;
       // (every warp sees every phase of these barriers, one after the other)
-      if (np >= C::kMergeBufs && !wait_all(&merge_empty[tile][buf], parity ^ 1, wait)) return;
+      if (nm >= C::kMergeBufs && !wait_all(&merge_empty[buf], parity ^ 1, wait)) return;
+      ++nm;
       if (from_one > 0) {
-        float4* to = bufs + ((from_one - 1) * p.row_warps + tile) * (C::kMerge / 16);
+        float4* to = bufs + ((from_one - 1) * row_warps + tile) * (C::kMerge / 16);
 #pragma unroll
         for (int t = 0; t < kNt; ++t) {
 #pragma unroll
@@ -933,12 +987,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
           to += 32;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&merge_full[tile][buf]);
+        if (lane == 0) mbar_arrive_n(&merge_full[buf], kMergeArrivals / (kWorkers - row_warps));
         continue;
       }
-      if (!wait_all(&merge_full[tile][buf], parity, wait)) return;
+      if (!wait_all(&merge_full[buf], parity, wait)) return;
       for (int g = 1; g < kgs; ++g) {
-        const float4* from = bufs + ((g - 1) * p.row_warps + tile) * (C::kMerge / 16);
+        const float4* from = bufs + ((g - 1) * row_warps + tile) * (C::kMerge / 16);
 #pragma unroll
         for (int t = 0; t < kNt; ++t, from += 32 * (D / 16 + 1)) {
           const float4 ml = from[32 * (D / 16)];
@@ -963,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&merge_empty[tile][buf]);
+      if (lane == 0) mbar_arrive_n(&merge_empty[buf], kWorkers / row_warps);
     }
 
     // channels of o[d][t][0 / 2] (row 2 t; [1 / 3]: row 2 t + 1): bf16 16 d + n and 16 d + 8 + n, 8-bit types
@@ -1135,12 +1189,12 @@ marble_status_t launch(AttnParams& p, int grid, int join_rows, cudaStream_t s) {
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev & 63] || dev > 63) {
       const cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(2));
       if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(k_attn_cached)");
       done[dev & 63] = true;
     }
   }
-  kernel<<<grid, kThreads, C::kSmem, s>>>(p);
+  kernel<<<grid, kThreads, C::smem(p.row_warps), s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "marble_attn_cached launch");
   cudaLaunchAttribute early;

@@ -94,13 +94,19 @@ def test_many_sequences(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("d,group,counts", [(128, 2, None), (64, 4, None), (128, 4, [7, 1, 16])])
-def test_the_ring_goes_round(kind, d, group, counts):
+@pytest.mark.parametrize("d,group,counts,lens", [
+    (128, 2, None, [30000, 5, 21003]), (64, 4, None, [30000, 5, 21003]),
+    (128, 4, [7, 1, 16], [30000, 5, 21003]),
+    # items of up to and of more than 16 rows in turn: the places of the ring change hands
+    (128, 4, [1, 8, 3, 5, 4, 6, 2, 8] * 3, [700, 2900, 33, 1500, 64, 900, 2000, 1200] * 3),
+    (64, 8, [4, 1, 3, 2] * 6, [500, 77, 1900, 640] * 6)])
+def test_the_ring_goes_round(kind, d, group, counts, lens):
     """Enough keys that every CTA fills its ring many times over."""
-    batch = Batch(kind, [30000, 5, 21003], counts, 6, d, 64, seed=5)
+    batch = Batch(kind, lens, counts, 6, d, 64, seed=5)
     q = _q(batch.n, 6 * group, d, 10)
     o, lse = _run(batch, q)
     check_attn(batch, q, o, lse)
+    batch.seqs.check()
     for _ in range(20):
         again = _run(batch, q)
         assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
