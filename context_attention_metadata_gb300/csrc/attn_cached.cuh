@@ -7,10 +7,10 @@
 // value is read once, at 2 or 1 bytes a channel.  One sequence of 1,048,576 tokens, 8 kv heads of
 // 128, microseconds, and the time that a plain copy's rate gives:
 //   rows        4       12      20      64     copy
-//   bf16       584     607     606    1054      642
-//   e4m3       332     380     548    1058      331
-//   int8       336     397     581    1133      331
-// and with heads of 64, 4 rows: bf16 301 (321), e4m3 180 (171).  Above 16 rows the computing
+//   bf16       591     626     655    1137      642
+//   e4m3       335     387     577    1111      331
+//   int8       337     398     600    1159      331
+// and with heads of 64, 4 rows: bf16 306 (321), e4m3 183 (171).  Above 16 rows the computing
 // warps' instructions are the bound (of bf16 above 32).
 //
 // - An item is a (sequence, kv head, tile of 8, 16, 32 or 64 rows); its cost is its chunks of keys

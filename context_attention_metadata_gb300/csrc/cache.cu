@@ -5,11 +5,15 @@
 //   int8:  s = top / 127;                             code = x * 127 / top rounded to an integer
 // and back: bf16(code * s).
 //
-// Both kernels are bound by memory: 2 bytes a channel on one side, 2 or 1 on the other.  A thread
-// holds 16 channels of a head, d / 16 lanes a head, so that `top` is a butterfly and a code's
-// store or load is 16 bytes.  A warp resolves where the tokens of a run of rows are cached with a
-// lane for each (the table look-up is a chain of three loads), then moves them one after the
-// other, its group of heads of k and of v side by side.
+// Bound by memory: 2 bytes a channel on one side, 2 or 1 on the other.  A thread holds 16 channels
+// of a head, d / 16 lanes a head, so that `top` is a butterfly and a code's store or load is 16
+// bytes.  A CTA takes a tile of up to 16 rows: one warp finds where the next tile's tokens are cached
+// (a chain of three loads, a lane each) while all move the present one's heads, a warp one head
+// of k or v of all rows.  Those are contiguous in a page, and the warps' heads are contiguous in
+// the rows, so that both sides' accesses fall together: with a warp for all heads of a row the
+// figures below were 271, 324 and 293 us.  Measured, heads of 8 x 128: 213,194 rows in plan order into
+// e4m3 207 us (6.39 TB/s, 95% of a plain copy's rate), into bf16 268 (97%); 262,144 rows out of int8
+// 250 us (97%), out of bf16 328 (98%).
 #include <algorithm>
 #include <cstring>
 
