@@ -31,7 +31,7 @@
 // - The products are m16n8k16 matrix instructions with the keys (channels) as the 16 rows and the q
 //   rows as the 8 columns: tcgen05's 128 x 8 would have the same shape, but its operands come from
 //   shared memory, where 8-bit codes would have to be written as fp16 first, and what memory
-//   feeds at these sizes is a quarter of the warp-level instructions' rate.  (e4m3 products with
+//   feeds for 8 rows is 15% of the warp-level instructions' rate.  (e4m3 products with
 //   q in two e4m3 terms were exact too, but slower: twice the sums.)
 // - 8-bit codes become fp16 exactly in registers; k's scales multiply scores, v's scales the
 //   weights, so that nothing but the weights (and q, by a power of two a row) is rounded to fp16.

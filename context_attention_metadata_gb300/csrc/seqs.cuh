@@ -35,6 +35,8 @@ inline SeqsParams seqs_params(const marble_seqs_t& s, const marble_cache_t& c, i
   return p;
 }
 
+static_assert(kErrTimeout == MARBLE_SEQS_TIMEOUT, "waits set this bit of the status");
+
 __device__ __forceinline__ void seqs_bad(const SeqsParams& p) {
   if (p.status) atomicOr(p.status, MARBLE_SEQS_BAD);
 }
