@@ -60,6 +60,7 @@ constexpr int kUnitOver = 3;  // an item's constant cost, in chunks (1 to 6: 3 a
 constexpr int kMergeArrivals = 6;  // of the warps whose O is handed over: 3 or 2
 constexpr float kLazy = 8.f;  // O is rescaled when m grows by more (base 2)
 constexpr float kPUp = 64.f;  // fp16 weights are raised by this (see below)
+constexpr uint32_t kLeastUnit = (127 - 120) << 23;  // 2^-120 as fp32's bits: v's scales' least unit
 
 // kNt: tiles of 8 rows that a warp computes
 template <int D, int kType, int kNt>
@@ -716,14 +717,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       if constexpr (kQuant) {
         // fp16 weights p * v's scale in units of vref, the power of two at or above the largest
         // scale so far, raised by kPUp: at most 2^(8 + 6 + 1), and nothing is lost above 2^-20
-        // of the largest.
+        // of the largest.  vref is at least 2^-120, so that kPUp / vref is finite: scales go down
+        // to fp32's least, whose quotient would be infinite and, times a weight of 0, NaN.
         uint32_t big = 0;
 #pragma unroll
         for (int x = 0; x < kKeys / 32; ++x)
           big = max(big, __float_as_uint(vs[32 * x + lane]) & 0x7fffffffu);
         big = __reduce_max_sync(0xffffffffu, big);
         if (big > __float_as_uint(vref)) {
-          const float to = __uint_as_float(min((big + 0x7fffffu) & 0xff800000u, 0x7f000000u));
+          const float to = __uint_as_float(
+              max(min((big + 0x7fffffu) & 0xff800000u, 0x7f000000u), kLeastUnit));
           if (to > vref) {
             const float by = vref / to;
 #pragma unroll

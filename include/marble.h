@@ -683,7 +683,10 @@ marble_status_t marble_cache_read(const marble_plan_t *plan, int64_t n_tokens,
  * may be anything, infinities and NaN too; those that some row of it sees have to be finite.
  * Sums and the softmax are in fp32.  bf16 caches: the weights enter their product with v as two
  * bf16 terms (16 bits).  8-bit caches: q enters in fp16 after a power of two for each row (no
- * bits are lost above 2^-29 of its largest channel), the weights, times v's scale, in fp16.
+ * bits are lost above 2^-29 of its largest channel), the weights (1 at the softmax's maximum),
+ * times v's scale, in fp16 too (11 bits): with u the power of two at or above the largest of v's
+ * scales among the keys that some row of the sequence sees, and at least 2^-120, products below
+ * 2^-20 u lose bits and those below 2^-31 u are lost.
  * The keys of all (sequence, kv head, tile of up to 64 rows) are dealt evenly to the SMs, whatever
  * the lengths; the pieces of one softmax are joined in order, so that results do not depend on
  * timing.  Rows of a kv head beyond 64 read the cache again.
