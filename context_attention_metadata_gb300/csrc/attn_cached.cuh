@@ -938,15 +938,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       const bool masked = base < all_lo || base + kKeys > all_hi;
       if (base < pc.lo || base + kKeys > pc.hi) {
         // Keys outside the item: their weights are 0, and what the ring holds for their values
-        // and scales becomes 0 too (another warp of the chunk writes the same).
-        uint4* v = reinterpret_cast<uint4*>(ring + (2 * st + 1) * C::kTile);
-        for (int x = lane; x < C::kTile / 16; x += 32) {
+        // and scales becomes 0 too (another warp of the chunk writes the same).  With a cap so do
+        // the keys: the way to tanh is chosen by all of a warp's scores.
+        const bool keys_too = kScored && p.cap2 > 0.f;
+        constexpr int kVecs = C::kTile / 16;
+        uint4* tiles = reinterpret_cast<uint4*>(ring + 2 * st * C::kTile);  // k, v
+        for (int x = (keys_too ? 0 : kVecs) + lane; x < 2 * kVecs; x += 32) {
           const int key = base + x / (C::kPitch / 16) % kKeys;
-          if (key < pc.lo || key >= pc.hi) v[x] = make_uint4(0, 0, 0, 0);
+          if (key < pc.lo || key >= pc.hi) tiles[x] = make_uint4(0, 0, 0, 0);
         }
         if constexpr (kQuant)
-          for (int x = lane; x < kKeys; x += 32)
-            if (base + x < pc.lo || base + x >= pc.hi) scales[(2 * st + 1) * kKeys + x] = 0.f;
+          for (int x = (keys_too ? 0 : kKeys) + lane; x < 2 * kKeys; x += 32) {
+            const int key = base + x % kKeys;
+            if (key < pc.lo || key >= pc.hi) scales[2 * st * kKeys + x] = 0.f;
+          }
         fence_proxy_async_smem();  // before the copies that follow these writes
         __syncwarp();
       }

@@ -62,3 +62,54 @@ def test_values_near_fp32s_lower_end(kind, least, code, tiny, counts, group, d, 
     assert (np.abs(np64(o) - ref["o"]) <= bo).all()
     assert (np.abs(np64(lse) - ref["lse"]) <= bl).all()
     batch.seqs.check()
+
+
+def _fill_unseen(batch, value, lo):
+    """Slots that no row sees become `value`: the keys' and values' channels, or their scales over
+    codes of a large number.  lo: the first position that some row of each sequence sees."""
+    seen = torch.zeros((batch.body.shape[0], batch.page), dtype=torch.bool, device="cuda")
+    for b, length in enumerate(batch.lens):
+        seen[_slots(batch, b, np.arange(min(lo[b], length), length))] = True
+    g, t = (~seen).nonzero(as_tuple=True)
+    if batch.kind == "bf16":
+        batch.body[g, :, :, t] = value
+    else:
+        batch.body.view(torch.int8)[g, :, :, t] = 126  # 448 as e4m3
+        batch.scale[g, :, :, t] = value
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("cap,bias", [(50.0, False), (50.0, True), (0.0, True), (0.0, False)])
+@pytest.mark.parametrize("lens,counts,group,d,page,window", [
+    ([5, 700, 33], None, 4, 128, 16, None), ([5, 700, 33], None, 4, 64, 16, None),
+    ([70, 300, 2], [3, 4, 2], 4, 128, 16, 40), ([70, 300, 9], [8, 5, 3], 8, 64, 32, 37)])
+def test_what_no_row_sees_changes_no_bit(kind, cap, bias, lens, counts, group, d, page, window):
+    """Unused slots of the pool and what is left of earlier calls in the kernel's ring may hold any
+    finite number too.  Scores are far below the cap, where tanh is taken by its polynomial; those of
+    the unseen keys would be beyond its reach."""
+    batch = Batch(kind, lens, counts, 2, d, page, seed=21)
+    new = np.ones(len(lens), int) if counts is None else np.asarray(counts)
+    lo = np.zeros(len(lens), int) if window is None else \
+        np.maximum(np.asarray(lens) - new - window + 1, 0)
+    q = _q(batch.n, 2 * group, d, 2, 0.5)
+    slopes = torch.tensor([2.0 ** -(4 + h) for h in range(2 * group)], device="cuda") if bias \
+        else None
+    score = M.Score(cap, slopes) if cap or bias else None
+    # a batch whose keys are all large, to leave them in the ring
+    large = Batch(kind, [4000] * 40, None, 2, d, page, seed=22, fill=False)
+    _fill_unseen(large, 3e3, [4000] * 40)
+    large_q = _q(40, 2 * group, d, 3)
+
+    def run():
+        return M.attn_cached(batch.cache, batch.seqs, q, score=score,
+                             window=M.WINDOW_INF if window is None else window)
+
+    want = None
+    for value in (0.0, 3e3, -3e3, 0.0):
+        _fill_unseen(batch, value, lo)
+        for _ in range(3):
+            M.attn_cached(large.cache, large.seqs, large_q, score=score)
+            got = run()
+            want = want or got
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert all(bool(torch.isfinite(x).all()) for x in want)
