@@ -173,7 +173,14 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache(const __grid_constant__ C
     if (tile < tiles && lane < p.run)
       places[buf][lane] = i < s.n ? place_of(s, p.perm ? p.perm[i] : i) : Place{-2, 0};
   };
-  if (warp == 0) look(blockIdx.x, 0);
+  if (warp == 0) {
+    look(blockIdx.x, 0);
+  } else if (s.start && s.status) {
+    // sequences that no row leads to may be out of bounds too (without start each has its row)
+    constexpr int kLookers = kThreads - 32;
+    for (long long b = blockIdx.x * kLookers + threadIdx.x - 32; b < s.n_seqs; b += gridDim.x * kLookers)
+      seq_at<true>(s, (int)b);
+  }
   int buf = 0;
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
     __syncthreads();

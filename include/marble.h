@@ -632,10 +632,12 @@ typedef struct {
  * a call needs may hold anything.  All arrays are read when the kernels run.
  * What is out of bounds when they run (an entry outside [0, n_pages) where a page is needed, lens
  * outside [0, table_pages * page_tokens] or above 2^31 - 65536, a start that decreases or passes
- * n_tokens) touches no memory outside the arrays; the results of that sequence are then unspecified, nothing of a bad
- * page is written, and *status, if given, gets MARBLE_SEQS_BAD.  The kernels only ever set bits
- * of *status; a wait in a kernel that runs out of time (marble_set_wait_limit_ns) sets
- * MARBLE_SEQS_TIMEOUT, and the call's results are then unspecified. */
+ * n_tokens) touches no memory outside the arrays; the results of that sequence (of all, where
+ * start is bad: it says whose the rows are) are then unspecified, nothing of a bad page is
+ * written, and *status, if given, gets MARBLE_SEQS_BAD, whether or not the sequence has rows.
+ * The kernels only ever set bits of *status; a wait in a kernel that runs out of time
+ * (marble_set_wait_limit_ns) sets MARBLE_SEQS_TIMEOUT, and the call's results are then
+ * unspecified: without a status nothing tells. */
 #define MARBLE_SEQS_TIMEOUT 1
 #define MARBLE_SEQS_BAD 2
 typedef struct {

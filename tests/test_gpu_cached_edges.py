@@ -113,3 +113,41 @@ def test_what_no_row_sees_changes_no_bit(kind, cap, bias, lens, counts, group, d
             want = want or got
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert all(bool(torch.isfinite(x).all()) for x in want)
+
+
+@pytest.mark.parametrize("call", ["write", "read"])
+@pytest.mark.parametrize("start,lens", [
+    ([0, 10, 5, 20], [16, 16, 16]),      # one that decreases; the rows' own look-ups miss it
+    ([0, 8, 20, 20], [16, 16, -3]),      # lens of sequences without rows
+    ([0, 20, 20, 20], [32, 1 << 20, 0]),
+    ([0, 20, 20, 1 << 20], [32, 0, 0])])
+def test_bad_metadata_of_sequences_that_no_row_leads_to(call, start, lens):
+    """What is out of bounds is told whichever sequence holds it."""
+    batch = Batch("bf16", [32, 32, 32], [8, 8, 4], 2, 64, 16)
+    k, v = (_q(20, 2, 64, s) for s in (4, 5))
+
+    def run():
+        if call == "write":
+            M.cache_write(batch.cache, batch.seqs, k, v)
+        else:
+            M.cache_read(batch.cache, batch.seqs, n=20)
+
+    run()
+    batch.seqs.check()
+    batch.seqs.start.copy_(torch.tensor(start, dtype=torch.int32))
+    batch.seqs.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    run()
+    assert int(batch.status) == M.SEQS_BAD
+
+
+def test_many_sequences_without_rows_are_all_looked_at():
+    batch = Batch("bf16", [16] * 3000, [1] * 2 + [0] * 2998, 1, 64, 16)
+    k, v = (_q(2, 1, 64, s) for s in (4, 5))
+    M.cache_write(batch.cache, batch.seqs, k, v)
+    batch.seqs.check()
+    for b in (2, 224, 225, 1500, 2999):
+        batch.seqs.lens[b] = 17
+        M.cache_write(batch.cache, batch.seqs, k, v)
+        assert int(batch.status) == M.SEQS_BAD
+        batch.seqs.lens[b] = 16
+        batch.status.zero_()
