@@ -937,6 +937,11 @@ marble_status_t check_cache(const marble_cache_t* c, const marble_seqs_t* s, int
       if (stride < heads || stride % 4 || stride >= ((int64_t)1 << 38))
         return fail(MARBLE_ERR_INVALID_ARG,
                     "a page stride of the scales must hold the page's heads and be a multiple of 4");
+  // (so products of pages and strides do not overflow)
+  const int64_t most = ((int64_t)1 << 60) / c->n_pages;
+  if (c->k_stride * es > most || c->v_stride * es > most ||
+      (quant && (c->k_scale_stride * 4 > most || c->v_scale_stride * 4 > most)))
+    return fail(MARBLE_ERR_INVALID_ARG, "the pages must lie within 2^60 bytes");
   if (s->n_seqs < 0 || s->n_seqs >= INT_MAX || s->table_pages < 1 ||
       s->table_stride < s->table_pages || s->table_stride > ((int64_t)1 << 31))
     return fail(MARBLE_ERR_INVALID_ARG,

@@ -613,7 +613,7 @@ typedef struct {
   int32_t type;           /* marble_cache_type_t */
   int32_t hkv, d;         /* d = 64 or 128 */
   int32_t page_tokens;    /* a positive multiple of 16, at most 65536 */
-  int64_t n_pages;        /* >= 1, < 2^31 */
+  int64_t n_pages;        /* >= 1, < 2^31; all pages within 2^60 bytes */
   void *k, *v;            /* device, 16-byte aligned, pages k_stride / v_stride elements apart */
   int64_t k_stride, v_stride; /* hkv * page_tokens * d or more, multiples of 16 bytes, under 2^40
                                  bytes */
