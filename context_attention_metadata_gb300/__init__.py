@@ -1060,6 +1060,9 @@ def attn_cached(cache: Cache, seqs: Sequences, q, scale: float = 0.0, window: in
     width = hq * d
     if new_tokens <= 0:
         new_tokens = -(-n // max(1, seqs._n)) or 1
+    # (the descriptor holds 32 bits, and ctypes cuts off the others)
+    new_tokens = min(new_tokens, WINDOW_INF)
+    window = max(-1, min(window, WINDOW_INF))
     c = _AttnCached(q.data_ptr(), sq[0] if n > 1 else width, o.data_ptr(),
                     so[0] if n > 1 else width, None if lse is None else lse.data_ptr(), hq,
                     scale, window, 1 if span else 0, new_tokens, workspace.data_ptr())

@@ -151,3 +151,26 @@ def test_many_sequences_without_rows_are_all_looked_at():
         assert int(batch.status) == M.SEQS_BAD
         batch.seqs.lens[b] = 16
         batch.status.zero_()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+def test_windows_beyond_32_bits(kind):
+    """A window is any whole number: none of its bits are cut off on the way."""
+    batch = Batch(kind, [90, 40], [2, 3], 2, 64, 16)
+    q = _q(5, 4, 64, 6)
+    want = M.attn_cached(batch.cache, batch.seqs, q)
+    for window in (1 << 31, 1 << 32, (1 << 32) + 5, 1 << 70):
+        got = M.attn_cached(batch.cache, batch.seqs, q, window=window)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for window in (-1, -(1 << 31) - 1, -(1 << 32), 5 - (1 << 32)):
+        with pytest.raises(M.MarbleError, match="window"):
+            M.attn_cached(batch.cache, batch.seqs, q, window=window)
+    # the hint too
+    got = M.attn_cached(batch.cache, batch.seqs, q, new_tokens=(1 << 32) + 1)
+    ref = C.attention(np64(q), batch.k, batch.v, batch.lens, batch.start)
+    assert torch.isfinite(got[1]).all()
+    bo, bl = attn_bounds(ref, kind, 64, 90, max(np.abs(x).max() for x in batch.v))
+    assert (np.abs(np64(got[0]) - ref["o"]) <= bo).all()
+    assert (np.abs(np64(got[1]) - ref["lse"]) <= bl).all()
+    many = M.attn_cached(batch.cache, batch.seqs, q, new_tokens=1 << 20)
+    assert torch.equal(got[0], many[0]) and torch.equal(got[1], many[1])
