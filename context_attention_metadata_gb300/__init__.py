@@ -904,7 +904,9 @@ class Sequences:
     tensors: ``table`` [n_seqs, table_pages] (rows may be strided), ``lens`` [n_seqs] (the call's
     tokens counted), ``start`` [n_seqs + 1] or None (one row a sequence).  Their values are read
     when the kernels run; update them in place from step to step.  ``status`` (int32 [1], zeroed
-    by the caller, or None) collects SEQS_* bits; check() reads it."""
+    by the caller, or None) collects SEQS_* bits; check() reads it.  Without one, metadata out of
+    bounds and waits that ran out of time go unseen: results are then unspecified, and no call
+    says so."""
 
     def __init__(self, table, lens, start=None, status=None):
         import torch
@@ -938,9 +940,13 @@ class Sequences:
     def __reduce__(self):
         return Sequences, self._parts
 
-    def check(self):
-        """Wait for the status word and raise for what it holds."""
-        bits = 0 if self.status is None else int(self.status.item())
+    def check(self, stream=None):
+        """Wait for what was launched on the stream (None: the current one), the one that the calls
+        ran on, and raise for what the status word then holds.  Without a status there is nothing
+        to see."""
+        import torch
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            bits = 0 if self.status is None else int(self.status.item())
         if bits & SEQS_TIMEOUT:
             raise MarbleError(ERR_TIMEOUT, "a bounded wait in marble_attn_cached ran out")
         if bits & SEQS_BAD:

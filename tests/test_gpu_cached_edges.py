@@ -174,3 +174,25 @@ def test_windows_beyond_32_bits(kind):
     assert (np.abs(np64(got[1]) - ref["lse"]) <= bl).all()
     many = M.attn_cached(batch.cache, batch.seqs, q, new_tokens=1 << 20)
     assert torch.equal(got[0], many[0]) and torch.equal(got[1], many[1])
+
+
+@pytest.mark.parametrize("handed", [True, False])
+def test_check_waits_for_the_calls_stream(handed):
+    """The status of calls on another stream than the current one."""
+    batch = Batch("bf16", [40, 9], None, 2, 64, 16)
+    q = _q(2, 4, 64, 7)
+    M.attn_cached(batch.cache, batch.seqs, q)
+    batch.seqs.check()
+    batch.seqs.table[0, 1] = 1 << 30
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    M.attn_cached(batch.cache, batch.seqs, q, stream=side)
+    with pytest.raises(M.MarbleError, match="out of bounds"):
+        if handed:
+            batch.seqs.check(stream=side)
+        else:
+            with torch.cuda.stream(side):
+                batch.seqs.check()
+    torch.cuda.synchronize()
