@@ -196,3 +196,38 @@ def test_check_waits_for_the_calls_stream(handed):
             with torch.cuda.stream(side):
                 batch.seqs.check()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind,counts,group,d", [
+    ("bf16", None, 4, 128), ("int8", [8] * 12, 8, 128), ("e4m3", [1, 4] * 6, 8, 64)])
+def test_waits_that_run_out_of_time(kind, counts, group, d):
+    """With a limit of a nanosecond some wait of a long batch gives up: the call ends, the status says
+    so, and after the limit is put back the same call is right."""
+    lens = [20000 + 777 * b for b in range(12)]
+    batch = Batch(kind, lens, counts, 2, d, 16, fill=False)
+    batch.body.view(torch.int16 if kind == "bf16" else torch.int8).zero_()
+    if batch.scale is not None:
+        batch.scale.zero_()
+    q = _q(batch.n, 2 * group, d, 8)
+    run = lambda: M.attn_cached(batch.cache, batch.seqs, q)
+    M.set_wait_limit_ns(1)
+    try:
+        for _ in range(20):
+            run()
+        torch.cuda.synchronize()
+    finally:
+        M.set_wait_limit_ns(2_000_000_000)
+    assert int(batch.status) == M.SEQS_TIMEOUT
+    with pytest.raises(M.MarbleError, match="wait") as e:
+        batch.seqs.check()
+    assert e.value.status == M.ERR_TIMEOUT
+    batch.status.zero_()
+    o, lse = run()
+    batch.seqs.check()
+    # All scores are 0, all values are 0: weights and their sums are whole numbers below 2^24, so
+    # lse has log2's error (2^-23 of it), that of ln 2 and the product's (2^-24 each).
+    new = np.ones(12, int) if counts is None else np.asarray(counts)
+    seen = np.concatenate([n - c + 1 + np.arange(c) for n, c in zip(lens, new)])
+    assert not o.any()
+    np.testing.assert_allclose(np64(lse), np.broadcast_to(np.log(seen), lse.shape),
+                               rtol=2.0 ** -22)
