@@ -231,3 +231,27 @@ def test_waits_that_run_out_of_time(kind, counts, group, d):
     assert not o.any()
     np.testing.assert_allclose(np64(lse), np.broadcast_to(np.log(seen), lse.shape),
                                rtol=2.0 ** -22)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("cap", [1e-30, 1e-3, 1.0, 8.0, 50.0, 1e4, 1e30])
+@pytest.mark.parametrize("size", [1e-3, 1.0, 20.0])
+def test_caps_of_every_size(kind, cap, size):
+    """What a cap may add to a score's error is 4 u of the score: the polynomial and tanhf are off
+    relative to it (2^-22.7 and 2 ulp), and the cap's own roundings are counted with the factors."""
+    for counts, group, d, page in (([2, 3], 3, 128, 16), (None, 5, 64, 64)):
+        batch = Batch(kind, [600, 45], counts, 2, d, page, seed=31)
+        q = _q(batch.n, 2 * group, d, 9, size)
+        o, lse = M.attn_cached(batch.cache, batch.seqs, q, score=M.Score(cap, None))
+        ref = C.attention(np64(q), batch.k, batch.v, batch.lens, batch.start, cap=cap)
+        vmax = max(np.abs(x).max() for x in batch.v)
+        bo, bl = attn_bounds(ref, kind, d, 600, vmax)
+        more = 4 * 2.0 ** -24 * np.minimum(cap, ref["terms"])
+        bl = bl + more
+        bo = bo + (1 + HALF["bf16"]) * 2 * more.T[..., None] * ref["abs"]
+        assert (np.abs(np64(o) - ref["o"]) <= bo).all()
+        assert (np.abs(np64(lse) - ref["lse"]) <= bl).all()
+        if cap == 1e30:  # as without one: a score's cube over cap^2 is nothing
+            plain = M.attn_cached(batch.cache, batch.seqs, q)
+            assert (np.abs(np64(lse) - np64(plain[1])) <= 2 * bl).all()
+            assert (np.abs(np64(o) - np64(plain[0])) <= 2 * bo).all()
