@@ -39,8 +39,8 @@ marble_status_t run_attn_cached(int64_t n, const marble_cache_t* c, const marble
   if (scored) {
     p.slopes = score->slopes;
     if (score->cap > 0.f) {
-      p.to_cap = (float)(scale / score->cap);
       p.cap2 = (float)(score->cap * 1.4426950408889634);
+      p.inv_cap2 = (float)(1.0 / (score->cap * 1.4426950408889634));
     }
   }
   p.hkv = c->hkv;

@@ -100,7 +100,7 @@ struct AttnParams {
   long long q_stride, o_stride;
   const float* slopes;
   float scale2;      // scale * log2 e
-  float to_cap;      // scale / cap
+  float inv_cap2;    // 1 / cap2
   float cap2;        // cap * log2 e, 0: none
   int hkv, group, hq;
   int window, span;
@@ -674,8 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
       float m2[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        m2[x] = __shfl_sync(0xffffffffu, up, 4 * (2 * qt + x)) *
-                (kScored && p.cap2 > 0.f ? p.to_cap : p.scale2);
+        m2[x] = __shfl_sync(0xffffffffu, up, 4 * (2 * qt + x)) * p.scale2;
         const RowAt ra = row_at(p, pc.s, pc.head, row0 + 8 * t + 2 * qt + x);
         pos[t][x] = ra.live ? ra.pos : -1;
         slope[t][x] = 0.f;
@@ -803,7 +802,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
           };
           if (p.cap2 > 0.f) {
             each(scaled);
-            // tanh by its polynomial where all of the warp's scores are within its reach (score.cuh)
+            // tanh by its polynomial where all of the warp's scores are within its reach (score.cuh).
+            // The scores are divided by the cap only here: its quotient with the rows' and keys'
+            // factors could be below fp32's range.
+            const float reach = 0.875f * p.cap2;
             float top = 0.f;
             each([&](F2 v, int, int) {
               float v0, v1;
@@ -811,19 +813,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
               top = fmaxf(top, fmaxf(fabsf(v0), fabsf(v1)));
               return v;
             });
-            if (__any_sync(0xffffffffu, top > 0.875f)) {
+            if (__any_sync(0xffffffffu, top > reach)) {
               each([&](F2 v, int, int) {
                 float v0, v1;
                 split(v, &v0, &v1);
-                return f2(p.cap2 * tanhf(v0), p.cap2 * tanhf(v1));
+                return f2(p.cap2 * tanhf(v0 * p.inv_cap2), p.cap2 * tanhf(v1 * p.inv_cap2));
               });
             } else {  // (a NaN's way too)
               each([&](F2 v, int, int) {
-                const F2 u = mul2(v, v);
+                const F2 y = mul2(v, f2(p.inv_cap2)), u = mul2(y, y);
                 F2 r = f2((float)tanh_coef(5));
 #pragma unroll
                 for (int i = 4; i >= 0; --i) r = fma2(r, u, f2((float)tanh_coef(i)));
-                return mul2(mul2(r, v), f2(p.cap2));
+                return mul2(r, v);
               });
             }
             if (p.slopes) each(biased);

@@ -255,3 +255,23 @@ def test_caps_of_every_size(kind, cap, size):
             plain = M.attn_cached(batch.cache, batch.seqs, q)
             assert (np.abs(np64(lse) - np64(plain[1])) <= 2 * bl).all()
             assert (np.abs(np64(o) - np64(plain[0])) <= 2 * bo).all()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("cap", [50.0, 1e30])
+@pytest.mark.parametrize("down", [20, 40])
+def test_caps_of_small_queries_and_large_keys(kind, cap, down):
+    """Scores of ordinary size whose factors are not, far below the cap."""
+    batch = Batch(kind, [600, 45], [2, 3], 2, 128, 16, seed=32)
+    for b, length in enumerate(batch.lens):
+        g, t = _slots(batch, b, np.arange(length))
+        batch.scale[g, 0, :, t] *= 2.0 ** down
+        batch.k[b] = batch.k[b] * 2.0 ** down
+    q = (_q(batch.n, 6, 128, 10).float() * 2.0 ** -down).bfloat16()
+    o, lse = M.attn_cached(batch.cache, batch.seqs, q, score=M.Score(cap, None))
+    ref = C.attention(np64(q), batch.k, batch.v, batch.lens, batch.start, cap=cap)
+    bo, bl = attn_bounds(ref, kind, 128, 600, max(np.abs(x).max() for x in batch.v))
+    more = 4 * 2.0 ** -24 * np.minimum(cap, ref["terms"])
+    bo = bo + (1 + HALF["bf16"]) * 2 * more.T[..., None] * ref["abs"]
+    assert (np.abs(np64(lse) - ref["lse"]) <= bl + more).all()
+    assert (np.abs(np64(o) - ref["o"]) <= bo).all()
