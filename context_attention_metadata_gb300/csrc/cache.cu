@@ -51,7 +51,7 @@ __device__ __forceinline__ Place place_of(const SeqsParams& s, long long row) {
     // the sequence whose rows end first behind `row`
     int lo = 0, hi = s.n_seqs;
     while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
+      const int mid = lo + ((hi - lo) >> 1);  // (the sum may pass 2^31)
       if (__ldg(s.start + mid + 1) <= row) lo = mid + 1; else hi = mid;
     }
     b = lo;

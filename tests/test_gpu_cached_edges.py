@@ -275,3 +275,23 @@ def test_caps_of_small_queries_and_large_keys(kind, cap, down):
     bo = bo + (1 + HALF["bf16"]) * 2 * more.T[..., None] * ref["abs"]
     assert (np.abs(np64(lse) - ref["lse"]) <= bl + more).all()
     assert (np.abs(np64(o) - ref["o"]) <= bo).all()
+
+
+def test_more_than_2_to_30_sequences():
+    """All places of a batch but the last are without rows: the search for a row's sequence adds
+    numbers of more than 31 bits."""
+    n = (1 << 30) + 5
+    table, lens = (torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((n, 1), (n,)))
+    start = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    table[-1], lens[-1], start[-1] = 1, 10, 4
+    cache = M.Cache.empty(2, 1, 16, 64)
+    cache.k.zero_()
+    cache.v.zero_()
+    seqs = M.Sequences(table, lens, start)
+    k, v = (_q(4, 1, 64, s) for s in (51, 52))
+    M.cache_write(cache, seqs, k, v)
+    for x, y in ((cache.k, k), (cache.v, v)):
+        assert not x[0].any() and not x[1, 0, :6].any() and not x[1, 0, 10:].any()
+        assert torch.equal(x[1, 0, 6:10], y[:, 0])
+    rk, rv = M.cache_read(cache, seqs, n=4)
+    assert torch.equal(rk, k) and torch.equal(rv, v)
