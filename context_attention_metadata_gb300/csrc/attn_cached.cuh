@@ -395,8 +395,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attn_cached(const __grid_consta
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // this CTA's range of units
-  const int ns = p.seqs.n_seqs, share = (ns + kThreads - 1) / kThreads;
-  const int b0 = min(tid * share, ns), b1 = min(b0 + share, ns);
+  // (n_seqs is at least 1; no sum here passes 2^31)
+  const int ns = p.seqs.n_seqs, share = (ns - 1) / kThreads + 1;
+  const int b0 = min(tid * share, ns), b1 = b0 + min(share, ns - b0);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
     const Work w = blockIdx.x == 0 ? work_of<kKeys, kNt, true>(p, b) : work_of<kKeys, kNt, false>(p, b);
