@@ -12,7 +12,7 @@
 // of k or v of all rows.  Those are contiguous in a page, and the warps' heads are contiguous in
 // the rows, so that both sides' accesses fall together: with a warp for all heads of a row the
 // figures below were 271, 324 and 293 us.  Measured, heads of 8 x 128: 213,194 rows in plan order into
-// e4m3 207 us (6.39 TB/s, 95% of a plain copy's rate), into bf16 268 (97%); 262,144 rows out of int8
+// e4m3 208 us (6.35 TB/s, 95% of a plain copy's rate), into bf16 268 (97%); 262,144 rows out of int8
 // 250 us (97%), out of bf16 328 (98%).
 #include <algorithm>
 #include <cstring>
@@ -25,6 +25,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRun = 16;  // rows of a CTA's tile, at most
+constexpr int kLooks = 4;  // sequences that a thread looks over at a time
 
 struct CachePart {
   char* rows;              // bf16 [n, hkv, d], null: not in the call
@@ -39,6 +40,7 @@ struct CacheParams {
   const int32_t* perm;     // plan index -> original index, or null
   int hkv;
   int run;                 // rows of a tile
+  unsigned ctas;           // that move rows
 };
 
 // where the token of row i is: its page (-1: none, -2: the row belongs to no sequence) and slot
@@ -157,7 +159,20 @@ __device__ __forceinline__ void restore(const uint4& codes, float scale, uint32_
   }
 }
 
-template <int D, int kType, bool kWrite>
+// Sequences that no row leads to may be out of bounds too.  Several a time, whose loads are under way
+// together.
+__device__ __forceinline__ void look_over(const SeqsParams& s, int cta, int ctas) {
+  bool off = false;
+#pragma unroll kLooks
+  for (long long b = cta * kThreads + threadIdx.x; b < s.n_seqs; b += ctas * kThreads)
+    off |= seq_off(s, __ldg(s.lens + b), __ldg(s.start + b), __ldg(s.start + b + 1));
+  if (off) seqs_bad(s);
+}
+
+// kLook: there are CTAs behind those of the rows that look the sequences over.  (A variant of its
+// own, as the e4m3 write is at the limit of its registers: with them in
+// one kernel the large write above takes 209.4 instead of 208.4 us, inlined among the rows' 212.)
+template <int D, int kType, bool kWrite, bool kLook>
 __global__ void __launch_bounds__(kThreads, 4) k_cache(const __grid_constant__ CacheParams p) {
   constexpr int kTpr = D / 16, kRows = 32 / kTpr, kEs = kType == MARBLE_CACHE_BF16 ? 2 : 1;
   // passes of kRows rows whose loads are under way together (of 1, 2 and 4, by time: more loads do
@@ -166,6 +181,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache(const __grid_constant__ C
   __shared__ Place places[2][kRun];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % kTpr, sub = lane / kTpr;
   const SeqsParams& s = p.seqs;
+  if (kLook && blockIdx.x >= p.ctas) {
+    look_over(s, blockIdx.x - p.ctas, gridDim.x - p.ctas);
+    return;
+  }
+  const int ctas = kLook ? p.ctas : gridDim.x;
   const int tiles = (int)((s.n + p.run - 1) / p.run);
   const int steps = (p.run + kRows * kPasses - 1) / (kRows * kPasses);  // of a head's rows
   auto look = [&](int tile, int buf) {
@@ -173,18 +193,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache(const __grid_constant__ C
     if (tile < tiles && lane < p.run)
       places[buf][lane] = i < s.n ? place_of(s, p.perm ? p.perm[i] : i) : Place{-2, 0};
   };
-  if (warp == 0) {
-    look(blockIdx.x, 0);
-  } else if (s.start && s.status) {
-    // sequences that no row leads to may be out of bounds too (without start each has its row)
-    constexpr int kLookers = kThreads - 32;
-    for (long long b = blockIdx.x * kLookers + threadIdx.x - 32; b < s.n_seqs; b += gridDim.x * kLookers)
-      seq_at<true>(s, (int)b);
-  }
+  if (warp == 0) look(blockIdx.x, 0);
   int buf = 0;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+  for (int tile = blockIdx.x; tile < tiles; tile += ctas, buf ^= 1) {
     __syncthreads();
-    if (warp == 0) look(tile + gridDim.x, buf ^ 1);
+    if (warp == 0) look(tile + ctas, buf ^ 1);
     const long long i0 = (long long)tile * p.run;
     for (int unit = warp; unit < steps * 2 * p.hkv; unit += kWarps) {
       const int step = unit % steps, x = unit / steps & 1, h = unit / steps >> 1;
@@ -265,26 +278,34 @@ cudaError_t launch_cache(bool write, const marble_plan_t* plan, int64_t n, const
   p.seqs = seqs_params(*seqs, *c, n);
   p.perm = plan ? plan->perm : nullptr;
   p.hkv = c->hkv;
-  // Tiles of up to 32 rows, fewer where that leaves SMs without work; as many CTAs as run at once,
-  // or fewer that take the same number of rounds.
+  // Tiles of up to kRun rows, fewer where that leaves SMs without work; as many CTAs as run at once,
+  // or fewer that take the same number of rounds.  With start and a status, one CTA for 1024
+  // sequences beside them (without start each sequence has its row).
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   p.run = kRun;
   while (p.run > 512 / c->d && n < (int64_t)p.run * sms * 4) p.run /= 2;
-  const int64_t tiles = (n + p.run - 1) / p.run, most = (int64_t)sms * 4;
+  const int64_t lookers = !seqs->start || !seqs->status ? 0
+                          : std::min<int64_t>((seqs->n_seqs - 1) / (kThreads * kLooks) + 1, sms);
+  const int64_t tiles = (n + p.run - 1) / p.run, most = (int64_t)sms * 4 - (lookers ? 1 : 0);
   const int64_t rounds = (tiles + most - 1) / most;
-  const int grid = (int)((tiles + rounds - 1) / rounds);
-  auto pick = [&](auto dd) {
+  p.ctas = (unsigned)((tiles + rounds - 1) / rounds);
+  const unsigned grid = (unsigned)(p.ctas + lookers);
+  auto pick = [&](auto dd, auto ll) {
     constexpr int D = decltype(dd)::value;
+    constexpr bool L = decltype(ll)::value;
     if (c->type == MARBLE_CACHE_BF16)
-      return write ? k_cache<D, MARBLE_CACHE_BF16, true> : k_cache<D, MARBLE_CACHE_BF16, false>;
+      return write ? k_cache<D, MARBLE_CACHE_BF16, true, L> : k_cache<D, MARBLE_CACHE_BF16, false, L>;
     if (c->type == MARBLE_CACHE_E4M3)
-      return write ? k_cache<D, MARBLE_CACHE_E4M3, true> : k_cache<D, MARBLE_CACHE_E4M3, false>;
-    return write ? k_cache<D, MARBLE_CACHE_INT8, true> : k_cache<D, MARBLE_CACHE_INT8, false>;
+      return write ? k_cache<D, MARBLE_CACHE_E4M3, true, L> : k_cache<D, MARBLE_CACHE_E4M3, false, L>;
+    return write ? k_cache<D, MARBLE_CACHE_INT8, true, L> : k_cache<D, MARBLE_CACHE_INT8, false, L>;
   };
-  auto kernel = c->d == 128 ? pick(std::integral_constant<int, 128>{})
-                            : pick(std::integral_constant<int, 64>{});
+  auto at_d = [&](auto ll) {
+    return c->d == 128 ? pick(std::integral_constant<int, 128>{}, ll)
+                       : pick(std::integral_constant<int, 64>{}, ll);
+  };
+  auto kernel = lookers ? at_d(std::true_type{}) : at_d(std::false_type{});
   kernel<<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }

@@ -45,6 +45,10 @@ __device__ __forceinline__ void seqs_bad(const SeqsParams& p) {
 struct Seq {
   int first, count, len;
 };
+// is a sequence's length or its rows [s0, s1) out of bounds?
+__device__ __forceinline__ bool seq_off(const SeqsParams& p, int len, int s0, int s1) {
+  return len < 0 || len > p.top || s0 < 0 || s1 < s0 || s1 > (int)p.n;
+}
 template <bool kTell>
 __device__ __forceinline__ Seq seq_at(const SeqsParams& p, int b) {
   const int len = p.lens[b];
@@ -54,7 +58,7 @@ __device__ __forceinline__ Seq seq_at(const SeqsParams& p, int b) {
     s1 = p.start[b + 1];
   }
   const int n = (int)p.n;
-  if (kTell && (len < 0 || len > p.top || s0 < 0 || s1 < s0 || s1 > n)) seqs_bad(p);
+  if (kTell && seq_off(p, len, s0, s1)) seqs_bad(p);
   Seq s;
   s.first = min(max(s0, 0), n);
   s.count = min(max(s1, s.first), n) - s.first;
