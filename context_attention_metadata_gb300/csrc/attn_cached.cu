@@ -20,8 +20,14 @@ marble_status_t run_attn_cached(int64_t n, const marble_cache_t* c, const marble
   const int keys = !quant && c->d == 128 ? 32 : 64;
   p.box = 16;
   while (p.box < keys && c->page_tokens % (2 * p.box) == 0) p.box *= 2;
-  if (!cached::pages_map(&p.kmap, c->k, c->type, c->k_stride, *c, p.box) ||
-      !cached::pages_map(&p.vmap, c->v, c->type, c->v_stride, *c, p.box))
+  const auto maps = [&] {
+    return cached::pages_map(&p.kmap, c->k, c->type, c->k_stride, *c, p.box) &&
+           cached::pages_map(&p.vmap, c->v, c->type, c->v_stride, *c, p.box);
+  };
+  // (a thread that no call has given the device's context yet gets it from cudaSetDevice)
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  if (!maps() && (cudaSetDevice(dev) != cudaSuccess || !maps()))
     return fail(MARBLE_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
   p.seqs = seqs_params(*seqs, *c, n);
   p.k_scale = c->k_scale;
@@ -57,8 +63,6 @@ marble_status_t run_attn_cached(int64_t n, const marble_cache_t* c, const marble
   p.grain = nt == 1 ? 5 : 4 * 5;
   p.limit_ns = wait_limit_ns();
   p.drain_ns = std::max<uint64_t>(p.limit_ns, 1000000000ull);  // copies under way always land
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   // workspace: a word for timeouts without a status, the joins, the pieces
   const int64_t piece = p.rows * (int64_t)(c->d + 2) * 4;

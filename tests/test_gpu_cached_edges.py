@@ -295,3 +295,29 @@ def test_more_than_2_to_30_sequences():
         assert torch.equal(x[1, 0, 6:10], y[:, 0])
     rk, rv = M.cache_read(cache, seqs, n=4)
     assert torch.equal(rk, k) and torch.equal(rv, v)
+
+
+def test_a_threads_first_call():
+    """A thread that has made no CUDA call before: nothing in the call itself relies on one."""
+    import threading
+    batch = Batch("bf16", [90, 30], None, 2, 64, 16, seed=61)
+    q = _q(2, 4, 64, 62)
+    want = M.attn_cached(batch.cache, batch.seqs, q)
+    out = (torch.empty_like(q), torch.empty((4, 2), device="cuda"))
+    ws = torch.empty(M.ATTN_CACHED_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    failed = []
+
+    def work():
+        try:
+            M.attn_cached(batch.cache, batch.seqs, q, out=out, workspace=ws, stream=stream)
+        except M.MarbleError as e:
+            failed.append(e)
+
+    thread = threading.Thread(target=work)
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert not failed, failed[0]
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
