@@ -1,6 +1,7 @@
 // The attention over the paged cache (attn_cached.cuh): what a call's kernels get, and the kernels
 // for heads of 128.
 #include <cstring>
+#include <mutex>
 
 #include "attn_cached.cuh"
 
@@ -73,6 +74,10 @@ marble_status_t run_attn_cached(int64_t n, const marble_cache_t* c, const marble
   p.joins = reinterpret_cast<int4*>(ws + 256);
   p.part_ml = reinterpret_cast<float2*>(ws + 65536);
   p.part_o = reinterpret_cast<float*>(ws + 65536 + 2 * (int64_t)grid * p.rows * 8);
+  // The call's two kernels follow each other in the stream: another thread's call with the same
+  // workspace, ordered by the stream, must not come between them.
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
   return c->d == 128 ? launch_d128(p, c->type, nt, scored, grid, (int)rows, s)
                      : launch_d64(p, c->type, nt, scored, grid, (int)rows, s);
 }

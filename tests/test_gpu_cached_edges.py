@@ -321,3 +321,40 @@ def test_a_threads_first_call():
     torch.cuda.synchronize()
     assert not failed, failed[0]
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_threads_on_one_stream(side):
+    """Calls with one workspace on one stream from several threads at once, as those on the same
+    sequences are: a call's two kernels follow each other."""
+    import ctypes
+    import threading
+    batch = Batch("bf16", [9000, 3000], None, 2, 64, 64, seed=61)
+    qs = [_q(2, 8, 64, s) for s in range(62, 70)]
+    stream = torch.cuda.Stream() if side else torch.cuda.current_stream()
+    want = [M.attn_cached(batch.cache, batch.seqs, q) for q in qs]
+    ws = torch.empty(M.ATTN_CACHED_WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros((1000, *q.shape), dtype=torch.bfloat16, device="cuda") for q in qs]
+    torch.cuda.synchronize()
+    call, raw = M.lib().marble_attn_cached, stream.cuda_stream
+    gate = threading.Barrier(len(qs))
+    failed = []
+
+    def work(q, out):
+        descs = [M._AttnCached(q.data_ptr(), 512, o.data_ptr(), 512, None, 8, 0.0, M.WINDOW_INF, 0,
+                               1, ws.data_ptr()) for o in out]
+        descs = [ctypes.byref(d) for d in descs]
+        gate.wait()
+        for d in descs:
+            if call(2, batch.cache._ref, batch.seqs._ref, d, None, raw) != M.OK:
+                failed.append(M.lib().marble_last_error().decode())
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(qs, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed[0]
+    wrong = [int((out != w[0]).flatten(1).any(1).sum()) for out, w in zip(outs, want)]
+    assert wrong == [0] * len(qs)
