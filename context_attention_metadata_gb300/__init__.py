@@ -1027,7 +1027,7 @@ def attn_cached(cache: Cache, seqs: Sequences, q, scale: float = 0.0, window: in
     the rows of a sequence all see each other; ``new_tokens``: how many rows a sequence has at
     most, a hint (0: n over the number of sequences).  ``workspace``: uint8 CUDA tensor of
     ATTN_CACHED_WORKSPACE_BYTES for this call alone, or None (the sequences keep one for every
-    stream; a captured call gets its own).
+    stream; a call that torch.cuda.graph captures gets one in its graph's memory).
     Returns (o, lse), bf16 [n, hq, d] and fp32 [hq, n]: ``out`` (its lse may be None) or new
     tensors; rows of no sequence are left as they are (undefined in new tensors)."""
     import torch

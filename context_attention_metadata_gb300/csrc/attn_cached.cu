@@ -51,7 +51,6 @@ marble_status_t run_attn_cached(int64_t n, const marble_cache_t* c, const marble
     }
   }
   p.hkv = c->hkv;
-  p.hq = a->hq;
   p.group = a->hq / c->hkv;
   p.window = a->window;
   p.span = a->span ? 1 : 0;

@@ -3,15 +3,15 @@
 //   s_j = scale q.k_j (capped, lowered by a slope times the distance, in base 2),
 //   m = running maximum, p_j = 2^(s_j - m), l = sum p_j, O = sum p_j v_j,   o = O / l.
 //
-// Bound by memory for up to 16 rows (new tokens x q heads of a group) of a kv head: every key and
-// value is read once, at 2 or 1 bytes a channel.  One sequence of 1,048,576 tokens, 8 kv heads of
+// Bound by memory for few rows (new tokens x q heads of a group) of a kv head: every key and value
+// is read once, at 2 or 1 bytes a channel.  One sequence of 1,048,576 tokens, 8 kv heads of
 // 128, microseconds, and the time that a plain copy's rate gives:
 //   rows        4       12      20      64     copy
-//   bf16       591     626     655    1137      642
-//   e4m3       335     387     577    1111      331
-//   int8       337     398     600    1159      331
-// and with heads of 64, 4 rows: bf16 306 (321), e4m3 183 (171).  Above 16 rows the computing
-// warps' instructions are the bound (of bf16 above 32).
+//   bf16       593     628     657    1142      642
+//   e4m3       336     388     580    1115      331
+//   int8       338     398     600    1159      331
+// and with heads of 64, 4 rows: bf16 306 (321), e4m3 180 to 184 (171).  From 12 rows on for 8-bit
+// types, above 20 for bf16, the computing warps' instructions are the bound.
 //
 // - An item is a (sequence, kv head, tile of 8, 16, 32 or 64 rows); its cost is its chunks of keys
 //   and a constant.  Every CTA takes an equal range of the sum of all costs, so that ragged
@@ -74,7 +74,7 @@ struct Cfg {
   static constexpr int kSub = kNt == 2 && kQuant && D == 128 ? 32 : kKeys;
   static constexpr int kTile = kKeys * kRow;
   static constexpr int kStages = kTile == 8192 ? 4 : 8;
-  static_assert(kStages % kWorkers == 0, "a place of the ring belongs to the same warps");
+  static_assert(kStages % kWorkers == 0, "a place keeps its warps while chunks are dealt the same way");
   static constexpr int kScales = kQuant ? kStages * 2 * kKeys * 4 : 0;
   // pieces that the fetching warp may be ahead; their q; the warps' O, m and l on their way together
   static constexpr int kPieces = kNt == 1 ? 4 : 2;
@@ -102,12 +102,12 @@ struct AttnParams {
   float scale2;      // scale * log2 e
   float inv_cap2;    // 1 / cap2
   float cap2;        // cap * log2 e, 0: none
-  int hkv, group, hq;
+  int hkv, group;
   int window, span;
   int row_warps;     // warps that an item's rows are split over, at most: 1, 2 or 4
   int rows, rows_log;  // of an item: 8 * kNt * row_warps
   int box;           // keys of a TMA box
-  int grain;         // units a CTA takes at least
+  int grain;         // as many CTAs work as the sum of units holds grains, rounded up
   float* part_o;     // [2 * CTAs][rows][D] pieces
   float2* part_ml;   // [2 * CTAs][rows]
   int4* joins;       // [CTAs][2]: pieces (0: none), the sequence's first row and rows; kv head, first row

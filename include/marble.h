@@ -666,8 +666,9 @@ marble_status_t marble_cache_write(const marble_plan_t *plan, int64_t n_tokens,
 /*
  * Read n_tokens rows back, bf16 (code * scale rounded once): dst->k and dst->v [n_tokens, hkv, d].
  * With a plan dst is in plan order, ready for the attention calls (a chunk of a prompt behind its
- * cached prefix: one row for each of both).  Rows without a token become zeros; rows that belong
- * to no sequence stay as they are.  dst may not overlap the cache, nor its tensors each other.
+ * cached prefix: those calls take a q row for every row of both, and the prefix's are wasted).
+ * Rows without a token become zeros; rows that belong to no sequence stay as they are.  dst may not
+ * overlap the cache, nor its tensors each other.
  * May be captured into a graph.  Errors: INVALID_ARG; CUDA.
  */
 marble_status_t marble_cache_read(const marble_plan_t *plan, int64_t n_tokens,
@@ -683,12 +684,13 @@ marble_status_t marble_cache_read(const marble_plan_t *plan, int64_t n_tokens,
  *   o = sum_j softmax(s)_j v_j as bf16,   lse = ln sum_j exp(s_j).
  * A row that sees nothing gives o = 0, lse = -inf.  Cached values that no row of a sequence sees
  * may be anything, infinities and NaN too; those that some row of it sees have to be finite.
- * Sums and the softmax are in fp32.  bf16 caches: the weights enter their product with v as two
- * bf16 terms (16 bits).  8-bit caches: q enters in fp16 after a power of two for each row (no
- * bits are lost above 2^-29 of its largest channel), the weights (1 at the softmax's maximum),
- * times v's scale, in fp16 too (11 bits): with u the power of two at or above the largest of v's
- * scales among the keys that some row of the sequence sees, and at least 2^-120, products below
- * 2^-20 u lose bits and those below 2^-31 u are lost.
+ * Sums and the softmax are in fp32, before the division by the softmax's sum: with weights of up
+ * to 2^8 a key, values up to 2^119 / lens cannot overflow.  bf16 caches: the weights enter their
+ * product with v as two bf16 terms (16 bits).  8-bit caches: q enters in fp16 after a power of two
+ * for each row (no bits are lost above 2^-29 of its largest channel), the weights (1 at the
+ * softmax's maximum), times v's scale, in fp16 too (11 bits): with u the power of two at or above
+ * the largest of v's scales among the keys that some row of the sequence sees, and at least
+ * 2^-120, products below 2^-20 u lose bits and those below 2^-31 u are lost.
  * The keys of all (sequence, kv head, tile of up to 64 rows) are dealt evenly to the SMs, whatever
  * the lengths; the pieces of one softmax are joined in order, so that results do not depend on
  * timing.  Rows of a kv head beyond 64 read the cache again.
